@@ -509,6 +509,73 @@ lora_status_t lora_linear_forward_fp8(const void *x, const uint8_t *wq, const fl
                                       lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
                                       lora_stream_t stream);
 
+/* ---- between the blocks: residual addition and root-mean-square norm ------------- */
+
+/* The rows that a block's projections read: for every row t
+ *     z = x[t,:] + residual[t,:],   y = z / sqrt(mean(z^2) + eps) * weight
+ * residual_out gets z and y the normed row, each rounded once from fp32 (the
+ * norm is of the unrounded z).  All of `dtype`: x, residual, residual_out, y
+ * DEVICE [T, d], weight DEVICE [d].  residual may be NULL (z = x);
+ * residual_out may be NULL (z not stored).  residual_out may be residual's
+ * or x's own buffer and y may be x's or residual's (the same address;
+ * residual_out and y differ).  d a positive multiple of 8; eps finite and
+ * positive. */
+lora_status_t lora_add_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int32_t T,
+                               int32_t d, lora_dtype_t dtype, void *residual_out, void *y,
+                               lora_stream_t stream);
+
+/* The same for bf16 rows that feed an FP8 base weight: also the E4M3 codes
+ * and power-of-two scales of the rows of y, bitwise as lora_quantize_rows_fp8
+ * gives them for the stored y: yq DEVICE uint8 [T, d], y_scale DEVICE fp32
+ * [T].  y may be NULL (codes only: rows that no adapter reads).  d a positive
+ * multiple of 16.  Rows must be finite where the codes are used. */
+lora_status_t lora_add_rmsnorm_fp8(const void *x, const void *residual, const void *weight, float eps, int32_t T,
+                                   int32_t d, void *residual_out, void *y, uint8_t *yq, float *y_scale,
+                                   lora_stream_t stream);
+
+/* ---- the gated feed-forward pair --------------------------------------------------- */
+
+/* Gate and up of a feed-forward block, each with its own pool, and what is
+ * made of them, in one kernel: for every row t, a = ids[t],
+ *     g = x W_gate + s_a (x A_a) B_a   (pools[0]),
+ *     u = x W_up   + s_a (x A_a) B_a   (pools[1]),      h = act(g) * u
+ * with h rounded once from the fp32 g and u. */
+typedef enum {
+    LORA_ACT_SILU = 0,      /* x / (1 + exp(-x)) */
+    LORA_ACT_GELU = 1,      /* x times the normal distribution's cdf */
+    LORA_ACT_GELU_TANH = 2  /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+} lora_act_t;
+
+/* Workspace bytes for the two forwards below on batches of up to T rows and
+ * for the backward pass; 0 on bad arguments.  2 * max_rank <= 128.  d_out is
+ * h's width (0 in the forwards' sizes: no room for a K split, as in
+ * lora_workspace_bytes). */
+size_t lora_workspace_bytes_gated(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_out);
+size_t lora_workspace_bytes_gated_fp8(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out);
+
+/* x DEVICE [T, d_in], W_gate and W_up DEVICE [d_in, d_out], h DEVICE [T, d_out],
+ * of the pools' dtype; pools HOST [2] (gate, up) with the conditions of
+ * lora_linear_forward_sliced and one d_out.  gate and up DEVICE [T, d_out]
+ * keep g and u, each rounded once, for lora_gated_backward; both may be NULL.
+ * mode, ids and bad ids as in lora_linear_forward; a row whose slot is empty
+ * in one pool has only the other's term (and is recorded).  flags: 0 or
+ * LORA_FLAG_SEGMENTS_READY (segments built by lora_build_segments, by this
+ * function or by an SGMV-mode forward in this workspace for these ids). */
+lora_status_t lora_gated_forward(const void *x, const void *W_gate, const void *W_up, void *h, void *gate, void *up,
+                                 int32_t T, const lora_pool_t *pools, const int32_t *ids, lora_act_t act,
+                                 lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
+                                 lora_stream_t stream);
+
+/* The same on FP8 base weights (bf16 x, h and pools; d_in a multiple of 16):
+ * wq_* and w_scale_* from lora_quantize_weight_fp8.  xq and x_scale are the
+ * codes and scales of x's rows (lora_add_rmsnorm_fp8, lora_quantize_rows_fp8;
+ * DEVICE uint8 [T, d_in] and fp32 [T]); both NULL: x is quantized into ws. */
+lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const float *x_scale, const uint8_t *wq_gate,
+                                     const float *w_scale_gate, const uint8_t *wq_up, const float *w_scale_up,
+                                     void *h, void *gate, void *up, int32_t T, const lora_pool_t *pools,
+                                     const int32_t *ids, lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws,
+                                     size_t ws_bytes, lora_stream_t stream);
+
 /* ---- the layer without a caller workspace ---------------------------------------- */
 
 /* For callers that cannot allocate device memory at call time: code under

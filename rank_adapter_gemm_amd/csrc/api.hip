@@ -588,6 +588,144 @@ lora_status_t lora_linear_forward_fp8(const void *x, const uint8_t *wq, const fl
     return st;
 }
 
+// The gated pair's pools: two slices of one width.
+static lora_status_t check_pair(const lora_pool_t *pools) {
+    lora_status_t st = check_slices(pools, 2);
+    if (st != LORA_OK) return st;
+    return pools[0].d_out == pools[1].d_out ? LORA_OK : LORA_ERR_INVALID_ARGUMENT;
+}
+
+static inline bool valid_act(int32_t a) { return a == LORA_ACT_SILU || a == LORA_ACT_GELU || a == LORA_ACT_GELU_TANH; }
+
+// Segments (where the mode uses them) and both slices' rank vectors, then the
+// pair.  c holds everything but ids' order, v and the partials.
+static lora_status_t run_gated(gated_call &c, lora_mode_t mode, uint32_t flags, const ws_layout &L, void *ws,
+                               size_t ws_bytes, hipStream_t s) {
+    const bool sgmv = use_sgmv(mode, c.T);
+    if (sgmv && !(flags & LORA_FLAG_SEGMENTS_READY)) {
+        // every row's term goes into the pair's accumulators (h is not linear
+        // in it), so no segment is left to a separate expand
+        const lora_status_t st = launch_segments(c.ids, c.T, c.pools[0].n_slots, L, ws, s, 1);
+        if (st != LORA_OK) return st;
+    }
+    float *v = ws_ptr<float>(ws, L.v);
+    const lora_status_t st = launch_shrink(c.x, c.T, c.pools, 2, c.ids, sgmv, v, L, ws, s);
+    if (st != LORA_OK) return st;
+    c.v = v;
+    c.perm = sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr;
+    c.partial = ws_ptr<float>(ws, L.gemm_partial);
+    c.partial_bytes = ws_bytes - L.gemm_partial;
+    return launch_gated_forward(c, s);
+}
+
+size_t lora_workspace_bytes_gated(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_out) {
+    if (d_out < 0 || d_out > INT32_MAX / 2) return 0;
+    return lora_workspace_bytes_sliced(T, n_slots, max_rank, 2, 2 * d_out);
+}
+
+size_t lora_workspace_bytes_gated_fp8(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out) {
+    if (lora_workspace_bytes_gated(T, n_slots, max_rank, d_out) == 0 || d_in <= 0 || (d_in % 16)) return 0;
+    return make_ws_layout(T, n_slots, 2 * max_rank, 2 * d_out, d_in).total;
+}
+
+lora_status_t lora_gated_forward(const void *x, const void *W_gate, const void *W_up, void *h, void *gate, void *up,
+                                 int32_t T, const lora_pool_t *pools, const int32_t *ids, lora_act_t act,
+                                 lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
+                                 lora_stream_t stream) {
+    lora_status_t st = check_pair(pools);
+    if (st != LORA_OK) return st;
+    if (T < 0 || !valid_act(act) || !valid_mode(mode) || (flags & ~LORA_FLAG_SEGMENTS_READY) || !gate != !up)
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!x || !W_gate || !W_up || !h || !ids || !aligned16(x) || !aligned16(W_gate) || !aligned16(W_up) ||
+                  !aligned16(h) || !aligned16(gate) || !aligned16(up)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    ws_layout L;
+    st = check_ws(ws, ws_bytes, T, pools[0].n_slots, 2 * pools[0].max_rank, &L);
+    if (st != LORA_OK || T == 0) return st;
+    gated_call c{};
+    c.x = x;
+    c.W[0] = W_gate;
+    c.W[1] = W_up;
+    c.h = h;
+    c.gate = gate;
+    c.up = up;
+    c.T = T;
+    c.act = act;
+    c.pools = pools;
+    c.ids = ids;
+    return run_gated(c, mode, flags, L, ws, ws_bytes, hs(stream));
+}
+
+lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const float *x_scale, const uint8_t *wq_gate,
+                                     const float *w_scale_gate, const uint8_t *wq_up, const float *w_scale_up,
+                                     void *h, void *gate, void *up, int32_t T, const lora_pool_t *pools,
+                                     const int32_t *ids, lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws,
+                                     size_t ws_bytes, lora_stream_t stream) {
+    lora_status_t st = check_pair(pools);
+    if (st != LORA_OK) return st;
+    if (pools[0].dtype != LORA_BF16 || (pools[0].d_in % 16) || T < 0 || !valid_act(act) || !valid_mode(mode) ||
+        (flags & ~LORA_FLAG_SEGMENTS_READY) || !gate != !up || !xq != !x_scale)
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!x || !wq_gate || !w_scale_gate || !wq_up || !w_scale_up || !h || !ids || !aligned16(x) ||
+                  !aligned16(xq) || !aligned16(x_scale) || !aligned16(wq_gate) || !aligned16(w_scale_gate) ||
+                  !aligned16(wq_up) || !aligned16(w_scale_up) || !aligned16(h) || !aligned16(gate) ||
+                  !aligned16(up)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    ws_layout L;
+    st = check_ws_fp8(ws, ws_bytes, T, pools[0].n_slots, 2 * pools[0].max_rank, xq ? 0 : pools[0].d_in, &L);
+    if (st != LORA_OK || T == 0) return st;
+    const hipStream_t s = hs(stream);
+    if (!xq) {
+        uint8_t *q = ws_ptr<uint8_t>(ws, L.xq);
+        float *qs = ws_ptr<float>(ws, L.xs);
+        st = launch_quant_rows_fp8(x, T, pools[0].d_in, q, qs, s);
+        if (st != LORA_OK) return st;
+        xq = q;
+        x_scale = qs;
+    }
+    gated_call c{};
+    c.x = x;
+    c.xq = xq;
+    c.xs = x_scale;
+    c.wq[0] = wq_gate;
+    c.wq[1] = wq_up;
+    c.wsc[0] = w_scale_gate;
+    c.wsc[1] = w_scale_up;
+    c.h = h;
+    c.gate = gate;
+    c.up = up;
+    c.T = T;
+    c.act = act;
+    c.pools = pools;
+    c.ids = ids;
+    return run_gated(c, mode, flags, L, ws, ws_bytes, s);
+}
+
+// What both norms ask of their arguments (T > 0: the pointers too).
+static bool valid_norm(const void *x, const void *residual, const void *weight, float eps, int32_t T, int32_t d,
+                       int32_t d_step, const void *residual_out, const void *y) {
+    if (T < 0 || d <= 0 || (d % d_step) || !(eps > 0.0f) || !(eps < __builtin_inff())) return false;
+    if (T == 0) return true;
+    return x && weight && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(residual_out) &&
+           aligned16(y) && !(y && residual_out == y);
+}
+
+lora_status_t lora_add_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int32_t T,
+                               int32_t d, lora_dtype_t dtype, void *residual_out, void *y, lora_stream_t stream) {
+    if (!valid_dtype(dtype) || !valid_norm(x, residual, weight, eps, T, d, 8, residual_out, y) || (T > 0 && !y))
+        return LORA_ERR_INVALID_ARGUMENT;
+    return launch_add_rmsnorm(x, residual, weight, eps, T, d, dtype, residual_out, y, nullptr, nullptr, hs(stream));
+}
+
+lora_status_t lora_add_rmsnorm_fp8(const void *x, const void *residual, const void *weight, float eps, int32_t T,
+                                   int32_t d, void *residual_out, void *y, uint8_t *yq, float *y_scale,
+                                   lora_stream_t stream) {
+    if (!valid_norm(x, residual, weight, eps, T, d, 16, residual_out, y) ||
+        (T > 0 && (!yq || !y_scale || !aligned16(yq) || !aligned16(y_scale))))
+        return LORA_ERR_INVALID_ARGUMENT;
+    return launch_add_rmsnorm(x, residual, weight, eps, T, d, LORA_BF16, residual_out, y, yq, y_scale, hs(stream));
+}
+
 lora_status_t lora_linear_forward_noalloc(const void *x, const void *W, void *y, int32_t T,
                                           const lora_pool_t *pool, const int32_t *ids, lora_mode_t mode,
                                           uint32_t flags, int32_t *err_out, lora_stream_t stream) {

@@ -292,4 +292,29 @@ lora_status_t launch_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t 
                               const int32_t *ids, const float *v, int32_t v_stride, const int32_t *perm,
                               float *partial, size_t partial_bytes, hipStream_t s, const int32_t *n_fused = nullptr);
 
+// The gated pair h = act(g) * u of two projections of x with their pools (bf16
+// or fp32; wq, wsc: FP8 base codes and column scales instead of W, with the
+// rows' codes and scales xq, xs).  v: rank vectors [T][2 max_rank] of both
+// slices; gate, up: kept projections or null.
+struct gated_call {
+    const void *x, *W[2];
+    const uint8_t *xq, *wq[2];
+    const float *xs, *wsc[2];
+    void *h, *gate, *up;
+    int32_t T, act;
+    const lora_pool_t *pools;
+    const int32_t *ids, *perm;
+    const float *v;
+    float *partial;
+    size_t partial_bytes;
+};
+lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s);
+
+// z = x + residual (residual may be null), y = z / sqrt(mean(z^2) + eps) * weight
+// per row of d; residual_out (z) and y may be null; yq, ys: bf16 rows' E4M3
+// codes and scales, or null.
+lora_status_t launch_add_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int32_t T,
+                                 int32_t d, int32_t dtype, void *residual_out, void *y, uint8_t *yq, float *ys,
+                                 hipStream_t s);
+
 }  // namespace lora

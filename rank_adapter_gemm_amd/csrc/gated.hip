@@ -1,0 +1,151 @@
+// The gated feed-forward pair h = act(g) * u, g = x Wg + s_a (x Ag_a) Bg_a and u
+// likewise: the launcher of the bf16 and FP8 kernels (the base GEMMs' gated
+// instantiations, gemm.hip and gemm_fp8.hip) and the fp32 kernel.
+#include "gated_common.hpp"
+
+namespace lora {
+
+// ---------------------------------------------------------------------------
+// fp32: 64 rows x 64 columns of h per workgroup of 4 wavefronts (2 x 2), each
+// with 32 rows x 32 columns of both projections on v_mfma_f32_32x32x2_f32
+// (fp32 products and sums).  K in steps of 32, staged through LDS with the
+// next step's loads in registers under the current one's products.
+// ---------------------------------------------------------------------------
+struct gated_f32_args {
+    const float *x, *W[2], *b[2], *scale[2];
+    const int32_t *rank[2], *row0[2];
+    float *h, *keep[2];
+    const int32_t *ids, *perm;
+    const float *v;
+    int32_t T, K, N, n_slots, max_rank, act, n_tiles_n;
+};
+
+__global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
+    constexpr int BK = 32, XS = 64 + 4, WS = 128 + 4;
+    __shared__ __attribute__((aligned(16))) float s_x[BK][XS], s_w[BK][WS];   // s_w: 64 gate columns, 64 up columns
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w >> 1, wn = w & 1;
+    const int m0 = blockIdx.x / g.n_tiles_n * 64, n0 = blockIdx.x % g.n_tiles_n * 64;
+    const int K = g.K, N = g.N, T = g.T;
+    // x: thread -> row tid / 4, 8 k from 8 (tid % 4); W: thread -> k tid / 8, 8 columns from 8 (tid % 8), both weights
+    const int xr = tid >> 2, xk = (tid & 3) * 8, wk = tid >> 3, wc = (tid & 7) * 8;
+    const int32_t t_x = m0 + xr < T ? perm_row(g.perm, m0 + xr, T) : -1;
+    const float *xp = g.x + (int64_t)(t_x < 0 ? 0 : t_x) * K;
+    float4 rx[2], rw[2][2];
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto load = [&](int k0) {
+        const bool xok = t_x >= 0 && k0 + xk < K, wok = k0 + wk < K && n0 + wc < N;   // K, N multiples of 8
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rx[i] = xok ? *reinterpret_cast<const float4 *>(xp + k0 + xk + 4 * i) : zero;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                rw[m][i] = wok ? *reinterpret_cast<const float4 *>(g.W[m] + (int64_t)(k0 + wk) * N + n0 + wc + 4 * i)
+                               : zero;
+        }
+    };
+    f32x16_t acc[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
+    load(0);
+    for (int k0 = 0; k0 < K; k0 += BK) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s_x[xk + 4 * i + 0][xr] = rx[i].x;
+            s_x[xk + 4 * i + 1][xr] = rx[i].y;
+            s_x[xk + 4 * i + 2][xr] = rx[i].z;
+            s_x[xk + 4 * i + 3][xr] = rx[i].w;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) *reinterpret_cast<float4 *>(&s_w[wk][64 * m + wc + 4 * i]) = rw[m][i];
+        }
+        __syncthreads();
+        if (k0 + BK < K) load(k0 + BK);
+#pragma unroll
+        for (int k = 0; k < BK; k += 2) {
+            const float a = s_x[k + (lane >> 5)][wm * 32 + (lane & 31)];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, s_w[k + (lane >> 5)][64 * m + wn * 32 + (lane & 31)],
+                                                              acc[m], 0, 0, 0);
+        }
+    }
+    const int n = n0 + wn * 32 + (lane & 31);
+    if (n >= N) return;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int p = m0 + wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        const int64_t t = p < T ? perm_row(g.perm, p, T) : -1;
+        if (t < 0) continue;
+        const int32_t id = g.ids[t];
+        float val[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float d = 0.0f, sc = 0.0f;
+            if (id >= 0 && id < g.n_slots) {
+                const int r = min(g.rank[m][id], g.max_rank);
+                const float *b = g.b[m] + (slot_row0(g.row0[m], id, g.max_rank) * N + (int64_t)n * 8);
+                const float *vt = g.v + t * 2 * g.max_rank + m * g.max_rank;
+                for (int j = 0; j < r; ++j) d = fmaf(vt[j], b[(int64_t)(j >> 3) * N * 8 + (j & 7)], d);
+                if (r > 0) sc = g.scale[m][id];
+            }
+            val[m] = fmaf(sc, d, acc[m][e]);
+            if (g.keep[m]) g.keep[m][t * N + n] = val[m];
+        }
+        g.h[t * N + n] = act_value<true>(g.act, val[0]) * val[1];
+    }
+}
+
+lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {
+    const lora_pool_t *p = c.pools;
+    if (p[0].dtype == LORA_F32) {
+        gated_f32_args g{};
+        g.x = (const float *)c.x;
+        for (int m = 0; m < 2; ++m) {
+            g.W[m] = (const float *)c.W[m];
+            g.b[m] = (const float *)p[m].b;
+            g.scale[m] = p[m].scale;
+            g.rank[m] = p[m].rank;
+            g.row0[m] = p[m].row0;
+        }
+        g.h = (float *)c.h;
+        g.keep[0] = (float *)c.gate;
+        g.keep[1] = (float *)c.up;
+        g.ids = c.ids;
+        g.perm = c.perm;
+        g.v = c.v;
+        g.T = c.T;
+        g.K = p[0].d_in;
+        g.N = p[0].d_out;
+        g.n_slots = p[0].n_slots;
+        g.max_rank = p[0].max_rank;
+        g.act = c.act;
+        g.n_tiles_n = ceil_div(g.N, 64);
+        hipLaunchKernelGGL(k_gated_f32, dim3(ceil_div(c.T, 64) * g.n_tiles_n), dim3(256), 0, s, g);
+        return hip_status(hipGetLastError());
+    }
+    gemm_args g{};
+    g.x = (const uint16_t *)c.x;
+    g.xq = c.xq;
+    g.xs = c.xs;
+    g.y = (uint16_t *)c.h;
+    g.T = c.T;
+    g.K = p[0].d_in;
+    g.N = p[0].d_out;
+    g.perm = c.perm;
+    g.n_slots = p[0].n_slots;
+    g.max_rank = p[0].max_rank;
+    g.ids = c.ids;
+    g.v = c.v;
+    g.v_stride = 2 * p[0].max_rank;
+    g.partial = c.partial;
+    g.act = c.act;
+    void *keep[2] = {c.gate, c.up};
+    for (int m = 0; m < 2; ++m)
+        g.sl[m] = gemm_slice{(const uint16_t *)c.W[m], (uint16_t *)keep[m], g.N, 0, (const uint16_t *)p[m].b,
+                             p[m].scale, p[m].rank, p[m].row0, m * p[0].max_rank, c.wq[m], c.wsc[m]};
+    return c.xq ? launch_gemm_gated_fp8(g, c.partial_bytes, s) : launch_gemm_gated(g, c.partial_bytes, s);
+}
+
+}  // namespace lora

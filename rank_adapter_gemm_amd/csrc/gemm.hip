@@ -23,7 +23,7 @@
 //   * Split-K (small grids): each workgroup sums a K range and writes fp32
 //     partials in sorted-row order; k_splitk_reduce adds them in split order
 //     (deterministic, no atomics) and applies the same epilogue.
-#include "gemm_common.hpp"
+#include "gated_common.hpp"
 
 namespace lora {
 
@@ -43,13 +43,18 @@ template <int BM, int BN, int BK, int NS, bool SH, int WV = 4, int WR = 2> struc
     static constexpr int LDS = NS * STAGE * 2 > EPI ? NS * STAGE * 2 : EPI;
 };
 
-template <bool LORA, int BM, int BN, int BK, int NS, bool SPLIT, bool SH = false, int WV = 4, int WR = 2>
+//   * GATED: the tile's columns are pairs of 32 gate and 32 up columns (see
+//     gated_col), each with its own weight and adapter pool; the epilogue
+//     writes h = act(gate) * up, so gate and up need not leave the chip.
+template <bool LORA, int BM, int BN, int BK, int NS, bool SPLIT, bool SH = false, int WV = 4, int WR = 2,
+          bool GATED = false>
 __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     static_assert(!SH || SPLIT, "the fused shrink runs in split-K mode");
     static_assert(!SH || (WV == 4 || WV == 8), "the fused shrink maps 4 or 8 threads to a (row, rank) pair");
     // The single-stage LoRA instantiation is the expand-only pass
     // (launch_expand_tiles: no K steps): it adds its tile to y.
     constexpr bool ADD = LORA && !SPLIT && NS == 1;
+    static_assert(!GATED || (!SH && !ADD), "the gated pair has its own shrink and epilogue");
     typedef gemm_cfg<BM, BN, BK, NS, SH, WV, WR> C;
     constexpr int WM = C::WM, WN = C::WN, RB = C::RB, CB = C::CB;
     constexpr int XCH = C::XCH, WCH = C::WCH, XSTAGE = C::XSTAGE, WSTAGE = C::WSTAGE;
@@ -82,12 +87,17 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     // W stage: BK rows x WCH chunks, chunk c at row c / WCH, slot c % WCH,
     // holding the row's chunk slot ^ swz_w(row).
     int wrow[WI], wcol[WI];
+    const uint16_t *wmat[GATED ? WI : 1];                // gated: the chunk's weight
 #pragma unroll
     for (int j = 0; j < WI; ++j) {
         const int c = (w * WI + j) * 64 + lane;
         const int k = c / WCH, slot = c % WCH;
         wrow[j] = k;
         wcol[j] = n0 + 8 * (slot ^ swz_w<BN>(k));
+        if constexpr (GATED) {
+            wmat[j] = gated_up(wcol[j]) ? g.sl[1].W : g.sl[0].W;
+            wcol[j] = gated_col(wcol[j]);
+        }
     }
     // Fused shrink (decode-sized batches): this workgroup also computes the
     // rank partials v[t][j] over its K range for the rows
@@ -143,7 +153,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
 #pragma unroll
         for (int j = 0; j < WI; ++j) {
             const int k = k0 + wrow[j];
-            const void *src = (k < k_end && wcol[j] < N) ? (const void *)(g.W + (int64_t)k * N + wcol[j])
+            const uint16_t *W = GATED ? wmat[GATED ? j : 0] : g.W;
+            const void *src = (k < k_end && wcol[j] < N) ? (const void *)(W + (int64_t)k * N + wcol[j])
                                                           : (const void *)g_zero16;
             dma16(src, wsm + (w * WI + j) * 64 * 8);
         }
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
             int32_t id = -1;
             if (LORA && t >= 0 && (!g.n_fused || p < n_fused)) {
                 const int32_t raw = g.ids[t];
-                if (raw >= 0 && raw < g.n_slots && g.rank[raw] > 0) id = raw;
+                if (raw >= 0 && raw < g.n_slots && (GATED || g.rank[raw] > 0)) id = raw;
             }
             s_meta_t[i] = (ADD && id < 0) ? -1 : t;   // adding: rows without a term stay untouched
             s_meta_id[i] = id;
@@ -286,7 +297,10 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     // The low-rank term goes into the accumulators before the K loop, while
     // the first stages load.  (Split-K tiles leave it to the reduction, whose
     // one-thread-per-row-chunk layout hides the per-row loads of B.)
-    if (LORA && !SPLIT)
+    if constexpr (GATED && LORA && !SPLIT)
+        gated_lora_pass<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, wm * WM,
+                                                                       gated_col(n0 + wn * WN), lane);
+    else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN,
                                                     lane);
     wait_stage(min(NS - 1, nk - 1));
@@ -340,8 +354,13 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
             flag_bad_row(g.err, fl_t);
     }
 
-    gemm_store_tile<BM, BN, WV, WR, SPLIT, ADD>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane,
-                                              tidx, split);
+    if constexpr (GATED && !SPLIT)
+        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane);
+    else if constexpr (GATED)
+        gated_store_partial<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), n0, w, lane, tidx, split);
+    else
+        gemm_store_tile<BM, BN, WV, WR, SPLIT, ADD>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane,
+                                                    tidx, split);
 }
 
 struct gemm_f32_args {
@@ -702,6 +721,41 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
         else
             hipLaunchKernelGGL(k_gemm_f32<false>, dim3(tiles), dim3(256), 0, s, g);
     }
+    return hip_status(hipGetLastError());
+}
+
+template <int BM, int BN, int NS, int WV, int WR, int NST, int WVT, int WRT>
+static void launch_gated_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s) {
+    if (pl.n_dp > 0) {
+        g.tile_base = 0;
+        g.n_tiles = pl.n_dp;
+        g.splits = 1;
+        g.k_chunk = g.K;
+        hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, 64, NS, false, false, WV, WR, true>), dim3(pl.n_dp),
+                           dim3(WV * 64), 0, s, g);
+    }
+    if (pl.tail > 0) {
+        g.tile_base = pl.n_dp;
+        g.n_tiles = pl.tail;
+        g.splits = pl.splits;
+        g.k_chunk = pl.k_chunk;
+        hipLaunchKernelGGL((k_gemm_bf16<false, BM, BN, 64, NST, true, false, WVT, WRT, true>),
+                           dim3(pl.tail * pl.splits), dim3(WVT * 64), 0, s, g);
+        launch_gated_reduce<BM, BN>(g, s);
+    }
+}
+
+// h = act(x Wg + ...) * (x Wu + ...), the bf16 pair.
+// Wavefronts of 64 columns (one gate block, one up block): the 256 x 128
+// tiles therefore run their 8 wavefronts 4 x 2.
+lora_status_t launch_gemm_gated(gemm_args &g, size_t partial_bytes, hipStream_t s) {
+    const gemm_plan pl = plan_gated(g.T, g.K, g.N, partial_bytes);
+    g.n_tiles_m = ceil_div(g.T, pl.bm);
+    g.n_tiles_n = ceil_div(2 * (int64_t)g.N, pl.bn);
+    g.col_strips = col_strips_pay(g.T, 2 * g.N, g.n_tiles_n);
+    if (pl.bm == 256 && pl.bn == 256) launch_gated_cfg<256, 256, 2, 8, 2, 2, 8, 2>(g, pl, s);
+    else if (pl.bm == 256) launch_gated_cfg<256, 128, 2, 8, 4, 2, 8, 2>(g, pl, s);
+    else launch_gated_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
     return hip_status(hipGetLastError());
 }
 

@@ -19,6 +19,8 @@ struct gemm_slice {
     const int32_t *rank;
     const int32_t *row0;
     int32_t v_off;
+    const uint8_t *wq;      // FP8 base: codes and column scales
+    const float *wsc;
 };
 
 struct gemm_args {
@@ -50,6 +52,7 @@ struct gemm_args {
     int32_t col_strips;            // tile order: 1 = strips of kGroupN column tiles (see grouped_tile)
     int32_t n_slices;              // grouped launch: 0 (one output), else slices sl[0..n_slices)
     gemm_slice sl[kMaxSlices];     // column tiles numbered slice after slice
+    int32_t act;                   // gated pair: the activation (sl[0] gate, sl[1] up, y = h, N = h's width)
 };
 
 // Grouped launch: point g at the slice that owns global column tile tn and
@@ -191,8 +194,9 @@ __device__ __forceinline__ void lora_step_load(const gemm_args &g, int32_t a, in
 
 // acc += (s_a v) B for one step from loaded operands; lanes with `use` false
 // (rows of other adapters, ranks past the slot's) contribute zero.
-template <int CB>
-__device__ __forceinline__ void lora_step_mfma(f32x16_t (&acc)[CB], float sa, bool use, const float4 &v0,
+// Column block cb is acc[cb * ST + OF] (every block, or one of a gated pair).
+template <int CB, int ST, int OF>
+__device__ __forceinline__ void lora_step_mfma(f32x16_t (&acc)[CB * ST], float sa, bool use, const float4 &v0,
                                                const float4 &v1, const uint4 (&bq)[CB]) {
     const uint32_t m = use ? ~0u : 0u;
     const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
@@ -216,9 +220,10 @@ __device__ __forceinline__ void lora_step_mfma(f32x16_t (&acc)[CB], float sa, bo
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
         const bf16x8_t bb = __builtin_bit_cast(bf16x8_t, bq[cb]);
-        acc[cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ahi, bb, acc[cb], 0, 0, 0);
-        acc[cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(amd, bb, acc[cb], 0, 0, 0);
-        acc[cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(alo, bb, acc[cb], 0, 0, 0);
+        f32x16_t &c = acc[cb * ST + OF];
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ahi, bb, c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(amd, bb, c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(alo, bb, c, 0, 0, 0);
     }
 }
 
@@ -236,8 +241,8 @@ __device__ __forceinline__ void lora_step_mfma(f32x16_t (&acc)[CB], float sa, bo
 // the slot's rank and scale read per adapter (kernels with no registers to
 // spare).  Per block the MFMAs run in the same order either way: adapters
 // by lowest row, ranks ascending.
-template <int RB, int CB, int RG = 1, int KB = 1, int RF = 1>
-__device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&acc)[RB][CB],
+template <int RB, int CB, int RG = 1, int KB = 1, int RF = 1, int ST = 1, int OF = 0>
+__device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&acc)[RB][CB * ST],
                                                const int32_t *s_t, const int32_t *s_id, int n0,
                                                int wrow0, int wcol0, int lane) {
     static_assert(RB % RG == 0 && (RF == 0 || RB % RF == 0), "row blocks come in whole groups");
@@ -275,7 +280,7 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
 #pragma unroll
                 for (int u = 0; u < KB; ++u)
                     if (16 * (ks0 + u) < ra0[r0 + i])      // wave-uniform
-                        lora_step_mfma<CB>(acc[r0 + i], sa0[r0 + i],
+                        lora_step_mfma<CB, ST, OF>(acc[r0 + i], sa0[r0 + i],
                                            my_id[r0 + i] == a0[r0 + i] && 16 * (ks0 + u) + 8 * half < ra0[r0 + i],
                                            v0[i][u], v1[i][u], bq[i][u]);
         }
@@ -298,7 +303,7 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
                     float4 v0, v1;
                     uint4 bq[CB];
                     lora_step_load<CB>(g, a, ra, ro, mine, my_t[rb], ks, half, wcol0, lane, v0, v1, bq);
-                    lora_step_mfma<CB>(acc[rb], sa, mine && 16 * ks + 8 * half < ra, v0, v1, bq);
+                    lora_step_mfma<CB, ST, OF>(acc[rb], sa, mine && 16 * ks + 8 * half < ra, v0, v1, bq);
                 }
             }
         }
@@ -354,7 +359,7 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
 #pragma unroll
                 for (int i = 0; i < RFG; ++i)
                     if (16 * ks < ra[i])                   // wave-uniform
-                        lora_step_mfma<CB>(acc[r0 + i], sa[i], mine[i] && 16 * ks + 8 * half < ra[i], v0[i], v1[i],
+                        lora_step_mfma<CB, ST, OF>(acc[r0 + i], sa[i], mine[i] && 16 * ks + 8 * half < ra[i], v0[i], v1[i],
                                            bq[i]);
             }
         }
@@ -637,6 +642,22 @@ inline gemm_plan plan_gemm(int T, int K, const int32_t *Ns, int nN, size_t parti
     }
     const int k_chunk = ceil_div(ceil_div(K, splits), kgran) * kgran;
     return {bm, bn, 0, tiles, ceil_div(K, k_chunk), k_chunk};
+}
+
+// The gated pair of width N each: a tile's columns are half gate's, half up's
+// (see gated_col), so it is one output of width 2N, on tiles that hold whole
+// pairs per wavefront (no 64-column tiles: those grids split K instead).
+inline gemm_plan plan_gated(int T, int K, int N, size_t partial_bytes, int kgran = 64) {
+    const int32_t n = 2 * N;
+    gemm_plan p = plan_gemm(T, K, &n, 1, partial_bytes, kgran);
+    if (p.bn != 64) return p;
+    const int tiles = ceil_div(T, 128) * ceil_div(n, 128);
+    int splits = ceil_div(256, tiles);
+    if (splits > K / 256) splits = K / 256;
+    while (splits > 1 && (size_t)splits * tiles * 128 * 128 * 4 > partial_bytes) --splits;
+    if (splits <= 1) return gemm_plan{128, 128, tiles, 0, 1, K};
+    const int k_chunk = ceil_div(ceil_div(K, splits), kgran) * kgran;
+    return {128, 128, 0, tiles, ceil_div(K, k_chunk), k_chunk};
 }
 
 // One output of width N.

@@ -29,7 +29,7 @@
 // scale operand of lane l applies to row (column) l % 32 in K-block l / 32 --
 // with one scale per row and column, lanes l and l + 32 pass the same one.
 // The output layout is that of the bf16 32x32 MFMAs.
-#include "gemm_common.hpp"
+#include "gated_common.hpp"
 #include "fp8_common.hpp"
 
 namespace lora {
@@ -160,7 +160,8 @@ template <int BM, int BN, int NS, int WV, int WR> struct fp8_cfg {
     static_assert(XI * 64 * WV == BM * CH && WI * 64 * WV == BN * CH, "DMA plan must cover the tiles");
 };
 
-template <bool LORA, int BM, int BN, int NS, bool SPLIT, int WV = 4, int WR = 2>
+// GATED: pairs of 32 gate and 32 up columns, as in the bf16 kernel.
+template <bool LORA, int BM, int BN, int NS, bool SPLIT, int WV = 4, int WR = 2, bool GATED = false>
 __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     typedef fp8_cfg<BM, BN, NS, WV, WR> C;
     constexpr int BK = C::BK, CH = C::CH, WM = C::WM, WN = C::WN, RB = C::RB, CB = C::CB;
@@ -192,9 +193,11 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     for (int j = 0; j < WI; ++j) {
         const int c = (w * WI + j) * 64 + lane;
         const int r = c / CH, slot = c % CH;
-        wrow[j] = (n0 + r < N) ? (int64_t)(n0 + r) * K : -1;
+        const int n = GATED ? gated_col(n0 + r) : n0 + r;
+        wrow[j] = (n < N) ? (int64_t)n * K : -1;
         wcol[j] = 16 * (slot ^ swz_x<64>(r));
     }
+    const int wu = uniform_i(w);
     auto dma_stage = [&](int kt, int buf) {
         uint8_t *xs = smem + buf * STAGE;
         uint8_t *wsm = xs + XSTAGE;
@@ -209,7 +212,9 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
 #pragma unroll
         for (int j = 0; j < WI; ++j) {
             const int kk = k0 + wcol[j];
-            const void *src = (wrow[j] >= 0 && kk < k_end) ? (const void *)(g.wq + wrow[j] + kk)
+            // gated: an instruction's 64 / CH rows are one projection's (a scalar choice)
+            const uint8_t *wq = !GATED ? g.wq : (gated_up((wu * WI + j) * (64 / CH)) ? g.sl[1].wq : g.sl[0].wq);
+            const void *src = (wrow[j] >= 0 && kk < k_end) ? (const void *)(wq + wrow[j] + kk)
                                                              : (const void *)g_zero16;
             dma16(src, wsm + (w * WI + j) * 64 * 16);
         }
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
         int32_t id = -1;
         if (LORA && t >= 0 && (!g.n_fused || p < n_fused)) {
             const int32_t raw = g.ids[t];
-            if (raw >= 0 && raw < g.n_slots && g.rank[raw] > 0) id = raw;
+            if (raw >= 0 && raw < g.n_slots && (GATED || g.rank[raw] > 0)) id = raw;
         }
         s_meta_t[i] = t;
         s_meta_id[i] = id;
@@ -284,8 +289,9 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     };
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
-        const int col = n0 + wn * WN + cb * 32 + fr;
-        esb[cb] = col < N ? e8m0_of(g.wsc[col]) : 127;
+        const int vcol = n0 + wn * WN + cb * 32 + fr, col = GATED ? gated_col(vcol) : vcol;
+        const float *wsc = GATED ? (gated_up(vcol) ? g.sl[1].wsc : g.sl[0].wsc) : g.wsc;
+        esb[cb] = col < N ? e8m0_of(wsc[col]) : 127;
     }
 #pragma unroll
     for (int st = 0; st < NS; ++st)
@@ -297,7 +303,9 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     for (int rb = 0; rb < RB; ++rb) esa[rb] = s_esx[wm * WM + rb * 32 + fr];
     // The low-rank term goes into the accumulators before the K loop, while
     // the first stages load (split-K tiles leave it to the reduction).
-    if (LORA && !SPLIT)
+    if constexpr (GATED && LORA && !SPLIT)
+        gated_lora_pass<RB, CB, 1, 1, 0>(g, acc, s_meta_t, s_meta_id, wm * WM, gated_col(n0 + wn * WN), lane);
+    else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 4 ? RB : 1), 1, 0>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN, lane);
     wait_stage(min(NS - 1, nk - 1));
     __builtin_amdgcn_s_barrier();
@@ -335,8 +343,13 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 
-    gemm_store_tile<BM, BN, WV, WR, SPLIT, false>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane,
-                                         tidx, split);
+    if constexpr (GATED && !SPLIT)
+        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane);
+    else if constexpr (GATED)
+        gated_store_partial<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), n0, w, lane, tidx, split);
+    else
+        gemm_store_tile<BM, BN, WV, WR, SPLIT, false>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane,
+                                                      tidx, split);
 }
 
 // NST, WVT: stages and wavefronts of the split-K pieces.
@@ -412,6 +425,38 @@ lora_status_t launch_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t 
     else if (pl.bm == 256 && pl.bn == 128) launch_fp8_cfg<256, 128, 2, 8>(g, pl, lora, s);
     else if (pl.bn == 128) launch_fp8_cfg<128, 128, 2, 4, 2, 4, 8>(g, pl, lora, s);
     else launch_fp8_cfg<128, 64>(g, pl, lora, s);
+    return hip_status(hipGetLastError());
+}
+
+template <int BM, int BN, int NS, int WV, int WR, int NST, int WVT, int WRT>
+static void launch_gated_fp8_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s) {
+    if (pl.n_dp > 0) {
+        g.tile_base = 0;
+        g.n_tiles = pl.n_dp;
+        g.splits = 1;
+        g.k_chunk = g.K;
+        hipLaunchKernelGGL((k_gemm_fp8<true, BM, BN, NS, false, WV, WR, true>), dim3(pl.n_dp), dim3(WV * 64), 0, s,
+                           g);
+    }
+    if (pl.tail > 0) {
+        g.tile_base = pl.n_dp;
+        g.n_tiles = pl.tail;
+        g.splits = pl.splits;
+        g.k_chunk = pl.k_chunk;
+        hipLaunchKernelGGL((k_gemm_fp8<false, BM, BN, NST, true, WVT, WRT, true>), dim3(pl.tail * pl.splits),
+                           dim3(WVT * 64), 0, s, g);
+        launch_gated_reduce<BM, BN>(g, s);
+    }
+}
+
+lora_status_t launch_gemm_gated_fp8(gemm_args &g, size_t partial_bytes, hipStream_t s) {
+    const gemm_plan pl = plan_gated(g.T, g.K, g.N, partial_bytes, 128);
+    g.n_tiles_m = ceil_div(g.T, pl.bm);
+    g.n_tiles_n = ceil_div(2 * (int64_t)g.N, pl.bn);
+    g.col_strips = col_strips_pay(g.T, 2 * g.N, g.n_tiles_n);
+    if (pl.bm == 256 && pl.bn == 256) launch_gated_fp8_cfg<256, 256, 2, 4, 2, 2, 4, 2>(g, pl, s);
+    else if (pl.bm == 256) launch_gated_fp8_cfg<256, 128, 2, 8, 4, 2, 8, 2>(g, pl, s);
+    else launch_gated_fp8_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
     return hip_status(hipGetLastError());
 }
 

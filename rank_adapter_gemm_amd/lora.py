@@ -30,6 +30,10 @@ LORA_MODE_BGMV = 1
 LORA_MODE_SGMV = 2
 LORA_AUTO_SGMV_MIN_ROWS = 512      # AUTO builds segments from this many rows on
 
+LORA_ACT_SILU = 0
+LORA_ACT_GELU = 1
+LORA_ACT_GELU_TANH = 2
+
 LORA_FLAG_SEGMENTS_READY = 0x1
 LORA_FLAG_SEPARATE_EXPAND = 0x2
 
@@ -49,6 +53,8 @@ EXPORTED = (
     "lora_cache_commit", "lora_cache_slot_of", "lora_cache_stats",
     "lora_quantize_rows_fp8", "lora_quantize_weight_fp8", "lora_gemm_fp8", "lora_workspace_bytes_fp8",
     "lora_linear_forward_fp8",
+    "lora_add_rmsnorm", "lora_add_rmsnorm_fp8",
+    "lora_workspace_bytes_gated", "lora_workspace_bytes_gated_fp8", "lora_gated_forward", "lora_gated_forward_fp8",
     "lora_linear_forward_noalloc",
     "lora_get_device_error",
     "lora_status_string", "lora_version",
@@ -143,6 +149,14 @@ def load(path: str = LIB_PATH):
         "lora_workspace_bytes_fp8": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
         "lora_linear_forward_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_u32,
                                             c_vp, c_sz, c_vp]),
+        "lora_add_rmsnorm": (c_i32, [c_vp, c_vp, c_vp, c_f, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
+        "lora_add_rmsnorm_fp8": (c_i32, [c_vp, c_vp, c_vp, c_f, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "lora_workspace_bytes_gated": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+        "lora_workspace_bytes_gated_fp8": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
+        "lora_gated_forward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_i32,
+                                       c_u32, c_vp, c_sz, c_vp]),
+        "lora_gated_forward_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,
+                                           P(lora_pool_t), c_vp, c_i32, c_i32, c_u32, c_vp, c_sz, c_vp]),
         "lora_linear_forward_noalloc": (c_i32, [c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_u32, c_vp,
                                                 c_vp]),
         "lora_get_device_error": (c_i32, [c_vp, c_sz, c_vp, P(c_i32)]),
@@ -312,6 +326,12 @@ def _pool_array(pools):
     return arr
 
 
+def _pool_pair(pools):
+    if len(pools) != 2:
+        raise LoraError(LORA_ERR_INVALID_ARGUMENT, "gate's and up's pools")
+    return _pool_array(pools)
+
+
 def lora_shrink_sliced(x, T, pools, ids, mode, v, ws, stream=None):
     """pools: a list of lora_pool_t (one per slice)."""
     _ok(load().lora_shrink_sliced(_ptr(x), T, _pool_array(pools), len(pools), _ptr(ids), mode, _ptr(v),
@@ -416,6 +436,43 @@ def lora_linear_forward_fp8(x, wq, w_scale, y, T, pool, ids, mode, flags, ws, st
                                        _stream(stream)), "lora_linear_forward_fp8")
 
 
+def lora_add_rmsnorm(x, residual, weight, eps, T, d, dtype, residual_out, y, stream=None):
+    """z = x + residual; y = z / sqrt(mean(z^2) + eps) * weight.  residual, residual_out: tensors or None."""
+    _ok(load().lora_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), T, d, dtype, _ptr(residual_out),
+                                _ptr(y), _stream(stream)), "lora_add_rmsnorm")
+
+
+def lora_add_rmsnorm_fp8(x, residual, weight, eps, T, d, residual_out, y, yq, y_scale, stream=None):
+    """The same on bf16 rows, with the E4M3 codes and scales of y's rows; y may be None."""
+    _ok(load().lora_add_rmsnorm_fp8(_ptr(x), _ptr(residual), _ptr(weight), float(eps), T, d, _ptr(residual_out),
+                                    _ptr(y), _ptr(yq), _ptr(y_scale), _stream(stream)), "lora_add_rmsnorm_fp8")
+
+
+def lora_workspace_bytes_gated(T, n_slots, max_rank, d_out=0) -> int:
+    return int(load().lora_workspace_bytes_gated(T, n_slots, max_rank, d_out))
+
+
+def lora_workspace_bytes_gated_fp8(T, n_slots, max_rank, d_in, d_out=0) -> int:
+    return int(load().lora_workspace_bytes_gated_fp8(T, n_slots, max_rank, d_in, d_out))
+
+
+def lora_gated_forward(x, W_gate, W_up, h, T, pools, ids, act, mode, flags, ws, gate=None, up=None, stream=None):
+    """h = act(gate projection) * up projection; pools: [gate's, up's] lora_pool_t; gate, up: tensors that keep
+    the projections for the backward pass, or None."""
+    _ok(load().lora_gated_forward(_ptr(x), _ptr(W_gate), _ptr(W_up), _ptr(h), _ptr(gate), _ptr(up), T,
+                                  _pool_pair(pools), _ptr(ids), act, mode, flags, _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_forward")
+
+
+def lora_gated_forward_fp8(x, xq, x_scale, wq_gate, w_scale_gate, wq_up, w_scale_up, h, T, pools, ids, act, mode,
+                           flags, ws, gate=None, up=None, stream=None):
+    """The same on FP8 base weights; xq, x_scale: the codes and scales of x's rows, or None (made in ws)."""
+    _ok(load().lora_gated_forward_fp8(_ptr(x), _ptr(xq), _ptr(x_scale), _ptr(wq_gate), _ptr(w_scale_gate),
+                                      _ptr(wq_up), _ptr(w_scale_up), _ptr(h), _ptr(gate), _ptr(up), T,
+                                      _pool_pair(pools), _ptr(ids), act, mode, flags, _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_forward_fp8")
+
+
 class Fp8Weight:
     """E4M3 codes [d_out, d_in] and fp32 column scales of a bf16 base weight
     W [d_in, d_out], made on the device by lora_quantize_weight_fp8."""
@@ -480,10 +537,16 @@ class AdapterPool:
 
 
 class Workspace:
-    """A device workspace sized for (T, n_slots, max_rank, d_out), initialised."""
+    """A device workspace sized for (T, n_slots, max_rank, d_out), initialised.
+    With `gated` it serves the gated pair of width d_out."""
 
-    def __init__(self, T, n_slots, max_rank, d_out=0, device="cuda", stream=None, n_slices=1, fp8_d_in=0):
-        if fp8_d_in:
+    def __init__(self, T, n_slots, max_rank, d_out=0, device="cuda", stream=None, n_slices=1, fp8_d_in=0,
+                 gated=False):
+        if gated:
+            n_slices = 2
+            n = (lora_workspace_bytes_gated_fp8(T, n_slots, max_rank, fp8_d_in, d_out) if fp8_d_in else
+                 lora_workspace_bytes_gated(T, n_slots, max_rank, d_out))
+        elif fp8_d_in:
             if n_slices != 1:
                 raise LoraError(LORA_ERR_INVALID_ARGUMENT, "lora_workspace_bytes_fp8")
             n = lora_workspace_bytes_fp8(T, n_slots, max_rank, fp8_d_in, d_out)
