@@ -576,6 +576,29 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
                                      const int32_t *ids, lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws,
                                      size_t ws_bytes, lora_stream_t stream);
 
+/* Backward pass of the pair, the base weights frozen: from dh DEVICE
+ * [T, d_out], the gradient of h, and gate and up as lora_gated_forward kept
+ * them for the same x, ids and adapters, with s = scale[a], a = ids[t]:
+ *     dg = dh u act'(g),   du = dh act(g)        (bf16 pools: rounded once)
+ *     dx = dg W_gate^T + du W_up^T + dv_g A_a^T + dv_u A_a^T,   dv = s d{g,u} B_a^T
+ *     dA_a = sum over a's rows of x^T dv,        dB_a = s sum of (x A_a)^T d{g,u}
+ * dx DEVICE [T, d_in], overwritten (NULL: not computed).  dA and dB HOST
+ * arrays of 2 DEVICE pointers (gate's, up's), dA[i] [n_slots, d_in, max_rank]
+ * and dB[i] [n_slots, max_rank, d_out], row-major as lora_pool_upload takes
+ * one slot's (lda = max_rank, ldb = d_out); padded so for packed pools too.
+ * All of them are overwritten: a slot with no row in the batch, and ranks at
+ * and past a slot's, get zeros (T == 0 too).  Both NULL: not computed.  All of
+ * the pools' dtype, sums in fp32.  Rows without a usable adapter have only the base
+ * term.  The sums over an adapter's rows are in batch order: the same inputs
+ * give bitwise the same gradients.  ws: lora_workspace_bytes_gated_backward,
+ * cleared by lora_workspace_init. */
+size_t lora_workspace_bytes_gated_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out,
+                                           lora_dtype_t dtype);
+lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void *W_up, int32_t T,
+                                  const lora_pool_t *pools, const int32_t *ids, lora_act_t act, const void *gate,
+                                  const void *up, const void *dh, void *dx, void *const *dA, void *const *dB,
+                                  void *ws, size_t ws_bytes, lora_stream_t stream);
+
 /* ---- the layer without a caller workspace ---------------------------------------- */
 
 /* For callers that cannot allocate device memory at call time: code under

@@ -701,6 +701,49 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
     return run_gated(c, mode, flags, L, ws, ws_bytes, s);
 }
 
+size_t lora_workspace_bytes_gated_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out,
+                                           lora_dtype_t dtype) {
+    if (lora_workspace_bytes_gated(T, n_slots, max_rank, 0) == 0 || !valid_dtype(dtype) || d_in <= 0 || d_out <= 0 ||
+        !valid_dims(n_slots, d_in, d_out, 2 * max_rank))
+        return 0;
+    return make_bwd_layout(T, n_slots, max_rank, d_in, d_out, dtype).total;
+}
+
+lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void *W_up, int32_t T,
+                                  const lora_pool_t *pools, const int32_t *ids, lora_act_t act, const void *gate,
+                                  const void *up, const void *dh, void *dx, void *const *dA, void *const *dB,
+                                  void *ws, size_t ws_bytes, lora_stream_t stream) {
+    lora_status_t st = check_pair(pools);
+    if (st != LORA_OK) return st;
+    if (T < 0 || !valid_act(act) || !dA != !dB) return LORA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!x || !W_gate || !W_up || !ids || !gate || !up || !dh || !aligned16(x) || !aligned16(W_gate) ||
+                  !aligned16(W_up) || !aligned16(gate) || !aligned16(up) || !aligned16(dh) || !aligned16(dx)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < 2 && dA; ++i)
+        if (!dA[i] || !dB[i] || !aligned16(dA[i]) || !aligned16(dB[i])) return LORA_ERR_INVALID_ARGUMENT;
+    const lora_pool_t &p = pools[0];
+    if (!valid_dims(p.n_slots, p.d_in, p.d_out, 2 * p.max_rank)) return LORA_ERR_UNSUPPORTED;
+    const bwd_layout B = make_bwd_layout(T, p.n_slots, p.max_rank, p.d_in, p.d_out, p.dtype);
+    if (!ws || !aligned16(ws)) return LORA_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < B.partial) return LORA_ERR_WORKSPACE_TOO_SMALL;
+    const hipStream_t s = hs(stream);
+    if (T == 0) {
+        const size_t slots = (size_t)p.n_slots * p.max_rank * dtype_bytes(p.dtype);
+        for (int i = 0; i < 2 && dA && st == LORA_OK; ++i) {
+            st = launch_zero(dA[i], slots * p.d_in, s);
+            if (st == LORA_OK) st = launch_zero(dB[i], slots * p.d_out, s);
+        }
+        return st;
+    }
+    gated_bwd_call c{x, {W_gate, W_up}, gate, up, dh, dx, {nullptr, nullptr}, {nullptr, nullptr}, T, (int32_t)act,
+                     pools, ids, ws, ws_bytes};
+    for (int i = 0; i < 2 && dA; ++i) {
+        c.dA[i] = dA[i];
+        c.dB[i] = dB[i];
+    }
+    return launch_gated_backward(c, B, s);
+}
+
 // What both norms ask of their arguments (T > 0: the pointers too).
 static bool valid_norm(const void *x, const void *residual, const void *weight, float eps, int32_t T, int32_t d,
                        int32_t d_step, const void *residual_out, const void *y) {

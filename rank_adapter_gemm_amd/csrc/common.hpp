@@ -310,6 +310,30 @@ struct gated_call {
 };
 lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s);
 
+// Its backward pass: the workspace of a forward (segments, v and the shrink's
+// partials for 2 max_rank columns) and what follows it.
+struct bwd_layout {
+    ws_layout L;
+    size_t dy;          // dg, du: [2][T][d_out], the pools' dtype
+    size_t dv;          // fp32 [T][2 max_rank]
+    size_t oct;         // bf16: both slices' A in rank octets, one set per segment
+    size_t row0, rank, scale;   // their pool tables, [n_slots]
+    size_t partial;     // dx's split-K partials
+    size_t total;
+};
+struct gated_bwd_call {
+    const void *x, *W[2], *gate, *up, *dh;
+    void *dx, *dA[2], *dB[2];
+    int32_t T, act;
+    const lora_pool_t *pools;
+    const int32_t *ids;
+    void *ws;
+    size_t ws_bytes;
+};
+bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out, int32_t dtype);
+lora_status_t launch_gated_backward(const gated_bwd_call &c, const bwd_layout &B, hipStream_t s);
+lora_status_t launch_zero(void *p, size_t bytes, hipStream_t s);   // bytes: a multiple of 16
+
 // z = x + residual (residual may be null), y = z / sqrt(mean(z^2) + eps) * weight
 // per row of d; residual_out (z) and y may be null; yq, ys: bf16 rows' E4M3
 // codes and scales, or null.

@@ -55,6 +55,7 @@ EXPORTED = (
     "lora_linear_forward_fp8",
     "lora_add_rmsnorm", "lora_add_rmsnorm_fp8",
     "lora_workspace_bytes_gated", "lora_workspace_bytes_gated_fp8", "lora_gated_forward", "lora_gated_forward_fp8",
+    "lora_workspace_bytes_gated_backward", "lora_gated_backward",
     "lora_linear_forward_noalloc",
     "lora_get_device_error",
     "lora_status_string", "lora_version",
@@ -157,6 +158,9 @@ def load(path: str = LIB_PATH):
                                        c_u32, c_vp, c_sz, c_vp]),
         "lora_gated_forward_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,
                                            P(lora_pool_t), c_vp, c_i32, c_i32, c_u32, c_vp, c_sz, c_vp]),
+        "lora_workspace_bytes_gated_backward": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+        "lora_gated_backward": (c_i32, [c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                        P(c_vp), P(c_vp), c_vp, c_sz, c_vp]),
         "lora_linear_forward_noalloc": (c_i32, [c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_u32, c_vp,
                                                 c_vp]),
         "lora_get_device_error": (c_i32, [c_vp, c_sz, c_vp, P(c_i32)]),
@@ -473,6 +477,20 @@ def lora_gated_forward_fp8(x, xq, x_scale, wq_gate, w_scale_gate, wq_up, w_scale
                                       ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_forward_fp8")
 
 
+def lora_workspace_bytes_gated_backward(T, n_slots, max_rank, d_in, d_out, dtype) -> int:
+    return int(load().lora_workspace_bytes_gated_backward(T, n_slots, max_rank, d_in, d_out, dtype))
+
+
+def lora_gated_backward(x, W_gate, W_up, T, pools, ids, act, gate, up, dh, dx, dA, dB, ws, stream=None):
+    """Gradients of lora_gated_forward: dx (or None) and, per projection, dA = [gate's, up's] of
+    [n_slots, d_in, max_rank] and dB of [n_slots, max_rank, d_out] (or None for both)."""
+    a_arr = (ctypes.c_void_p * 2)(*[_ptr(t) for t in dA]) if dA is not None else None
+    b_arr = (ctypes.c_void_p * 2)(*[_ptr(t) for t in dB]) if dB is not None else None
+    _ok(load().lora_gated_backward(_ptr(x), _ptr(W_gate), _ptr(W_up), T, _pool_pair(pools), _ptr(ids), act,
+                                   _ptr(gate), _ptr(up), _ptr(dh), _ptr(dx), a_arr, b_arr, _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_backward")
+
+
 class Fp8Weight:
     """E4M3 codes [d_out, d_in] and fp32 column scales of a bf16 base weight
     W [d_in, d_out], made on the device by lora_quantize_weight_fp8."""
@@ -538,11 +556,17 @@ class AdapterPool:
 
 class Workspace:
     """A device workspace sized for (T, n_slots, max_rank, d_out), initialised.
-    With `gated` it serves the gated pair of width d_out."""
+    With `gated` it serves the gated pair of width d_out, or with backward_d_in
+    (x's width) and dtype the pair's backward pass."""
 
     def __init__(self, T, n_slots, max_rank, d_out=0, device="cuda", stream=None, n_slices=1, fp8_d_in=0,
-                 gated=False):
-        if gated:
+                 gated=False, backward_d_in=0, dtype=torch.bfloat16):
+        if backward_d_in and not gated:
+            raise LoraError(LORA_ERR_INVALID_ARGUMENT, "lora_workspace_bytes_gated_backward")
+        if backward_d_in:
+            n_slices = 2
+            n = lora_workspace_bytes_gated_backward(T, n_slots, max_rank, backward_d_in, d_out, dtype_code(dtype))
+        elif gated:
             n_slices = 2
             n = (lora_workspace_bytes_gated_fp8(T, n_slots, max_rank, fp8_d_in, d_out) if fp8_d_in else
                  lora_workspace_bytes_gated(T, n_slots, max_rank, d_out))

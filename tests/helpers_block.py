@@ -136,3 +136,65 @@ def run_forward(p, act, mode=L.LORA_MODE_AUTO, keep=False, ws=None, flags=0, str
         L.lora_gated_forward(p.x, p.W[0], p.W[1], h, p.T, p.desc, p.ids_dev, ACTS[act], mode, flags, ws.buf,
                              gate=gate, up=up, stream=stream)
     return h, gate, up, ws
+
+
+def backward64(p, act, gate, up, dh):
+    """The gradients in 64 bits for gate and up as given, and their bounds:
+    dg and du are a few fp32 steps and one rounding off; every sum adds one
+    step per term; vectors of rank width reach the matrix cores as two bf16
+    parts at least (2^-17 of the value left out)."""
+    half, step, split = HALF[p.dtype], STEP32, 2.0 ** -17
+    x, dh = p.x.double(), dh.double()
+    g, u = gate.double(), up.double()
+    a, slope = act64(act, g)
+    dy = [dh * u * slope, dh * a]
+    act_dev = 32 * step * (1 + g.abs())
+    ddy = [half * dy[0].abs() + act_dev * (dh * u).abs(), half * dy[1].abs() + act_dev * (dh * a).abs()
+           + dh.abs() * g.abs() * 2.0 ** -46]
+    if p.dtype == torch.float32:
+        split = 0.0
+    dx, tx = torch.zeros_like(x), torch.zeros_like(x)
+    dA, tA, dB, tB = [], [], [], []
+    for m in range(2):
+        W = p.W[m].double()
+        size = dy[m].abs() @ W.t().abs()
+        dx += dy[m] @ W.t()
+        tx += ddy[m] @ W.t().abs() + (2 * p.f + 2 * p.R + 8) * step * size
+        da = torch.zeros(p.S, p.d, p.R, dtype=torch.float64, device="cuda")
+        db = torch.zeros(p.S, p.R, p.f, dtype=torch.float64, device="cuda")
+        ta, tb = torch.zeros_like(da), torch.zeros_like(db)
+        for s, r in enumerate(p.ranks[m]):
+            t = p.owners(s)
+            if not r or not len(t):
+                continue
+            A, B = p.A[m][s, :, :r].double(), p.B[m][s, :r].double()
+            sc = float(np.float32(p.alphas[s]) / np.float32(r))
+            dv = sc * (dy[m][t] @ B.t())
+            tv = sc * (ddy[m][t] @ B.t().abs() + (p.f + 8) * step * (dy[m][t].abs() @ B.t().abs())) + split * dv.abs()
+            dx[t] += dv @ A.t()
+            tx[t] += tv @ A.t().abs() + (2 * p.R + 8) * step * (dv.abs() @ A.t().abs())
+            n = len(t) + 8
+            da[s, :, :r] = x[t].t() @ dv
+            ta[s, :, :r] = x[t].t().abs() @ tv + n * step * (x[t].t().abs() @ dv.abs())
+            v = x[t] @ A
+            dev_v = (p.d + 8) * step * (x[t].abs() @ A.abs()) + split * v.abs()
+            db[s, :r] = sc * (v.t() @ dy[m][t])
+            tb[s, :r] = sc * (dev_v.t() @ dy[m][t].abs() + v.t().abs() @ ddy[m][t] +
+                              n * step * (v.t().abs() @ dy[m][t].abs()))
+        dA.append(da)
+        dB.append(db)
+        tA.append(ta * (1 + half) + half * da.abs() + 2.0 ** -120)
+        tB.append(tb * (1 + half) + half * db.abs() + 2.0 ** -120)
+    return dx, tx * (1 + half) + half * dx.abs() + 2.0 ** -120, dA, tA, dB, tB
+
+
+def run_backward(p, act, gate, up, dh, ws=None, stream=None, want_dx=True, want_ab=True, fill=7.0):
+    new = lambda *shape: torch.full(shape, fill, dtype=p.dtype, device="cuda")  # noqa: E731
+    dx = new(p.T, p.d) if want_dx else None
+    dA = [new(p.S, p.d, p.R) for _ in range(2)] if want_ab else None
+    dB = [new(p.S, p.R, p.f) for _ in range(2)] if want_ab else None
+    if ws is None:
+        ws = L.Workspace(p.T, p.S, p.R, p.f, gated=True, backward_d_in=p.d, dtype=p.dtype, stream=stream)
+    L.lora_gated_backward(p.x, p.W[0], p.W[1], p.T, p.desc, p.ids_dev, ACTS[act], gate, up, dh, dx, dA, dB, ws.buf,
+                          stream=stream)
+    return dx, dA, dB, ws

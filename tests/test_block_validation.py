@@ -102,3 +102,27 @@ def test_the_binding_takes_two_pools():
     p = pools()
     with pytest.raises(L.LoraError):
         L.lora_gated_forward(FAKE, FAKE, FAKE, FAKE, 1, [p[0]], FAKE, 0, 0, 0, None)
+
+
+def test_gated_backward(lib):
+    need = L.lora_workspace_bytes_gated_backward(8, 4, 16, 64, 96, L.LORA_BF16)
+    assert need >= 2 * 8 * 96 * 2 + 8 * 32 * 4
+    for bad in ((-1, 4, 16, 64, 96, 1), (8, 0, 16, 64, 96, 1), (8, 4, 72, 64, 96, 1), (8, 4, 16, 60, 96, 1),
+                (8, 4, 16, 64, 0, 1), (8, 4, 16, 64, 96, 2)):
+        assert L.lora_workspace_bytes_gated_backward(*bad) == 0, bad
+    two = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    one = (ctypes.c_void_p * 2)(FAKE, None)
+    odd = (ctypes.c_void_p * 2)(FAKE, FAKE + 8)
+
+    def call(x=FAKE, wg=FAKE, wu=FAKE, T=8, p=pools(), ids=FAKE, act=0, g=FAKE, u=FAKE, dh=FAKE, dx=FAKE, dA=two,
+             dB=two, ws=FAKE, n=need):
+        return lib.lora_gated_backward(x, wg, wu, T, p, ids, act, g, u, dh, dx, dA, dB, ws, n, None)
+
+    for bad in (dict(x=None), dict(wg=None), dict(wu=None), dict(T=-1), dict(ids=None), dict(act=3), dict(g=None),
+                dict(u=None), dict(dh=None), dict(dA=None), dict(dB=None), dict(dA=one), dict(dB=one), dict(dA=odd),
+                dict(dB=odd), dict(dx=FAKE + 8), dict(dh=FAKE + 2), dict(g=FAKE + 8), dict(ws=None), dict(ws=FAKE + 4),
+                dict(p=None), dict(p=pools(d_out=(96, 104))), dict(p=pools(dtype=(1, 0)))):
+        assert call(**bad) == INVALID, bad
+    assert call(p=pools(max_rank=(72, 72))) == UNSUPPORTED
+    assert call(n=1024) == SMALL
+    assert call(T=0, x=None, dA=None, dB=None) == OK
