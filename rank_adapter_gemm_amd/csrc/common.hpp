@@ -316,6 +316,7 @@ struct bwd_layout {
     ws_layout L;
     size_t dy;          // dg, du: [2][T][d_out], the pools' dtype
     size_t dv;          // fp32 [T][2 max_rank]
+    size_t vt;          // bf16 parts of s v and dv, transposed (see k_rank_finish)
     size_t oct;         // bf16: both slices' A in rank octets, one set per segment
     size_t row0, rank, scale;   // their pool tables, [n_slots]
     size_t partial;     // dx's split-K partials

@@ -101,6 +101,204 @@ __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>:
     }
 }
 
+// bf16: a grouped product over adapter segments, as k_shrink_grouped, of up to
+// 32 rows of dg (or du, blockIdx.z) with the adapter's B.  Both operands go
+// global -> LDS by DMA, NS stages of 128 n; B's octets ([n][8 ranks], 16 bytes
+// a column) lie in LDS as in memory and are read transposed
+// (ds_read_b64_tr_b16: 4 n of 16 ranks per instruction).  Each of the 4
+// wavefronts takes a 32-n quarter of every stage; N is split over blockIdx.y.
+// Partial sums go to part[m][split][sorted position][R].
+template <int RCH> struct rank_grad_cfg {
+    static constexpr int BR = kShrinkRows, NR = RCH * 16, BK = 128, CH = BK / 8, NS = 3;
+    static constexpr int OCT = BK * 8 + 16;              // elements between octets (32 bytes apart in the banks)
+    static constexpr int YST = BR * BK, STAGE = YST + (NR / 8) * OCT;
+    static constexpr int YI = BR * CH / 256, BI = NR / 8 * BK / 256;   // DMA instructions per wave per stage
+    static constexpr int RED = 4 * BR * (NR + 1);
+    static constexpr int LDS_BYTES = NS * STAGE * 2 > RED * 4 ? NS * STAGE * 2 : RED * 4;
+};
+
+struct rank_grad_args {
+    const uint16_t *dy;                // [2][T][N]
+    int32_t T, N, R, n_slots, n_chunk;
+    const int32_t *perm, *seg_id, *seg_start, *n_seg, *blk_start, *blk_seg;
+    float *part;
+};
+
+template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_args g, pair_pools pp) {
+    typedef rank_grad_cfg<RCH> C;
+    constexpr int BR = C::BR, NR = C::NR, BK = C::BK, CH = C::CH, NS = C::NS, PER = C::YI + C::BI;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[C::LDS_BYTES / 2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = blockIdx.z;
+    const int nseg = min(*g.n_seg, g.n_slots);
+    if (nseg <= 0 || (int)blockIdx.x >= g.blk_start[nseg]) return;
+    const int seg = g.blk_seg[blockIdx.x];
+    if (seg < 0 || seg >= nseg) return;
+    const int32_t id = g.seg_id[seg];
+    if (id < 0 || id >= g.n_slots) return;
+    const int64_t s0 = g.seg_start[seg], s1 = g.seg_start[seg + 1];
+    const int64_t q0 = s0 + ((int64_t)blockIdx.x - g.blk_start[seg]) * BR;
+    if (s0 < 0 || s1 > g.T || q0 < s0 || q0 >= s1) return;
+    const int p0 = (int)q0, pend = (int)(s1 < q0 + BR ? s1 : q0 + BR);
+    const int32_t rk = min(pp.rank[m][id], g.R);
+    const int n_begin = blockIdx.y * g.n_chunk, n_end = min(g.N, n_begin + g.n_chunk);
+    const uint16_t *dy = g.dy + (int64_t)m * g.T * g.N;
+    const uint16_t *b = (const uint16_t *)pp.b[m] + slot_row0(pp.row0[m], id, g.R) * g.N;
+
+    int64_t yrow[C::YI];
+    int ycol[C::YI];
+#pragma unroll
+    for (int j = 0; j < C::YI; ++j) {
+        const int c = (wave * C::YI + j) * 64 + lane, r = c / CH, p = p0 + r;
+        const int32_t t = p < pend ? perm_row(g.perm, p, g.T) : -1;
+        yrow[j] = t >= 0 ? (int64_t)t * g.N : -1;
+        ycol[j] = 8 * ((c % CH) ^ (r % CH));
+    }
+    auto dma_stage = [&](int kt, int buf) {
+        uint16_t *ys = smem + buf * C::STAGE, *bs = ys + C::YST;
+        const int k0 = n_begin + kt * BK;
+#pragma unroll
+        for (int j = 0; j < C::YI; ++j) {
+            const int n = k0 + ycol[j];
+            dma16(yrow[j] >= 0 && n < n_end ? (const void *)(dy + yrow[j] + n) : (const void *)g_zero16,
+                  ys + (wave * C::YI + j) * 64 * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < C::BI; ++j) {                 // half an octet's 128 columns per instruction
+            const int i = wave * C::BI + j, o = i >> 1, n = k0 + (i & 1) * 64 + lane;
+            dma16(8 * o < rk && n < n_end ? (const void *)(b + ((int64_t)o * g.N + n) * 8) : (const void *)g_zero16,
+                  bs + o * C::OCT + (i & 1) * 64 * 8);
+        }
+    };
+    auto wait_stage = [&](int ahead) {
+        if (ahead >= 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PER) : "memory");
+        else if (ahead == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    };
+    f32x4_t acc[2][RCH];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+        for (int rc = 0; rc < RCH; ++rc) acc[rb][rc] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int l16 = lane & 15, kg = lane >> 4;
+    const int nk = rk > 0 ? (n_end - n_begin + BK - 1) / BK : 0;
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st)
+        if (st < nk) dma_stage(st, st);
+    for (int kt = 0; kt < nk; ++kt) {
+        wait_stage(min(NS - 2, nk - 1 - kt));
+        // and this wave's reads of the stage before, whose buffer is refilled next
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
+        const uint16_t *ys = smem + (kt % NS) * C::STAGE, *bs = ys + C::YST;
+        uint4 yq[2];
+        bf16x8_t bq[RCH];
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) {
+            const int r = rb * 16 + l16;
+            yq[rb] = *reinterpret_cast<const uint4 *>(ys + r * BK + 8 * ((4 * wave + kg) ^ (r % CH)));
+        }
+#pragma unroll
+        for (int rc = 0; rc < RCH; ++rc) {
+            // lane's address: n of its quarter's k group, ranks 4 (l16 & 3) .. + 3 of 16
+            short4_t h[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = 32 * wave + 8 * kg + 4 * i + (l16 >> 2);
+                const uint16_t *at = bs + (2 * rc + ((l16 & 3) >> 1)) * C::OCT + n * 8 + 4 * (l16 & 1);
+                h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t *)(reinterpret_cast<uintptr_t>(at)));
+            }
+            const short8_t hv = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
+            bq[rc] = __builtin_bit_cast(bf16x8_t, hv);
+        }
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+            for (int rc = 0; rc < RCH; ++rc)
+                acc[rb][rc] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, yq[rb]), bq[rc],
+                                                                      acc[rb][rc], 0, 0, 0);
+    }
+    __syncthreads();                                      // all waves done with the stages
+    float (*red)[BR][NR + 1] = reinterpret_cast<float (*)[BR][NR + 1]>(smem);
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+        for (int rc = 0; rc < RCH; ++rc)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) red[wave][rb * 16 + 4 * kg + q][rc * 16 + l16] = acc[rb][rc][q];
+    __syncthreads();
+    float *part = g.part + (int64_t)(m * gridDim.y + blockIdx.y) * g.T * g.R;
+    for (int e = tid; e < BR * g.R; e += 256) {
+        const int i = e / g.R, j = e % g.R;
+        if (p0 + i < pend)
+            part[(int64_t)(p0 + i) * g.R + j] = (red[0][i][j] + red[1][i][j]) + (red[2][i][j] + red[3][i][j]);
+    }
+}
+
+// The rank vectors as the products that follow read them.  dv, fp32 [T][2R]
+// in batch order: the partial sums added in split order, times the slot's
+// scale; zero for rows without an adapter.  vt, bf16 [2][2][2R][Tp]: s v and
+// dv, transposed, in adapter order with every segment's start on a multiple
+// of 32 (its first work block), each value as two bf16 parts (hi = bf16(f),
+// lo = bf16(f - hi): together within 2^-17 of f, far below the rounding of
+// the bf16 gradients they add up to).  Places past a segment's rows are
+// filled with zeros.  A workgroup: 32 positions of one work block, or 32 rows
+// of the base block (grid.x from n_work on).
+struct rank_finish_args {
+    const float *v, *part;
+    int32_t n_split, T, R, n_slots, n_work, Tp;
+    const int32_t *perm, *offsets, *seg_id, *seg_start, *n_seg, *blk_start, *blk_seg;
+    float *dv;
+    uint16_t *vt;
+};
+
+__global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_pools pp) {
+    constexpr int BR = kShrinkRows;
+    const int R2 = 2 * g.R;
+    if ((int)blockIdx.x >= g.n_work) {
+        const int p0 = ((int)blockIdx.x - g.n_work) * BR, pend = min(min(g.offsets[1], p0 + BR), g.T);
+        for (int e = threadIdx.x; e < BR * R2; e += 256) {
+            const int p = p0 + e / R2;
+            const int64_t t = p < pend ? perm_row(g.perm, p, g.T) : -1;
+            if (t >= 0) g.dv[t * R2 + e % R2] = 0.0f;
+        }
+        return;
+    }
+    const int nseg = min(*g.n_seg, g.n_slots);
+    if (nseg <= 0 || (int)blockIdx.x >= g.blk_start[nseg]) return;
+    const int seg = g.blk_seg[blockIdx.x];
+    if (seg < 0 || seg >= nseg) return;
+    const int32_t id = g.seg_id[seg];
+    if (id < 0 || id >= g.n_slots) return;
+    const int p0 = g.seg_start[seg] + ((int)blockIdx.x - g.blk_start[seg]) * BR;
+    const int pend = min(min(g.seg_start[seg + 1], p0 + BR), g.T);
+    const int i = threadIdx.x & 31, p = p0 + i;
+    const int64_t t = p >= 0 && p < pend ? perm_row(g.perm, p, g.T) : -1;
+    const int64_t at = (int64_t)blockIdx.x * BR + i;
+    for (int j = threadIdx.x >> 5; j < R2; j += 8) {
+        const int m = j >= g.R, jj = j - m * g.R;
+        float f[2] = {0.0f, 0.0f};                        // s v, dv
+        if (t >= 0 && jj < min(pp.rank[m][id], g.R)) {
+            const float s = pp.scale[m][id];
+            f[0] = s * g.v[t * R2 + j];
+            const float *part = g.part + ((int64_t)m * g.n_split * g.T + p) * g.R + jj;
+            for (int c = 0; c < g.n_split; ++c) f[1] += part[(int64_t)c * g.T * g.R];
+            f[1] *= s;
+        }
+        if (t >= 0) g.dv[t * R2 + j] = f[1];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint32_t hi = f32_to_bf16_bits(f[w]);
+            // an infinite or NaN value has no second part
+            const float rest = f[w] - __uint_as_float(hi << 16);
+            uint16_t *o = g.vt + (int64_t)w * 2 * R2 * g.Tp + (int64_t)j * g.Tp + at;
+            o[0] = (uint16_t)hi;
+            o[(int64_t)R2 * g.Tp] = (uint16_t)f32_to_bf16_bits(rest == rest ? rest : 0.0f);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // A of the batch's slots in rank octets, gate's ranks then up's: [segment][2R /
 // 8][d_in][8], with the tables (row0, rank, scale) that make them one pool of
@@ -316,6 +514,24 @@ static void launch_nt_cfg(gemm_args g, const nt_args &nt, const gemm_plan &pl, h
     }
 }
 
+// The sum over both projections is long (twice d_out), so a grid that would
+// not fill the chip with the largest tiles splits it over K rather than take
+// smaller tiles (2048 x 28672 x 4096: 128 tiles in two pieces each against
+// 256 tiles of 256 x 128).
+static gemm_plan plan_dx(int T, int K, int N, size_t partial_bytes) {
+    const int tiles = ceil_div(T, 256) * ceil_div(N, 256);
+    if (tiles < 208 && K >= 8192 && T >= 256) {
+        int splits = 256 / tiles;
+        if (splits > kMaxGemmSplit) splits = kMaxGemmSplit;
+        if (splits > K / 2048) splits = K / 2048;
+        if (splits >= 2 && tiles * splits >= 208 && (size_t)splits * tiles * 256 * 256 * 4 <= partial_bytes) {
+            const int kc = ceil_div(ceil_div(K, splits), 64) * 64;
+            return gemm_plan{256, 256, 0, tiles, ceil_div(K, kc), kc};
+        }
+    }
+    return plan_gemm(T, K, N, partial_bytes);
+}
+
 // ---------------------------------------------------------------------------
 // dx, fp32: 64 x 64 tiles on v_mfma_f32_32x32x2_f32, the sum over F of dg then
 // of du; the low-rank term from A's rows in the store.
@@ -434,6 +650,175 @@ template <int DT> __global__ void __launch_bounds__(256) k_seg_outer(outer_args 
     }
 }
 
+// bf16, on the matrix cores: out[j][n] = sum_t vt[j][t] q[t][n] over a slot's
+// rows, 32 rows a stage.  A workgroup takes 128 columns n, 32 per wavefront,
+// and MB blocks of 32 ranks; q's rows (through perm) and both bf16 parts of
+// vt's rows are DMA'd into a ring of stages, q read transposed as the base
+// GEMM reads W.  One launch holds both gradients: the workgroups of dA (both
+// projections' ranks at once, so x is read once) come first, then dB's.
+constexpr int kOuterCols = 128, kOuterRows = 1024;
+struct seg_outer_args {
+    const uint16_t *x, *dy, *vt;       // [T][K], [2][T][N], see k_rank_finish
+    uint16_t *dA[2], *dB[2];
+    int32_t T, K, N, R, n_slots, Tp;
+    const int32_t *perm, *offsets, *rank[2], *seg_id, *seg_start, *n_seg, *blk_start;
+    int32_t tiles_k, tiles_n;          // column tiles of x and of dy
+};
+
+template <int MB> struct outer_cfg {
+    static constexpr int BT = 32, NS = MB > 2 ? 3 : 4;
+    static constexpr int QST = BT * kOuterCols, PST = 32 * MB * BT, STAGE = QST + 2 * PST;
+    static constexpr int QI = QST / 8 / 256, PI = 2 * PST / 8 / 256;   // DMA instructions per wave per stage
+};
+
+// rank rows [0, nj) at vt + j Tp (and, 2 R Tp on, their second parts), rows p0..p1 of
+// perm at places b0.., columns [n0, n0 + 128) of q [T][N].
+template <int MB>
+__device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *smem, int32_t *s_row,
+                                              const seg_outer_args &g,
+                                              const uint16_t *q, int N, int n0, const uint16_t *vt, int nj, int p0,
+                                              int p1, int64_t b0) {
+    typedef outer_cfg<MB> C;
+    constexpr int BT = C::BT, NS = C::NS, QI = C::QI, PI = C::PI, PER = QI + PI;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto dma_stage = [&](int kt, int buf) {
+        uint16_t *qs = smem + buf * C::STAGE, *ps = qs + C::QST;
+#pragma unroll
+        for (int j = 0; j < QI; ++j) {
+            const int c = (wave * QI + j) * 64 + lane, r = c >> 4, col = n0 + 8 * ((c & 15) ^ swz_w<kOuterCols>(r));
+            const int32_t t = s_row[kt * BT + r];
+            dma16(t >= 0 && col < N ? (const void *)(q + (int64_t)t * N + col) : (const void *)g_zero16,
+                  qs + (wave * QI + j) * 64 * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < PI; ++j) {                    // rank rows of 4 chunks: first parts, then second parts
+            const int c = (wave * PI + j) * 64 + lane, part = c / (32 * MB * 4), r = c / 4 % (32 * MB);
+            const int ch = (c & 3) ^ ((r >> 1) & 3);
+            dma16(r < nj ? (const void *)(vt + ((int64_t)part * 2 * g.R + r) * g.Tp + b0 + kt * BT + 8 * ch)
+                         : (const void *)g_zero16,
+                  ps + (wave * PI + j) * 64 * 8);
+        }
+    };
+    auto wait_stage = [&](int ahead) {
+        if (ahead >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER) : "memory");
+        else if (ahead == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PER) : "memory");
+        else if (ahead == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    };
+    const int fr = lane & 31, fk = lane >> 5, grp = lane >> 4, s16 = lane & 15;
+    const int b_kofs = 8 * (grp >> 1) + (s16 >> 2), b_col = 32 * wave + 16 * (grp & 1) + 4 * (s16 & 3);
+    // The rows' indices lie in LDS, kOuterRows at a time: a load of them in the
+    // loop would wait for every stage in flight.
+    for (; p0 < p1; p0 += kOuterRows, b0 += kOuterRows) {
+    const int rows = min(p1 - p0, kOuterRows), nk = (rows + BT - 1) / BT;
+    __syncthreads();
+    for (int i = tid; i < nk * BT; i += 256) s_row[i] = i < rows ? perm_row(g.perm, p0 + i, g.T) : -1;
+    __syncthreads();
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st)
+        if (st < nk) dma_stage(st, st);
+    for (int kt = 0; kt < nk; ++kt) {
+        wait_stage(min(NS - 2, nk - 1 - kt));
+        // and this wave's reads of the stage before, whose buffer is refilled next
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
+        const uint16_t *qs = smem + (kt % NS) * C::STAGE, *ps = qs + C::QST;
+#pragma unroll
+        for (int ks = 0; ks < BT / 16; ++ks) {
+            short4_t h[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = 16 * ks + 4 * i + b_kofs;
+                const uint16_t *at = qs + k * kOuterCols + 8 * ((b_col >> 3) ^ swz_w<kOuterCols>(k)) + (b_col & 7);
+                h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t *)(reinterpret_cast<uintptr_t>(at)));
+            }
+            const short8_t hv = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
+            const bf16x8_t bq = __builtin_bit_cast(bf16x8_t, hv);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const int r = mb * 32 + fr, ch = (2 * ks + fk) ^ ((r >> 1) & 3);
+                    const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(ps + part * C::PST + r * BT + 8 * ch);
+                    acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, bq, acc[mb], 0, 0, 0);
+                }
+        }
+    }
+    }
+}
+
+template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
+    constexpr int LA = outer_cfg<MBA>::NS * outer_cfg<MBA>::STAGE, LB = outer_cfg<MBB>::NS * outer_cfg<MBB>::STAGE;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[LA > LB ? LA : LB];
+    __shared__ int32_t s_row[kOuterRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n_a = g.n_slots * g.tiles_k;
+    const bool is_a = (int)blockIdx.x < n_a;
+    int item = is_a ? blockIdx.x : blockIdx.x - n_a;
+    const int tiles = is_a ? g.tiles_k : 2 * g.tiles_n;
+    const int slot = item / tiles;
+    item -= slot * tiles;
+    const int m = !is_a && item >= g.tiles_n, tile = item - m * g.tiles_n;
+    const int n0 = tile * kOuterCols, N = is_a ? g.K : g.N;
+    const int p0 = max(g.offsets[slot + 1], 0), p1 = min(g.offsets[slot + 2], g.T);
+    // the segment of this slot, for its first work block (seg_id ascends)
+    int64_t b0 = 0;
+    if (p1 > p0) {
+        int lo = 0, hi = min(*g.n_seg, g.n_slots) - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (g.seg_id[mid] < slot) lo = mid + 1;
+            else hi = mid;
+        }
+        b0 = (int64_t)g.blk_start[lo] * kShrinkRows;
+    }
+    const int col = n0 + 32 * wave + (lane & 31), j4 = 4 * (lane >> 5);
+    // ranks past the slot's get zeros whatever the rows hold
+    const int R = g.R, rk[2] = {min(g.rank[0][slot], R), min(g.rank[1][slot], R)};
+    if (is_a) {
+        f32x16_t acc[MBA];
+#pragma unroll
+        for (int mb = 0; mb < MBA; ++mb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
+        seg_outer_sum<MBA>(acc, smem, s_row, g, g.x, N, n0, g.vt + (int64_t)2 * 2 * R * g.Tp, 2 * R, p0, p1, b0);
+        if (col >= N) return;
+        // [slot][k][j]: a lane's accumulators hold groups of 4 neighbouring ranks of its k
+#pragma unroll
+        for (int mb = 0; mb < MBA; ++mb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = mb * 32 + 8 * q + j4;
+                if (j >= 2 * R) continue;
+                const int jj = j < R ? j : j - R, r = j < R ? rk[0] : rk[1];
+                uint16_t *out = (j < R ? g.dA[0] : g.dA[1]) + ((int64_t)slot * N + col) * R + jj;
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = jj + e < r ? acc[mb][4 * q + e] : 0.0f;
+                *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+            }
+    } else {
+        f32x16_t acc[MBB];
+#pragma unroll
+        for (int mb = 0; mb < MBB; ++mb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
+        seg_outer_sum<MBB>(acc, smem, s_row, g, g.dy + (int64_t)m * g.T * N, N, n0, g.vt + (int64_t)m * R * g.Tp, R, p0, p1,
+                           b0);
+        if (col >= N) return;
+        uint16_t *out = (m ? g.dB[1] : g.dB[0]) + (int64_t)slot * R * N + col;
+#pragma unroll
+        for (int mb = 0; mb < MBB; ++mb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int j = mb * 32 + 8 * (e >> 2) + j4 + (e & 3);
+                if (j < R) out[(int64_t)j * N] = j < rk[m] ? (uint16_t)f32_to_bf16_bits(acc[mb][e]) : (uint16_t)0;
+            }
+    }
+}
+
 __global__ void __launch_bounds__(256) k_zero16(uint4 *p, int64_t n) {
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
@@ -447,6 +832,8 @@ bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t R, int32_t d_in, 
     size_t o = B.L.total;
     B.dy = o;      o = align256(o + 2 * t * (size_t)d_out * eb);
     B.dv = o;      o = align256(o + 4 * t * 2 * (size_t)R);
+    // transposed bf16 parts of s v and dv, every segment from a work block on
+    B.vt = o;      o = align256(o + (dtype == LORA_BF16 ? 16 * (size_t)R * 32 * ((t + 31) / 32 + segs) : 0));
     B.oct = o;     o = align256(o + (dtype == LORA_BF16 ? segs * 2 * (size_t)R * (size_t)d_in * 2 : 0));
     B.row0 = o;    o = align256(o + 4 * (size_t)n_slots);
     B.rank = o;    o = align256(o + 4 * (size_t)n_slots);
@@ -496,8 +883,34 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     // v = x A (also records the bad ids); dv
     st = launch_shrink(c.x, T, p, 2, c.ids, true, v, L, ws, s);
     if (st != LORA_OK) return st;
-    hipLaunchKernelGGL(k_rank_grad_rows<DT>, dim3(T, 2), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R, c.ids,
-                       dv);
+    const int32_t row_blocks = ceil_div(T, kShrinkRows), n_work = row_blocks + (S < T ? S : T), Tp = n_work * 32;
+    uint16_t *vt = ws_ptr<uint16_t>(ws, B.vt);
+    if constexpr (DT == LORA_F32) {
+        hipLaunchKernelGGL(k_rank_grad_rows<DT>, dim3(T, 2), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R,
+                           c.ids, dv);
+    } else {
+        // about 1024 workgroups with work, of at least 512 columns
+        int split = ceil_div(512, row_blocks + 1);
+        if (split > kMaxKSplit) split = kMaxKSplit;
+        if (split > F / 512) split = F / 512;
+        if (split < 1) split = 1;
+        const int n_chunk = ceil_div(ceil_div(F, split), 128) * 128;
+        split = ceil_div(F, n_chunk);
+        float *part = ws_ptr<float>(ws, L.partial);
+        rank_grad_args g{(const uint16_t *)dg, T, F, R, S, n_chunk, perm, ws_ptr<int32_t>(ws, L.seg_id),
+                         ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
+                         ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg), part};
+        const dim3 grid(n_work, split, 2);
+        switch ((R + 15) / 16) {
+            case 1: hipLaunchKernelGGL(k_rank_grad<1>, grid, dim3(256), 0, s, g, pp); break;
+            case 2: hipLaunchKernelGGL(k_rank_grad<2>, grid, dim3(256), 0, s, g, pp); break;
+            case 3: hipLaunchKernelGGL(k_rank_grad<3>, grid, dim3(256), 0, s, g, pp); break;
+            default: hipLaunchKernelGGL(k_rank_grad<4>, grid, dim3(256), 0, s, g, pp); break;
+        }
+        rank_finish_args f{v, part, split, T, R, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
+                           g.blk_start, g.blk_seg, dv, vt};
+        hipLaunchKernelGGL(k_rank_finish, dim3(n_work + row_blocks), dim3(256), 0, s, f, pp);
+    }
     if (c.dx && DT == LORA_F32) {
         dx_f32_args g{{(const float *)dg, (const float *)du}, {(const float *)c.W[0], (const float *)c.W[1]},
                       (float *)c.dx, dv, c.ids, perm, T, F, K, S, R, ceil_div(K, 64)};
@@ -527,7 +940,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         g.v = dv;
         g.v_stride = 2 * R;
         g.partial = ws_ptr<float>(ws, B.partial);
-        const gemm_plan pl = plan_gemm(T, g.K, g.N, c.ws_bytes - B.partial);
+        const gemm_plan pl = plan_dx(T, g.K, g.N, c.ws_bytes - B.partial);
         g.n_tiles_m = ceil_div(T, pl.bm);
         g.n_tiles_n = ceil_div(g.N, pl.bn);
         g.col_strips = col_strips_pay(T, g.N, g.n_tiles_n);
@@ -536,7 +949,20 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         else if (pl.bn == 128) launch_nt_cfg<128, 128, 2, 4, 2, 4, 8>(g, nt, pl, s);
         else launch_nt_cfg<128, 64, 2, 4, 2, 2, 4>(g, nt, pl, s);
     }
-    if (c.dA[0]) {
+    if (c.dA[0] && DT == LORA_BF16) {
+        seg_outer_args g{(const uint16_t *)c.x, (const uint16_t *)dg, vt,
+                         {(uint16_t *)c.dA[0], (uint16_t *)c.dA[1]}, {(uint16_t *)c.dB[0], (uint16_t *)c.dB[1]},
+                         T, K, F, R, S, Tp, perm, offsets, {p[0].rank, p[1].rank}, ws_ptr<int32_t>(ws, L.seg_id),
+                         ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
+                         ws_ptr<int32_t>(ws, L.blk_start), ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
+        const dim3 grid((uint32_t)S * (g.tiles_k + 2 * g.tiles_n));
+        switch ((R + 15) / 16) {
+            case 1: hipLaunchKernelGGL((k_seg_outer_mfma<1, 1>), grid, dim3(256), 0, s, g); break;
+            case 2: hipLaunchKernelGGL((k_seg_outer_mfma<2, 1>), grid, dim3(256), 0, s, g); break;
+            case 3: hipLaunchKernelGGL((k_seg_outer_mfma<3, 2>), grid, dim3(256), 0, s, g); break;
+            default: hipLaunchKernelGGL((k_seg_outer_mfma<4, 2>), grid, dim3(256), 0, s, g); break;
+        }
+    } else if (c.dA[0]) {
         outer_args g{};
         g.offsets = offsets;
         g.perm = perm;
