@@ -609,7 +609,8 @@ static lora_status_t run_gated(gated_call &c, lora_mode_t mode, uint32_t flags, 
         if (st != LORA_OK) return st;
     }
     float *v = ws_ptr<float>(ws, L.v);
-    const lora_status_t st = launch_shrink(c.x, c.T, c.pools, 2, c.ids, sgmv, v, L, ws, s);
+    const lora_status_t st = sgmv ? launch_shrink(c.x, c.T, c.pools, 2, c.ids, sgmv, v, L, ws, s)
+                                  : launch_shrink_pair(c.x, c.T, c.pools, c.ids, v, ws_ptr<int32_t>(ws, L.header), s);
     if (st != LORA_OK) return st;
     c.v = v;
     c.perm = sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr;

@@ -309,6 +309,9 @@ struct gated_call {
     size_t partial_bytes;
 };
 lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s);
+// The pair's rank vectors for rows in their own order: v[t][m max_rank + j].
+lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *pools, const int32_t *ids, float *v,
+                                 int32_t *err, hipStream_t s);
 
 // Its backward pass: the workspace of a forward (segments, v and the shrink's
 // partials for 2 max_rank columns) and what follows it.

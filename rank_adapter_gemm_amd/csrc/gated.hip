@@ -97,6 +97,86 @@ __global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// v = x A of both slices for rows in their own order.  A wavefront sums four
+// ranks of one row and slice: the row's few workgroups spread over the chip
+// (a single token's 2 x 16 ranks over 8 wavefronts, not one workgroup), and
+// each lane has all its loads of a stretch of 8 vectors in flight.  x is read
+// again for every four ranks, from cache.
+// ---------------------------------------------------------------------------
+constexpr int kPairRanks = 4;
+
+template <int DT>
+__global__ void __launch_bounds__(256) k_shrink_pair(const typename elem<DT>::T *x, int32_t T, int32_t d, pair_pools pp,
+                                                     int32_t n_slots, int32_t R, const int32_t *ids, float *v,
+                                                     int32_t *err) {
+    typedef typename elem<DT>::T E;
+    constexpr int VN = vec16<DT>::n, U = 8;
+    const int lane = threadIdx.x & 63;
+    const int groups = 2 * R / kPairRanks;                // per row; R is a multiple of 8
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t t = item / groups;
+    if (t >= T) return;
+    const int j2 = (int)(item - t * groups) * kPairRanks, m = j2 >= R, j0 = j2 - m * R;
+    const int32_t id = ids[t];
+    const bool in = id >= 0 && id < n_slots;
+    int32_t r = in ? min(pp.rank[m][id], R) : 0;
+    const int32_t other = in ? pp.rank[1][id] : 1;
+    float acc[kPairRanks] = {};
+    // A padded slot has all its max_rank rows (zeros from its rank on), so its
+    // loads need not wait for the rank; a packed one ends with its capacity.
+    if (in && (!pp.row0[m] || j0 < r)) {
+        const E *row = x + t * d, *a = (const E *)pp.a[m] + (slot_row0(pp.row0[m], id, R) + j0) * d;
+        const int n = d / VN;
+        for (int c0 = lane; c0 < n; c0 += 64 * U) {
+            uint4 xq[U], aq[U][kPairRanks];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = (int64_t)min(c0 + 64 * u, n - 1) * VN;   // past the end: the last vector, not summed
+                xq[u] = ldg16(row + c);
+#pragma unroll
+                for (int q = 0; q < kPairRanks; ++q) aq[u][q] = ldg16(a + q * (int64_t)d + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + 64 * u >= n) break;
+                float xf[VN], af[VN];
+                vec16<DT>::widen(xq[u], xf);
+#pragma unroll
+                for (int q = 0; q < kPairRanks; ++q) {
+                    vec16<DT>::widen(aq[u][q], af);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) acc[q] = fmaf(xf[e], af[e], acc[q]);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kPairRanks; ++q)
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) acc[q] += __shfl_xor(acc[q], o, 64);
+    }
+    if (lane == 0 && j2 == 0 && (id < -1 || id >= n_slots || (in && (r <= 0 || other <= 0))))
+        flag_bad_row(err, (int32_t)t);
+    if (lane == 0)
+        *reinterpret_cast<float4 *>(v + t * 2 * R + j2) =
+            make_float4(j0 < r ? acc[0] : 0.f, j0 + 1 < r ? acc[1] : 0.f, j0 + 2 < r ? acc[2] : 0.f,
+                        j0 + 3 < r ? acc[3] : 0.f);
+}
+
+lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *p, const int32_t *ids, float *v,
+                                 int32_t *err, hipStream_t s) {
+    const pair_pools pp = make_pair_pools(p);
+    const int64_t items = (int64_t)T * (2 * p[0].max_rank / kPairRanks);
+    const dim3 grid((uint32_t)((items + 3) / 4));
+    if (p[0].dtype == LORA_F32)
+        hipLaunchKernelGGL(k_shrink_pair<LORA_F32>, grid, dim3(256), 0, s, (const float *)x, T, p[0].d_in, pp,
+                           p[0].n_slots, p[0].max_rank, ids, v, err);
+    else
+        hipLaunchKernelGGL(k_shrink_pair<LORA_BF16>, grid, dim3(256), 0, s, (const uint16_t *)x, T, p[0].d_in, pp,
+                           p[0].n_slots, p[0].max_rank, ids, v, err);
+    return hip_status(hipGetLastError());
+}
+
 lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {
     const lora_pool_t *p = c.pools;
     if (p[0].dtype == LORA_F32) {

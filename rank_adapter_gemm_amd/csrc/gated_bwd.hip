@@ -58,12 +58,6 @@ __global__ void __launch_bounds__(256) k_gated_dact(const typename elem<DT>::T *
 // dv.  One workgroup per row and projection: rank octet by octet, each thread
 // strides the row's N values against the slot's B octets.
 // ---------------------------------------------------------------------------
-struct pair_pools {
-    const void *a[2], *b[2];
-    const float *scale[2];
-    const int32_t *rank[2], *row0[2];
-};
-
 template <int DT>
 __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>::T *dy, int64_t dy_stride, int32_t T,
                                                         int32_t N, pair_pools pp, int32_t n_slots, int32_t R,
@@ -455,7 +449,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if constexpr (!SPLIT)
-        lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, n0, wm * WM,
+        lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1), 1, 0, true>(g, acc, s_meta_t, s_meta_id, n0, wm * WM,
                                                                       n0 + wn * WN, lane);
     wait_stage(min(NS - 1, nk - 1));
     __builtin_amdgcn_s_barrier();
@@ -869,14 +863,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     const int32_t *perm = ws_ptr<int32_t>(ws, L.perm), *offsets = ws_ptr<int32_t>(ws, L.offsets);
     float *v = ws_ptr<float>(ws, L.v), *dv = ws_ptr<float>(ws, B.dv);
     E *dg = ws_ptr<E>(ws, B.dy), *du = dg + (int64_t)T * F;
-    pair_pools pp;
-    for (int m = 0; m < 2; ++m) {
-        pp.a[m] = p[m].a;
-        pp.b[m] = p[m].b;
-        pp.scale[m] = p[m].scale;
-        pp.rank[m] = p[m].rank;
-        pp.row0[m] = p[m].row0;
-    }
+    const pair_pools pp = make_pair_pools(p);
     const int64_t n_vec = (int64_t)T * F / vec16<DT>::n;
     hipLaunchKernelGGL(k_gated_dact<DT>, dim3((uint32_t)(n_vec < (1 << 24) ? (n_vec + 255) / 256 : 1 << 16)),
                        dim3(256), 0, s, (const E *)c.gate, (const E *)c.up, (const E *)c.dh, dg, du, n_vec, c.act);

@@ -7,6 +7,18 @@
 
 namespace lora {
 
+// Gate's and up's pools, by value.
+struct pair_pools {
+    const void *a[2], *b[2];
+    const float *scale[2];
+    const int32_t *rank[2], *row0[2];
+};
+
+inline pair_pools make_pair_pools(const lora_pool_t *p) {
+    return pair_pools{{p[0].a, p[1].a}, {p[0].b, p[1].b}, {p[0].scale, p[1].scale}, {p[0].rank, p[1].rank},
+                      {p[0].row0, p[1].row0}};
+}
+
 // A launch numbers the columns of gate and up together, in groups of 64: 32
 // columns of gate, then the same 32 of up.  So a wavefront of 64 columns
 // holds both values of 32 columns of h in the same lanes' accumulators.
@@ -21,8 +33,6 @@ template <bool FINE> __device__ __forceinline__ float logistic(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
 
-template <int V> struct int_const { static constexpr int value = V; };
-
 constexpr float kGeluTanhK = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluTanhC = 0.044715f;
 
@@ -35,8 +45,74 @@ template <bool FINE> __device__ __forceinline__ float act_value(int act, float x
     return x * logistic<FINE>(kGeluTanhK * fmaf(kGeluTanhC * x * x, x, x));
 }
 
-// The low-rank terms of both pools: gate's into the even column blocks, up's
-// into the odd ones.  col0: the wavefront's first column of h.
+// A row's slot in both pools: what the per-row low-rank terms need of it.
+struct row_slot {
+    int32_t rank[2], row0[2];
+    float scale[2];
+};
+
+// Whether the 32 rows of this thread's half-wavefront (one block of a tile's
+// rows, one row a thread) name more than `most` adapters.
+__device__ __forceinline__ bool many_adapters(int32_t id, int most) {
+    const int sh = (threadIdx.x & 32);
+    uint32_t pend = (uint32_t)(__ballot(id >= 0) >> sh);
+    int n = 0;
+    while (__any(pend != 0 && n <= most)) {
+        const int32_t a = __shfl(id, pend ? __ffs((int)pend) - 1 + sh : 0, 64);
+        const uint32_t same = (uint32_t)(__ballot(id == a) >> sh);
+        n += pend != 0;
+        pend &= ~same;
+    }
+    return n > most;
+}
+
+__device__ __forceinline__ row_slot load_row_slot(const gemm_args &g, int32_t id) {
+    row_slot r{{0, 0}, {0, 0}, {0.f, 0.f}};
+    if (id >= 0 && id < g.n_slots) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            r.rank[m] = min(g.sl[m].rank[id], g.max_rank);
+            r.row0[m] = (int32_t)slot_row0(g.sl[m].row0, id, g.max_rank);
+            r.scale[m] = g.sl[m].scale[id];
+        }
+    }
+    return r;
+}
+
+// One projection's low-rank terms for kernels at their register limit: one
+// block and one adapter at a time, nothing held for the next.
+template <int RB, int CB, int ST, int OF>
+__device__ __forceinline__ void lora_pass_lean(const gemm_args &g, const gemm_slice &sl, f32x16_t (&acc)[RB][CB * ST],
+                                               const int32_t *s_t, const int32_t *s_id, int wrow0, int wcol0,
+                                               int lane) {
+    gemm_args q = g;
+    q.b = sl.b;
+    q.v = g.v + sl.v_off;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int row = wrow0 + rb * 32 + (lane & 31);
+        const int32_t my_id = s_id[row], my_t = s_t[row];
+        const uint32_t live = (uint32_t)__ballot(my_t >= 0);
+        uint32_t pend = (uint32_t)__ballot(my_id >= 0);
+        while (pend) {
+            const int32_t a = uniform_i(__shfl(my_id, __ffs((int)pend) - 1, 64));
+            const uint32_t rows = (uint32_t)__ballot(my_id == a);
+            pend &= ~rows;
+            const int32_t ra = sl.rank[a], ro = sl.row0 ? sl.row0[a] : a * g.max_rank;
+            const float sa = sl.scale[a];
+            for (int ks = 0; ks * 16 < ra; ++ks) {
+                float4 v0, v1;
+                uint4 bq[CB];
+                lora_step_load<CB>(q, a, ra, ro, my_id == a, my_t, ks, lane >> 5, wcol0, lane, v0, v1, bq);
+                lora_step_mfma<CB, ST, OF>(acc[rb], sa, my_id == a && 16 * ks + 8 * (lane >> 5) < ra, v0, v1, bq,
+                                           (live & ~rows) != 0, rows);
+            }
+        }
+    }
+}
+
+// The low-rank terms of both pools on the matrix cores: gate's into the even
+// column blocks, up's into the odd ones.  col0: the wavefront's first column of h.
 template <int RB, int CB, int RG, int KB, int RF>
 __device__ __forceinline__ void gated_lora_pass(const gemm_args &g, f32x16_t (&acc)[RB][CB], const int32_t *s_t,
                                                 const int32_t *s_id, int wrow0, int col0, int lane) {
@@ -46,63 +122,116 @@ __device__ __forceinline__ void gated_lora_pass(const gemm_args &g, f32x16_t (&a
     q.scale = g.sl[0].scale;
     q.rank = g.sl[0].rank;
     q.row0 = g.sl[0].row0;
-    lora_pass_impl<RB, CB / 2, RG, KB, RF, 2, 0>(q, acc, s_t, s_id, 0, wrow0, col0, lane);
+    lora_pass_impl<RB, CB / 2, RG, KB, RF, 2, 0, true>(q, acc, s_t, s_id, 0, wrow0, col0, lane);
     q.b = g.sl[1].b;
     q.scale = g.sl[1].scale;
     q.rank = g.sl[1].rank;
     q.row0 = g.sl[1].row0;
     q.v = g.v + g.sl[1].v_off;
-    lora_pass_impl<RB, CB / 2, RG, KB, RF, 2, 1>(q, acc, s_t, s_id, 0, wrow0, col0, lane);
+    lora_pass_impl<RB, CB / 2, RG, KB, RF, 2, 1, true>(q, acc, s_t, s_id, 0, wrow0, col0, lane);
 }
 
-// The store: a wavefront's block of 32 rows goes through its LDS area once
-// per output (h, and gate and up where they are kept), so that each lane
-// writes 8 consecutive columns of a row, rounded once.
-template <int BM, int BN, int WV, int WR, int RB, int CB>
-__device__ __forceinline__ void gated_store_tile(const gemm_args &g, f32x16_t (&acc)[RB][CB], float *smem_f,
-                                                 const int32_t *s_meta_t, int n0, int w, int lane) {
-    constexpr int WM = BM / WR, WN = BN / (WV / WR), HN = WN / 2, SLD = HN + 4;
-    static_assert(CB % 2 == 0 && WN % 64 == 0, "a wavefront holds whole pairs");
-    const int wm = w / (WV / WR), wn = w % (WV / WR);
-    const int N = g.N;
-    constexpr int QN = HN / 8, RPP = 64 / QN, PASSES = 32 / RPP;
-    float *stage = smem_f + w * 32 * SLD;
-    const int q = lane % QN, rr = lane / QN;
-    const int n = gated_col(n0 + wn * WN) + 8 * q;
+// Both low-rank terms of 8 columns of one row: o[m] += s sum_j v[j]
+// B[j][n..n+8], rank octets in order, both projections' loads of an octet in
+// flight together.
+__device__ __forceinline__ void add_low_rank8(const gemm_args &g, const row_slot &rs, int64_t t, int n,
+                                              float (&o)[2][8]) {
+    const int oct = (max(rs.rank[0], rs.rank[1]) + 7) >> 3;
+    if (oct <= 0) return;
+    float d[2][8] = {};
+    for (int gg = 0; gg < oct; ++gg) {
+        float vv[2][8];
+        uint4 bq[2][8];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        // every other column block, from OF on
-        auto put = [&](uint16_t *out, auto of) {
-            constexpr int OF = decltype(of)::value;
-            __syncthreads();
+        for (int m = 0; m < 2; ++m) {
+            const bool in = 8 * gg < rs.rank[m];
+            const float *vrow = g.v + t * g.v_stride + g.sl[m].v_off + gg * 8;
+            const uint16_t *b = g.sl[m].b + ((int64_t)rs.row0[m] + 8 * gg) * g.N + (int64_t)n * 8;
 #pragma unroll
-            for (int p = 0; p < CB / 2; ++p)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    stage[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * SLD + p * 32 + (lane & 31)] =
-                        acc[rb][2 * p + OF][e];
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < PASSES; ++k) {
-                const int32_t t = s_meta_t[wm * WM + rb * 32 + rr + RPP * k];
-                if (t < 0 || n >= N) continue;
-                const float *src = stage + (rr + RPP * k) * SLD + 8 * q;
-                float f[8];
-                *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(src);
-                *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(src + 4);
-                stg16(out + (int64_t)t * N + n, vec16<LORA_BF16>::narrow(f));
+            for (int q = 0; q < 2; ++q) {
+                const float4 f = in ? *reinterpret_cast<const float4 *>(vrow + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                vv[m][4 * q] = f.x; vv[m][4 * q + 1] = f.y; vv[m][4 * q + 2] = f.z; vv[m][4 * q + 3] = f.w;
             }
-        };
-        if (g.sl[0].y) {
-            put(g.sl[0].y, int_const<0>{});
-            put(g.sl[1].y, int_const<1>{});
+#pragma unroll
+            for (int q = 0; q < 8; ++q) bq[m][q] = in ? ldg16(b + q * 8) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int p = 0; p < CB / 2; ++p)
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float bf[8];
+                vec16<LORA_BF16>::widen(bq[m][q], bf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[m][q] = fmaf(vv[m][e], bf[e], d[m][q]);
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[m][q] = fmaf(rs.scale[m], d[m][q], o[m][q]);
+}
+
+// 8 columns of one row: gate and up stored where they are kept, and h.
+__device__ __forceinline__ void gated_finish8(const gemm_args &g, int64_t t, int n, float (&o)[2][8]) {
+    const int64_t at = t * g.N + n;
+    if (g.sl[0].y) {
+        stg16(g.sl[0].y + at, vec16<LORA_BF16>::narrow(o[0]));
+        stg16(g.sl[1].y + at, vec16<LORA_BF16>::narrow(o[1]));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[0][e] = act_value<false>(g.act, o[0][e]) * o[1][e];
+    stg16(g.y + at, vec16<LORA_BF16>::narrow(o[0]));
+}
+
+// A tile row's part in the low-rank terms.  Blocks of 32 rows with few
+// adapters (long segments) take them on the matrix cores, from s_id, an adapter
+// after the other; the rows of other blocks each from their own adapter in
+// the store, from s_slot.  The border was measured: 192 single tokens of 64
+// adapters (FP8 base, 4096 x 14336) take 87 us row by row and 148 us block by
+// block; the 70B-sized mixed batch (2 to 4 adapters of rank 8-64 a block)
+// 4478 and 4241 us.
+constexpr int kBlockAdapters = 4;
+
+__device__ __forceinline__ void set_row(const gemm_args &g, int32_t id, bool per_row, int32_t &s_id, row_slot &s_slot) {
+    const bool apart = per_row || many_adapters(id, kBlockAdapters);
+    s_id = apart ? -1 : id;
+    s_slot = load_row_slot(g, apart ? id : -1);
+}
+
+// The store of a whole tile: the fp32 sums of WR * 32 rows at a time go
+// through LDS, and a thread then owns 8 neighbouring columns of gate, up and
+// h of one row (16-byte stores, one rounding each), to which it adds the
+// row's low-rank terms if they are not in the sums.
+template <int BM, int BN, int WV, int WR, int RB, int CB>
+__device__ __forceinline__ void gated_store_tile(const gemm_args &g, f32x16_t (&acc)[RB][CB], float *smem_f,
+                                                 const int32_t *s_t, const row_slot *s_slot, int n0, int w, int lane) {
+    constexpr int WM = BM / WR, WN = BN / (WV / WR), SLD = BN + 4, CPR = BN / 16, ITEMS = WR * 32 * CPR;
+    const int wm = w / (WV / WR), wn = w % (WV / WR), tid = w * 64 + lane;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        __syncthreads();
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                acc[rb][2 * p][e] = act_value<false>(g.act, acc[rb][2 * p][e]) * acc[rb][2 * p + 1][e];
-        put(g.y, int_const<0>{});
+                smem_f[(wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * SLD + wn * WN + cb * 32 + (lane & 31)] =
+                    acc[rb][cb][e];
+        __syncthreads();
+        for (int i = tid; i < ITEMS; i += WV * 64) {
+            const int r = i / CPR, c = (i % CPR) * 8, row = (r >> 5) * WM + rb * 32 + (r & 31);
+            const int32_t t = s_t[row];
+            const int n = gated_col(n0) + c;
+            if (t < 0 || n >= g.N) continue;
+            const float *src = smem_f + r * SLD + (c >> 5) * 64 + (c & 31);
+            float o[2][8];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                *reinterpret_cast<float4 *>(o[m]) = *reinterpret_cast<const float4 *>(src + 32 * m);
+                *reinterpret_cast<float4 *>(o[m] + 4) = *reinterpret_cast<const float4 *>(src + 32 * m + 4);
+            }
+            add_low_rank8(g, s_slot[row], t, n, o);
+            gated_finish8(g, t, n, o);
+        }
     }
 }
 
@@ -114,35 +243,6 @@ __device__ __forceinline__ void gated_store_partial(const gemm_args &g, f32x16_t
     gemm_args q = g;
     q.N = g.n_tiles_n * BN;
     gemm_store_tile<BM, BN, WV, WR, true, false>(q, acc, smem_f, nullptr, n0, w, lane, tidx, split);
-}
-
-// 8 columns of one row of the low-rank term, for the reduction: o += s sum_j
-// v[j] B[j][n..n+8], rank octets in order.
-__device__ __forceinline__ void add_low_rank8(const gemm_args &g, const gemm_slice &sl, int32_t id, int64_t t, int n,
-                                              float *o) {
-    const int32_t rk = min(sl.rank[id], g.max_rank);
-    if (rk <= 0) return;
-    const float sc = sl.scale[id];
-    const float *vrow = g.v + t * g.v_stride + sl.v_off;
-    const uint16_t *b = sl.b + slot_row0(sl.row0, id, g.max_rank) * g.N + (int64_t)n * 8;
-    float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int gg = 0; gg < (rk + 7) >> 3; ++gg) {
-        float vv[8];
-        *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(vrow + gg * 8);
-        *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(vrow + gg * 8 + 4);
-        uint4 bq[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) bq[q] = ldg16(b + (int64_t)gg * g.N * 8 + q * 8);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            float bf[8];
-            vec16<LORA_BF16>::widen(bq[q], bf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[q] = fmaf(vv[e], bf[e], d[q]);
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) o[q] = fmaf(sc, d[q], o[q]);
 }
 
 // Split-K reduction of the gated tiles: a thread owns 8 columns of h of one
@@ -162,6 +262,7 @@ __global__ void __launch_bounds__(256) k_gated_reduce(gemm_args g) {
     if (p >= g.T || n >= g.N) return;
     const int32_t t = perm_row(g.perm, p, g.T);
     if (t < 0) return;
+    const row_slot rs = load_row_slot(g, g.ids[t]);
     const int cg = (c >> 5) * 64 + (c & 31);              // gate's column of the partial tile; up's is 32 on
     float o[2][8] = {};
     const float *src = g.partial + ((int64_t)tidx * g.splits * BM + r) * BN + cg;
@@ -174,19 +275,8 @@ __global__ void __launch_bounds__(256) k_gated_reduce(gemm_args g) {
             o[m][4] += b.x; o[m][5] += b.y; o[m][6] += b.z; o[m][7] += b.w;
         }
     }
-    const int32_t id = g.ids[t];
-    if (id >= 0 && id < g.n_slots) {
-        add_low_rank8(g, g.sl[0], id, t, n, o[0]);
-        add_low_rank8(g, g.sl[1], id, t, n, o[1]);
-    }
-    const int64_t at = (int64_t)t * g.N + n;
-    if (g.sl[0].y) {
-        stg16(g.sl[0].y + at, vec16<LORA_BF16>::narrow(o[0]));
-        stg16(g.sl[1].y + at, vec16<LORA_BF16>::narrow(o[1]));
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[0][e] = act_value<false>(g.act, o[0][e]) * o[1][e];
-    stg16(g.y + at, vec16<LORA_BF16>::narrow(o[0]));
+    add_low_rank8(g, rs, t, n, o);
+    gated_finish8(g, t, n, o);
 }
 
 template <int BM, int BN> static void launch_gated_reduce(const gemm_args &g, hipStream_t s) {

@@ -47,7 +47,7 @@ template <int BM, int BN, int BK, int NS, bool SH, int WV = 4, int WR = 2> struc
 //     gated_col), each with its own weight and adapter pool; the epilogue
 //     writes h = act(gate) * up, so gate and up need not leave the chip.
 template <bool LORA, int BM, int BN, int BK, int NS, bool SPLIT, bool SH = false, int WV = 4, int WR = 2,
-          bool GATED = false>
+          bool GATED = false>   // GATED without LORA: the rows' terms are added in the store, row by row
 __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     static_assert(!SH || SPLIT, "the fused shrink runs in split-K mode");
     static_assert(!SH || (WV == 4 || WV == 8), "the fused shrink maps 4 or 8 threads to a (row, rank) pair");
@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     constexpr bool ADD = LORA && !SPLIT && NS == 1;
     static_assert(!GATED || (!SH && !ADD), "the gated pair has its own shrink and epilogue");
     typedef gemm_cfg<BM, BN, BK, NS, SH, WV, WR> C;
+    static_assert(!GATED || WR * 32 * (BN + 4) * 4 <= C::LDS, "the gated store fits the stages' LDS");
     constexpr int WM = C::WM, WN = C::WN, RB = C::RB, CB = C::CB;
     constexpr int XCH = C::XCH, WCH = C::WCH, XSTAGE = C::XSTAGE, WSTAGE = C::WSTAGE;
     constexpr int XI = C::XI, WI = C::WI, AI = C::AI, ACH = C::ACH, STAGE = C::STAGE;
@@ -220,6 +221,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     // -1).  Split pieces keep none: they write every row of their partial
     // tile (rows past T hold zeros) and the reduction skips those rows.
     int32_t *s_meta_t = nullptr, *s_meta_id = nullptr;
+    constexpr bool SLOTS = GATED && !SPLIT;
+    __shared__ row_slot s_slot[SLOTS ? BM : 1];
     if constexpr (!SPLIT) {
         __shared__ int32_t s_meta_t_buf[BM], s_meta_id_buf[BM];
         s_meta_t = s_meta_t_buf;
@@ -231,12 +234,13 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
             const int p = m0 + i;
             const int32_t t = (p < T) ? perm_row(g.perm, p, T) : -1;
             int32_t id = -1;
-            if (LORA && t >= 0 && (!g.n_fused || p < n_fused)) {
+            if ((LORA || GATED) && t >= 0 && (!g.n_fused || p < n_fused)) {
                 const int32_t raw = g.ids[t];
                 if (raw >= 0 && raw < g.n_slots && (GATED || g.rank[raw] > 0)) id = raw;
             }
             s_meta_t[i] = (ADD && id < 0) ? -1 : t;   // adding: rows without a term stay untouched
-            s_meta_id[i] = id;
+            if constexpr (SLOTS) set_row(g, id, !LORA, s_meta_id[i], s_slot[i]);
+            else s_meta_id[i] = id;
         }
     }
 
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     // the first stages load.  (Split-K tiles leave it to the reduction, whose
     // one-thread-per-row-chunk layout hides the per-row loads of B.)
     if constexpr (GATED && LORA && !SPLIT)
-        gated_lora_pass<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, wm * WM,
+        gated_lora_pass<RB, CB, (RB >= 4 ? 2 : 1), 1, (RB >= 4 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, wm * WM,
                                                                        gated_col(n0 + wn * WN), lane);
     else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN,
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
                 load_frags((kt + 1) % NS, 0, af[nxt], bfr[nxt]);
                 if (SH && kt + 1 < nk) shrink_load((kt + 1) % NS);
                 mfmas(af[cur], bfr[cur], RB / 2, RB);
-                sched_interleave<NREAD, RB / 2 * CB>();
+                sched_interleave<NREAD, (RB - RB / 2) * CB>();
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     }
 
     if constexpr (GATED && !SPLIT)
-        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane);
+        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_slot, n0, w, lane);
     else if constexpr (GATED)
         gated_store_partial<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), n0, w, lane, tidx, split);
     else
@@ -745,9 +749,25 @@ static void launch_gated_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s) {
     }
 }
 
-// h = act(x Wg + ...) * (x Wu + ...), the bf16 pair.
-// Wavefronts of 64 columns (one gate block, one up block): the 256 x 128
-// tiles therefore run their 8 wavefronts 4 x 2.
+// Up to 32 rows: four wavefronts side by side over the tile's 128 columns.
+static void launch_gated_few(gemm_args g, const gemm_plan &pl, hipStream_t s) {
+    g.tile_base = 0;
+    g.n_tiles = pl.n_dp + pl.tail;
+    g.splits = pl.splits;
+    g.k_chunk = pl.k_chunk;
+    if (pl.splits == 1)
+        hipLaunchKernelGGL((k_gemm_bf16<false, 32, 128, 64, 3, false, false, 4, 1, true>), dim3(g.n_tiles), dim3(256),
+                           0, s, g);
+    else {
+        hipLaunchKernelGGL((k_gemm_bf16<false, 32, 128, 64, 3, true, false, 4, 1, true>), dim3(g.n_tiles * pl.splits),
+                           dim3(256), 0, s, g);
+        launch_gated_reduce<32, 128>(g, s);
+    }
+}
+
+// h = act(x Wg + ...) * (x Wu + ...), the bf16 pair.  Wavefronts hold 64
+// columns (a gate and an up block): the 256 x 128 tiles therefore run their 8
+// wavefronts 4 x 2.
 lora_status_t launch_gemm_gated(gemm_args &g, size_t partial_bytes, hipStream_t s) {
     const gemm_plan pl = plan_gated(g.T, g.K, g.N, partial_bytes);
     g.n_tiles_m = ceil_div(g.T, pl.bm);
@@ -755,7 +775,9 @@ lora_status_t launch_gemm_gated(gemm_args &g, size_t partial_bytes, hipStream_t 
     g.col_strips = col_strips_pay(g.T, 2 * g.N, g.n_tiles_n);
     if (pl.bm == 256 && pl.bn == 256) launch_gated_cfg<256, 256, 2, 8, 2, 2, 8, 2>(g, pl, s);
     else if (pl.bm == 256) launch_gated_cfg<256, 128, 2, 8, 4, 2, 8, 2>(g, pl, s);
-    else launch_gated_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
+    else if (pl.bm == 128) launch_gated_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
+    else if (pl.bm == 64) launch_gated_cfg<64, 128, 3, 4, 2, 3, 4, 2>(g, pl, s);
+    else launch_gated_few(g, pl, s);
     return hip_status(hipGetLastError());
 }
 

@@ -195,9 +195,35 @@ __device__ __forceinline__ void lora_step_load(const gemm_args &g, int32_t a, in
 // acc += (s_a v) B for one step from loaded operands; lanes with `use` false
 // (rows of other adapters, ranks past the slot's) contribute zero.
 // Column block cb is acc[cb * ST + OF] (every block, or one of a gated pair).
+// apart (wave-uniform): the block holds rows of others than this adapter,
+// whose operands are zeros -- but a zero times an infinite or NaN value of B is
+// NaN.  Such values are then taken out of the product, and the adapter's own
+// rows (bits of `rows`) get NaN in their columns.
 template <int CB, int ST, int OF>
 __device__ __forceinline__ void lora_step_mfma(f32x16_t (&acc)[CB * ST], float sa, bool use, const float4 &v0,
-                                               const float4 &v1, const uint4 (&bq)[CB]) {
+                                               const float4 &v1, uint4 (&bq)[CB], bool apart = false,
+                                               uint32_t rows = 0) {
+    if (apart) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            const uint32_t w[4] = {bq[cb].x, bq[cb].y, bq[cb].z, bq[cb].w};
+            uint32_t bad = 0;                              // a half of x with all exponent bits set
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = (w[e] & 0x7f807f80u) ^ 0x7f807f80u;
+                bad |= (x - 0x00010001u) & ~x & 0x80008000u;
+            }
+            if (__ballot(bad != 0) != 0) {                 // rare
+                bad |= __shfl_xor(bad, 32, 64);            // the column's other 8 ranks
+                const int half = (threadIdx.x >> 5) & 1;
+                const uint32_t mine = bad ? rows >> (4 * half) : 0u;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if ((mine >> (8 * (e >> 2) + (e & 3))) & 1u) acc[cb * ST + OF][e] = __builtin_nanf("");
+                if (bad) bq[cb] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
     const uint32_t m = use ? ~0u : 0u;
     const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     // s v as three bf16 parts: hi = bf16(f), mid = bf16(f - hi), lo =
@@ -241,7 +267,7 @@ __device__ __forceinline__ void lora_step_mfma(f32x16_t (&acc)[CB * ST], float s
 // the slot's rank and scale read per adapter (kernels with no registers to
 // spare).  Per block the MFMAs run in the same order either way: adapters
 // by lowest row, ranks ascending.
-template <int RB, int CB, int RG = 1, int KB = 1, int RF = 1, int ST = 1, int OF = 0>
+template <int RB, int CB, int RG = 1, int KB = 1, int RF = 1, int ST = 1, int OF = 0, bool ISO = false>
 __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&acc)[RB][CB * ST],
                                                const int32_t *s_t, const int32_t *s_id, int n0,
                                                int wrow0, int wcol0, int lane) {
@@ -250,6 +276,8 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
     const int half = lane >> 5;
     int32_t my_id[RB], my_t[RB], my_r[RB], my_o[RB], a0[RB], ra0[RB], ro0[RB];
     float my_s[RB], sa0[RB];
+    uint32_t rows0[RB];                                   // ISO: the rows of a block's first adapter, and whether
+    bool apart0[RB];                                      // there are rows of others beside them
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int row = wrow0 + rb * 32 + (lane & 31);
@@ -260,6 +288,8 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
         ra0[rb] = a0[rb] >= 0 ? g.rank[a0[rb]] : 0;
         sa0[rb] = a0[rb] >= 0 ? g.scale[a0[rb]] : 0.0f;
         ro0[rb] = slot_row0_i(g, a0[rb]);
+        rows0[rb] = ISO ? (uint32_t)__ballot(my_id[rb] == a0[rb]) : 0u;
+        apart0[rb] = ISO && ((uint32_t)__ballot(my_t[rb] >= 0) & ~rows0[rb]) != 0;
     }
 #pragma unroll
     for (int r0 = 0; r0 < RB; r0 += RG) {
@@ -282,7 +312,7 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
                     if (16 * (ks0 + u) < ra0[r0 + i])      // wave-uniform
                         lora_step_mfma<CB, ST, OF>(acc[r0 + i], sa0[r0 + i],
                                            my_id[r0 + i] == a0[r0 + i] && 16 * (ks0 + u) + 8 * half < ra0[r0 + i],
-                                           v0[i][u], v1[i][u], bq[i][u]);
+                                           v0[i][u], v1[i][u], bq[i][u], ISO && apart0[r0 + i], rows0[r0 + i]);
         }
     }
     if (RF == 0) {
@@ -303,7 +333,8 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
                     float4 v0, v1;
                     uint4 bq[CB];
                     lora_step_load<CB>(g, a, ra, ro, mine, my_t[rb], ks, half, wcol0, lane, v0, v1, bq);
-                    lora_step_mfma<CB, ST, OF>(acc[rb], sa, mine && 16 * ks + 8 * half < ra, v0, v1, bq);
+                    lora_step_mfma<CB, ST, OF>(acc[rb], sa, mine && 16 * ks + 8 * half < ra, v0, v1, bq, ISO,
+                                               ISO ? (uint32_t)__ballot(mine) : 0u);
                 }
             }
         }
@@ -360,7 +391,7 @@ __device__ __forceinline__ void lora_pass_impl(const gemm_args &g, f32x16_t (&ac
                 for (int i = 0; i < RFG; ++i)
                     if (16 * ks < ra[i])                   // wave-uniform
                         lora_step_mfma<CB, ST, OF>(acc[r0 + i], sa[i], mine[i] && 16 * ks + 8 * half < ra[i], v0[i], v1[i],
-                                           bq[i]);
+                                                   bq[i], ISO, ISO ? (uint32_t)__ballot(mine[i]) : 0u);
             }
         }
     }
@@ -649,15 +680,25 @@ inline gemm_plan plan_gemm(int T, int K, const int32_t *Ns, int nN, size_t parti
 // pairs per wavefront (no 64-column tiles: those grids split K instead).
 inline gemm_plan plan_gated(int T, int K, int N, size_t partial_bytes, int kgran = 64) {
     const int32_t n = 2 * N;
-    gemm_plan p = plan_gemm(T, K, &n, 1, partial_bytes, kgran);
-    if (p.bn != 64) return p;
-    const int tiles = ceil_div(T, 128) * ceil_div(n, 128);
-    int splits = ceil_div(256, tiles);
+    // Few rows are bound by the weights' bytes: tiles of 32 or 64 rows, whose x
+    // stages are small, so that two workgroups of a CU stream at once (one row,
+    // 4096 x 14336 twice: 49 us, 4.8 TB/s, where 256-row tiles take 86).  They
+    // are not split while whole tiles give most CUs one.
+    int bm = 128;
+    if (T <= 64) {
+        bm = T <= 32 ? 32 : 64;
+    } else {
+        const gemm_plan p = plan_gemm(T, K, &n, 1, partial_bytes, kgran);
+        if (p.bn != 64) return p;
+    }
+    const int tiles = ceil_div(T, bm) * ceil_div(n, 128);
+    int splits = tiles >= 160 ? 1 : ceil_div(256, tiles);
+    if (splits > kMaxGemmSplit) splits = kMaxGemmSplit;
     if (splits > K / 256) splits = K / 256;
-    while (splits > 1 && (size_t)splits * tiles * 128 * 128 * 4 > partial_bytes) --splits;
-    if (splits <= 1) return gemm_plan{128, 128, tiles, 0, 1, K};
+    while (splits > 1 && (size_t)splits * tiles * bm * 128 * 4 > partial_bytes) --splits;
+    if (splits <= 1) return gemm_plan{bm, 128, tiles, 0, 1, K};
     const int k_chunk = ceil_div(ceil_div(K, splits), kgran) * kgran;
-    return {128, 128, 0, tiles, ceil_div(K, k_chunk), k_chunk};
+    return {bm, 128, 0, tiles, ceil_div(K, k_chunk), k_chunk};
 }
 
 // One output of width N.

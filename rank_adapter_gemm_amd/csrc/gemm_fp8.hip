@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     typedef fp8_cfg<BM, BN, NS, WV, WR> C;
     constexpr int BK = C::BK, CH = C::CH, WM = C::WM, WN = C::WN, RB = C::RB, CB = C::CB;
     constexpr int XI = C::XI, WI = C::WI, XSTAGE = C::XSTAGE, STAGE = C::STAGE;
+    static_assert(!GATED || WR * 32 * (BN + 4) * 4 <= C::LDS, "the gated store fits the stages' LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int wm = w / (WV / WR), wn = w % (WV / WR);
@@ -202,11 +203,19 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
         uint8_t *xs = smem + buf * STAGE;
         uint8_t *wsm = xs + XSTAGE;
         const int k0 = k_begin + kt * BK;
+        // Gated: only a last, partial stage looks at its chunks' columns, which
+        // it makes anew (the asm): the 256 x 256 tiles hold no register for them.
+        const bool whole = k0 + BK <= k_end;
+        int ln = lane;
+        if (GATED && !whole) asm volatile("" : "+v"(ln));
+        auto in_k = [&](int j, int per) {
+            return whole || k0 + 16 * ((ln ^ (ln >> 3) ^ (wu * per + j)) & (CH - 1)) < k_end;
+        };
 #pragma unroll
         for (int j = 0; j < XI; ++j) {
             const int kk = k0 + xcol[j];
-            const void *src = (xrow[j] >= 0 && kk < k_end) ? (const void *)(g.xq + xrow[j] + kk)
-                                                             : (const void *)g_zero16;
+            const bool in = GATED ? in_k(j, XI) : kk < k_end;
+            const void *src = (xrow[j] >= 0 && in) ? (const void *)(g.xq + xrow[j] + kk) : (const void *)g_zero16;
             dma16(src, xs + (w * XI + j) * 64 * 16);
         }
 #pragma unroll
@@ -214,8 +223,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
             const int kk = k0 + wcol[j];
             // gated: an instruction's 64 / CH rows are one projection's (a scalar choice)
             const uint8_t *wq = !GATED ? g.wq : (gated_up((wu * WI + j) * (64 / CH)) ? g.sl[1].wq : g.sl[0].wq);
-            const void *src = (wrow[j] >= 0 && kk < k_end) ? (const void *)(wq + wrow[j] + kk)
-                                                             : (const void *)g_zero16;
+            const bool in = GATED ? in_k(j, WI) : kk < k_end;
+            const void *src = (wrow[j] >= 0 && in) ? (const void *)(wq + wrow[j] + kk) : (const void *)g_zero16;
             dma16(src, wsm + (w * WI + j) * 64 * 16);
         }
     };
@@ -264,25 +273,31 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
 
     // Per-row metadata: token row, usable adapter slot or -1, E8M0 code of
     // the row scale (1.0 for rows past T).
+    constexpr bool SLOTS = GATED && !SPLIT;
+    __shared__ row_slot s_slot[SLOTS ? BM : 1];
     __shared__ int32_t s_meta_t[BM], s_meta_id[BM], s_esx[BM];
     const int32_t n_fused = (LORA && g.n_fused) ? *g.n_fused : T;   // short-segment rows: separate expand
     for (int i = tid; i < BM; i += WV * 64) {
         const int p = m0 + i;
         const int32_t t = (p < T) ? perm_row(g.perm, p, T) : -1;
         int32_t id = -1;
-        if (LORA && t >= 0 && (!g.n_fused || p < n_fused)) {
+        if ((LORA || GATED) && t >= 0 && (!g.n_fused || p < n_fused)) {
             const int32_t raw = g.ids[t];
             if (raw >= 0 && raw < g.n_slots && (GATED || g.rank[raw] > 0)) id = raw;
         }
         s_meta_t[i] = t;
-        s_meta_id[i] = id;
+        if constexpr (SLOTS) set_row(g, id, !LORA, s_meta_id[i], s_slot[i]);
+        else s_meta_id[i] = id;
         s_esx[i] = t >= 0 ? e8m0_of(g.xs[t]) : 127;
     }
 
     const int nk = (k_end - k_begin + BK - 1) / BK;
     constexpr int PER = XI + WI;                          // DMA instructions per stage per wave
     auto wait_stage = [&](int ahead) {                    // later stages still in flight
-        if (ahead >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER) : "memory");
+        constexpr int V5 = 5 * PER > 63 ? 63 : 5 * PER, V4 = 4 * PER > 63 ? 63 : 4 * PER;
+        if (NS > 5 && ahead >= 5) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(V5) : "memory");
+        else if (NS > 4 && ahead >= 4) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(V4) : "memory");
+        else if (ahead >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER) : "memory");
         else if (ahead == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PER) : "memory");
         else if (ahead == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER) : "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -304,7 +319,10 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     // The low-rank term goes into the accumulators before the K loop, while
     // the first stages load (split-K tiles leave it to the reduction).
     if constexpr (GATED && LORA && !SPLIT)
-        gated_lora_pass<RB, CB, 1, 1, 0>(g, acc, s_meta_t, s_meta_id, wm * WM, gated_col(n0 + wn * WN), lane);
+    {
+        lora_pass_lean<RB, CB / 2, 2, 0>(g, g.sl[0], acc, s_meta_t, s_meta_id, wm * WM, gated_col(n0 + wn * WN), lane);
+        lora_pass_lean<RB, CB / 2, 2, 1>(g, g.sl[1], acc, s_meta_t, s_meta_id, wm * WM, gated_col(n0 + wn * WN), lane);
+    }
     else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 4 ? RB : 1), 1, 0>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN, lane);
     wait_stage(min(NS - 1, nk - 1));
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     __syncthreads();
 
     if constexpr (GATED && !SPLIT)
-        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane);
+        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_slot, n0, w, lane);
     else if constexpr (GATED)
         gated_store_partial<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), n0, w, lane, tidx, split);
     else
@@ -449,6 +467,21 @@ static void launch_gated_fp8_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s
     }
 }
 
+// Up to 32 rows, as the bf16 pair's.
+static void launch_gated_fp8_few(gemm_args g, const gemm_plan &pl, hipStream_t s) {
+    g.tile_base = 0;
+    g.n_tiles = pl.n_dp + pl.tail;
+    g.splits = pl.splits;
+    g.k_chunk = pl.k_chunk;
+    if (pl.splits == 1)
+        hipLaunchKernelGGL((k_gemm_fp8<false, 32, 128, 3, false, 4, 1, true>), dim3(g.n_tiles), dim3(256), 0, s, g);
+    else {
+        hipLaunchKernelGGL((k_gemm_fp8<false, 32, 128, 3, true, 4, 1, true>), dim3(g.n_tiles * pl.splits), dim3(256),
+                           0, s, g);
+        launch_gated_reduce<32, 128>(g, s);
+    }
+}
+
 lora_status_t launch_gemm_gated_fp8(gemm_args &g, size_t partial_bytes, hipStream_t s) {
     const gemm_plan pl = plan_gated(g.T, g.K, g.N, partial_bytes, 128);
     g.n_tiles_m = ceil_div(g.T, pl.bm);
@@ -456,7 +489,9 @@ lora_status_t launch_gemm_gated_fp8(gemm_args &g, size_t partial_bytes, hipStrea
     g.col_strips = col_strips_pay(g.T, 2 * g.N, g.n_tiles_n);
     if (pl.bm == 256 && pl.bn == 256) launch_gated_fp8_cfg<256, 256, 2, 4, 2, 2, 4, 2>(g, pl, s);
     else if (pl.bm == 256) launch_gated_fp8_cfg<256, 128, 2, 8, 4, 2, 8, 2>(g, pl, s);
-    else launch_gated_fp8_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
+    else if (pl.bm == 128) launch_gated_fp8_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
+    else if (pl.bm == 64) launch_gated_fp8_cfg<64, 128, 3, 4, 2, 3, 4, 2>(g, pl, s);
+    else launch_gated_fp8_few(g, pl, s);
     return hip_status(hipGetLastError());
 }
 

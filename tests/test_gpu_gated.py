@@ -226,3 +226,26 @@ def test_the_pair_is_what_the_projections_give():
         assert (d <= 2.0 ** -6 * (1 + y.double().abs())).all()
     ref = torch.nn.functional.silu(ys[0].double()) * ys[1].double()
     assert ((h[0].double() - ref).abs() <= 2.0 ** -5 * (1 + ref.abs())).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,f,order", [(20, 264, "random"), (90, 264, "random"), (300, 3400, "random"), (700, 1032, "sorted"),
+                                       (2100, 3400, "sorted")])
+def test_a_nan_adapter_stays_with_its_rows(T, f, order, what):
+    """A value that is not finite in one adapter's B (and its A): rows of other
+    adapters and of none get what they get beside a sound one."""
+    for fp8 in (False, True):
+        p = Pair(T, 256, f, [16, 16, 5, 9], 16, BF16, seed=13, order=order)
+        parts = fp8_parts(p)[0] if fp8 else None
+        modes = (L.LORA_MODE_BGMV, L.LORA_MODE_SGMV)
+        clean = [run_forward(p, "silu", mode, fp8=parts)[0] for mode in modes]
+        for m in range(2):
+            p.A[m][1, 7, 3] = what
+            p.B[m][1, 2, 100] = what
+            p.B[m][1, 15, 230] = -what
+            p.pools[m].upload(1, p.A[m][1], p.B[m][1], 16, p.alphas[1], lda=16, ldb=p.f)
+        others = torch.as_tensor(p.ids != 1, device="cuda")
+        for mode, ref in zip(modes, clean):
+            h = run_forward(p, "silu", mode, fp8=parts)[0]
+            assert torch.equal(h[others], ref[others])
+            assert not torch.isfinite(h[~others][:, [100, 230]].float()).any()

@@ -241,3 +241,25 @@ def test_a_block_forward_and_backward():
     dh = (0.01 * out.double() @ Wd.double().t()).to(BF16)      # of the loss 0.005 |out|^2
     got = run_backward(p, "silu", gate, up, dh)
     check(p, "silu", gate, up, dh, got, "block")
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_a_nan_adapter_stays_with_its_rows(what):
+    """Values that are not finite in one adapter's A and B: dx of other rows, and
+    other adapters' gradients, as if that adapter were sound."""
+    for T, order in ((40, "random"), (700, "sorted")):
+        for dtype in (BF16, F32):
+            p = Pair(T, 136, 264, [16, 16, 5, 9], 16, dtype, seed=13, order=order)
+            k = kept(p)
+            clean = run_backward(p, "silu", *k)
+            for m in range(2):
+                p.A[m][1, 7, 3] = what
+                p.B[m][1, 2, 100] = what
+                p.pools[m].upload(1, p.A[m][1], p.B[m][1], 16, p.alphas[1], lda=16, ldb=p.f)
+            got = run_backward(p, "silu", *k)
+            others = torch.as_tensor(p.ids != 1, device="cuda")
+            assert torch.equal(got[0][others], clean[0][others])
+            assert not torch.isfinite(got[0][~others].float()).all(1).any()
+            for m in range(2):
+                assert torch.equal(got[1][m][[0, 2, 3]], clean[1][m][[0, 2, 3]])
+                assert torch.equal(got[2][m][[0, 2, 3]], clean[2][m][[0, 2, 3]])
