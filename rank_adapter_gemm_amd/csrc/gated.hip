@@ -8,8 +8,11 @@ namespace lora {
 // ---------------------------------------------------------------------------
 // fp32: 64 rows x 64 columns of h per workgroup of 4 wavefronts (2 x 2), each
 // with 32 rows x 32 columns of both projections on v_mfma_f32_32x32x2_f32
-// (fp32 products and sums).  K in steps of 32, staged through LDS with the
-// next step's loads in registers under the current one's products.
+// (fp32 products and sums; the matrix cores' fp32 rate is twice the vector
+// units').  K in steps of 32, staged through LDS with the next step's loads in
+// registers under the current one's products.  Grids of few tiles split K;
+// the sums then go through LDS or the partial buffer to threads that own 4
+// columns of a row, which add the row's low-rank terms.
 // ---------------------------------------------------------------------------
 struct gated_f32_args {
     const float *x, *W[2], *b[2], *scale[2];
@@ -17,30 +20,75 @@ struct gated_f32_args {
     float *h, *keep[2];
     const int32_t *ids, *perm;
     const float *v;
-    int32_t T, K, N, n_slots, max_rank, act, n_tiles_n;
+    float *partial;                    // [tile][split][64][128]
+    int32_t T, K, N, n_slots, max_rank, act, n_tiles_n, splits, k_chunk;
 };
 
-__global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
+// 4 columns of one row from both projections' sums.
+__device__ __forceinline__ void gated_finish4(const gated_f32_args &g, int64_t t, int n, float (&o)[2][4]) {
+    const int32_t id = g.ids[t];
+    if (id >= 0 && id < g.n_slots) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int r = min(g.rank[m][id], g.max_rank);
+            if (r <= 0) continue;
+            const float *b = g.b[m] + (slot_row0(g.row0[m], id, g.max_rank) * g.N + (int64_t)n * 8);
+            const float *vt = g.v + t * 2 * g.max_rank + m * g.max_rank;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j0 = 0; j0 < r; j0 += 8, b += (int64_t)g.N * 8) {
+                float vv[8], bb[4][8];
+                *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(vt + j0);
+                *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(vt + j0 + 4);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    *reinterpret_cast<float4 *>(bb[q]) = *reinterpret_cast<const float4 *>(b + 8 * q);
+                    *reinterpret_cast<float4 *>(bb[q] + 4) = *reinterpret_cast<const float4 *>(b + 8 * q + 4);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[q] = fmaf(vv[e], bb[q][e], d[q]);
+            }
+            const float s = g.scale[m][id];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[m][q] = fmaf(s, d[q], o[m][q]);
+        }
+    }
+    const int64_t at = t * g.N + n;
+    float4 h;
+    h.x = act_value<true>(g.act, o[0][0]) * o[1][0];
+    h.y = act_value<true>(g.act, o[0][1]) * o[1][1];
+    h.z = act_value<true>(g.act, o[0][2]) * o[1][2];
+    h.w = act_value<true>(g.act, o[0][3]) * o[1][3];
+    *reinterpret_cast<float4 *>(g.h + at) = h;
+    if (g.keep[0]) {
+        *reinterpret_cast<float4 *>(g.keep[0] + at) = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+        *reinterpret_cast<float4 *>(g.keep[1] + at) = make_float4(o[1][0], o[1][1], o[1][2], o[1][3]);
+    }
+}
+
+template <bool SPLIT> __global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
     constexpr int BK = 32, XS = 64 + 4, WS = 128 + 4;
-    __shared__ __attribute__((aligned(16))) float s_x[BK][XS], s_w[BK][WS];   // s_w: 64 gate columns, 64 up columns
+    __shared__ __attribute__((aligned(16))) float smem[64 * WS];    // stages: x [BK][XS], W [BK][WS]; sums: [64][WS]
+    float *s_x = smem, *s_w = smem + BK * XS;
+    static_assert(BK * (XS + WS) <= 64 * WS, "a stage fits the sums' LDS");
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w >> 1, wn = w & 1;
-    const int m0 = blockIdx.x / g.n_tiles_n * 64, n0 = blockIdx.x % g.n_tiles_n * 64;
-    const int K = g.K, N = g.N, T = g.T;
+    const int tile = SPLIT ? blockIdx.x / g.splits : blockIdx.x, split = SPLIT ? blockIdx.x % g.splits : 0;
+    const int m0 = tile / g.n_tiles_n * 64, n0 = tile % g.n_tiles_n * 64;
+    const int N = g.N, T = g.T, k_begin = split * g.k_chunk, k_end = min(g.K, k_begin + g.k_chunk);
     // x: thread -> row tid / 4, 8 k from 8 (tid % 4); W: thread -> k tid / 8, 8 columns from 8 (tid % 8), both weights
     const int xr = tid >> 2, xk = (tid & 3) * 8, wk = tid >> 3, wc = (tid & 7) * 8;
     const int32_t t_x = m0 + xr < T ? perm_row(g.perm, m0 + xr, T) : -1;
-    const float *xp = g.x + (int64_t)(t_x < 0 ? 0 : t_x) * K;
-    float4 rx[2], rw[2][2];
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *xp = g.x + (int64_t)(t_x < 0 ? 0 : t_x) * g.K;
+    f32x4_t rx[2], rw[2][2];
     auto load = [&](int k0) {
-        const bool xok = t_x >= 0 && k0 + xk < K, wok = k0 + wk < K && n0 + wc < N;   // K, N multiples of 8
+        const bool xok = t_x >= 0 && k0 + xk < k_end, wok = k0 + wk < k_end && n0 + wc < N;   // K, N multiples of 8
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            rx[i] = xok ? *reinterpret_cast<const float4 *>(xp + k0 + xk + 4 * i) : zero;
+            rx[i] = load4(xok, xp + k0 + xk + 4 * i);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-                rw[m][i] = wok ? *reinterpret_cast<const float4 *>(g.W[m] + (int64_t)(k0 + wk) * N + n0 + wc + 4 * i)
-                               : zero;
+                rw[m][i] = load4(wok, g.W[m] + (int64_t)(k0 + wk) * N + n0 + wc + 4 * i);
         }
     };
     f32x16_t acc[2];
@@ -48,53 +96,69 @@ __global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
-    load(0);
-    for (int k0 = 0; k0 < K; k0 += BK) {
+    if (k_begin < k_end) load(k_begin);
+    for (int k0 = k_begin; k0 < k_end; k0 += BK) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            s_x[xk + 4 * i + 0][xr] = rx[i].x;
-            s_x[xk + 4 * i + 1][xr] = rx[i].y;
-            s_x[xk + 4 * i + 2][xr] = rx[i].z;
-            s_x[xk + 4 * i + 3][xr] = rx[i].w;
+            s_x[(xk + 4 * i + 0) * XS + xr] = rx[i].x;
+            s_x[(xk + 4 * i + 1) * XS + xr] = rx[i].y;
+            s_x[(xk + 4 * i + 2) * XS + xr] = rx[i].z;
+            s_x[(xk + 4 * i + 3) * XS + xr] = rx[i].w;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) *reinterpret_cast<float4 *>(&s_w[wk][64 * m + wc + 4 * i]) = rw[m][i];
+            for (int m = 0; m < 2; ++m) *reinterpret_cast<f32x4_t *>(s_w + wk * WS + 64 * m + wc + 4 * i) = rw[m][i];
         }
         __syncthreads();
-        if (k0 + BK < K) load(k0 + BK);
+        if (k0 + BK < k_end) load(k0 + BK);
 #pragma unroll
         for (int k = 0; k < BK; k += 2) {
-            const float a = s_x[k + (lane >> 5)][wm * 32 + (lane & 31)];
+            const int kk = k + (lane >> 5);
+            const float a = s_x[kk * XS + wm * 32 + (lane & 31)];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-                acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, s_w[k + (lane >> 5)][64 * m + wn * 32 + (lane & 31)],
-                                                              acc[m], 0, 0, 0);
+                acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, s_w[kk * WS + 64 * m + wn * 32 + (lane & 31)], acc[m],
+                                                              0, 0, 0);
         }
     }
-    const int n = n0 + wn * 32 + (lane & 31);
-    if (n >= N) return;
+    float *part = SPLIT ? g.partial + ((int64_t)tile * g.splits + split) * 64 * 128 : nullptr;
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const int p = m0 + wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        const int64_t t = p < T ? perm_row(g.perm, p, T) : -1;
-        if (t < 0) continue;
-        const int32_t id = g.ids[t];
-        float val[2];
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int r = wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), c = 64 * m + wn * 32 + (lane & 31);
+            if (SPLIT) part[r * 128 + c] = acc[m][e];
+            else smem[r * WS + c] = acc[m][e];
+        }
+    if (SPLIT) return;
+    __syncthreads();
+    for (int i = tid; i < 64 * 16; i += 256) {
+        const int r = i >> 4, c = (i & 15) * 4, n = n0 + c;
+        const int64_t t = m0 + r < T ? perm_row(g.perm, m0 + r, T) : -1;
+        if (t < 0 || n >= N) continue;
+        float o[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            *reinterpret_cast<float4 *>(o[m]) = *reinterpret_cast<const float4 *>(smem + r * WS + 64 * m + c);
+        gated_finish4(g, t, n, o);
+    }
+}
+
+// The pieces' sums, in split order: 16 rows of one tile per workgroup.
+__global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
+    const int tile = blockIdx.x >> 2, r = (blockIdx.x & 3) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    const int p = tile / g.n_tiles_n * 64 + r, n = tile % g.n_tiles_n * 64 + c;
+    const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
+    if (t < 0 || n >= g.N) return;
+    float o[2][4] = {};
+    const float *part = g.partial + (int64_t)tile * g.splits * 64 * 128 + r * 128 + c;
+    for (int s = 0; s < g.splits; ++s, part += 64 * 128)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            float d = 0.0f, sc = 0.0f;
-            if (id >= 0 && id < g.n_slots) {
-                const int r = min(g.rank[m][id], g.max_rank);
-                const float *b = g.b[m] + (slot_row0(g.row0[m], id, g.max_rank) * N + (int64_t)n * 8);
-                const float *vt = g.v + t * 2 * g.max_rank + m * g.max_rank;
-                for (int j = 0; j < r; ++j) d = fmaf(vt[j], b[(int64_t)(j >> 3) * N * 8 + (j & 7)], d);
-                if (r > 0) sc = g.scale[m][id];
-            }
-            val[m] = fmaf(sc, d, acc[m][e]);
-            if (g.keep[m]) g.keep[m][t * N + n] = val[m];
+            const float4 f = *reinterpret_cast<const float4 *>(part + 64 * m);
+            o[m][0] += f.x; o[m][1] += f.y; o[m][2] += f.z; o[m][3] += f.w;
         }
-        g.h[t * N + n] = act_value<true>(g.act, val[0]) * val[1];
-    }
+    gated_finish4(g, t, n, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -202,7 +266,15 @@ lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {
         g.max_rank = p[0].max_rank;
         g.act = c.act;
         g.n_tiles_n = ceil_div(g.N, 64);
-        hipLaunchKernelGGL(k_gated_f32, dim3(ceil_div(c.T, 64) * g.n_tiles_n), dim3(256), 0, s, g);
+        g.partial = c.partial;
+        const int tiles = ceil_div(c.T, 64) * g.n_tiles_n;
+        g.splits = f32_splits(tiles, g.K, 64 * 128, c.partial_bytes, g.k_chunk);
+        if (g.splits == 1) {
+            hipLaunchKernelGGL(k_gated_f32<false>, dim3(tiles), dim3(256), 0, s, g);
+        } else {
+            hipLaunchKernelGGL(k_gated_f32<true>, dim3(tiles * g.splits), dim3(256), 0, s, g);
+            hipLaunchKernelGGL(k_gated_reduce_f32, dim3(tiles * 4), dim3(256), 0, s, g);
+        }
         return hip_status(hipGetLastError());
     }
     gemm_args g{};

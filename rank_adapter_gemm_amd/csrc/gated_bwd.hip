@@ -237,8 +237,8 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
 // of 32 (its first work block), each value as two bf16 parts (hi = bf16(f),
 // lo = bf16(f - hi): together within 2^-17 of f, far below the rounding of
 // the bf16 gradients they add up to).  Places past a segment's rows are
-// filled with zeros.  A workgroup: 32 positions of one work block, or 32 rows
-// of the base block (grid.x from n_work on).
+// filled with zeros.  A workgroup: 32 positions of one work block and 8 ranks
+// (blockIdx.y), or 32 rows of the base block (grid.x from n_work on).
 struct rank_finish_args {
     const float *v, *part;
     int32_t n_split, T, R, n_slots, n_work, Tp;
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_po
     constexpr int BR = kShrinkRows;
     const int R2 = 2 * g.R;
     if ((int)blockIdx.x >= g.n_work) {
+        if (blockIdx.y) return;
         const int p0 = ((int)blockIdx.x - g.n_work) * BR, pend = min(min(g.offsets[1], p0 + BR), g.T);
         for (int e = threadIdx.x; e < BR * R2; e += 256) {
             const int p = p0 + e / R2;
@@ -270,8 +271,8 @@ __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_po
     const int i = threadIdx.x & 31, p = p0 + i;
     const int64_t t = p >= 0 && p < pend ? perm_row(g.perm, p, g.T) : -1;
     const int64_t at = (int64_t)blockIdx.x * BR + i;
-    for (int j = threadIdx.x >> 5; j < R2; j += 8) {
-        const int m = j >= g.R, jj = j - m * g.R;
+    {
+        const int j = blockIdx.y * 8 + (threadIdx.x >> 5), m = j >= g.R, jj = j - m * g.R;
         float f[2] = {0.0f, 0.0f};                        // s v, dv
         if (t >= 0 && jj < min(pp.rank[m][id], g.R)) {
             const float s = pp.scale[m][id];
@@ -307,15 +308,15 @@ __global__ void __launch_bounds__(256) k_a_octets(pair_pools pp, const int32_t *
     const int32_t id = seg_id[i];
     if (id < 0 || id >= n_slots) return;
     const int32_t r[2] = {min(pp.rank[0][id], R), min(pp.rank[1][id], R)};
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
         row0[id] = i * 2 * R;
         rank[id] = r[0] > 0 || r[1] > 0 ? 2 * R : 0;
         scale[id] = 1.0f;
     }
     const int k = blockIdx.y * 256 + threadIdx.x;
     if (k >= K) return;
-    for (int o = 0; o < 2 * R / 8; ++o) {
-        const int m = 8 * o >= R, j0 = 8 * o - m * R;
+    {
+        const int o = blockIdx.z, m = 8 * o >= R, j0 = 8 * o - m * R;
         const uint16_t *a = (const uint16_t *)pp.a[m] + (slot_row0(pp.row0[m], id, R) + j0) * K + k;
         uint32_t e[8];
 #pragma unroll
@@ -334,7 +335,17 @@ __global__ void __launch_bounds__(256) k_a_octets(pair_pools pp, const int32_t *
 struct nt_args {
     const uint16_t *a[2], *w[2];       // [T][F], [N][F]
     int32_t F, Fp;                     // F rounded up to whole K steps
+    const int32_t *n_seg;
 };
+
+// Where a product split over K gets its low-rank term: on the matrix cores by
+// the first piece of each tile where the adapters have 64 rows or more on
+// average, else row by row in the reduction.  (2048 rows of 4 adapters, 8B
+// sizes: pieces and reduction 475 us against 511 row by row; 777 rows of 24
+// adapters of up to 40 ranks, 1048 x 2744: 80 against 62.)
+__device__ __forceinline__ bool term_in_reduction(const gemm_args &g, const nt_args &nt) {
+    return (int64_t)*nt.n_seg * 64 > g.T;
+}
 
 template <int BM, int BN, int NS, bool SPLIT, int WV, int WR>
 __global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
@@ -417,11 +428,10 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
     };
     constexpr int NREAD = RB + CB, PER = XI + WI;
 
-    int32_t *s_meta_t = nullptr, *s_meta_id = nullptr;
-    if constexpr (!SPLIT) {
-        __shared__ int32_t s_t[BM], s_id[BM];
-        s_meta_t = s_t;
-        s_meta_id = s_id;
+    __shared__ int32_t s_t[BM], s_id[BM];
+    int32_t *s_meta_t = SPLIT ? nullptr : s_t;            // a piece stores every row of its partial tile
+    const bool low_rank = !SPLIT || (split == 0 && !term_in_reduction(g, nt));
+    if (low_rank) {
         for (int i = tid; i < BM; i += WV * 64) {
             const int p = m0 + i;
             const int32_t t = p < T ? perm_row(g.perm, p, T) : -1;
@@ -448,8 +458,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if constexpr (!SPLIT)
-        lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1), 1, 0, true>(g, acc, s_meta_t, s_meta_id, n0, wm * WM,
+    if (low_rank)
+        lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1), 1, 0, true>(g, acc, s_t, s_id, n0, wm * WM,
                                                                       n0 + wn * WN, lane);
     wait_stage(min(NS - 1, nk - 1));
     __builtin_amdgcn_s_barrier();
@@ -487,6 +497,49 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
                                                   tidx, split);
 }
 
+// The pieces' sums in split order; a thread owns 8 columns of one row.
+template <int BM, int BN> __global__ void __launch_bounds__(256) k_nt_reduce(gemm_args g, nt_args nt) {
+    constexpr int CPR = BN / 8, RW = 256 / CPR, CHUNKS = BM / RW;
+    const int per = gridDim.x / kXcds, rem = gridDim.x % kXcds, xcd = blockIdx.x % kXcds;
+    const int item = xcd * per + min(xcd, rem) + blockIdx.x / kXcds;   // whole tiles per XCD, as k_splitk_reduce
+    const int tidx = item / CHUNKS, chunk = item % CHUNKS;
+    int tm, tn;
+    grouped_tile(g.tile_base + tidx, g.n_tiles_m, g.n_tiles_n, g.col_strips, tm, tn);
+    const int r = chunk * RW + threadIdx.x / CPR, c = (threadIdx.x % CPR) * 8;
+    const int p = tm * BM + r, n = tn * BN + c;
+    const int64_t t = p < g.T && n < g.N ? perm_row(g.perm, p, g.T) : -1;
+    if (t < 0) return;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const float *src = g.partial + ((int64_t)tidx * g.splits * BM + r) * BN + c;
+    for (int s = 0; s < g.splits; ++s, src += BM * BN) {
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+        o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+        o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+    }
+    const int32_t id = g.ids[t];
+    if (term_in_reduction(g, nt) && id >= 0 && id < g.n_slots) {
+        const int32_t rk = g.rank[id];
+        const float *vrow = g.v + t * g.v_stride;
+        const uint16_t *b = g.b + (int64_t)g.row0[id] * g.N + (int64_t)n * 8;
+        for (int j = 0; j < rk; j += 8, b += (int64_t)g.N * 8) {
+            float vv[8];
+            *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(vrow + j);
+            *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(vrow + j + 4);
+            uint4 bq[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) bq[q] = ldg16(b + q * 8);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float bf[8];
+                vec16<LORA_BF16>::widen(bq[q], bf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[q] = fmaf(vv[e], bf[e], o[q]);
+            }
+        }
+    }
+    stg16(g.y + t * g.N + n, vec16<LORA_BF16>::narrow(o));
+}
+
 template <int BM, int BN, int NS, int WV, int WR, int NST, int WVT>
 static void launch_nt_cfg(gemm_args g, const nt_args &nt, const gemm_plan &pl, hipStream_t s) {
     if (pl.n_dp > 0) {
@@ -503,8 +556,7 @@ static void launch_nt_cfg(gemm_args g, const nt_args &nt, const gemm_plan &pl, h
         g.k_chunk = pl.k_chunk;
         hipLaunchKernelGGL((k_gemm_nt<BM, BN, NST, true, WVT, WR>), dim3(pl.tail * pl.splits), dim3(WVT * 64), 0, s,
                            g, nt);
-        hipLaunchKernelGGL((k_splitk_reduce<true, false, BM, BN>), dim3(pl.tail * (BM / (2048 / BN))), dim3(256), 0,
-                           s, g);
+        hipLaunchKernelGGL((k_nt_reduce<BM, BN>), dim3(pl.tail * (BM / (2048 / BN))), dim3(256), 0, s, g, nt);
     }
 }
 
@@ -527,120 +579,196 @@ static gemm_plan plan_dx(int T, int K, int N, size_t partial_bytes) {
 }
 
 // ---------------------------------------------------------------------------
-// dx, fp32: 64 x 64 tiles on v_mfma_f32_32x32x2_f32, the sum over F of dg then
-// of du; the low-rank term from A's rows in the store.
+// dx, fp32: 64 x 64 tiles on v_mfma_f32_32x32x2_f32, the sum over dg's columns
+// then du's (each in whole steps of 32); grids of few tiles split the steps.
+// Threads that own 4 columns of a row then add the low-rank terms from A's rows.
 // ---------------------------------------------------------------------------
 struct dx_f32_args {
-    const float *a[2], *w[2];
+    const float *a0, *a1, *w0, *w1;
     float *dx;
     const float *dv;
     const int32_t *ids, *perm;
-    int32_t T, F, N, n_slots, R, n_tiles_n;
+    float *partial;                    // [tile][split][64][64]
+    int32_t T, F, N, n_slots, R, n_tiles_n, splits, k_chunk;
 };
 
-__global__ void __launch_bounds__(256) k_dx_f32(dx_f32_args g, pair_pools pp) {
+__device__ __forceinline__ void dx_finish4(const dx_f32_args &g, const pair_pools &pp, int64_t t, int n,
+                                           float (&o)[4]) {
+    const int32_t id = g.ids[t];
+    if (id >= 0 && id < g.n_slots) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int32_t rk = min(pp.rank[m][id], g.R);
+            const float *a = (const float *)pp.a[m] + slot_row0(pp.row0[m], id, g.R) * g.N + n;
+            const float *dv = g.dv + t * 2 * g.R + m * g.R;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+            for (int j = 0; j < rk; ++j) {
+                const float4 f = *reinterpret_cast<const float4 *>(a + (int64_t)j * g.N);
+                const float s = dv[j];
+                d[0] = fmaf(s, f.x, d[0]);
+                d[1] = fmaf(s, f.y, d[1]);
+                d[2] = fmaf(s, f.z, d[2]);
+                d[3] = fmaf(s, f.w, d[3]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] += d[q];
+        }
+    }
+    *reinterpret_cast<float4 *>(g.dx + t * g.N + n) = make_float4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool SPLIT> __global__ void __launch_bounds__(256) k_dx_f32(dx_f32_args g, pair_pools pp) {
     constexpr int BK = 32, LD = 64 + 4;
-    __shared__ __attribute__((aligned(16))) float s_a[BK][LD], s_w[BK][LD];
+    __shared__ __attribute__((aligned(16))) float smem[2 * BK * LD];
+    float *s_a = smem, *s_w = smem + BK * LD;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w >> 1, wn = w & 1;
-    const int m0 = blockIdx.x / g.n_tiles_n * 64, n0 = blockIdx.x % g.n_tiles_n * 64;
+    const int tile = SPLIT ? blockIdx.x / g.splits : blockIdx.x, split = SPLIT ? blockIdx.x % g.splits : 0;
+    const int m0 = tile / g.n_tiles_n * 64, n0 = tile % g.n_tiles_n * 64;
     const int r = tid >> 2, kk = (tid & 3) * 8;
     const int32_t t_a = m0 + r < g.T ? perm_row(g.perm, m0 + r, g.T) : -1;
     const int64_t arow = (int64_t)(t_a < 0 ? 0 : t_a) * g.F;
     const bool wok = n0 + r < g.N;
     const int64_t wrow = (int64_t)(wok ? n0 + r : 0) * g.F;
+    const int Fp = (g.F + BK - 1) / BK * BK;
+    const int k_begin = split * g.k_chunk, k_end = min(2 * Fp, k_begin + g.k_chunk);
+    f32x4_t ra[2], rw[2];
+    auto load = [&](int k0) {
+        const bool second = k0 >= Fp;
+        const float *a = (second ? g.a1 : g.a0) + arow, *wt = (second ? g.w1 : g.w0) + wrow;
+        const int f = k0 - (second ? Fp : 0) + kk;
+        const bool in = f < g.F;                           // F is a multiple of 8
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            ra[i] = load4(in && t_a >= 0, a + f + 4 * i);
+            rw[i] = load4(in && wok, wt + f + 4 * i);
+        }
+    };
     f32x16_t acc;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-    for (int m = 0; m < 2; ++m)
-        for (int f0 = 0; f0 < g.F; f0 += BK) {
-            float4 ra[2], rw[2];
-            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-            const bool in = f0 + kk < g.F;                 // F is a multiple of 8
+    if (k_begin < k_end) load(k_begin);
+    for (int k0 = k_begin; k0 < k_end; k0 += BK) {
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ra[i] = in && t_a >= 0 ? *reinterpret_cast<const float4 *>(g.a[m] + arow + f0 + kk + 4 * i) : zero;
-                rw[i] = in && wok ? *reinterpret_cast<const float4 *>(g.w[m] + wrow + f0 + kk + 4 * i) : zero;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                s_a[kk + 4 * i + 0][r] = ra[i].x;
-                s_a[kk + 4 * i + 1][r] = ra[i].y;
-                s_a[kk + 4 * i + 2][r] = ra[i].z;
-                s_a[kk + 4 * i + 3][r] = ra[i].w;
-                s_w[kk + 4 * i + 0][r] = rw[i].x;
-                s_w[kk + 4 * i + 1][r] = rw[i].y;
-                s_w[kk + 4 * i + 2][r] = rw[i].z;
-                s_w[kk + 4 * i + 3][r] = rw[i].w;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < BK; k += 2)
-                acc = __builtin_amdgcn_mfma_f32_32x32x2f32(s_a[k + (lane >> 5)][wm * 32 + (lane & 31)],
-                                                           s_w[k + (lane >> 5)][wn * 32 + (lane & 31)], acc, 0, 0, 0);
+        for (int i = 0; i < 2; ++i) {
+            s_a[(kk + 4 * i + 0) * LD + r] = ra[i].x;
+            s_a[(kk + 4 * i + 1) * LD + r] = ra[i].y;
+            s_a[(kk + 4 * i + 2) * LD + r] = ra[i].z;
+            s_a[(kk + 4 * i + 3) * LD + r] = ra[i].w;
+            s_w[(kk + 4 * i + 0) * LD + r] = rw[i].x;
+            s_w[(kk + 4 * i + 1) * LD + r] = rw[i].y;
+            s_w[(kk + 4 * i + 2) * LD + r] = rw[i].z;
+            s_w[(kk + 4 * i + 3) * LD + r] = rw[i].w;
         }
-    const int n = n0 + wn * 32 + (lane & 31);
-    if (n >= g.N) return;
+        __syncthreads();
+        if (k0 + BK < k_end) load(k0 + BK);
+#pragma unroll
+        for (int k = 0; k < BK; k += 2)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(s_a[(k + (lane >> 5)) * LD + wm * 32 + (lane & 31)],
+                                                       s_w[(k + (lane >> 5)) * LD + wn * 32 + (lane & 31)], acc, 0, 0,
+                                                       0);
+    }
+    float *part = SPLIT ? g.partial + ((int64_t)tile * g.splits + split) * 64 * 64 : nullptr;
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        const int p = m0 + wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        const int i = wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), c = wn * 32 + (lane & 31);
+        if (SPLIT) part[i * 64 + c] = acc[e];
+        else smem[i * LD + c] = acc[e];
+    }
+    if (SPLIT) return;
+    __syncthreads();
+    for (int i = tid; i < 64 * 16; i += 256) {
+        const int c = (i & 15) * 4, p = m0 + (i >> 4), n = n0 + c;
         const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
-        if (t < 0) continue;
-        float val = acc[e];
-        const int32_t id = g.ids[t];
-        if (id >= 0 && id < g.n_slots)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int32_t rk = min(pp.rank[m][id], g.R);
-                const float *a = (const float *)pp.a[m] + slot_row0(pp.row0[m], id, g.R) * g.N + n;
-                const float *dv = g.dv + t * 2 * g.R + m * g.R;
-                float d = 0.0f;
-                for (int j = 0; j < rk; ++j) d = fmaf(dv[j], a[(int64_t)j * g.N], d);
-                val += d;
-            }
-        g.dx[t * g.N + n] = val;
+        if (t < 0 || n >= g.N) continue;
+        float o[4];
+        *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(smem + (i >> 4) * LD + c);
+        dx_finish4(g, pp, t, n, o);
     }
 }
 
+__global__ void __launch_bounds__(256) k_dx_reduce_f32(dx_f32_args g, pair_pools pp) {
+    const int tile = blockIdx.x >> 2, r = (blockIdx.x & 3) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    const int p = tile / g.n_tiles_n * 64 + r, n = tile % g.n_tiles_n * 64 + c;
+    const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
+    if (t < 0 || n >= g.N) return;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    const float *part = g.partial + (int64_t)tile * g.splits * 64 * 64 + r * 64 + c;
+    for (int s = 0; s < g.splits; ++s, part += 64 * 64) {
+        const float4 f = *reinterpret_cast<const float4 *>(part);
+        o[0] += f.x; o[1] += f.y; o[2] += f.z; o[3] += f.w;
+    }
+    dx_finish4(g, pp, t, n, o);
+}
+
 // ---------------------------------------------------------------------------
-// dA and dB: out[slot][j][n] = s sum over the slot's rows t of p[t][j] q[t][n].
-// A workgroup takes 256 columns n of one slot, 8 ranks j at a time; slots
-// without rows, and ranks past the slot's, get zeros.
+// dA and dB, fp32: out[slot][j][n] = s sum over the slot's rows t of p[t][j]
+// q[t][n].  A workgroup takes 256 columns n of one slot and projection, 16
+// ranks j at a time; 64 rows' indices and rank values at a time lie in LDS,
+// so that the loads of q do not wait for them.  dA's workgroups and dB's are
+// one launch.  Slots without rows, and ranks past the slot's, get zeros.
 // ---------------------------------------------------------------------------
-struct outer_args {
-    const void *q[2];                  // per projection: the rows' wide side
-    const float *p;                    // [T][2R]
-    const float *scale[2];             // null: p holds the scale
-    const int32_t *rank[2];
-    void *out[2];
-    int64_t slot_stride, j_stride, n_stride;    // of out, in elements
+struct outer_f32_args {
+    const float *x, *dg, *du, *v, *dv;  // [T][K], [T][F], [T][F], [T][2R] (times the scale: dv), [T][2R]
+    float *dA0, *dA1, *dB0, *dB1;
     const int32_t *offsets, *perm;
-    int32_t T, N, R, n_slots;
+    int32_t T, K, F, R, n_slots, tiles_k, tiles_f;
 };
 
-template <int DT> __global__ void __launch_bounds__(256) k_seg_outer(outer_args g) {
-    typedef typename elem<DT>::T E;
-    const int slot = blockIdx.x, m = blockIdx.z, n = blockIdx.y * 256 + threadIdx.x;
-    if (n >= g.N) return;
+__global__ void __launch_bounds__(256) k_seg_outer_f32(outer_f32_args g, pair_pools pp) {
+    constexpr int J = 16, U = 8, CH = 64;
+    __shared__ __attribute__((aligned(16))) float s_p[CH][J];
+    __shared__ int32_t s_row[CH];
+    const int n_a = 2 * g.n_slots * g.tiles_k;
+    const bool is_a = (int)blockIdx.x < n_a;
+    const int tiles = is_a ? g.tiles_k : g.tiles_f;
+    int item = is_a ? blockIdx.x : blockIdx.x - n_a;
+    const int tile = item % tiles;
+    item /= tiles;
+    const int m = item & 1, slot = item >> 1;
+    const int N = is_a ? g.K : g.F, R = g.R, n = tile * 256 + threadIdx.x;
     const int p0 = max(g.offsets[slot + 1], 0), p1 = min(g.offsets[slot + 2], g.T);
-    const int32_t r = min(g.rank[m][slot], g.R);
-    const E *q = (const E *)g.q[m];
-    E *out = (E *)g.out[m] + slot * g.slot_stride + n * g.n_stride;
-    const float sc = g.scale[m] ? g.scale[m][slot] : 1.0f;
-    for (int j0 = 0; j0 < g.R; j0 += 8) {
-        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int32_t r = min(m ? pp.rank[1][slot] : pp.rank[0][slot], R);
+    const float *q = (is_a ? g.x : (m ? g.du : g.dg)) + (n < N ? n : 0);
+    const float *pv = (is_a ? g.dv : g.v) + m * R;
+    float *out = is_a ? (m ? g.dA1 : g.dA0) + ((int64_t)slot * N + n) * R : (m ? g.dB1 : g.dB0) + (int64_t)slot * R * N + n;
+    const int64_t j_stride = is_a ? 1 : N;
+    const float sc = is_a ? 1.0f : (m ? pp.scale[1][slot] : pp.scale[0][slot]);
+    for (int j0 = 0; j0 < R; j0 += J) {
+        float acc[J] = {};
         if (j0 < r)
-            for (int p = p0; p < p1; ++p) {
-                const int64_t t = perm_row(g.perm, p, g.T);
-                if (t < 0) continue;
-                const float f = elem<DT>::load(q, t * g.N + n);
-                const float *pv = g.p + t * 2 * g.R + m * g.R + j0;
+            for (int p = p0; p < p1; p += CH) {
+                const int rows = min(CH, p1 - p);
+                __syncthreads();
+                if ((int)threadIdx.x < CH)
+                    s_row[threadIdx.x] = (int)threadIdx.x < rows ? perm_row(g.perm, p + threadIdx.x, g.T) : -1;
+                {
+                    const int i = threadIdx.x >> 2, j = (threadIdx.x & 3) * 4;
+                    const int32_t t = i < rows ? perm_row(g.perm, p + i, g.T) : -1;
+                    *reinterpret_cast<f32x4_t *>(&s_p[i][j]) = load4(t >= 0 && j0 + j < R, pv + (int64_t)t * 2 * R + j0 + j);
+                }
+                __syncthreads();
+                for (int u0 = 0; u0 < rows; u0 += U) {
+                    float f[U];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(pv[e], f, acc[e]);
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t t = s_row[u0 + u];
+                        f[u] = q[t < 0 ? 0 : t * N];
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (s_row[u0 + u] < 0) continue;  // (uniform) no row: whatever was read is not used
+#pragma unroll
+                        for (int e = 0; e < J; ++e) acc[e] = fmaf(s_p[u0 + u][e], f[u], acc[e]);
+                    }
+                }
             }
+        if (n < N)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            elem<DT>::store(out, (j0 + e) * g.j_stride, j0 + e < r ? sc * acc[e] : 0.0f);
+            for (int e = 0; e < J; ++e)
+                if (j0 + e < R) out[(j0 + e) * j_stride] = j0 + e < r ? sc * acc[e] : 0.0f;
     }
 }
 
@@ -834,14 +962,9 @@ bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t R, int32_t d_in, 
     B.scale = o;   o = align256(o + 4 * (size_t)n_slots);
     B.partial = o;
     const size_t tp = (t + 255) / 256 * 256, np = ((size_t)d_in + 255) / 256 * 256;
-    const size_t need = dtype == LORA_BF16 && T > 0 ? 4 * (size_t)kMaxGemmSplit * tp * np : 0;
+    const size_t need = T > 0 ? 4 * (size_t)kMaxGemmSplit * tp * np : 0;
     B.total = align256(o + (need < kGemmPartialCap ? need : kGemmPartialCap));
     return B;
-}
-
-template <int DT>
-static void launch_outer(outer_args g, hipStream_t s) {
-    hipLaunchKernelGGL(k_seg_outer<DT>, dim3(g.n_slots, ceil_div(g.N, 256), 2), dim3(256), 0, s, g);
 }
 
 lora_status_t launch_zero(void *p, size_t bytes, hipStream_t s) {
@@ -868,7 +991,8 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     hipLaunchKernelGGL(k_gated_dact<DT>, dim3((uint32_t)(n_vec < (1 << 24) ? (n_vec + 255) / 256 : 1 << 16)),
                        dim3(256), 0, s, (const E *)c.gate, (const E *)c.up, (const E *)c.dh, dg, du, n_vec, c.act);
     // v = x A (also records the bad ids); dv
-    st = launch_shrink(c.x, T, p, 2, c.ids, true, v, L, ws, s);
+    st = DT == LORA_F32 ? launch_shrink_pair(c.x, T, p, c.ids, v, ws_ptr<int32_t>(ws, L.header), s)
+                        : launch_shrink(c.x, T, p, 2, c.ids, true, v, L, ws, s);
     if (st != LORA_OK) return st;
     const int32_t row_blocks = ceil_div(T, kShrinkRows), n_work = row_blocks + (S < T ? S : T), Tp = n_work * 32;
     uint16_t *vt = ws_ptr<uint16_t>(ws, B.vt);
@@ -896,21 +1020,28 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         }
         rank_finish_args f{v, part, split, T, R, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
                            g.blk_start, g.blk_seg, dv, vt};
-        hipLaunchKernelGGL(k_rank_finish, dim3(n_work + row_blocks), dim3(256), 0, s, f, pp);
+        hipLaunchKernelGGL(k_rank_finish, dim3(n_work + row_blocks, 2 * R / 8), dim3(256), 0, s, f, pp);
     }
     if (c.dx && DT == LORA_F32) {
-        dx_f32_args g{{(const float *)dg, (const float *)du}, {(const float *)c.W[0], (const float *)c.W[1]},
-                      (float *)c.dx, dv, c.ids, perm, T, F, K, S, R, ceil_div(K, 64)};
-        hipLaunchKernelGGL(k_dx_f32, dim3(ceil_div(T, 64) * g.n_tiles_n), dim3(256), 0, s, g, pp);
+        dx_f32_args g{(const float *)dg, (const float *)du, (const float *)c.W[0], (const float *)c.W[1],
+                      (float *)c.dx, dv, c.ids, perm, ws_ptr<float>(ws, B.partial), T, F, K, S, R, ceil_div(K, 64), 1, 0};
+        const int tiles = ceil_div(T, 64) * g.n_tiles_n;
+        g.splits = f32_splits(tiles, 2 * ceil_div(F, 32) * 32, 64 * 64, c.ws_bytes - B.partial, g.k_chunk);
+        if (g.splits == 1) {
+            hipLaunchKernelGGL(k_dx_f32<false>, dim3(tiles), dim3(256), 0, s, g, pp);
+        } else {
+            hipLaunchKernelGGL(k_dx_f32<true>, dim3(tiles * g.splits), dim3(256), 0, s, g, pp);
+            hipLaunchKernelGGL(k_dx_reduce_f32, dim3(tiles * 4), dim3(256), 0, s, g, pp);
+        }
     } else if (c.dx) {
         uint16_t *oct = ws_ptr<uint16_t>(ws, B.oct);
         int32_t *row0 = ws_ptr<int32_t>(ws, B.row0), *rank = ws_ptr<int32_t>(ws, B.rank);
         float *scale = ws_ptr<float>(ws, B.scale);
-        hipLaunchKernelGGL(k_a_octets, dim3(S < T ? S : T, ceil_div(K, 256)), dim3(256), 0, s, pp,
+        hipLaunchKernelGGL(k_a_octets, dim3(S < T ? S : T, ceil_div(K, 256), 2 * R / 8), dim3(256), 0, s, pp,
                            ws_ptr<int32_t>(ws, L.seg_id), ws_ptr<int32_t>(ws, L.n_seg), S, K, R, oct, row0, rank,
                            scale);
         nt_args nt{{(const uint16_t *)dg, (const uint16_t *)du}, {(const uint16_t *)c.W[0], (const uint16_t *)c.W[1]},
-                   F, ceil_div(F, 64) * 64};
+                   F, ceil_div(F, 64) * 64, ws_ptr<int32_t>(ws, L.n_seg)};
         gemm_args g{};
         g.y = (uint16_t *)c.dx;
         g.T = T;
@@ -950,35 +1081,10 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
             default: hipLaunchKernelGGL((k_seg_outer_mfma<4, 2>), grid, dim3(256), 0, s, g); break;
         }
     } else if (c.dA[0]) {
-        outer_args g{};
-        g.offsets = offsets;
-        g.perm = perm;
-        g.T = T;
-        g.R = R;
-        g.n_slots = S;
-        g.rank[0] = p[0].rank;
-        g.rank[1] = p[1].rank;
-        g.slot_stride = (int64_t)R * K;
-        g.j_stride = 1;
-        g.n_stride = R;
-        g.q[0] = g.q[1] = c.x;
-        g.p = dv;
-        g.N = K;
-        g.out[0] = c.dA[0];
-        g.out[1] = c.dA[1];
-        launch_outer<DT>(g, s);
-        g.slot_stride = (int64_t)R * F;
-        g.j_stride = F;
-        g.n_stride = 1;
-        g.q[0] = dg;
-        g.q[1] = du;
-        g.p = v;
-        g.scale[0] = p[0].scale;
-        g.scale[1] = p[1].scale;
-        g.N = F;
-        g.out[0] = c.dB[0];
-        g.out[1] = c.dB[1];
-        launch_outer<DT>(g, s);
+        const outer_f32_args g{(const float *)c.x, (const float *)dg, (const float *)du, v, dv,
+                               (float *)c.dA[0], (float *)c.dA[1], (float *)c.dB[0], (float *)c.dB[1],
+                               offsets, perm, T, K, F, R, S, ceil_div(K, 256), ceil_div(F, 256)};
+        hipLaunchKernelGGL(k_seg_outer_f32, dim3((uint32_t)(2 * S) * (g.tiles_k + g.tiles_f)), dim3(256), 0, s, g, pp);
     }
     return hip_status(hipGetLastError());
 }

@@ -284,6 +284,32 @@ template <int BM, int BN> static void launch_gated_reduce(const gemm_args &g, hi
     hipLaunchKernelGGL((k_gated_reduce<BM, BN>), dim3(g.n_tiles * (BM / RW)), dim3(256), 0, s, g);
 }
 
+// 4 fp32 values, zeros where not ok.  (A branch, not a choice between two
+// values in memory, which would put the zeros and the result there.)
+__device__ __forceinline__ f32x4_t load4(bool ok, const float *p) {
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (ok) v = *reinterpret_cast<const f32x4_t *>(p);
+    return v;
+}
+
+// K ranges per tile of the fp32 kernels (tiles of `area` sums): the count with
+// the least rounds of 256 workgroups, each 1 / count of a tile long, with a
+// fiftieth of a tile for each range's partial sums; ranges of at least 128
+// terms.  (258 tiles alone take two rounds: 95 us; F32_NOTE.)
+inline int f32_splits(int tiles, int K, int area, size_t partial_bytes, int &k_chunk) {
+    int best = 1, best_cost = 1 << 30;
+    for (int s = 1; s <= kMaxGemmSplit && s * 128 <= (K > 128 ? K : 128); ++s) {
+        if (s > 1 && (size_t)s * tiles * area * 4 > partial_bytes) break;
+        const int cost = 1000 * ceil_div((int64_t)tiles * s, 256) / s + (s > 1 ? 20 * s : 0);
+        if (cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    k_chunk = ceil_div(ceil_div(K, best), 32) * 32;
+    return ceil_div(K, k_chunk);
+}
+
 // Implemented beside their base GEMMs; g holds everything but the tile plan.
 lora_status_t launch_gemm_gated(gemm_args &g, size_t partial_bytes, hipStream_t s);
 lora_status_t launch_gemm_gated_fp8(gemm_args &g, size_t partial_bytes, hipStream_t s);

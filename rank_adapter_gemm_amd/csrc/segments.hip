@@ -20,8 +20,10 @@
 //      with that key; offsets[], the GEMM order's key bases (long segments
 //      first, short ones last), then the compaction of non-empty keys >= 1
 //   3. per tile, each row's rank among the earlier rows of its tile with the
-//      same key (stable: the tile's (key, row) pairs sorted in LDS),
-//      perm[base + rank] = t, and its place in the GEMM order.
+//      same key (stable), perm[base + rank] = t, and its place in the GEMM
+//      order.
+// A batch of one tile takes one launch of one workgroup (k_seg_one; 190 rows
+// of 6 slots: SEG_NOTE).
 #include "common.hpp"
 
 namespace lora {
@@ -165,42 +167,33 @@ __device__ void gemm_order(const int32_t *s_off, int32_t nb, int32_t T, int32_t 
     }
 }
 
-// The (key, row) pairs of one tile of kSegTile rows (rows t0 ...), sorted
-// ascending in LDS by a bitonic network; rows are distinct, so the order is
-// total and rows of one key stay in row order (stable).  Returns thread i's
-// sorted key (INT32_MAX for padding past T) and row, and the key's first
-// sorted position, so i - first is the row's rank among the tile's rows of
-// its key.  Every thread of the block (kSegTile of them) calls it.
-__device__ void sort_tile(const int32_t *__restrict__ ids, int32_t T, int32_t n_slots, int32_t t0,
-                          int32_t *s_key, int32_t *s_row, int32_t &key, int32_t &row, int32_t &first) {
-    const int i = threadIdx.x;
-    const int32_t t = t0 + i;
-    s_key[i] = (t < T) ? row_key(ids[t], n_slots) : INT32_MAX;         // padding sorts last
-    s_row[i] = t;
+// Each row's rank among the earlier rows of its tile with the same key
+// (stable), one row a thread of a workgroup of kSegTile: every wavefront finds
+// its lanes of equal keys, then the wavefronts take their turn at the running
+// counts in LDS.  count[nb]: zeroed here; holds the tile's histogram
+// afterwards.  key < 0: no row.  Every thread of the block calls it.
+__device__ __forceinline__ int32_t tile_rank(int32_t key, int32_t nb, int32_t *count) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int32_t k = threadIdx.x; k < nb; k += blockDim.x) count[k] = 0;
+    uint64_t same = 0, pend = __ballot(key >= 0);
+    while (pend) {                                        // wave-uniform: one distinct key a round
+        const int32_t k = __shfl(key, __ffsll((long long)pend) - 1, 64);
+        const uint64_t m = __ballot(key == k);
+        if (key == k) same = m;
+        pend &= ~m;
+    }
+    const uint64_t below = same & ((1ull << lane) - 1);
+    int32_t rank = __popcll(below);
+    const bool first = same && below == 0;
     __syncthreads();
-    for (int k = 2; k <= kSegTile; k <<= 1) {
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            const int p = i ^ j;
-            if (p > i) {
-                const int32_t ka = s_key[i], kb = s_key[p], ra = s_row[i], rb = s_row[p];
-                const bool a_gt_b = ka > kb || (ka == kb && ra > rb);
-                if (a_gt_b == ((i & k) == 0)) {                      // ascending where bit k of i is clear
-                    s_key[i] = kb; s_key[p] = ka;
-                    s_row[i] = rb; s_row[p] = ra;
-                }
-            }
-            __syncthreads();
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+        if (w == wave && same) {
+            rank += count[key];                           // read by all lanes before the first adds
+            if (first) count[key] += __popcll(same);
         }
+        __syncthreads();
     }
-    key = s_key[i];
-    row = s_row[i];
-    int lo = 0, hi = i;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_key[mid] < key) lo = mid + 1;
-        else hi = mid;
-    }
-    first = lo;
+    return rank;
 }
 
 constexpr int kScanItems = 4;
@@ -258,13 +251,50 @@ __global__ void __launch_bounds__(1024) k_seg_scatter(const int32_t *__restrict_
                                                       const int32_t *__restrict__ offsets,
                                                       const int32_t *__restrict__ gbase,
                                                       int32_t *__restrict__ gperm) {
-    __shared__ int32_t s_key[kSegTile], s_row[kSegTile];
-    int32_t key, row, first;
-    sort_tile(ids, T, n_slots, blockIdx.x * kSegTile, s_key, s_row, key, row, first);
-    if (key == INT32_MAX) return;
-    const int32_t pos = tile_hist[(size_t)key * n_tiles + blockIdx.x] + ((int)threadIdx.x - first);
-    perm[pos] = row;
-    gperm[gbase[key] + (pos - offsets[key])] = row;      // same place within its key's block
+    extern __shared__ int32_t s_count[];
+    const int32_t t = blockIdx.x * kSegTile + threadIdx.x;
+    const int32_t key = t < T ? row_key(ids[t], n_slots) : -1;
+    const int32_t rank = tile_rank(key, n_slots + 1, s_count);
+    if (key < 0) return;
+    const int32_t pos = tile_hist[(size_t)key * n_tiles + blockIdx.x] + rank;
+    perm[pos] = t;
+    gperm[gbase[key] + (pos - offsets[key])] = t;        // same place within its key's block
+}
+
+// Batches of one tile: everything above by one workgroup, in one launch.
+__global__ void __launch_bounds__(1024) k_seg_one(const int32_t *__restrict__ ids, int32_t T, int32_t n_slots,
+                                                  int32_t short_len, int32_t *__restrict__ offsets,
+                                                  int32_t *__restrict__ seg_id, int32_t *__restrict__ seg_start,
+                                                  int32_t *__restrict__ n_seg, int32_t *__restrict__ blk_start,
+                                                  int32_t *__restrict__ blk_seg, int32_t *gbase,
+                                                  int4 *__restrict__ srec, int32_t *__restrict__ header,
+                                                  int32_t *__restrict__ perm, int32_t *__restrict__ gperm,
+                                                  int32_t *err) {
+    extern __shared__ int32_t s_off[];        // [n_slots + 2]: counts, then first positions
+    __shared__ int32_t s_wave[48];
+    const int32_t nb = n_slots + 1, t = threadIdx.x;
+    const int32_t id = t < T ? ids[t] : -1;
+    const int32_t key = t < T ? row_key(id, n_slots) : -1;
+    if (t < T && !(id >= -1 && id < n_slots)) flag_bad_row(err, t);
+    const int32_t rank = tile_rank(key, nb, s_off);
+    int32_t carry = 0;
+    for (int32_t k0 = 0; k0 < nb; k0 += blockDim.x) {
+        const int32_t k = k0 + threadIdx.x;
+        int32_t tot;
+        const int32_t pos = block_exclusive_scan(k < nb ? s_off[k] : 0, s_wave, &tot) + carry;
+        if (k < nb) s_off[k] = pos;
+        carry += tot;
+    }
+    if (threadIdx.x == 0) s_off[nb] = T;
+    __syncthreads();
+    for (int32_t k = threadIdx.x; k <= nb; k += blockDim.x) offsets[k] = s_off[k];
+    gemm_order(s_off, nb, T, short_len, s_wave, gbase, srec, header);
+    compact_segments(s_off, nb, T, s_wave, seg_id, seg_start, n_seg, blk_start, blk_seg);
+    __threadfence_block();                    // gbase was written by other threads of this block
+    __syncthreads();
+    if (key < 0) return;
+    perm[s_off[key] + rank] = t;
+    gperm[gbase[key] + rank] = t;
 }
 
 lora_status_t launch_ws_init(void *ws, hipStream_t s, bool err_only) {
@@ -280,6 +310,15 @@ lora_status_t launch_segments(const int32_t *ids, int32_t T, int32_t n_slots, co
     int32_t *tile_hist = ws_ptr<int32_t>(ws, L.tile_hist);
     const size_t lds_hist = sizeof(int32_t) * (size_t)(n_slots + 1);
     const size_t lds_off = sizeof(int32_t) * (size_t)(n_slots + 2);
+    if (n_tiles == 1) {
+        hipLaunchKernelGGL(k_seg_one, dim3(1), dim3(kSegTile), lds_off, s, ids, T, n_slots, short_len,
+                           ws_ptr<int32_t>(ws, L.offsets), ws_ptr<int32_t>(ws, L.seg_id),
+                           ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
+                           ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg),
+                           ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int4>(ws, L.srec), ws_ptr<int32_t>(ws, L.header),
+                           ws_ptr<int32_t>(ws, L.perm), ws_ptr<int32_t>(ws, L.gperm), err);
+        return hip_status(hipGetLastError());
+    }
     hipLaunchKernelGGL(k_seg_hist, dim3(n_tiles), dim3(256), lds_hist, s, ids, T, n_slots,
                        tile_hist, n_tiles, err);
     hipLaunchKernelGGL(k_seg_scan, dim3(1), dim3(1024), lds_off, s, tile_hist, n_slots, n_tiles, T, short_len,
@@ -287,7 +326,7 @@ lora_status_t launch_segments(const int32_t *ids, int32_t T, int32_t n_slots, co
                        ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
                        ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg),
                        ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int4>(ws, L.srec), ws_ptr<int32_t>(ws, L.header));
-    hipLaunchKernelGGL(k_seg_scatter, dim3(n_tiles), dim3(kSegTile), 0, s, ids, T, n_slots,
+    hipLaunchKernelGGL(k_seg_scatter, dim3(n_tiles), dim3(kSegTile), lds_hist, s, ids, T, n_slots,
                        tile_hist, n_tiles, ws_ptr<int32_t>(ws, L.perm), ws_ptr<int32_t>(ws, L.offsets),
                        ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int32_t>(ws, L.gperm));
     return hip_status(hipGetLastError());
