@@ -6,11 +6,12 @@
 namespace lora {
 
 // ---------------------------------------------------------------------------
-// fp32: 64 rows x 64 columns of h per workgroup of 4 wavefronts (2 x 2), each
-// with 32 rows x 32 columns of both projections on v_mfma_f32_32x32x2_f32
-// (fp32 products and sums; the matrix cores' fp32 rate is twice the vector
-// units').  K in steps of 32, staged through LDS with the next step's loads in
-// registers under the current one's products.  Grids of few tiles split K;
+// fp32: 32 rows x 64 columns of h per workgroup of 4 wavefronts, each with 32
+// columns of one projection on v_mfma_f32_32x32x2_f32 (fp32 products and sums;
+// the matrix cores' fp32 rate is twice the vector units').  Small tiles leave
+// less of the chip idle in the last round, and several share a CU (333 x 1032
+// x 2744: F32_TILE_NOTE).  K in steps of 32, staged through LDS with the next
+// step's loads in registers under the current one's products.  Grids of few tiles split K;
 // the sums then go through LDS or the partial buffer to threads that own 4
 // columns of a row, which add the row's low-rank terms.
 // ---------------------------------------------------------------------------
@@ -20,7 +21,7 @@ struct gated_f32_args {
     float *h, *keep[2];
     const int32_t *ids, *perm;
     const float *v;
-    float *partial;                    // [tile][split][64][128]
+    float *partial;                    // [tile][split][32][128]
     int32_t T, K, N, n_slots, max_rank, act, n_tiles_n, splits, k_chunk;
 };
 
@@ -68,43 +69,38 @@ __device__ __forceinline__ void gated_finish4(const gated_f32_args &g, int64_t t
 }
 
 template <bool SPLIT> __global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
-    constexpr int BK = 32, XS = 64 + 4, WS = 128 + 4;
-    __shared__ __attribute__((aligned(16))) float smem[64 * WS];    // stages: x [BK][XS], W [BK][WS]; sums: [64][WS]
+    constexpr int BK = 32, XS = 32 + 4, WS = 128 + 4;
+    __shared__ __attribute__((aligned(16))) float smem[BK * (XS + WS)];   // stage: x [BK][XS], W [BK][WS]; sums: [32][WS]
     float *s_x = smem, *s_w = smem + BK * XS;
-    static_assert(BK * (XS + WS) <= 64 * WS, "a stage fits the sums' LDS");
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w >> 1, wn = w & 1;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int tile = SPLIT ? blockIdx.x / g.splits : blockIdx.x, split = SPLIT ? blockIdx.x % g.splits : 0;
-    const int m0 = tile / g.n_tiles_n * 64, n0 = tile % g.n_tiles_n * 64;
+    const int m0 = tile / g.n_tiles_n * 32, n0 = tile % g.n_tiles_n * 64;
     const int N = g.N, T = g.T, k_begin = split * g.k_chunk, k_end = min(g.K, k_begin + g.k_chunk);
-    // x: thread -> row tid / 4, 8 k from 8 (tid % 4); W: thread -> k tid / 8, 8 columns from 8 (tid % 8), both weights
-    const int xr = tid >> 2, xk = (tid & 3) * 8, wk = tid >> 3, wc = (tid & 7) * 8;
+    // x: thread -> row tid / 8, 4 k from 4 (tid % 8); W: thread -> k tid / 8, 8 columns from 8 (tid % 8), both weights
+    const int xr = tid >> 3, xk = (tid & 7) * 4, wk = tid >> 3, wc = (tid & 7) * 8;
     const int32_t t_x = m0 + xr < T ? perm_row(g.perm, m0 + xr, T) : -1;
     const float *xp = g.x + (int64_t)(t_x < 0 ? 0 : t_x) * g.K;
-    f32x4_t rx[2], rw[2][2];
+    f32x4_t rx, rw[2][2];
     auto load = [&](int k0) {
         const bool xok = t_x >= 0 && k0 + xk < k_end, wok = k0 + wk < k_end && n0 + wc < N;   // K, N multiples of 8
+        rx = load4(xok, xp + k0 + xk);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            rx[i] = load4(xok, xp + k0 + xk + 4 * i);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
                 rw[m][i] = load4(wok, g.W[m] + (int64_t)(k0 + wk) * N + n0 + wc + 4 * i);
         }
     };
-    f32x16_t acc[2];
+    f32x16_t acc;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
+    for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
     if (k_begin < k_end) load(k_begin);
     for (int k0 = k_begin; k0 < k_end; k0 += BK) {
         __syncthreads();
 #pragma unroll
+        for (int i = 0; i < 4; ++i) s_x[(xk + i) * XS + xr] = rx[i];
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-            s_x[(xk + 4 * i + 0) * XS + xr] = rx[i].x;
-            s_x[(xk + 4 * i + 1) * XS + xr] = rx[i].y;
-            s_x[(xk + 4 * i + 2) * XS + xr] = rx[i].z;
-            s_x[(xk + 4 * i + 3) * XS + xr] = rx[i].w;
 #pragma unroll
             for (int m = 0; m < 2; ++m) *reinterpret_cast<f32x4_t *>(s_w + wk * WS + 64 * m + wc + 4 * i) = rw[m][i];
         }
@@ -113,26 +109,21 @@ template <bool SPLIT> __global__ void __launch_bounds__(256) k_gated_f32(gated_f
 #pragma unroll
         for (int k = 0; k < BK; k += 2) {
             const int kk = k + (lane >> 5);
-            const float a = s_x[kk * XS + wm * 32 + (lane & 31)];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, s_w[kk * WS + 64 * m + wn * 32 + (lane & 31)], acc[m],
-                                                              0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(s_x[kk * XS + (lane & 31)], s_w[kk * WS + w * 32 + (lane & 31)],
+                                                       acc, 0, 0, 0);
         }
     }
-    float *part = SPLIT ? g.partial + ((int64_t)tile * g.splits + split) * 64 * 128 : nullptr;
+    float *part = SPLIT ? g.partial + ((int64_t)tile * g.splits + split) * 32 * 128 : nullptr;
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int r = wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), c = 64 * m + wn * 32 + (lane & 31);
-            if (SPLIT) part[r * 128 + c] = acc[m][e];
-            else smem[r * WS + c] = acc[m][e];
-        }
+    for (int e = 0; e < 16; ++e) {
+        const int r = 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), c = w * 32 + (lane & 31);
+        if (SPLIT) part[r * 128 + c] = acc[e];
+        else smem[r * WS + c] = acc[e];
+    }
     if (SPLIT) return;
     __syncthreads();
-    for (int i = tid; i < 64 * 16; i += 256) {
+    for (int i = tid; i < 32 * 16; i += 256) {
         const int r = i >> 4, c = (i & 15) * 4, n = n0 + c;
         const int64_t t = m0 + r < T ? perm_row(g.perm, m0 + r, T) : -1;
         if (t < 0 || n >= N) continue;
@@ -146,13 +137,13 @@ template <bool SPLIT> __global__ void __launch_bounds__(256) k_gated_f32(gated_f
 
 // The pieces' sums, in split order: 16 rows of one tile per workgroup.
 __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
-    const int tile = blockIdx.x >> 2, r = (blockIdx.x & 3) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
-    const int p = tile / g.n_tiles_n * 64 + r, n = tile % g.n_tiles_n * 64 + c;
+    const int tile = blockIdx.x >> 1, r = (blockIdx.x & 1) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    const int p = tile / g.n_tiles_n * 32 + r, n = tile % g.n_tiles_n * 64 + c;
     const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
     if (t < 0 || n >= g.N) return;
     float o[2][4] = {};
-    const float *part = g.partial + (int64_t)tile * g.splits * 64 * 128 + r * 128 + c;
-    for (int s = 0; s < g.splits; ++s, part += 64 * 128)
+    const float *part = g.partial + (int64_t)tile * g.splits * 32 * 128 + r * 128 + c;
+    for (int s = 0; s < g.splits; ++s, part += 32 * 128)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const float4 f = *reinterpret_cast<const float4 *>(part + 64 * m);
@@ -267,13 +258,13 @@ lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {
         g.act = c.act;
         g.n_tiles_n = ceil_div(g.N, 64);
         g.partial = c.partial;
-        const int tiles = ceil_div(c.T, 64) * g.n_tiles_n;
-        g.splits = f32_splits(tiles, g.K, 64 * 128, c.partial_bytes, g.k_chunk);
+        const int tiles = ceil_div(c.T, 32) * g.n_tiles_n;
+        g.splits = f32_splits(tiles, g.K, 32 * 128, c.partial_bytes, g.k_chunk);
         if (g.splits == 1) {
             hipLaunchKernelGGL(k_gated_f32<false>, dim3(tiles), dim3(256), 0, s, g);
         } else {
             hipLaunchKernelGGL(k_gated_f32<true>, dim3(tiles * g.splits), dim3(256), 0, s, g);
-            hipLaunchKernelGGL(k_gated_reduce_f32, dim3(tiles * 4), dim3(256), 0, s, g);
+            hipLaunchKernelGGL(k_gated_reduce_f32, dim3(tiles * 2), dim3(256), 0, s, g);
         }
         return hip_status(hipGetLastError());
     }

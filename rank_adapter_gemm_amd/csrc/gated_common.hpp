@@ -292,15 +292,15 @@ __device__ __forceinline__ f32x4_t load4(bool ok, const float *p) {
     return v;
 }
 
-// K ranges per tile of the fp32 kernels (tiles of `area` sums): the count with
-// the least rounds of 256 workgroups, each 1 / count of a tile long, with a
-// fiftieth of a tile for each range's partial sums; ranges of at least 128
-// terms.  (258 tiles alone take two rounds: 95 us; F32_NOTE.)
+// K ranges per tile of the fp32 kernels (tiles of `area` sums): one while the
+// tiles alone give nearly every CU one, else the count with the least rounds of
+// 512 workgroups (two a CU), each 1 / count of a tile long, with a sixteenth of a
+// tile for each range's partial sums; ranges of at least 128 terms.
 inline int f32_splits(int tiles, int K, int area, size_t partial_bytes, int &k_chunk) {
     int best = 1, best_cost = 1 << 30;
-    for (int s = 1; s <= kMaxGemmSplit && s * 128 <= (K > 128 ? K : 128); ++s) {
+    for (int s = 1; (s == 1 || tiles < 224) && s <= kMaxGemmSplit && s * 128 <= (K > 128 ? K : 128); ++s) {
         if (s > 1 && (size_t)s * tiles * area * 4 > partial_bytes) break;
-        const int cost = 1000 * ceil_div((int64_t)tiles * s, 256) / s + (s > 1 ? 20 * s : 0);
+        const int cost = 1000 * ceil_div((int64_t)tiles * s, 512) / s + (s > 1 ? 60 * s : 0);
         if (cost < best_cost) {
             best = s;
             best_cost = cost;
