@@ -322,6 +322,7 @@ struct bwd_layout {
     size_t vt;          // bf16 parts of s v and dv, transposed (see k_rank_finish)
     size_t oct;         // bf16: both slices' A in rank octets, one set per segment
     size_t row0, rank, scale;   // their pool tables, [n_slots]
+    size_t slot_blk;    // [n_slots]: first work block of a slot's segment
     size_t partial;     // dx's split-K partials
     size_t total;
 };

@@ -10,8 +10,8 @@ namespace lora {
 // columns of one projection on v_mfma_f32_32x32x2_f32 (fp32 products and sums;
 // the matrix cores' fp32 rate is twice the vector units').  Small tiles leave
 // less of the chip idle in the last round, and several share a CU (333 x 1032
-// x 2744: F32_TILE_NOTE).  K in steps of 32, staged through LDS with the next
-// step's loads in registers under the current one's products.  Grids of few tiles split K;
+// x 2744: F32_TILE_NOTE).  K in steps of 32, DMA'd into a ring of
+// three stages (a step's products take less time than a load from HBM).  Grids of few tiles split K;
 // the sums then go through LDS or the partial buffer to threads that own 4
 // columns of a row, which add the row's low-rank terms.
 // ---------------------------------------------------------------------------
@@ -22,39 +22,55 @@ struct gated_f32_args {
     const int32_t *ids, *perm;
     const float *v;
     float *partial;                    // [tile][split][32][128]
-    int32_t T, K, N, n_slots, max_rank, act, n_tiles_n, splits, k_chunk;
+    int32_t T, K, N, n_slots, max_rank, act, n_tiles_m, n_tiles_n, splits, k_chunk;
 };
 
-// 4 columns of one row from both projections' sums.
-__device__ __forceinline__ void gated_finish4(const gated_f32_args &g, int64_t t, int n, float (&o)[2][4]) {
-    const int32_t id = g.ids[t];
+// What a row's low-rank terms need of its slot in both pools.
+__device__ __forceinline__ row_slot load_row_slot(const gated_f32_args &g, int64_t t) {
+    row_slot r{{0, 0}, {0, 0}, {0.f, 0.f}};
+    const int32_t id = t >= 0 ? g.ids[t] : -1;
     if (id >= 0 && id < g.n_slots) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            const int r = min(g.rank[m][id], g.max_rank);
-            if (r <= 0) continue;
-            const float *b = g.b[m] + (slot_row0(g.row0[m], id, g.max_rank) * g.N + (int64_t)n * 8);
-            const float *vt = g.v + t * 2 * g.max_rank + m * g.max_rank;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int j0 = 0; j0 < r; j0 += 8, b += (int64_t)g.N * 8) {
-                float vv[8], bb[4][8];
-                *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(vt + j0);
-                *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(vt + j0 + 4);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    *reinterpret_cast<float4 *>(bb[q]) = *reinterpret_cast<const float4 *>(b + 8 * q);
-                    *reinterpret_cast<float4 *>(bb[q] + 4) = *reinterpret_cast<const float4 *>(b + 8 * q + 4);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d[q] = fmaf(vv[e], bb[q][e], d[q]);
-            }
-            const float s = g.scale[m][id];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) o[m][q] = fmaf(s, d[q], o[m][q]);
+            r.rank[m] = min(g.rank[m][id], g.max_rank);
+            r.row0[m] = (int32_t)slot_row0(g.row0[m], id, g.max_rank);
+            r.scale[m] = g.scale[m][id];
         }
     }
+    return r;
+}
+
+// 4 columns of one row from both projections' sums; an octet's loads of both
+// projections are in flight together.
+__device__ __forceinline__ void gated_finish4(const gated_f32_args &g, const row_slot &rs, int64_t t, int n,
+                                              float (&o)[2][4]) {
+    const int oct = (max(rs.rank[0], rs.rank[1]) + 7) >> 3;
+    float d[2][4] = {};
+    for (int gg = 0; gg < oct; ++gg) {
+        f32x4_t vv[2][2], bb[2][4][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const bool in = 8 * gg < rs.rank[m];
+            const float *b = g.b[m] + (((int64_t)rs.row0[m] + 8 * gg) * g.N + (int64_t)n * 8);
+            const float *vt = g.v + t * 2 * g.max_rank + m * g.max_rank + 8 * gg;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                vv[m][h] = load4(in, vt + 4 * h);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) bb[m][q][h] = load4(in, b + 8 * q + 4 * h);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[m][q] = fmaf(vv[m][e >> 2][e & 3], bb[m][q][e >> 2][e & 3], d[m][q]);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[m][q] = fmaf(rs.scale[m], d[m][q], o[m][q]);
     const int64_t at = t * g.N + n;
     float4 h;
     h.x = act_value<true>(g.act, o[0][0]) * o[1][0];
@@ -68,50 +84,62 @@ __device__ __forceinline__ void gated_finish4(const gated_f32_args &g, int64_t t
     }
 }
 
-template <bool SPLIT> __global__ void __launch_bounds__(256) k_gated_f32(gated_f32_args g) {
-    constexpr int BK = 32, XS = 32 + 4, WS = 128 + 4;
-    __shared__ __attribute__((aligned(16))) float smem[BK * (XS + WS)];   // stage: x [BK][XS], W [BK][WS]; sums: [32][WS]
-    float *s_x = smem, *s_w = smem + BK * XS;
+template <bool SPLIT> __global__ void __launch_bounds__(256, 2) k_gated_f32(gated_f32_args g) {
+    constexpr int BK = 32, NS = 3, XST = 32 * BK, STAGE = XST + BK * 128, WS = 128 + 4, PER = 5;
+    __shared__ __attribute__((aligned(1024))) float smem[NS * STAGE];     // stages: x [32][BK], W [BK][128]; sums: [32][WS]
+    static_assert(32 * WS <= NS * STAGE, "the sums fit the stages' LDS");
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int tile = SPLIT ? blockIdx.x / g.splits : blockIdx.x, split = SPLIT ? blockIdx.x % g.splits : 0;
-    const int m0 = tile / g.n_tiles_n * 32, n0 = tile % g.n_tiles_n * 64;
+    int tm, tn, split;
+    f32_tile(blockIdx.x, gridDim.x, g.n_tiles_m, SPLIT ? g.splits : 1, tm, tn, split);
+    const int tile = tm * g.n_tiles_n + tn, m0 = tm * 32, n0 = tn * 64;
     const int N = g.N, T = g.T, k_begin = split * g.k_chunk, k_end = min(g.K, k_begin + g.k_chunk);
-    // x: thread -> row tid / 8, 4 k from 4 (tid % 8); W: thread -> k tid / 8, 8 columns from 8 (tid % 8), both weights
-    const int xr = tid >> 3, xk = (tid & 7) * 4, wk = tid >> 3, wc = (tid & 7) * 8;
+    __shared__ row_slot s_slot[SPLIT ? 1 : 32];
+    if (!SPLIT && tid < 32) s_slot[tid] = load_row_slot(g, m0 + tid < T ? perm_row(g.perm, m0 + tid, T) : -1);
+    // DMA, 16-byte chunks.  x: thread -> row tid / 8, place tid % 8, which holds
+    // the row's chunk place ^ (row % 8).  W: chunk 256 j + tid -> row / 32, gate's 16
+    // chunks then up's.
+    const int xr = tid >> 3, xk = 4 * ((tid & 7) ^ (xr & 7));
     const int32_t t_x = m0 + xr < T ? perm_row(g.perm, m0 + xr, T) : -1;
-    const float *xp = g.x + (int64_t)(t_x < 0 ? 0 : t_x) * g.K;
-    f32x4_t rx, rw[2][2];
-    auto load = [&](int k0) {
-        const bool xok = t_x >= 0 && k0 + xk < k_end, wok = k0 + wk < k_end && n0 + wc < N;   // K, N multiples of 8
-        rx = load4(xok, xp + k0 + xk);
+    const float *xp = g.x + (int64_t)(t_x < 0 ? 0 : t_x) * g.K + xk;
+    const int wr = tid >> 5, wc = (tid & 15) * 4;
+    const bool wok = n0 + wc < N;
+    const float *wp = ((tid & 16) ? g.W[1] : g.W[0]) + (int64_t)wr * N + (wok ? n0 + wc : 0);
+    auto dma_stage = [&](int kt, int buf) {
+        float *xs = smem + buf * STAGE, *wsm = xs + XST;
+        const int k0 = k_begin + kt * BK;
+        dma16(t_x >= 0 && k0 + xk < k_end ? (const void *)(xp + k0) : (const void *)g_zero16, xs + w * 64 * 4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                rw[m][i] = load4(wok, g.W[m] + (int64_t)(k0 + wk) * N + n0 + wc + 4 * i);
-        }
+        for (int j = 0; j < 4; ++j)
+            dma16(wok && k0 + 8 * j + wr < k_end ? (const void *)(wp + (int64_t)(k0 + 8 * j) * N) : (const void *)g_zero16,
+                  wsm + (256 * j + w * 64) * 4);
     };
     f32x16_t acc;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-    if (k_begin < k_end) load(k_begin);
-    for (int k0 = k_begin; k0 < k_end; k0 += BK) {
-        __syncthreads();
+    const int nk = (k_end - k_begin + BK - 1) / BK;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_x[(xk + i) * XS + xr] = rx[i];
+    for (int st = 0; st < NS - 1; ++st)
+        if (st < nk) dma_stage(st, st);
+    for (int kt = 0; kt < nk; ++kt) {
+        if (kt + 1 < nk) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * PER) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and this wave's reads of the stage refilled next
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
+        // product i of a step takes k = i from the lower half-wavefront and
+        // k = 16 + i from the upper: a lane's 16 values of x are neighbours
+        const float *xs = smem + (kt % NS) * STAGE + (lane & 31) * BK;
+        const float *wsm = smem + (kt % NS) * STAGE + XST + 16 * (lane >> 5) * 128 + w * 32 + (lane & 31);
+        float a[16], b[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4_t *>(a + 4 * i) =
+                *reinterpret_cast<const f32x4_t *>(xs + 4 * ((4 * (lane >> 5) + i) ^ (lane & 7)));
 #pragma unroll
-            for (int m = 0; m < 2; ++m) *reinterpret_cast<f32x4_t *>(s_w + wk * WS + 64 * m + wc + 4 * i) = rw[m][i];
-        }
-        __syncthreads();
-        if (k0 + BK < k_end) load(k0 + BK);
+        for (int i = 0; i < 16; ++i) b[i] = wsm[i * 128];
 #pragma unroll
-        for (int k = 0; k < BK; k += 2) {
-            const int kk = k + (lane >> 5);
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(s_x[kk * XS + (lane & 31)], s_w[kk * WS + w * 32 + (lane & 31)],
-                                                       acc, 0, 0, 0);
-        }
+        for (int i = 0; i < 16; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], acc, 0, 0, 0);
     }
     float *part = SPLIT ? g.partial + ((int64_t)tile * g.splits + split) * 32 * 128 : nullptr;
     __syncthreads();
@@ -131,7 +159,7 @@ template <bool SPLIT> __global__ void __launch_bounds__(256) k_gated_f32(gated_f
 #pragma unroll
         for (int m = 0; m < 2; ++m)
             *reinterpret_cast<float4 *>(o[m]) = *reinterpret_cast<const float4 *>(smem + r * WS + 64 * m + c);
-        gated_finish4(g, t, n, o);
+        gated_finish4(g, s_slot[r], t, n, o);
     }
 }
 
@@ -141,6 +169,7 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
     const int p = tile / g.n_tiles_n * 32 + r, n = tile % g.n_tiles_n * 64 + c;
     const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
     if (t < 0 || n >= g.N) return;
+    const row_slot rs = load_row_slot(g, t);
     float o[2][4] = {};
     const float *part = g.partial + (int64_t)tile * g.splits * 32 * 128 + r * 128 + c;
     for (int s = 0; s < g.splits; ++s, part += 32 * 128)
@@ -149,7 +178,7 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
             const float4 f = *reinterpret_cast<const float4 *>(part + 64 * m);
             o[m][0] += f.x; o[m][1] += f.y; o[m][2] += f.z; o[m][3] += f.w;
         }
-    gated_finish4(g, t, n, o);
+    gated_finish4(g, rs, t, n, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -258,7 +287,8 @@ lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {
         g.act = c.act;
         g.n_tiles_n = ceil_div(g.N, 64);
         g.partial = c.partial;
-        const int tiles = ceil_div(c.T, 32) * g.n_tiles_n;
+        g.n_tiles_m = ceil_div(c.T, 32);
+        const int tiles = g.n_tiles_m * g.n_tiles_n;
         g.splits = f32_splits(tiles, g.K, 32 * 128, c.partial_bytes, g.k_chunk);
         if (g.splits == 1) {
             hipLaunchKernelGGL(k_gated_f32<false>, dim3(tiles), dim3(256), 0, s, g);

@@ -245,6 +245,7 @@ struct rank_finish_args {
     const int32_t *perm, *offsets, *seg_id, *seg_start, *n_seg, *blk_start, *blk_seg;
     float *dv;
     uint16_t *vt;
+    int32_t *slot_blk;                 // [n_slots]: a segment's first work block, by its slot
 };
 
 __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_pools pp) {
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_po
     if (seg < 0 || seg >= nseg) return;
     const int32_t id = g.seg_id[seg];
     if (id < 0 || id >= g.n_slots) return;
+    if (threadIdx.x == 0 && blockIdx.y == 0 && (int)blockIdx.x == g.blk_start[seg]) g.slot_blk[id] = blockIdx.x;
     const int p0 = g.seg_start[seg] + ((int)blockIdx.x - g.blk_start[seg]) * BR;
     const int pend = min(min(g.seg_start[seg + 1], p0 + BR), g.T);
     const int i = threadIdx.x & 31, p = p0 + i;
@@ -521,20 +523,26 @@ template <int BM, int BN> __global__ void __launch_bounds__(256) k_nt_reduce(gem
         const int32_t rk = g.rank[id];
         const float *vrow = g.v + t * g.v_stride;
         const uint16_t *b = g.b + (int64_t)g.row0[id] * g.N + (int64_t)n * 8;
-        for (int j = 0; j < rk; j += 8, b += (int64_t)g.N * 8) {
-            float vv[8];
-            *reinterpret_cast<float4 *>(vv) = *reinterpret_cast<const float4 *>(vrow + j);
-            *reinterpret_cast<float4 *>(vv + 4) = *reinterpret_cast<const float4 *>(vrow + j + 4);
-            uint4 bq[8];
+        // two octets at a time (rk is 2 max_rank, a multiple of 16)
+        for (int j = 0; j < rk; j += 16, b += (int64_t)g.N * 16) {
+            float vv[2][8];
+            uint4 bq[2][8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) bq[q] = ldg16(b + q * 8);
+            for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<float4 *>(vv[h]) = *reinterpret_cast<const float4 *>(vrow + j + 8 * h);
+                *reinterpret_cast<float4 *>(vv[h] + 4) = *reinterpret_cast<const float4 *>(vrow + j + 8 * h + 4);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                float bf[8];
-                vec16<LORA_BF16>::widen(bq[q], bf);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[q] = fmaf(vv[e], bf[e], o[q]);
+                for (int q = 0; q < 8; ++q) bq[h][q] = ldg16(b + (int64_t)h * g.N * 8 + q * 8);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float bf[8];
+                    vec16<LORA_BF16>::widen(bq[h][q], bf);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[q] = fmaf(vv[h][e], bf[e], o[q]);
+                }
         }
     }
     stg16(g.y + t * g.N + n, vec16<LORA_BF16>::narrow(o));
@@ -618,56 +626,67 @@ __device__ __forceinline__ void dx_finish4(const dx_f32_args &g, const pair_pool
     *reinterpret_cast<float4 *>(g.dx + t * g.N + n) = make_float4(o[0], o[1], o[2], o[3]);
 }
 
-template <bool SPLIT> __global__ void __launch_bounds__(256) k_dx_f32(dx_f32_args g, pair_pools pp) {
-    constexpr int BK = 32, LD = 64 + 4;
-    __shared__ __attribute__((aligned(16))) float smem[2 * BK * LD];
-    float *s_a = smem, *s_w = smem + BK * LD;
+template <bool SPLIT> __global__ void __launch_bounds__(256, 2) k_dx_f32(dx_f32_args g, pair_pools pp) {
+    constexpr int BK = 32, NS = 3, AST = 64 * BK, STAGE = 2 * AST, LD = 64 + 4, PER = 4;
+    __shared__ __attribute__((aligned(1024))) float smem[NS * STAGE];     // stages: [64][BK] of each; sums: [64][LD]
+    static_assert(64 * LD <= NS * STAGE, "the sums fit the stages' LDS");
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w >> 1, wn = w & 1;
-    const int tile = SPLIT ? blockIdx.x / g.splits : blockIdx.x, split = SPLIT ? blockIdx.x % g.splits : 0;
-    const int m0 = tile / g.n_tiles_n * 64, n0 = tile % g.n_tiles_n * 64;
-    const int r = tid >> 2, kk = (tid & 3) * 8;
-    const int32_t t_a = m0 + r < g.T ? perm_row(g.perm, m0 + r, g.T) : -1;
-    const int64_t arow = (int64_t)(t_a < 0 ? 0 : t_a) * g.F;
-    const bool wok = n0 + r < g.N;
-    const int64_t wrow = (int64_t)(wok ? n0 + r : 0) * g.F;
+    int tm, tn, split;
+    f32_tile(blockIdx.x, gridDim.x, (g.T + 63) / 64, SPLIT ? g.splits : 1, tm, tn, split);
+    const int tile = tm * g.n_tiles_n + tn, m0 = tm * 64, n0 = tn * 64;
     const int Fp = (g.F + BK - 1) / BK * BK;
     const int k_begin = split * g.k_chunk, k_end = min(2 * Fp, k_begin + g.k_chunk);
-    f32x4_t ra[2], rw[2];
-    auto load = [&](int k0) {
-        const bool second = k0 >= Fp;
-        const float *a = (second ? g.a1 : g.a0) + arow, *wt = (second ? g.w1 : g.w0) + wrow;
-        const int f = k0 - (second ? Fp : 0) + kk;
-        const bool in = f < g.F;                           // F is a multiple of 8
+    // DMA: 16-byte chunk 256 j + tid of an operand is at row / 8, place % 8, and
+    // holds the row's chunk place ^ (row % 8)
+    int64_t arow[2], wrow[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            ra[i] = load4(in && t_a >= 0, a + f + 4 * i);
-            rw[i] = load4(in && wok, wt + f + 4 * i);
+    for (int j = 0; j < 2; ++j) {
+        const int r = 32 * j + (tid >> 3);
+        const int32_t t = m0 + r < g.T ? perm_row(g.perm, m0 + r, g.T) : -1;
+        arow[j] = t >= 0 ? (int64_t)t * g.F : -1;
+        wrow[j] = n0 + r < g.N ? (int64_t)(n0 + r) * g.F : -1;
+    }
+    const int kk = 4 * ((tid & 7) ^ ((tid >> 3) & 7));
+    auto dma_stage = [&](int kt, int buf) {
+        float *as = smem + buf * STAGE, *wsm = as + AST;
+        const int k0 = k_begin + kt * BK;
+        const bool second = k0 >= Fp;                      // a step lies in one projection
+        const float *a = second ? g.a1 : g.a0, *wt = second ? g.w1 : g.w0;
+        const int f = k0 - (second ? Fp : 0) + kk;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            dma16(arow[j] >= 0 && f < g.F ? (const void *)(a + arow[j] + f) : (const void *)g_zero16,
+                  as + (256 * j + w * 64) * 4);
+            dma16(wrow[j] >= 0 && f < g.F ? (const void *)(wt + wrow[j] + f) : (const void *)g_zero16,
+                  wsm + (256 * j + w * 64) * 4);
         }
     };
     f32x16_t acc;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-    if (k_begin < k_end) load(k_begin);
-    for (int k0 = k_begin; k0 < k_end; k0 += BK) {
-        __syncthreads();
+    const int nk = (k_end - k_begin + BK - 1) / BK;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s_a[(kk + 4 * i + 0) * LD + r] = ra[i].x;
-            s_a[(kk + 4 * i + 1) * LD + r] = ra[i].y;
-            s_a[(kk + 4 * i + 2) * LD + r] = ra[i].z;
-            s_a[(kk + 4 * i + 3) * LD + r] = ra[i].w;
-            s_w[(kk + 4 * i + 0) * LD + r] = rw[i].x;
-            s_w[(kk + 4 * i + 1) * LD + r] = rw[i].y;
-            s_w[(kk + 4 * i + 2) * LD + r] = rw[i].z;
-            s_w[(kk + 4 * i + 3) * LD + r] = rw[i].w;
+    for (int st = 0; st < NS - 1; ++st)
+        if (st < nk) dma_stage(st, st);
+    for (int kt = 0; kt < nk; ++kt) {
+        if (kt + 1 < nk) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * PER) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and this wave's reads of the stage refilled next
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
+        // product i takes k = i from the lower half-wavefront, 16 + i from the upper
+        const float *as = smem + (kt % NS) * STAGE + (wm * 32 + (lane & 31)) * BK;
+        const float *wsm = smem + (kt % NS) * STAGE + AST + (wn * 32 + (lane & 31)) * BK;
+        float a[16], b[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = 4 * ((4 * (lane >> 5) + i) ^ (lane & 7));
+            *reinterpret_cast<f32x4_t *>(a + 4 * i) = *reinterpret_cast<const f32x4_t *>(as + c);
+            *reinterpret_cast<f32x4_t *>(b + 4 * i) = *reinterpret_cast<const f32x4_t *>(wsm + c);
         }
-        __syncthreads();
-        if (k0 + BK < k_end) load(k0 + BK);
 #pragma unroll
-        for (int k = 0; k < BK; k += 2)
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(s_a[(k + (lane >> 5)) * LD + wm * 32 + (lane & 31)],
-                                                       s_w[(k + (lane >> 5)) * LD + wn * 32 + (lane & 31)], acc, 0, 0,
-                                                       0);
+        for (int i = 0; i < 16; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], acc, 0, 0, 0);
     }
     float *part = SPLIT ? g.partial + ((int64_t)tile * g.splits + split) * 64 * 64 : nullptr;
     __syncthreads();
@@ -783,7 +802,7 @@ struct seg_outer_args {
     const uint16_t *x, *dy, *vt;       // [T][K], [2][T][N], see k_rank_finish
     uint16_t *dA[2], *dB[2];
     int32_t T, K, N, R, n_slots, Tp;
-    const int32_t *perm, *offsets, *rank[2], *seg_id, *seg_start, *n_seg, *blk_start;
+    const int32_t *perm, *offsets, *rank[2], *slot_blk;
     int32_t tiles_k, tiles_n;          // column tiles of x and of dy
 };
 
@@ -885,17 +904,7 @@ template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_m
     const int m = !is_a && item >= g.tiles_n, tile = item - m * g.tiles_n;
     const int n0 = tile * kOuterCols, N = is_a ? g.K : g.N;
     const int p0 = max(g.offsets[slot + 1], 0), p1 = min(g.offsets[slot + 2], g.T);
-    // the segment of this slot, for its first work block (seg_id ascends)
-    int64_t b0 = 0;
-    if (p1 > p0) {
-        int lo = 0, hi = min(*g.n_seg, g.n_slots) - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (g.seg_id[mid] < slot) lo = mid + 1;
-            else hi = mid;
-        }
-        b0 = (int64_t)g.blk_start[lo] * kShrinkRows;
-    }
+    const int64_t b0 = p1 > p0 ? (int64_t)g.slot_blk[slot] * kShrinkRows : 0;
     const int col = n0 + 32 * wave + (lane & 31), j4 = 4 * (lane >> 5);
     // ranks past the slot's get zeros whatever the rows hold
     const int R = g.R, rk[2] = {min(g.rank[0][slot], R), min(g.rank[1][slot], R)};
@@ -958,6 +967,7 @@ bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t R, int32_t d_in, 
     B.vt = o;      o = align256(o + (dtype == LORA_BF16 ? 16 * (size_t)R * 32 * ((t + 31) / 32 + segs) : 0));
     B.oct = o;     o = align256(o + (dtype == LORA_BF16 ? segs * 2 * (size_t)R * (size_t)d_in * 2 : 0));
     B.row0 = o;    o = align256(o + 4 * (size_t)n_slots);
+    B.slot_blk = o; o = align256(o + 4 * (size_t)n_slots);
     B.rank = o;    o = align256(o + 4 * (size_t)n_slots);
     B.scale = o;   o = align256(o + 4 * (size_t)n_slots);
     B.partial = o;
@@ -996,6 +1006,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     if (st != LORA_OK) return st;
     const int32_t row_blocks = ceil_div(T, kShrinkRows), n_work = row_blocks + (S < T ? S : T), Tp = n_work * 32;
     uint16_t *vt = ws_ptr<uint16_t>(ws, B.vt);
+    int32_t *slot_blk = ws_ptr<int32_t>(ws, B.slot_blk);
     if constexpr (DT == LORA_F32) {
         hipLaunchKernelGGL(k_rank_grad_rows<DT>, dim3(T, 2), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R,
                            c.ids, dv);
@@ -1019,7 +1030,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
             default: hipLaunchKernelGGL(k_rank_grad<4>, grid, dim3(256), 0, s, g, pp); break;
         }
         rank_finish_args f{v, part, split, T, R, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
-                           g.blk_start, g.blk_seg, dv, vt};
+                           g.blk_start, g.blk_seg, dv, vt, slot_blk};
         hipLaunchKernelGGL(k_rank_finish, dim3(n_work + row_blocks, 2 * R / 8), dim3(256), 0, s, f, pp);
     }
     if (c.dx && DT == LORA_F32) {
@@ -1070,9 +1081,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     if (c.dA[0] && DT == LORA_BF16) {
         seg_outer_args g{(const uint16_t *)c.x, (const uint16_t *)dg, vt,
                          {(uint16_t *)c.dA[0], (uint16_t *)c.dA[1]}, {(uint16_t *)c.dB[0], (uint16_t *)c.dB[1]},
-                         T, K, F, R, S, Tp, perm, offsets, {p[0].rank, p[1].rank}, ws_ptr<int32_t>(ws, L.seg_id),
-                         ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
-                         ws_ptr<int32_t>(ws, L.blk_start), ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
+                         T, K, F, R, S, Tp, perm, offsets, {p[0].rank, p[1].rank}, slot_blk, ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
         const dim3 grid((uint32_t)S * (g.tiles_k + 2 * g.tiles_n));
         switch ((R + 15) / 16) {
             case 1: hipLaunchKernelGGL((k_seg_outer_mfma<1, 1>), grid, dim3(256), 0, s, g); break;

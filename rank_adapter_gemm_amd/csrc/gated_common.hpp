@@ -292,18 +292,32 @@ __device__ __forceinline__ f32x4_t load4(bool ok, const float *p) {
     return v;
 }
 
-// K ranges per tile of the fp32 kernels (tiles of `area` sums): one while the
-// tiles alone give nearly every CU one, else the count with the least rounds of
-// 512 workgroups (two a CU), each 1 / count of a tile long, with a sixteenth of a
-// tile for each range's partial sums; ranges of at least 128 terms.
+// Workgroup b's tile and K range in the fp32 kernels: each XCD takes a
+// contiguous run of (column tile, range, row tile), rows fastest, so the row
+// tiles that read the same weights run together on one XCD's L2 (333 x 1032 x
+// 2744: 79 us with the rows spread over the XCDs; F32_ORDER_NOTE).
+__device__ __forceinline__ void f32_tile(int b, int total, int n_tiles_m, int splits, int &tm, int &tn, int &split) {
+    const int per = total / kXcds, rem = total % kXcds, x = b % kXcds;
+    const int v = x * per + min(x, rem) + b / kXcds;
+    tm = v % n_tiles_m;
+    split = v / n_tiles_m % splits;
+    tn = v / n_tiles_m / splits;
+}
+
+// K ranges per tile of the fp32 kernels (tiles of `area` sums): the count whose
+// time is least by this estimate -- rounds of 512 workgroups (two a CU, each at
+// half a CU's 0.6 TFLOP/s) and the partial sums written and read at 4 TB/s.
+// Ranges have at least 128 terms.
 inline int f32_splits(int tiles, int K, int area, size_t partial_bytes, int &k_chunk) {
-    int best = 1, best_cost = 1 << 30;
-    for (int s = 1; (s == 1 || tiles < 224) && s <= kMaxGemmSplit && s * 128 <= (K > 128 ? K : 128); ++s) {
-        if (s > 1 && (size_t)s * tiles * area * 4 > partial_bytes) break;
-        const int cost = 1000 * ceil_div((int64_t)tiles * s, 512) / s + (s > 1 ? 60 * s : 0);
-        if (cost < best_cost) {
+    int best = 1;
+    double best_us = 1e30;
+    for (int s = 1; s <= kMaxGemmSplit && (s == 1 || s * 128 <= K); ++s) {
+        const double sums = (double)s * tiles * area * 4;
+        if (s > 1 && sums > (double)partial_bytes) break;
+        const double us = 2.0 * area * K / 0.3e6 * ceil_div((int64_t)tiles * s, 512) / s + (s > 1 ? 2 * sums / 4e6 : 0);
+        if (us < best_us) {
             best = s;
-            best_cost = cost;
+            best_us = us;
         }
     }
     k_chunk = ceil_div(ceil_div(K, best), 32) * 32;

@@ -488,7 +488,7 @@ lora_status_t launch_gemm_gated_fp8(gemm_args &g, size_t partial_bytes, hipStrea
     g.n_tiles_n = ceil_div(2 * (int64_t)g.N, pl.bn);
     g.col_strips = col_strips_pay(g.T, 2 * g.N, g.n_tiles_n);
     if (pl.bm == 256 && pl.bn == 256) launch_gated_fp8_cfg<256, 256, 2, 4, 2, 2, 4, 2>(g, pl, s);
-    else if (pl.bm == 256) launch_gated_fp8_cfg<256, 128, 2, 8, 4, 2, 8, 2>(g, pl, s);
+    else if (pl.bm == 256) launch_gated_fp8_cfg<256, 128, 3, 8, 4, 2, 8, 2>(g, pl, s);
     else if (pl.bm == 128) launch_gated_fp8_cfg<128, 128, 2, 4, 2, 4, 8, 2>(g, pl, s);
     else if (pl.bm == 64) launch_gated_fp8_cfg<64, 128, 3, 4, 2, 3, 4, 2>(g, pl, s);
     else launch_gated_fp8_few(g, pl, s);

@@ -134,6 +134,16 @@ __device__ void compact_segments(const int32_t *s_off, int32_t nb, int32_t T, in
 // block calls it.
 __device__ void gemm_order(const int32_t *s_off, int32_t nb, int32_t T, int32_t short_len, int32_t *s_wave,
                            int32_t *__restrict__ gbase, int4 *__restrict__ srec, int32_t *__restrict__ header) {
+    if (short_len <= 1) {                                 // no segment is short: the sorted order itself
+        for (int32_t k = threadIdx.x; k < nb; k += blockDim.x) gbase[k] = s_off[k];
+        for (int32_t i = threadIdx.x; i < min(nb - 1, T); i += blockDim.x) srec[i] = make_int4(0, 0, 0, 0);
+        if (threadIdx.x == 0) {
+            header[kHdrNLong] = T;
+            header[kHdrShortLen] = short_len;
+            header[kHdrNShort] = 0;
+        }
+        return;
+    }
     int32_t n_short = 0;
     for (int32_t k0 = 0; k0 < nb; k0 += blockDim.x) {
         const int32_t k = k0 + threadIdx.x;

@@ -192,8 +192,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (0.1 us for 3.4):
+# half of a small call's time on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
