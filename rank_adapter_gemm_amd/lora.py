@@ -447,16 +447,50 @@ def lora_linear_forward_fp8(x, wq, w_scale, y, T, pool, ids, mode, flags, ws, st
                                        _stream(stream)), "lora_linear_forward_fp8")
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _checked(where, *args):
+    """Addresses of (tensor, dtype or dtypes, least elements) triples: a tensor
+    must be dense, of that type, large enough and on the current device, or the
+    kernels would read other memory than the caller means.  None and plain
+    addresses pass as they are."""
+    out, cur = [], None
+    for t, dtype, n in args:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if cur is None:
+            cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        if (t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype)) or t.numel() < n \
+                or t.get_device() != cur or not t.is_contiguous():
+            raise LoraError(LORA_ERR_INVALID_ARGUMENT,
+                            "%s: a %s tensor of %d elements on device %d, where a dense %s one of %d on device %d is read"
+                            % (where, t.dtype, t.numel(), t.get_device(), dtype, n, cur))
+        out.append(t.data_ptr())
+    return out
+
+
+_TORCH_TYPES = {LORA_F32: torch.float32, LORA_BF16: torch.bfloat16}
+
+
 def lora_add_rmsnorm(x, residual, weight, eps, T, d, dtype, residual_out, y, stream=None):
     """z = x + residual; y = z / sqrt(mean(z^2) + eps) * weight.  residual, residual_out: tensors or None."""
-    _ok(load().lora_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), T, d, dtype, _ptr(residual_out),
-                                _ptr(y), _stream(stream)), "lora_add_rmsnorm")
+    dt, n = _TORCH_TYPES.get(dtype), T * d
+    x, residual, weight, residual_out, y = _checked("lora_add_rmsnorm", (x, dt, n), (residual, dt, n), (weight, dt, d),
+                                                    (residual_out, dt, n), (y, dt, n))
+    _ok(load().lora_add_rmsnorm(x, residual, weight, eps, T, d, dtype, residual_out, y, _stream(stream)),
+        "lora_add_rmsnorm")
 
 
 def lora_add_rmsnorm_fp8(x, residual, weight, eps, T, d, residual_out, y, yq, y_scale, stream=None):
     """The same on bf16 rows, with the E4M3 codes and scales of y's rows; y may be None."""
-    _ok(load().lora_add_rmsnorm_fp8(_ptr(x), _ptr(residual), _ptr(weight), float(eps), T, d, _ptr(residual_out),
-                                    _ptr(y), _ptr(yq), _ptr(y_scale), _stream(stream)), "lora_add_rmsnorm_fp8")
+    dt, n = torch.bfloat16, T * d
+    x, residual, weight, residual_out, y, yq, y_scale = _checked(
+        "lora_add_rmsnorm_fp8", (x, dt, n), (residual, dt, n), (weight, dt, d), (residual_out, dt, n), (y, dt, n),
+        (yq, _CODES, n), (y_scale, torch.float32, T))
+    _ok(load().lora_add_rmsnorm_fp8(x, residual, weight, eps, T, d, residual_out, y, yq, y_scale, _stream(stream)),
+        "lora_add_rmsnorm_fp8")
 
 
 def lora_workspace_bytes_gated(T, n_slots, max_rank, d_out=0) -> int:
@@ -467,21 +501,35 @@ def lora_workspace_bytes_gated_fp8(T, n_slots, max_rank, d_in, d_out=0) -> int:
     return int(load().lora_workspace_bytes_gated_fp8(T, n_slots, max_rank, d_in, d_out))
 
 
+def _ws_bytes(ws) -> int:
+    return 0 if ws is None or isinstance(ws, int) else ws.numel() * ws.element_size()
+
+
 def lora_gated_forward(x, W_gate, W_up, h, T, pools, ids, act, mode, flags, ws, gate=None, up=None, stream=None):
     """h = act(gate projection) * up projection; pools: [gate's, up's] lora_pool_t; gate, up: tensors that keep
     the projections for the backward pass, or None."""
-    _ok(load().lora_gated_forward(_ptr(x), _ptr(W_gate), _ptr(W_up), _ptr(h), _ptr(gate), _ptr(up), T,
-                                  _pool_pair(pools), _ptr(ids), act, mode, flags, _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_forward")
+    pair, p = _pool_pair(pools), pools[0]
+    dt, n, nw = _TORCH_TYPES.get(p.dtype), T * p.d_out, p.d_in * p.d_out
+    nbytes = _ws_bytes(ws)
+    x, W_gate, W_up, h, gate, up, ids, ws = _checked(
+        "lora_gated_forward", (x, dt, T * p.d_in), (W_gate, dt, nw), (W_up, dt, nw), (h, dt, n), (gate, dt, n),
+        (up, dt, n), (ids, torch.int32, T), (ws, torch.uint8, 0))
+    _ok(load().lora_gated_forward(x, W_gate, W_up, h, gate, up, T, pair, ids, act, mode, flags, ws, nbytes,
+                                  _stream(stream)), "lora_gated_forward")
 
 
 def lora_gated_forward_fp8(x, xq, x_scale, wq_gate, w_scale_gate, wq_up, w_scale_up, h, T, pools, ids, act, mode,
                            flags, ws, gate=None, up=None, stream=None):
     """The same on FP8 base weights; xq, x_scale: the codes and scales of x's rows, or None (made in ws)."""
-    _ok(load().lora_gated_forward_fp8(_ptr(x), _ptr(xq), _ptr(x_scale), _ptr(wq_gate), _ptr(w_scale_gate),
-                                      _ptr(wq_up), _ptr(w_scale_up), _ptr(h), _ptr(gate), _ptr(up), T,
-                                      _pool_pair(pools), _ptr(ids), act, mode, flags, _ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_forward_fp8")
+    pair, p = _pool_pair(pools), pools[0]
+    dt, f32, n, nw = torch.bfloat16, torch.float32, T * p.d_out, p.d_in * p.d_out
+    nbytes = _ws_bytes(ws)
+    x, xq, x_scale, wq_gate, w_scale_gate, wq_up, w_scale_up, h, gate, up, ids, ws = _checked(
+        "lora_gated_forward_fp8", (x, dt, T * p.d_in), (xq, _CODES, T * p.d_in), (x_scale, f32, T),
+        (wq_gate, _CODES, nw), (w_scale_gate, f32, p.d_out), (wq_up, _CODES, nw), (w_scale_up, f32, p.d_out),
+        (h, dt, n), (gate, dt, n), (up, dt, n), (ids, torch.int32, T), (ws, torch.uint8, 0))
+    _ok(load().lora_gated_forward_fp8(x, xq, x_scale, wq_gate, w_scale_gate, wq_up, w_scale_up, h, gate, up, T, pair,
+                                      ids, act, mode, flags, ws, nbytes, _stream(stream)), "lora_gated_forward_fp8")
 
 
 def lora_workspace_bytes_gated_backward(T, n_slots, max_rank, d_in, d_out, dtype) -> int:
@@ -491,11 +539,19 @@ def lora_workspace_bytes_gated_backward(T, n_slots, max_rank, d_in, d_out, dtype
 def lora_gated_backward(x, W_gate, W_up, T, pools, ids, act, gate, up, dh, dx, dA, dB, ws, stream=None):
     """Gradients of lora_gated_forward: dx (or None) and, per projection, dA = [gate's, up's] of
     [n_slots, d_in, max_rank] and dB of [n_slots, max_rank, d_out] (or None for both)."""
-    a_arr = (ctypes.c_void_p * 2)(*[_ptr(t) for t in dA]) if dA is not None else None
-    b_arr = (ctypes.c_void_p * 2)(*[_ptr(t) for t in dB]) if dB is not None else None
-    _ok(load().lora_gated_backward(_ptr(x), _ptr(W_gate), _ptr(W_up), T, _pool_pair(pools), _ptr(ids), act,
-                                   _ptr(gate), _ptr(up), _ptr(dh), _ptr(dx), a_arr, b_arr, _ptr(ws),
-                                   ws.numel() * ws.element_size(), _stream(stream)), "lora_gated_backward")
+    pair, p = _pool_pair(pools), pools[0]
+    dt, n, nw, nr = _TORCH_TYPES.get(p.dtype), T * p.d_out, p.d_in * p.d_out, p.n_slots * p.max_rank
+    nbytes = _ws_bytes(ws)
+    grads = [None, None] if dA is None else list(dA), [None, None] if dB is None else list(dB)
+    x, W_gate, W_up, ids, gate, up, dh, dx, ws, a0, a1, b0, b1 = _checked(
+        "lora_gated_backward", (x, dt, T * p.d_in), (W_gate, dt, nw), (W_up, dt, nw), (ids, torch.int32, T),
+        (gate, dt, n), (up, dt, n), (dh, dt, n), (dx, dt, T * p.d_in), (ws, torch.uint8, 0),
+        (grads[0][0], dt, nr * p.d_in), (grads[0][1], dt, nr * p.d_in), (grads[1][0], dt, nr * p.d_out),
+        (grads[1][1], dt, nr * p.d_out))
+    a_arr = (ctypes.c_void_p * 2)(a0, a1) if dA is not None else None
+    b_arr = (ctypes.c_void_p * 2)(b0, b1) if dB is not None else None
+    _ok(load().lora_gated_backward(x, W_gate, W_up, T, pair, ids, act, gate, up, dh, dx, a_arr, b_arr, ws, nbytes,
+                                   _stream(stream)), "lora_gated_backward")
 
 
 class Fp8Weight:

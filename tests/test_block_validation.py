@@ -126,3 +126,19 @@ def test_gated_backward(lib):
     assert call(p=pools(max_rank=(72, 72))) == UNSUPPORTED
     assert call(n=1024) == SMALL
     assert call(T=0, x=None, dA=None, dB=None) == OK
+
+
+def test_the_binding_refuses_tensors_the_kernels_would_misread():
+    """On a host without a GPU no tensor is on the current device; addresses pass."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("covered on the GPU")
+    t = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.ones(64, dtype=torch.bfloat16)
+    for call in (lambda: L.lora_add_rmsnorm(t, t, w, 1e-6, 4, 64, L.LORA_BF16, t, t),
+                 lambda: L.lora_add_rmsnorm_fp8(t, t, w, 1e-6, 4, 64, t, t, t, t),
+                 lambda: L.lora_gated_forward(t, t, t, t, 4, list(pools()), t, 0, 0, 0, t),
+                 lambda: L.lora_gated_backward(t, t, t, 4, list(pools()), t, 0, t, t, t, t, [t, t], [t, t], t)):
+        with pytest.raises(L.LoraError) as e:
+            call()
+        assert e.value.status == INVALID

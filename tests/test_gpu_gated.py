@@ -249,3 +249,48 @@ def test_a_nan_adapter_stays_with_its_rows(T, f, order, what):
             h = run_forward(p, "silu", mode, fp8=parts)[0]
             assert torch.equal(h[others], ref[others])
             assert not torch.isfinite(h[~others][:, [100, 230]].float()).any()
+
+
+def test_the_binding_refuses_tensors_the_kernels_would_misread():
+    p = Pair(6, 64, 72, [8, 8], 8, BF16, seed=3)
+    ws = L.Workspace(6, 2, 8, 72, gated=True)
+    h = torch.empty(6, 72, dtype=BF16, device="cuda")
+
+    def call(x=p.x, W=p.W[0], h=h, ids=p.ids_dev, w=ws.buf, gate=None, up=None):
+        L.lora_gated_forward(x, W, p.W[1], h, 6, p.desc, ids, 0, 0, 0, w, gate=gate, up=up)
+
+    call()
+    for bad in (dict(x=p.x.float()), dict(x=p.x.cpu()), dict(x=p.x[:5]), dict(W=p.W[0].t()), dict(W=p.W[0][:63]),
+                dict(h=h[:5]), dict(h=h.half()), dict(ids=p.ids_dev.long()), dict(ids=p.ids_dev.cpu()),
+                dict(ids=p.ids_dev[:3]), dict(w=ws.buf.cpu()), dict(w=ws.buf[:1024]), dict(gate=h[:2], up=h)):
+        with pytest.raises(L.LoraError):
+            call(**bad)
+
+
+@pytest.mark.parametrize("T", [1, 150, 700])
+def test_a_block_on_fp8_weights(T):
+    """Norm with codes, gated pair on them, down projection: each step against
+    the 64-bit form of what it was given, as a server runs them."""
+    d, f = 512, 1040
+    p = Pair(T, d, f, [16, 8, 4, 0], 16, BF16, seed=31, ids=np.arange(T) % 4 - 1)
+    delta, res = (0.5 * p.x.float()).to(BF16), p.x.roll(1, 1).contiguous()
+    w = (1 + 0.1 * torch.randn(d, device="cuda")).to(BF16)
+    z, y = torch.empty_like(res), torch.empty_like(res)
+    q, s = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+    L.lora_add_rmsnorm_fp8(delta, res, w, 1e-6, T, d, z, y, q, s)
+    p.x = y
+    parts, bases, extra = fp8_parts(p)
+    assert torch.equal(parts[0], q) and torch.equal(parts[1], s)
+    got = run_forward(p, "silu", fp8=(q, s, parts[2]))
+    check(p, "silu", got, "h", bases, extra)
+    Wd = (torch.randn(f, d, device="cuda") / f ** 0.5).to(BF16)
+    down = Pair(1, f, d, [16, 8, 4], 16, BF16, seed=32).pools[0]
+    wd, out = L.Fp8Weight(Wd), torch.empty(T, d, dtype=BF16, device="cuda")
+    ids = torch.where(p.ids_dev < 3, p.ids_dev, -1)
+    ws = L.Workspace(T, 3, 16, d, fp8_d_in=f)
+    L.lora_linear_forward_fp8(got[0], wd.codes, wd.scale, out, T, down.pool, ids, L.LORA_MODE_AUTO, 0, ws.buf)
+    nxt, codes, scales = torch.empty_like(y), torch.empty_like(q), torch.empty_like(s)
+    L.lora_add_rmsnorm_fp8(out, z, w, 1e-6, T, d, z, nxt, codes, scales)
+    assert torch.isfinite(nxt.float()).all()
+    want = out.double() + (delta.double() + res.double()).to(BF16).double()
+    assert ((z.double() - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -7 * (delta.double() + res.double()).abs()).all()

@@ -145,3 +145,17 @@ def test_deterministic_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((z, y, q, s), ref))
+
+
+def test_the_binding_refuses_tensors_the_kernels_would_misread():
+    """Other types, strides, sizes and devices than the kernel reads."""
+    x, r, w = make(6, 256, torch.bfloat16, seed=13)
+    z, y = torch.empty_like(x), torch.empty_like(x)
+    good = dict(x=x, r=r, w=w, z=z, y=y)
+    wide = torch.empty(6, 512, dtype=torch.bfloat16, device="cuda")
+    for name in good:
+        for other in (x.float(), x.cpu(), wide[:, :256], wide[:, ::2], x[:0]):
+            bad = dict(good, **{name: other})
+            with pytest.raises(L.LoraError) as e:
+                L.lora_add_rmsnorm(bad["x"], bad["r"], bad["w"], EPS, 6, 256, L.LORA_BF16, bad["z"], bad["y"])
+            assert e.value.status == L.LORA_ERR_INVALID_ARGUMENT
