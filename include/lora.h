@@ -557,6 +557,7 @@ size_t lora_workspace_bytes_gated_fp8(int32_t T, int32_t n_slots, int32_t max_ra
  * of the pools' dtype; pools HOST [2] (gate, up) with the conditions of
  * lora_linear_forward_sliced and one d_out.  gate and up DEVICE [T, d_out]
  * keep g and u, each rounded once, for lora_gated_backward; both may be NULL.
+ * No output is another's buffer, or x's.
  * mode, ids and bad ids as in lora_linear_forward; a row whose slot is empty
  * in one pool has only the other's term (and is recorded).  flags: 0 or
  * LORA_FLAG_SEGMENTS_READY (segments built by lora_build_segments, by this
@@ -582,7 +583,7 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
  *     dg = dh u act'(g),   du = dh act(g)        (bf16 pools: rounded once)
  *     dx = dg W_gate^T + du W_up^T + dv_g A_a^T + dv_u A_a^T,   dv = s d{g,u} B_a^T
  *     dA_a = sum over a's rows of x^T dv,        dB_a = s sum of (x A_a)^T d{g,u}
- * dx DEVICE [T, d_in], overwritten (NULL: not computed).  dA and dB HOST
+ * dx DEVICE [T, d_in], overwritten (NULL: not computed; a buffer of its own).  dA and dB HOST
  * arrays of 2 DEVICE pointers (gate's, up's), dA[i] [n_slots, d_in, max_rank]
  * and dB[i] [n_slots, max_rank, d_out], row-major as lora_pool_upload takes
  * one slot's (lda = max_rank, ldb = d_out); padded so for packed pools too.

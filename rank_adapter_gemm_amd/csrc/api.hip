@@ -597,6 +597,12 @@ static lora_status_t check_pair(const lora_pool_t *pools) {
 
 static inline bool valid_act(int32_t a) { return a == LORA_ACT_SILU || a == LORA_ACT_GELU || a == LORA_ACT_GELU_TANH; }
 
+// No output of the pair is another's buffer, or x's (tiles of x are read while
+// others' outputs are written).
+static bool apart(const void *x, const void *h, const void *gate, const void *up) {
+    return h != x && !(gate && (gate == up || gate == x || up == x || gate == h || up == h));
+}
+
 // Segments (where the mode uses them) and both slices' rank vectors, then the
 // pair.  c holds everything but ids' order, v and the partials.
 static lora_status_t run_gated(gated_call &c, lora_mode_t mode, uint32_t flags, const ws_layout &L, void *ws,
@@ -643,6 +649,7 @@ lora_status_t lora_gated_forward(const void *x, const void *W_gate, const void *
     ws_layout L;
     st = check_ws(ws, ws_bytes, T, pools[0].n_slots, 2 * pools[0].max_rank, &L);
     if (st != LORA_OK || T == 0) return st;
+    if (!apart(x, h, gate, up)) return LORA_ERR_INVALID_ARGUMENT;
     gated_call c{};
     c.x = x;
     c.W[0] = W_gate;
@@ -675,6 +682,7 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
     ws_layout L;
     st = check_ws_fp8(ws, ws_bytes, T, pools[0].n_slots, 2 * pools[0].max_rank, xq ? 0 : pools[0].d_in, &L);
     if (st != LORA_OK || T == 0) return st;
+    if (!apart(x, h, gate, up)) return LORA_ERR_INVALID_ARGUMENT;
     const hipStream_t s = hs(stream);
     if (!xq) {
         uint8_t *q = ws_ptr<uint8_t>(ws, L.xq);
@@ -736,6 +744,10 @@ lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void 
         }
         return st;
     }
+    if (dx && (dx == x || dx == gate || dx == up || dx == dh)) return LORA_ERR_INVALID_ARGUMENT;
+    if (dA && (dA[0] == dA[1] || dB[0] == dB[1] || dA[0] == dB[0] || dA[0] == dB[1] || dA[1] == dB[0] ||
+               dA[1] == dB[1] || dx == dA[0] || dx == dA[1] || dx == dB[0] || dx == dB[1]))
+        return LORA_ERR_INVALID_ARGUMENT;
     gated_bwd_call c{x, {W_gate, W_up}, gate, up, dh, dx, {nullptr, nullptr}, {nullptr, nullptr}, T, (int32_t)act,
                      pools, ids, ws, ws_bytes};
     for (int i = 0; i < 2 && dA; ++i) {

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256) k_shrink_pair(const typename elem<DT>::T 
     constexpr int VN = vec16<DT>::n, U = 8;
     const int lane = threadIdx.x & 63;
     const int groups = 2 * R / kPairRanks;                // per row; R is a multiple of 8
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t item = grid_index() * 4 + (threadIdx.x >> 6);
     const int64_t t = item / groups;
     if (t >= T) return;
     const int j2 = (int)(item - t * groups) * kPairRanks, m = j2 >= R, j0 = j2 - m * R;
@@ -251,7 +251,7 @@ lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *p,
                                  int32_t *err, hipStream_t s) {
     const pair_pools pp = make_pair_pools(p);
     const int64_t items = (int64_t)T * (2 * p[0].max_rank / kPairRanks);
-    const dim3 grid((uint32_t)((items + 3) / 4));
+    const dim3 grid = grid_of((items + 3) / 4);
     if (p[0].dtype == LORA_F32)
         hipLaunchKernelGGL(k_shrink_pair<LORA_F32>, grid, dim3(256), 0, s, (const float *)x, T, p[0].d_in, pp,
                            p[0].n_slots, p[0].max_rank, ids, v, err);

@@ -25,7 +25,8 @@ template <bool FINE> __device__ __forceinline__ void act_both(int act, float x, 
     } else {
         const float q = logistic<FINE>(kGeluTanhK * fmaf(kGeluTanhC * x * x, x, x));
         a = x * q;
-        da = fmaf(a * (1.0f - q), kGeluTanhK * fmaf(3.0f * kGeluTanhC * x, x, 1.0f), q);
+        // q is 0 or 1 long before x^2 overflows, where 0 times its slope is 0
+        da = fmaf(a * (1.0f - q), kGeluTanhK * fmaf(3.0f * kGeluTanhC, fminf(x * x, 1e30f), 1.0f), q);
     }
 }
 
@@ -63,7 +64,9 @@ __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>:
                                                         int32_t N, pair_pools pp, int32_t n_slots, int32_t R,
                                                         const int32_t *ids, float *dv) {
     typedef typename elem<DT>::T E;
-    const int t = blockIdx.x, m = blockIdx.y;
+    const int64_t wg = grid_index();
+    if (wg >= 2ll * T) return;
+    const int t = (int)(wg >> 1), m = (int)(wg & 1);
     float *out = dv + (int64_t)t * 2 * R + m * R;
     const int32_t id = ids[t];
     const int32_t r = id >= 0 && id < n_slots ? min(pp.rank[m][id], R) : 0;
@@ -740,10 +743,11 @@ __global__ void __launch_bounds__(256) k_seg_outer_f32(outer_f32_args g, pair_po
     constexpr int J = 16, U = 8, CH = 64;
     __shared__ __attribute__((aligned(16))) float s_p[CH][J];
     __shared__ int32_t s_row[CH];
-    const int n_a = 2 * g.n_slots * g.tiles_k;
-    const bool is_a = (int)blockIdx.x < n_a;
+    const int64_t wg = grid_index(), n_a = 2ll * g.n_slots * g.tiles_k;
+    const bool is_a = wg < n_a;
     const int tiles = is_a ? g.tiles_k : g.tiles_f;
-    int item = is_a ? blockIdx.x : blockIdx.x - n_a;
+    int item = (int)(is_a ? wg : wg - n_a);
+    if (!is_a && item >= 2 * g.n_slots * tiles) return;
     const int tile = item % tiles;
     item /= tiles;
     const int m = item & 1, slot = item >> 1;
@@ -895,11 +899,12 @@ template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_m
     __shared__ __attribute__((aligned(1024))) uint16_t smem[LA > LB ? LA : LB];
     __shared__ int32_t s_row[kOuterRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n_a = g.n_slots * g.tiles_k;
-    const bool is_a = (int)blockIdx.x < n_a;
-    int item = is_a ? blockIdx.x : blockIdx.x - n_a;
+    const int64_t wg = grid_index(), n_a = (int64_t)g.n_slots * g.tiles_k;
+    const bool is_a = wg < n_a;
+    int item = (int)(is_a ? wg : wg - n_a);
     const int tiles = is_a ? g.tiles_k : 2 * g.tiles_n;
     const int slot = item / tiles;
+    if (slot >= g.n_slots) return;
     item -= slot * tiles;
     const int m = !is_a && item >= g.tiles_n, tile = item - m * g.tiles_n;
     const int n0 = tile * kOuterCols, N = is_a ? g.K : g.N;
@@ -1008,7 +1013,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     uint16_t *vt = ws_ptr<uint16_t>(ws, B.vt);
     int32_t *slot_blk = ws_ptr<int32_t>(ws, B.slot_blk);
     if constexpr (DT == LORA_F32) {
-        hipLaunchKernelGGL(k_rank_grad_rows<DT>, dim3(T, 2), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R,
+        hipLaunchKernelGGL(k_rank_grad_rows<DT>, grid_of(2ll * T), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R,
                            c.ids, dv);
     } else {
         // about 1024 workgroups with work, of at least 512 columns
@@ -1082,7 +1087,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         seg_outer_args g{(const uint16_t *)c.x, (const uint16_t *)dg, vt,
                          {(uint16_t *)c.dA[0], (uint16_t *)c.dA[1]}, {(uint16_t *)c.dB[0], (uint16_t *)c.dB[1]},
                          T, K, F, R, S, Tp, perm, offsets, {p[0].rank, p[1].rank}, slot_blk, ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
-        const dim3 grid((uint32_t)S * (g.tiles_k + 2 * g.tiles_n));
+        const dim3 grid = grid_of((int64_t)S * (g.tiles_k + 2 * g.tiles_n));
         switch ((R + 15) / 16) {
             case 1: hipLaunchKernelGGL((k_seg_outer_mfma<1, 1>), grid, dim3(256), 0, s, g); break;
             case 2: hipLaunchKernelGGL((k_seg_outer_mfma<2, 1>), grid, dim3(256), 0, s, g); break;
@@ -1093,7 +1098,7 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         const outer_f32_args g{(const float *)c.x, (const float *)dg, (const float *)du, v, dv,
                                (float *)c.dA[0], (float *)c.dA[1], (float *)c.dB[0], (float *)c.dB[1],
                                offsets, perm, T, K, F, R, S, ceil_div(K, 256), ceil_div(F, 256)};
-        hipLaunchKernelGGL(k_seg_outer_f32, dim3((uint32_t)(2 * S) * (g.tiles_k + g.tiles_f)), dim3(256), 0, s, g, pp);
+        hipLaunchKernelGGL(k_seg_outer_f32, grid_of(2ll * S * (g.tiles_k + g.tiles_f)), dim3(256), 0, s, g, pp);
     }
     return hip_status(hipGetLastError());
 }

@@ -198,7 +198,8 @@ __device__ __forceinline__ int32_t tile_rank(int32_t key, int32_t nb, int32_t *c
     __syncthreads();
     for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
         if (w == wave && same) {
-            rank += count[key];                           // read by all lanes before the first adds
+            rank += count[key];
+            __builtin_amdgcn_wave_barrier();              // all lanes have read before the first of a key adds
             if (first) count[key] += __popcll(same);
         }
         __syncthreads();

@@ -142,3 +142,26 @@ def test_the_binding_refuses_tensors_the_kernels_would_misread():
         with pytest.raises(L.LoraError) as e:
             call()
         assert e.value.status == INVALID
+
+
+def test_outputs_are_buffers_of_their_own(lib):
+    """An output that is another's buffer, or an input's that is still read."""
+    a = [FAKE + (i << 20) for i in range(12)]
+    x, wg, wu, h, g, u, ids, ws = a[:8]
+    n = L.lora_workspace_bytes_gated_fp8(8, 4, 16, 64, 0)
+    for bx, bh, bg, bu in ((h, h, None, None), (x, h, g, g), (x, h, x, u), (x, h, g, x), (x, h, h, u), (x, h, g, h)):
+        assert lib.lora_gated_forward(bx, wg, wu, bh, bg, bu, 8, pools(), ids, 0, 0, 0, ws, n, None) == INVALID
+        assert lib.lora_gated_forward_fp8(bx, None, None, wg, wg, wu, wu, bh, bg, bu, 8, pools(), ids, 0, 0, 0, ws, n,
+                                          None) == INVALID
+    n = L.lora_workspace_bytes_gated_backward(8, 4, 16, 64, 96, L.LORA_BF16)
+    dx, d0, d1, d2 = a[8:]
+    d3 = FAKE + (12 << 20)
+
+    def back(dx, dA, dB):
+        return lib.lora_gated_backward(x, wg, wu, 8, pools(), ids, 0, g, u, h, dx, (ctypes.c_void_p * 2)(*dA),
+                                       (ctypes.c_void_p * 2)(*dB), ws, n, None)
+
+    for bad in (x, g, u, h, d0, d1, d2, d3):
+        assert back(bad, (d0, d1), (d2, d3)) == INVALID
+    for dA, dB in (((d0, d0), (d2, d3)), ((d0, d1), (d2, d2)), ((d0, d1), (d0, d3)), ((d0, d1), (d2, d1))):
+        assert back(dx, dA, dB) == INVALID

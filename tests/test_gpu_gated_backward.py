@@ -263,3 +263,27 @@ def test_a_nan_adapter_stays_with_its_rows(what):
             for m in range(2):
                 assert torch.equal(got[1][m][[0, 2, 3]], clean[1][m][[0, 2, 3]])
                 assert torch.equal(got[2][m][[0, 2, 3]], clean[2][m][[0, 2, 3]])
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gates_far_from_zero(act, dtype):
+    """Where the activation is 0 or its argument, its slope is 0 or 1, also where the argument's square overflows."""
+    p = Pair(6, 64, 72, [8, 3], 8, dtype, seed=3, ids=[-1] * 6)
+    gate, up, dh = kept(p)
+    big = [60.0, -60.0, 1e15, -1e15, 3e38, -3e38]
+    for t, f in enumerate(big):
+        gate[t] = f
+    dh[:] = dh * 2.0 ** -40
+    dx, _, _, _ = run_backward(p, act, gate, up, dh)
+    for t, f in enumerate(big):
+        # slope 1, act(g) = g; or both 0 (silu at -60: 60 exp(-60) < 2^-80, below every bound here)
+        dg = dh[t].double() * up[t].double() * (f > 0)
+        du = dh[t].double() * gate[t].double() * (f > 0)
+        half = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+        Wg, Wu = p.W[0].double(), p.W[1].double()
+        size = dg.abs() @ Wg.t().abs() + du.abs() @ Wu.t().abs()
+        ref = dg @ Wg.t() + du @ Wu.t()
+        # dg and du: 4 fp32 steps and one rounding; 2 f sums of one step; dx rounded
+        tol = (half + (2 * p.f + 12) * 2.0 ** -23) * size + half * ref.abs() * (1 + half) + 2.0 ** -110
+        within(dx[t], ref, tol, "%s gate %g" % (act, f))
