@@ -79,34 +79,57 @@ __device__ __forceinline__ row_slot load_row_slot(const gemm_args &g, int32_t id
     return r;
 }
 
-// One projection's low-rank terms for kernels at their register limit: one
-// block and one adapter at a time, nothing held for the next.
-template <int RB, int CB, int ST, int OF>
-__device__ __forceinline__ void lora_pass_lean(const gemm_args &g, const gemm_slice &sl, f32x16_t (&acc)[RB][CB * ST],
-                                               const int32_t *s_t, const int32_t *s_id, int wrow0, int wcol0,
+// One projection's (M: gate's or up's) low-rank terms for kernels at their
+// register limit.  The blocks' first adapters and ranks are loaded together,
+// what is left of them one step at a time; a row's rank, place and scale come
+// from LDS (a lookup in the pool would be one more trip to memory per adapter).
+template <int RB, int CB, int M>
+__device__ __forceinline__ void lora_pass_lean(const gemm_args &g, f32x16_t (&acc)[RB][CB * 2], const int32_t *s_t,
+                                               const int32_t *s_id, const row_slot *s_slot, int wrow0, int wcol0,
                                                int lane) {
     gemm_args q = g;
-    q.b = sl.b;
-    q.v = g.v + sl.v_off;
+    q.b = g.sl[M].b;
+    q.v = g.v + g.sl[M].v_off;
+    const int half = lane >> 5;
+    float4 v0[RB], v1[RB];
+    uint4 bq[RB][CB];
+    uint32_t rest[RB];
+    auto first_of = [&](int rb, uint32_t pend, int32_t &a, int32_t &ra, int32_t &ro, float &sa, uint32_t &rows) {
+        const int row0 = wrow0 + rb * 32, f = __ffs((int)pend) - 1;
+        a = uniform_i(s_id[row0 + f]);
+        ra = uniform_i(s_slot[row0 + f].rank[M]);
+        ro = uniform_i(s_slot[row0 + f].row0[M]);
+        sa = __int_as_float(uniform_i(__float_as_int(s_slot[row0 + f].scale[M])));
+        rows = (uint32_t)__ballot(s_id[row0 + (lane & 31)] == a);
+    };
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int row = wrow0 + rb * 32 + (lane & 31);
-        const int32_t my_id = s_id[row], my_t = s_t[row];
-        const uint32_t live = (uint32_t)__ballot(my_t >= 0);
-        uint32_t pend = (uint32_t)__ballot(my_id >= 0);
-        while (pend) {
-            const int32_t a = uniform_i(__shfl(my_id, __ffs((int)pend) - 1, 64));
-            const uint32_t rows = (uint32_t)__ballot(my_id == a);
-            pend &= ~rows;
-            const int32_t ra = sl.rank[a], ro = sl.row0 ? sl.row0[a] : a * g.max_rank;
-            const float sa = sl.scale[a];
+        rest[rb] = (uint32_t)__ballot(s_id[row] >= 0);
+        if (!rest[rb]) continue;
+        int32_t a, ra, ro;
+        float sa;
+        uint32_t rows;
+        first_of(rb, rest[rb], a, ra, ro, sa, rows);
+        lora_step_load<CB>(q, a, ra, ro, s_id[row] == a, s_t[row], 0, half, wcol0, lane, v0[rb], v1[rb], bq[rb]);
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int row = wrow0 + rb * 32 + (lane & 31);
+        const uint32_t live = (uint32_t)__ballot(s_t[row] >= 0);
+        for (uint32_t pend = rest[rb]; pend;) {
+            int32_t a, ra, ro;
+            float sa;
+            uint32_t rows;
+            first_of(rb, pend, a, ra, ro, sa, rows);
+            const bool mine = (rows >> (lane & 31)) & 1u;
             for (int ks = 0; ks * 16 < ra; ++ks) {
-                float4 v0, v1;
-                uint4 bq[CB];
-                lora_step_load<CB>(q, a, ra, ro, my_id == a, my_t, ks, lane >> 5, wcol0, lane, v0, v1, bq);
-                lora_step_mfma<CB, ST, OF>(acc[rb], sa, my_id == a && 16 * ks + 8 * (lane >> 5) < ra, v0, v1, bq,
-                                           (live & ~rows) != 0, rows);
+                if (ks > 0 || pend != rest[rb])
+                    lora_step_load<CB>(q, a, ra, ro, mine, s_t[row], ks, half, wcol0, lane, v0[rb], v1[rb], bq[rb]);
+                lora_step_mfma<CB, 2, M>(acc[rb], sa, mine && 16 * ks + 8 * half < ra, v0[rb], v1[rb], bq[rb],
+                                         (live & ~rows) != 0, rows);
             }
+            pend &= ~rows;
         }
     }
 }
@@ -131,29 +154,41 @@ __device__ __forceinline__ void gated_lora_pass(const gemm_args &g, f32x16_t (&a
     lora_pass_impl<RB, CB / 2, RG, KB, RF, 2, 1, true>(q, acc, s_t, s_id, 0, wrow0, col0, lane);
 }
 
-// Both low-rank terms of 8 columns of one row: o[m] += s sum_j v[j]
-// B[j][n..n+8], rank octets in order, both projections' loads of an octet in
-// flight together.
-__device__ __forceinline__ void add_low_rank8(const gemm_args &g, const row_slot &rs, int64_t t, int n,
-                                              float (&o)[2][8]) {
+// 4 fp32 values, zeros where not ok.  (A branch, not a choice between two
+// values in memory, which would put the zeros and the result there.)
+__device__ __forceinline__ f32x4_t load4(bool ok, const float *p) {
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (ok) v = *reinterpret_cast<const f32x4_t *>(p);
+    return v;
+}
+
+// Both low-rank sums of one row, d[m][q] = sum_j v[j] B[j][n] of the 8 columns
+// n = n0 + ST q below N: rank octets in order, both projections' loads of an octet
+// in flight together.  ST is the number of lanes that share a row, so that
+// neighbours read neighbouring columns (16 bytes each; a lane with 8
+// neighbouring columns would touch a cache line of its own with every load:
+// 2240 rows of which 192 single, FP8 4096 x 14336: 463 us).
+template <int ST>
+__device__ __forceinline__ void low_rank8(const gemm_args &g, const row_slot &rs, int64_t t, int n0,
+                                          float (&d)[2][8]) {
     const int oct = (max(rs.rank[0], rs.rank[1]) + 7) >> 3;
-    if (oct <= 0) return;
-    float d[2][8] = {};
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d[m][q] = 0.0f;
     for (int gg = 0; gg < oct; ++gg) {
-        float vv[2][8];
+        f32x4_t vv[2][2];
         uint4 bq[2][8];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const bool in = 8 * gg < rs.rank[m];
             const float *vrow = g.v + t * g.v_stride + g.sl[m].v_off + gg * 8;
-            const uint16_t *b = g.sl[m].b + ((int64_t)rs.row0[m] + 8 * gg) * g.N + (int64_t)n * 8;
+            const uint16_t *b = g.sl[m].b + ((int64_t)rs.row0[m] + 8 * gg) * g.N + (int64_t)n0 * 8;
+            vv[m][0] = load4(in, vrow);
+            vv[m][1] = load4(in, vrow + 4);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float4 f = in ? *reinterpret_cast<const float4 *>(vrow + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                vv[m][4 * q] = f.x; vv[m][4 * q + 1] = f.y; vv[m][4 * q + 2] = f.z; vv[m][4 * q + 3] = f.w;
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) bq[m][q] = in ? ldg16(b + q * 8) : make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < 8; ++q)
+                bq[m][q] = in && n0 + ST * q < g.N ? ldg16(b + ST * q * 8) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -162,13 +197,9 @@ __device__ __forceinline__ void add_low_rank8(const gemm_args &g, const row_slot
                 float bf[8];
                 vec16<LORA_BF16>::widen(bq[m][q], bf);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[m][q] = fmaf(vv[m][e], bf[e], d[m][q]);
+                for (int e = 0; e < 8; ++e) d[m][q] = fmaf(vv[m][e >> 2][e & 3], bf[e], d[m][q]);
             }
     }
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[m][q] = fmaf(rs.scale[m], d[m][q], o[m][q]);
 }
 
 // 8 columns of one row: gate and up stored where they are kept, and h.
@@ -195,16 +226,17 @@ constexpr int kBlockAdapters = 4;
 __device__ __forceinline__ void set_row(const gemm_args &g, int32_t id, bool per_row, int32_t &s_id, row_slot &s_slot) {
     const bool apart = per_row || many_adapters(id, kBlockAdapters);
     s_id = apart ? -1 : id;
-    s_slot = load_row_slot(g, apart ? id : -1);
+    s_slot = load_row_slot(g, id);
 }
 
 // The store of a whole tile: the fp32 sums of WR * 32 rows at a time go
-// through LDS, and a thread then owns 8 neighbouring columns of gate, up and
-// h of one row (16-byte stores, one rounding each), to which it adds the
-// row's low-rank terms if they are not in the sums.
+// through LDS, where the terms of rows that are not in the sums yet are added,
+// and a thread then owns 8 neighbouring columns of gate, up and h of one row
+// (16-byte stores, one rounding each).
 template <int BM, int BN, int WV, int WR, int RB, int CB>
 __device__ __forceinline__ void gated_store_tile(const gemm_args &g, f32x16_t (&acc)[RB][CB], float *smem_f,
-                                                 const int32_t *s_t, const row_slot *s_slot, int n0, int w, int lane) {
+                                                 const int32_t *s_t, const int32_t *s_id, const row_slot *s_slot, int n0,
+                                                 int w, int lane) {
     constexpr int WM = BM / WR, WN = BN / (WV / WR), SLD = BN + 4, CPR = BN / 16, ITEMS = WR * 32 * CPR;
     const int wm = w / (WV / WR), wn = w % (WV / WR), tid = w * 64 + lane;
 #pragma unroll
@@ -218,6 +250,21 @@ __device__ __forceinline__ void gated_store_tile(const gemm_args &g, f32x16_t (&
                     acc[rb][cb][e];
         __syncthreads();
         for (int i = tid; i < ITEMS; i += WV * 64) {
+            const int r = i / CPR, c = i % CPR, row = (r >> 5) * WM + rb * 32 + (r & 31);
+            if (s_t[row] < 0 || s_id[row] >= 0 || max(s_slot[row].rank[0], s_slot[row].rank[1]) <= 0) continue;
+            float d[2][8];
+            low_rank8<CPR>(g, s_slot[row], s_t[row], gated_col(n0) + c, d);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int cc = c + CPR * q;
+                    float *at = smem_f + r * SLD + (cc >> 5) * 64 + (cc & 31) + 32 * m;
+                    *at = fmaf(s_slot[row].scale[m], d[m][q], *at);
+                }
+        }
+        __syncthreads();
+        for (int i = tid; i < ITEMS; i += WV * 64) {
             const int r = i / CPR, c = (i % CPR) * 8, row = (r >> 5) * WM + rb * 32 + (r & 31);
             const int32_t t = s_t[row];
             const int n = gated_col(n0) + c;
@@ -229,7 +276,6 @@ __device__ __forceinline__ void gated_store_tile(const gemm_args &g, f32x16_t (&
                 *reinterpret_cast<float4 *>(o[m]) = *reinterpret_cast<const float4 *>(src + 32 * m);
                 *reinterpret_cast<float4 *>(o[m] + 4) = *reinterpret_cast<const float4 *>(src + 32 * m + 4);
             }
-            add_low_rank8(g, s_slot[row], t, n, o);
             gated_finish8(g, t, n, o);
         }
     }
@@ -259,10 +305,20 @@ __global__ void __launch_bounds__(256) k_gated_reduce(gemm_args g) {
     grouped_tile(g.tile_base + tidx, g.n_tiles_m, g.n_tiles_n, g.col_strips, tm, tn);
     const int r = chunk * RW + threadIdx.x / CPR, c = (threadIdx.x % CPR) * 8;
     const int p = tm * BM + r, n = tn * HN + c;
-    if (p >= g.T || n >= g.N) return;
-    const int32_t t = perm_row(g.perm, p, g.T);
-    if (t < 0) return;
-    const row_slot rs = load_row_slot(g, g.ids[t]);
+    __shared__ float s_d[2][RW][HN];                      // the rows' low-rank sums
+    const int32_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
+    const row_slot rs = load_row_slot(g, t >= 0 ? g.ids[t] : -1);
+    const int lr = threadIdx.x / CPR, lc = threadIdx.x % CPR;
+    {
+        float d[2][8];
+        low_rank8<CPR>(g, rs, t, tn * HN + lc, d);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s_d[m][lr][lc + CPR * q] = d[m][q];
+    }
+    __syncthreads();
+    if (t < 0 || n >= g.N) return;
     const int cg = (c >> 5) * 64 + (c & 31);              // gate's column of the partial tile; up's is 32 on
     float o[2][8] = {};
     const float *src = g.partial + ((int64_t)tidx * g.splits * BM + r) * BN + cg;
@@ -275,21 +331,16 @@ __global__ void __launch_bounds__(256) k_gated_reduce(gemm_args g) {
             o[m][4] += b.x; o[m][5] += b.y; o[m][6] += b.z; o[m][7] += b.w;
         }
     }
-    add_low_rank8(g, rs, t, n, o);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[m][q] = fmaf(rs.scale[m], s_d[m][lr][c + q], o[m][q]);
     gated_finish8(g, t, n, o);
 }
 
 template <int BM, int BN> static void launch_gated_reduce(const gemm_args &g, hipStream_t s) {
     constexpr int RW = 256 / (BN / 16);
     hipLaunchKernelGGL((k_gated_reduce<BM, BN>), dim3(g.n_tiles * (BM / RW)), dim3(256), 0, s, g);
-}
-
-// 4 fp32 values, zeros where not ok.  (A branch, not a choice between two
-// values in memory, which would put the zeros and the result there.)
-__device__ __forceinline__ f32x4_t load4(bool ok, const float *p) {
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    if (ok) v = *reinterpret_cast<const f32x4_t *>(p);
-    return v;
 }
 
 // Workgroup b's tile and K range in the fp32 kernels: each XCD takes a

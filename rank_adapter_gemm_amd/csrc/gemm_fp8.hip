@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     // the first stages load (split-K tiles leave it to the reduction).
     if constexpr (GATED && LORA && !SPLIT)
     {
-        lora_pass_lean<RB, CB / 2, 2, 0>(g, g.sl[0], acc, s_meta_t, s_meta_id, wm * WM, gated_col(n0 + wn * WN), lane);
-        lora_pass_lean<RB, CB / 2, 2, 1>(g, g.sl[1], acc, s_meta_t, s_meta_id, wm * WM, gated_col(n0 + wn * WN), lane);
+        lora_pass_lean<RB, CB / 2, 0>(g, acc, s_meta_t, s_meta_id, s_slot, wm * WM, gated_col(n0 + wn * WN), lane);
+        lora_pass_lean<RB, CB / 2, 1>(g, acc, s_meta_t, s_meta_id, s_slot, wm * WM, gated_col(n0 + wn * WN), lane);
     }
     else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 4 ? RB : 1), 1, 0>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN, lane);
@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     __syncthreads();
 
     if constexpr (GATED && !SPLIT)
-        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_slot, n0, w, lane);
+        gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_meta_id, s_slot, n0, w,
+                                         lane);
     else if constexpr (GATED)
         gated_store_partial<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), n0, w, lane, tidx, split);
     else
