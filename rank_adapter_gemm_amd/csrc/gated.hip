@@ -40,24 +40,28 @@ __device__ __forceinline__ row_slot load_row_slot(const gated_f32_args &g, int64
     return r;
 }
 
-// 4 columns of one row from both projections' sums; an octet's loads of both
-// projections are in flight together.
-__device__ __forceinline__ void gated_finish4(const gated_f32_args &g, const row_slot &rs, int64_t t, int n,
-                                              float (&o)[2][4]) {
+// Both low-rank sums of a row's columns n = n0 + 16 q (16 lanes share a row
+// and read neighbouring columns); an octet's loads of both projections are in
+// flight together.
+__device__ __forceinline__ void low_rank4(const gated_f32_args &g, const row_slot &rs, int64_t t, int n0,
+                                          float (&d)[2][4]) {
     const int oct = (max(rs.rank[0], rs.rank[1]) + 7) >> 3;
-    float d[2][4] = {};
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[m][q] = 0.0f;
     for (int gg = 0; gg < oct; ++gg) {
         f32x4_t vv[2][2], bb[2][4][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const bool in = 8 * gg < rs.rank[m];
-            const float *b = g.b[m] + (((int64_t)rs.row0[m] + 8 * gg) * g.N + (int64_t)n * 8);
+            const float *b = g.b[m] + (((int64_t)rs.row0[m] + 8 * gg) * g.N + (int64_t)n0 * 8);
             const float *vt = g.v + t * 2 * g.max_rank + m * g.max_rank + 8 * gg;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 vv[m][h] = load4(in, vt + 4 * h);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) bb[m][q][h] = load4(in, b + 8 * q + 4 * h);
+                for (int q = 0; q < 4; ++q) bb[m][q][h] = load4(in && n0 + 16 * q < g.N, b + 16 * q * 8 + 4 * h);
             }
         }
 #pragma unroll
@@ -67,10 +71,10 @@ __device__ __forceinline__ void gated_finish4(const gated_f32_args &g, const row
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[m][q] = fmaf(vv[m][e >> 2][e & 3], bb[m][q][e >> 2][e & 3], d[m][q]);
     }
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[m][q] = fmaf(rs.scale[m], d[m][q], o[m][q]);
+}
+
+// 4 neighbouring columns of one row from both projections' sums o.
+__device__ __forceinline__ void gated_finish4(const gated_f32_args &g, int64_t t, int n, const float (&o)[2][4]) {
     const int64_t at = t * g.N + n;
     float4 h;
     h.x = act_value<true>(g.act, o[0][0]) * o[1][0];
@@ -152,6 +156,21 @@ template <bool SPLIT> __global__ void __launch_bounds__(256, 2) k_gated_f32(gate
     if (SPLIT) return;
     __syncthreads();
     for (int i = tid; i < 32 * 16; i += 256) {
+        const int r = i >> 4, c = i & 15;
+        const int64_t t = m0 + r < T ? perm_row(g.perm, m0 + r, T) : -1;
+        if (t < 0 || max(s_slot[r].rank[0], s_slot[r].rank[1]) <= 0) continue;
+        float d[2][4];
+        low_rank4(g, s_slot[r], t, n0 + c, d);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float *at = smem + r * WS + 64 * m + c + 16 * q;
+                *at = fmaf(s_slot[r].scale[m], d[m][q], *at);
+            }
+    }
+    __syncthreads();
+    for (int i = tid; i < 32 * 16; i += 256) {
         const int r = i >> 4, c = (i & 15) * 4, n = n0 + c;
         const int64_t t = m0 + r < T ? perm_row(g.perm, m0 + r, T) : -1;
         if (t < 0 || n >= N) continue;
@@ -159,7 +178,7 @@ template <bool SPLIT> __global__ void __launch_bounds__(256, 2) k_gated_f32(gate
 #pragma unroll
         for (int m = 0; m < 2; ++m)
             *reinterpret_cast<float4 *>(o[m]) = *reinterpret_cast<const float4 *>(smem + r * WS + 64 * m + c);
-        gated_finish4(g, s_slot[r], t, n, o);
+        gated_finish4(g, t, n, o);
     }
 }
 
@@ -168,8 +187,18 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
     const int tile = blockIdx.x >> 1, r = (blockIdx.x & 1) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
     const int p = tile / g.n_tiles_n * 32 + r, n = tile % g.n_tiles_n * 64 + c;
     const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
-    if (t < 0 || n >= g.N) return;
     const row_slot rs = load_row_slot(g, t);
+    __shared__ float s_d[2][16][64];                      // the rows' low-rank sums
+    {
+        float d[2][4];
+        low_rank4(g, rs, t, tile % g.n_tiles_n * 64 + (threadIdx.x & 15), d);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s_d[m][threadIdx.x >> 4][(threadIdx.x & 15) + 16 * q] = d[m][q];
+    }
+    __syncthreads();
+    if (t < 0 || n >= g.N) return;
     float o[2][4] = {};
     const float *part = g.partial + (int64_t)tile * g.splits * 32 * 128 + r * 128 + c;
     for (int s = 0; s < g.splits; ++s, part += 32 * 128)
@@ -178,7 +207,11 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
             const float4 f = *reinterpret_cast<const float4 *>(part + 64 * m);
             o[m][0] += f.x; o[m][1] += f.y; o[m][2] += f.z; o[m][3] += f.w;
         }
-    gated_finish4(g, rs, t, n, o);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[m][q] = fmaf(rs.scale[m], s_d[m][threadIdx.x >> 4][c + q], o[m][q]);
+    gated_finish4(g, t, n, o);
 }
 
 // ---------------------------------------------------------------------------

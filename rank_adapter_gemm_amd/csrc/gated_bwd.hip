@@ -347,7 +347,7 @@ struct nt_args {
 // the first piece of each tile where the adapters have 64 rows or more on
 // average, else row by row in the reduction.  (2048 rows of 4 adapters, 8B
 // sizes: pieces and reduction 475 us against 511 row by row; 777 rows of 24
-// adapters of up to 40 ranks, 1048 x 2744: 80 against 62.)
+// adapters of up to 40 ranks, 1048 x 2744: 80 against 50.)
 __device__ __forceinline__ bool term_in_reduction(const gemm_args &g, const nt_args &nt) {
     return (int64_t)*nt.n_seg * 64 > g.T;
 }
@@ -512,30 +512,29 @@ template <int BM, int BN> __global__ void __launch_bounds__(256) k_nt_reduce(gem
     grouped_tile(g.tile_base + tidx, g.n_tiles_m, g.n_tiles_n, g.col_strips, tm, tn);
     const int r = chunk * RW + threadIdx.x / CPR, c = (threadIdx.x % CPR) * 8;
     const int p = tm * BM + r, n = tn * BN + c;
-    const int64_t t = p < g.T && n < g.N ? perm_row(g.perm, p, g.T) : -1;
-    if (t < 0) return;
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const float *src = g.partial + ((int64_t)tidx * g.splits * BM + r) * BN + c;
-    for (int s = 0; s < g.splits; ++s, src += BM * BN) {
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-        o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
-        o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
-    }
-    const int32_t id = g.ids[t];
-    if (term_in_reduction(g, nt) && id >= 0 && id < g.n_slots) {
-        const int32_t rk = g.rank[id];
-        const float *vrow = g.v + t * g.v_stride;
-        const uint16_t *b = g.b + (int64_t)g.row0[id] * g.N + (int64_t)n * 8;
+    const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
+    // The low-rank sums: the row's threads read neighbouring columns of the
+    // octets (16 bytes each), and hand them over in LDS.
+    __shared__ float s_d[RW][BN];
+    if (term_in_reduction(g, nt)) {                        // (uniform)
+        const int32_t id = t >= 0 ? g.ids[t] : -1;
+        const int32_t rk = id >= 0 && id < g.n_slots ? g.rank[id] : 0;
+        const int lr = threadIdx.x / CPR, lc = threadIdx.x % CPR, nc = tn * BN + lc;
+        float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const float *vrow = g.v + (t < 0 ? 0 : t) * g.v_stride;
+        const uint16_t *b = g.b + (rk > 0 ? (int64_t)g.row0[id] * g.N : 0) + (int64_t)nc * 8;
         // two octets at a time (rk is 2 max_rank, a multiple of 16)
         for (int j = 0; j < rk; j += 16, b += (int64_t)g.N * 16) {
-            float vv[2][8];
+            f32x4_t vv[2][2];
             uint4 bq[2][8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                *reinterpret_cast<float4 *>(vv[h]) = *reinterpret_cast<const float4 *>(vrow + j + 8 * h);
-                *reinterpret_cast<float4 *>(vv[h] + 4) = *reinterpret_cast<const float4 *>(vrow + j + 8 * h + 4);
+                vv[h][0] = *reinterpret_cast<const f32x4_t *>(vrow + j + 8 * h);
+                vv[h][1] = *reinterpret_cast<const f32x4_t *>(vrow + j + 8 * h + 4);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) bq[h][q] = ldg16(b + (int64_t)h * g.N * 8 + q * 8);
+                for (int q = 0; q < 8; ++q)
+                    bq[h][q] = nc + CPR * q < g.N ? ldg16(b + (int64_t)h * g.N * 8 + CPR * q * 8)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -544,10 +543,24 @@ template <int BM, int BN> __global__ void __launch_bounds__(256) k_nt_reduce(gem
                     float bf[8];
                     vec16<LORA_BF16>::widen(bq[h][q], bf);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[q] = fmaf(vv[h][e], bf[e], o[q]);
+                    for (int e = 0; e < 8; ++e) d[q] = fmaf(vv[h][e >> 2][e & 3], bf[e], d[q]);
                 }
         }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s_d[lr][lc + CPR * q] = d[q];
     }
+    __syncthreads();
+    if (t < 0 || n >= g.N) return;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const float *src = g.partial + ((int64_t)tidx * g.splits * BM + r) * BN + c;
+    for (int s = 0; s < g.splits; ++s, src += BM * BN) {
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+        o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
+        o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
+    }
+    if (term_in_reduction(g, nt))
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[q] += s_d[threadIdx.x / CPR][c + q];
     stg16(g.y + t * g.N + n, vec16<LORA_BF16>::narrow(o));
 }
 
