@@ -1,7 +1,7 @@
 // Backward pass of the gated pair h = act(g) * u, base weights frozen:
 //   dg = dh * u * act'(g),  du = dh * act(g)                        k_gated_dact
 //   dv = s_a dg B_a^T   [T, r] for each of the two                  k_rank_grad
-//   dx = dg Wg^T + du Wu^T + dv_g Ag_a^T + dv_u Au_a^T              k_gemm_nt / k_dx_f32
+//   dx = dg Wg^T + du Wu^T + dv_g Ag_a^T + dv_u Au_a^T              k_gemm_nt / dx_f32
 //   dA_a = sum over a's rows of x_t^T dv_t                          k_seg_outer
 //   dB_a = s_a sum over a's rows of v_t^T dg_t,  v = x A_a          k_seg_outer
 // Rows are visited in adapter order (the segment builder's perm), so every
@@ -236,6 +236,39 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
     }
 }
 
+// A of the batch's slots in rank octets, gate's ranks then up's: [segment][2R /
+// 8][d_in][8], with the tables (row0, rank, scale) that make them one pool of
+// max_rank 2R for the low-rank pass of the dx product.  dv holds the scales
+// already, so the table's are 1.  Octet o of 256 values of d_in of segment i.
+struct a_octets_args {
+    const int32_t *seg_id, *n_seg;
+    int32_t n_slots, K, R, k_blocks;
+    uint16_t *oct;
+    int32_t *row0, *rank;
+    float *scale;
+};
+
+__device__ __forceinline__ void a_octets(const a_octets_args &g, const pair_pools &pp, int i, int kb, int o) {
+    if (i >= min(*g.n_seg, g.n_slots)) return;
+    const int32_t id = g.seg_id[i], R = g.R;
+    if (id < 0 || id >= g.n_slots) return;
+    const int m = 8 * o >= R, j0 = 8 * o - m * R;
+    const int32_t r[2] = {min(pp.rank[0][id], R), min(pp.rank[1][id], R)};
+    if (kb == 0 && o == 0 && threadIdx.x == 0) {
+        g.row0[id] = i * 2 * R;
+        g.rank[id] = r[0] > 0 || r[1] > 0 ? 2 * R : 0;
+        g.scale[id] = 1.0f;
+    }
+    const int k = kb * 256 + threadIdx.x;
+    if (k >= g.K) return;
+    const uint16_t *a = (const uint16_t *)pp.a[m] + (slot_row0(pp.row0[m], id, R) + j0) * g.K + k;
+    uint32_t e[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) e[q] = j0 + q < (m ? r[1] : r[0]) ? a[(int64_t)q * g.K] : 0u;
+    stg16(g.oct + (((int64_t)i * 2 * R / 8 + o) * g.K + k) * 8,
+          make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16));
+}
+
 // The rank vectors as the products that follow read them.  dv, fp32 [T][2R]
 // in batch order: the partial sums added in split order, times the slot's
 // scale; zero for rows without an adapter.  vt, bf16 [2][2][2R][Tp]: s v and
@@ -244,8 +277,9 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
 // lo = bf16(f - hi): together within 2^-17 of f, far below the rounding of
 // the bf16 gradients they add up to).  Places past a segment's rows are
 // filled with zeros.  A workgroup: 32 positions of one work block and 8 ranks
-// (blockIdx.y), or 32 rows of the base block (grid.x from n_work on).  2048
-// rows: 7 us, latency.
+// (blockIdx.y), or 32 rows of the base block (grid.x from n_work on), or, from
+// first_octet on, A's octets, in the same launch because neither alone keeps
+// the chip busy.  2048 rows: 7 us, latency.
 struct rank_finish_args {
     const float *v, *part;
     int32_t n_split, T, R, n_slots, n_work, Tp;
@@ -253,11 +287,17 @@ struct rank_finish_args {
     float *dv;
     uint16_t *vt;
     int32_t *slot_blk;                 // [n_slots]: a segment's first work block, by its slot
+    int32_t first_octet;
 };
 
-__global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_pools pp) {
+__global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, a_octets_args oc, pair_pools pp) {
     constexpr int BR = kShrinkRows;
     const int R2 = 2 * g.R;
+    if ((int)blockIdx.x >= g.first_octet) {
+        const int item = (int)blockIdx.x - g.first_octet;
+        a_octets(oc, pp, item / oc.k_blocks, item % oc.k_blocks, blockIdx.y);
+        return;
+    }
     if ((int)blockIdx.x >= g.n_work) {
         if (blockIdx.y) return;
         const int p0 = ((int)blockIdx.x - g.n_work) * BR, pend = min(min(g.offsets[1], p0 + BR), g.T);
@@ -300,39 +340,6 @@ __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, pair_po
             o[0] = (uint16_t)hi;
             o[(int64_t)R2 * g.Tp] = (uint16_t)f32_to_bf16_bits(rest == rest ? rest : 0.0f);
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// A of the batch's slots in rank octets, gate's ranks then up's: [segment][2R /
-// 8][d_in][8], with the tables (row0, rank, scale) that make them one pool of
-// max_rank 2R for the low-rank pass of the dx product.  dv holds the scales
-// already, so the table's are 1.  Bound by latency (4 slots of 16 ranks, 4096
-// wide: 5 us).
-// ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) k_a_octets(pair_pools pp, const int32_t *seg_id, const int32_t *n_seg,
-                                                  int32_t n_slots, int32_t K, int32_t R, uint16_t *oct,
-                                                  int32_t *row0, int32_t *rank, float *scale) {
-    const int i = blockIdx.x;
-    if (i >= min(*n_seg, n_slots)) return;
-    const int32_t id = seg_id[i];
-    if (id < 0 || id >= n_slots) return;
-    const int32_t r[2] = {min(pp.rank[0][id], R), min(pp.rank[1][id], R)};
-    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
-        row0[id] = i * 2 * R;
-        rank[id] = r[0] > 0 || r[1] > 0 ? 2 * R : 0;
-        scale[id] = 1.0f;
-    }
-    const int k = blockIdx.y * 256 + threadIdx.x;
-    if (k >= K) return;
-    {
-        const int o = blockIdx.z, m = 8 * o >= R, j0 = 8 * o - m * R;
-        const uint16_t *a = (const uint16_t *)pp.a[m] + (slot_row0(pp.row0[m], id, R) + j0) * K + k;
-        uint32_t e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) e[q] = j0 + q < r[m] ? a[(int64_t)q * K] : 0u;
-        stg16(oct + (((int64_t)i * 2 * R / 8 + o) * K + k) * 8,
-              make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16));
     }
 }
 
@@ -613,7 +620,8 @@ static gemm_plan plan_dx(int T, int K, int N, size_t partial_bytes) {
 // dx, fp32: 64 x 64 tiles on v_mfma_f32_32x32x2_f32, the sum over dg's columns
 // then du's (each in whole steps of 32); grids of few tiles split the steps.
 // Threads that own 4 columns of a row then add the low-rank terms from A's rows.
-// (190 x 2768 x 520: 14 us and 11 for the reduction, both latency.)
+// (190 x 2768 x 520: 14 us and 11 for the reduction, both latency; see
+// k_dx_outer_f32.)
 // ---------------------------------------------------------------------------
 struct dx_f32_args {
     const float *a0, *a1, *w0, *w1;
@@ -650,13 +658,15 @@ __device__ __forceinline__ void dx_finish4(const dx_f32_args &g, const pair_pool
     *reinterpret_cast<float4 *>(g.dx + t * g.N + n) = make_float4(o[0], o[1], o[2], o[3]);
 }
 
-template <bool SPLIT> __global__ void __launch_bounds__(256, 2) k_dx_f32(dx_f32_args g, pair_pools pp) {
+// Workgroup b of n.
+template <bool SPLIT>
+__device__ __forceinline__ void dx_f32(const dx_f32_args &g, const pair_pools &pp, int b, int n) {
     constexpr int BK = 32, NS = 3, AST = 64 * BK, STAGE = 2 * AST, LD = 64 + 4, PER = 4;
     __shared__ __attribute__((aligned(1024))) float smem[NS * STAGE];     // stages: [64][BK] of each; sums: [64][LD]
     static_assert(64 * LD <= NS * STAGE, "the sums fit the stages' LDS");
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, wm = w >> 1, wn = w & 1;
     int tm, tn, split;
-    f32_tile(blockIdx.x, gridDim.x, (g.T + 63) / 64, SPLIT ? g.splits : 1, tm, tn, split);
+    f32_tile(b, n, (g.T + 63) / 64, SPLIT ? g.splits : 1, tm, tn, split);
     const int tile = tm * g.n_tiles_n + tn, m0 = tm * 64, n0 = tn * 64;
     const int Fp = (g.F + BK - 1) / BK * BK;
     const int k_begin = split * g.k_chunk, k_end = min(2 * Fp, k_begin + g.k_chunk);
@@ -761,11 +771,11 @@ struct outer_f32_args {
     int32_t T, K, F, R, n_slots, tiles_k, tiles_f;
 };
 
-__global__ void __launch_bounds__(256) k_seg_outer_f32(outer_f32_args g, pair_pools pp) {
+__device__ __forceinline__ void seg_outer_f32(const outer_f32_args &g, const pair_pools &pp, int64_t wg) {
     constexpr int J = 16, U = 8, CH = 64;
     __shared__ __attribute__((aligned(16))) float s_p[CH][J];
     __shared__ int32_t s_row[CH];
-    const int64_t wg = grid_index(), n_a = 2ll * g.n_slots * g.tiles_k;
+    const int64_t n_a = 2ll * g.n_slots * g.tiles_k;
     const bool is_a = wg < n_a;
     const int tiles = is_a ? g.tiles_k : g.tiles_f;
     int item = (int)(is_a ? wg : wg - n_a);
@@ -815,6 +825,16 @@ __global__ void __launch_bounds__(256) k_seg_outer_f32(outer_f32_args g, pair_po
             for (int e = 0; e < J; ++e)
                 if (j0 + e < R) out[(j0 + e) * j_stride] = j0 + e < r ? sc * acc[e] : 0.0f;
     }
+}
+
+// dx's tiles, then the adapters' gradients: neither needs the other, and
+// together they fill more of the chip (190 rows, 520 and 1384 wide: 17 us,
+// and 14 + 10 apart).
+template <bool SPLIT>
+__global__ void __launch_bounds__(256, 2) k_dx_outer_f32(dx_f32_args d, outer_f32_args o, pair_pools pp, int32_t n_dx) {
+    const int64_t wg = grid_index();
+    if (wg < n_dx) dx_f32<SPLIT>(d, pp, (int)wg, n_dx);
+    else seg_outer_f32(o, pp, wg - n_dx);
 }
 
 // bf16, on the matrix cores: out[j][n] = sum_t vt[j][t] q[t][n] over a slot's
@@ -1058,28 +1078,33 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
             case 3: hipLaunchKernelGGL(k_rank_grad<3>, grid, dim3(256), 0, s, g, pp); break;
             default: hipLaunchKernelGGL(k_rank_grad<4>, grid, dim3(256), 0, s, g, pp); break;
         }
-        rank_finish_args f{v, part, split, T, R, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
-                           g.blk_start, g.blk_seg, dv, vt, slot_blk};
-        hipLaunchKernelGGL(k_rank_finish, dim3(n_work + row_blocks, 2 * R / 8), dim3(256), 0, s, f, pp);
+        const int first_octet = n_work + row_blocks;
+        const rank_finish_args f{v, part, split, T, R, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
+                                 g.blk_start, g.blk_seg, dv, vt, slot_blk, first_octet};
+        const a_octets_args oc{g.seg_id, g.n_seg, S, K, R, ceil_div(K, 256), ws_ptr<uint16_t>(ws, B.oct),
+                               ws_ptr<int32_t>(ws, B.row0), ws_ptr<int32_t>(ws, B.rank), ws_ptr<float>(ws, B.scale)};
+        const int octets = c.dx ? (S < T ? S : T) * oc.k_blocks : 0;
+        hipLaunchKernelGGL(k_rank_finish, dim3(first_octet + octets, 2 * R / 8), dim3(256), 0, s, f, oc, pp);
     }
-    if (c.dx && DT == LORA_F32) {
+    if constexpr (DT == LORA_F32) {
         dx_f32_args g{(const float *)dg, (const float *)du, (const float *)c.W[0], (const float *)c.W[1],
                       (float *)c.dx, dv, c.ids, perm, ws_ptr<float>(ws, B.partial), T, F, K, S, R, ceil_div(K, 64), 1, 0};
-        const int tiles = ceil_div(T, 64) * g.n_tiles_n;
-        g.splits = f32_splits(tiles, 2 * ceil_div(F, 32) * 32, 64 * 64, c.ws_bytes - B.partial, g.k_chunk);
-        if (g.splits == 1) {
-            hipLaunchKernelGGL(k_dx_f32<false>, dim3(tiles), dim3(256), 0, s, g, pp);
-        } else {
-            hipLaunchKernelGGL(k_dx_f32<true>, dim3(tiles * g.splits), dim3(256), 0, s, g, pp);
-            hipLaunchKernelGGL(k_dx_reduce_f32, dim3(tiles * 4), dim3(256), 0, s, g, pp);
+        const outer_f32_args o{(const float *)c.x, (const float *)dg, (const float *)du, v, dv,
+                               (float *)c.dA[0], (float *)c.dA[1], (float *)c.dB[0], (float *)c.dB[1],
+                               offsets, perm, T, K, F, R, c.dA[0] ? S : 0, ceil_div(K, 256), ceil_div(F, 256)};
+        const int tiles = c.dx ? ceil_div(T, 64) * g.n_tiles_n : 0;
+        if (c.dx) g.splits = f32_splits(tiles, 2 * ceil_div(F, 32) * 32, 64 * 64, c.ws_bytes - B.partial, g.k_chunk);
+        const int n_dx = tiles * g.splits;
+        const dim3 grid = grid_of(n_dx + 2ll * o.n_slots * (o.tiles_k + o.tiles_f));
+        if (c.dx || c.dA[0]) {
+            if (g.splits == 1) hipLaunchKernelGGL(k_dx_outer_f32<false>, grid, dim3(256), 0, s, g, o, pp, n_dx);
+            else hipLaunchKernelGGL(k_dx_outer_f32<true>, grid, dim3(256), 0, s, g, o, pp, n_dx);
         }
+        if (g.splits > 1) hipLaunchKernelGGL(k_dx_reduce_f32, dim3(tiles * 4), dim3(256), 0, s, g, pp);
     } else if (c.dx) {
         uint16_t *oct = ws_ptr<uint16_t>(ws, B.oct);
         int32_t *row0 = ws_ptr<int32_t>(ws, B.row0), *rank = ws_ptr<int32_t>(ws, B.rank);
         float *scale = ws_ptr<float>(ws, B.scale);
-        hipLaunchKernelGGL(k_a_octets, dim3(S < T ? S : T, ceil_div(K, 256), 2 * R / 8), dim3(256), 0, s, pp,
-                           ws_ptr<int32_t>(ws, L.seg_id), ws_ptr<int32_t>(ws, L.n_seg), S, K, R, oct, row0, rank,
-                           scale);
         nt_args nt{{(const uint16_t *)dg, (const uint16_t *)du}, {(const uint16_t *)c.W[0], (const uint16_t *)c.W[1]},
                    F, ceil_div(F, 64) * 64, ws_ptr<int32_t>(ws, L.n_seg)};
         gemm_args g{};
@@ -1118,11 +1143,6 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
             case 3: hipLaunchKernelGGL((k_seg_outer_mfma<3, 2>), grid, dim3(256), 0, s, g); break;
             default: hipLaunchKernelGGL((k_seg_outer_mfma<4, 2>), grid, dim3(256), 0, s, g); break;
         }
-    } else if (c.dA[0]) {
-        const outer_f32_args g{(const float *)c.x, (const float *)dg, (const float *)du, v, dv,
-                               (float *)c.dA[0], (float *)c.dA[1], (float *)c.dB[0], (float *)c.dB[1],
-                               offsets, perm, T, K, F, R, S, ceil_div(K, 256), ceil_div(F, 256)};
-        hipLaunchKernelGGL(k_seg_outer_f32, grid_of(2ll * S * (g.tiles_k + g.tiles_f)), dim3(256), 0, s, g, pp);
     }
     return hip_status(hipGetLastError());
 }

@@ -287,3 +287,17 @@ def test_gates_far_from_zero(act, dtype):
         # dg and du: 4 fp32 steps and one rounding; 2 f sums of one step; dx rounded
         tol = (half + (2 * p.f + 12) * 2.0 ** -23) * size + half * ref.abs() * (1 + half) + 2.0 ** -110
         within(dx[t], ref, tol, "%s gate %g" % (act, f))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_each_part_alone_is_what_the_whole_gives(dtype):
+    """dx alone and the adapters' gradients alone: bitwise those of the call for both."""
+    p = Pair(150, 136, 264, RANKS, 16, dtype, seed=12)
+    k = kept(p)
+    dx, dA, dB, _ = run_backward(p, "silu", *k)
+    only_dx, none_a, none_b, _ = run_backward(p, "silu", *k, want_ab=False)
+    none_dx, only_a, only_b, _ = run_backward(p, "silu", *k, want_dx=False)
+    assert none_a is None and none_b is None and none_dx is None
+    assert torch.equal(dx, only_dx)
+    for m in range(2):
+        assert torch.equal(dA[m], only_a[m]) and torch.equal(dB[m], only_b[m])
