@@ -10,10 +10,10 @@
 // codes are those of y as stored (rounded to bf16), so they are bitwise what
 // lora_quantize_rows_fp8 gives for it.
 //
-// Bound by its bytes (34811 x 4096 with codes, 1.28 GB: 229 us, 5.6 TB/s, more
+// Bound by its bytes (34811 x 4096 with codes, 1.28 GB: 226 us, 5.7 TB/s, more
 // than a plain copy of 1 GiB reaches) and, for few rows, by one trip to memory
 // and back: a row has as many threads as give each one or two of its 16-byte
-// vectors, so that all of it is in flight at once (one row of 4096: 2.8 us).
+// vectors, so that all of it is in flight at once (one row of 4096: 2.2 us).
 #include "common.hpp"
 #include "fp8_common.hpp"
 
@@ -181,11 +181,17 @@ static lora_status_t launch_norm(const norm_args &a, hipStream_t s) {
         hipLaunchKernelGGL((k_add_rmsnorm<DT, NTV, VPTV, Q8>), dim3((uint32_t)(n < cap ? n : cap)),     \
                            dim3(NTV < 256 ? 256 : NTV), 0, s, a);                                       \
     } while (0)
+    // One vector a thread where nearly all threads have one (512 vectors, 34811
+    // rows with codes 226 us and one row 2.2, with two a thread 230 and 2.8, with
+    // eight 289 and 5.7), else two (386 vectors of fp32, 1111 rows: 7.0 us, with
+    // one 7.7).
     if (nvec <= 64) LORA_NORM(64, 1);
     else if (nvec <= 128) LORA_NORM(64, 2);
     else if (nvec <= 256) LORA_NORM(256, 1);
-    else if (nvec <= 512) LORA_NORM(256, 2);
-    else if (nvec <= 1024) LORA_NORM(512, 2);
+    else if (nvec <= 448) LORA_NORM(256, 2);
+    else if (nvec <= 512) LORA_NORM(512, 1);
+    else if (nvec <= 896) LORA_NORM(512, 2);
+    else if (nvec <= 1024) LORA_NORM(1024, 1);
     else if (nvec <= 2048) LORA_NORM(1024, 2);
     else if (nvec <= 4096) LORA_NORM(1024, 4);
     else LORA_NORM(1024, 0);

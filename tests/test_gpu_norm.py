@@ -159,3 +159,22 @@ def test_the_binding_refuses_tensors_the_kernels_would_misread():
             with pytest.raises(L.LoraError) as e:
                 L.lora_add_rmsnorm(bad["x"], bad["r"], bad["w"], EPS, 6, 256, L.LORA_BF16, bad["z"], bad["y"])
             assert e.value.status == L.LORA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("d", [1792, 1800, 3584, 3592, 3600, 4088, 7168, 7184, 8176])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_widths_at_the_borders_of_the_thread_counts(d, dtype):
+    """One vector a thread or two: the last widths of one count and the first of the next."""
+    T = 11
+    x, r, w = make(T, d, dtype, seed=d)
+    z, y = torch.empty_like(x), torch.empty_like(x)
+    L.lora_add_rmsnorm(x, r, w, EPS, T, d, L.dtype_code(dtype), z, y)
+    check(z, y, x, r, w)
+    if dtype == torch.bfloat16 and d % 16 == 0:
+        z2, y2 = torch.empty_like(x), torch.empty_like(x)
+        q, s = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+        q2, s2 = torch.empty_like(q), torch.empty_like(s)
+        L.lora_add_rmsnorm_fp8(x, r, w, EPS, T, d, z2, y2, q, s)
+        assert torch.equal(z, z2) and torch.equal(y, y2)
+        L.lora_quantize_rows_fp8(y2, T, d, q2, s2)
+        assert torch.equal(q, q2) and torch.equal(s, s2)
