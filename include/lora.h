@@ -583,7 +583,7 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
  *     dg = dh u act'(g),   du = dh act(g)        (bf16 pools: rounded once)
  *     dx = dg W_gate^T + du W_up^T + dv_g A_a^T + dv_u A_a^T,   dv = s d{g,u} B_a^T
  *     dA_a = sum over a's rows of x^T dv,        dB_a = s sum of (x A_a)^T d{g,u}
- * dx DEVICE [T, d_in], overwritten (NULL: not computed; a buffer of its own).  dA and dB HOST
+ * dx DEVICE [T, d_in], overwritten (NULL: not computed).  dA and dB HOST
  * arrays of 2 DEVICE pointers (gate's, up's), dA[i] [n_slots, d_in, max_rank]
  * and dB[i] [n_slots, max_rank, d_out], row-major as lora_pool_upload takes
  * one slot's (lda = max_rank, ldb = d_out); padded so for packed pools too.
@@ -591,7 +591,9 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
  * and past a slot's, get zeros (T == 0 too).  Both NULL: not computed.  All of
  * the pools' dtype, sums in fp32.  Rows without a usable adapter have only the base
  * term.  The sums over an adapter's rows are in batch order: the same inputs
- * give bitwise the same gradients.  ws: lora_workspace_bytes_gated_backward,
+ * give bitwise the same gradients.  dx, dA's and dB's buffers and ws share no
+ * byte with each other or with anything the call reads (T > 0; else
+ * LORA_ERR_INVALID_ARGUMENT).  ws: lora_workspace_bytes_gated_backward,
  * cleared by lora_workspace_init. */
 size_t lora_workspace_bytes_gated_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out,
                                            lora_dtype_t dtype);

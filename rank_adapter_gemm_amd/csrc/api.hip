@@ -603,6 +603,44 @@ static bool apart(const void *x, const void *h, const void *gate, const void *up
     return h != x && !(gate && (gate == up || gate == x || up == x || gate == h || up == h));
 }
 
+// Bytes that a call reads or writes; p null: none.
+struct span {
+    const void *p;
+    size_t n;
+};
+
+// Whether every output keeps clear of the other outputs and of what is read:
+// workgroups read the one while others write the other, in no fixed order.
+static bool outputs_clear(const span *out, int n_out, const span *in, int n_in) {
+    auto meet = [](const span &a, const span &b) {
+        const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+        return pa && pb && (pa <= pb ? pb - pa < a.n : pa - pb < b.n);
+    };
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return false;
+        for (int j = 0; j < n_in; ++j)
+            if (meet(out[i], in[j])) return false;
+    }
+    return true;
+}
+
+// What a call reads of a pair's pools: spans of both pools' a, b, scale, rank and
+// row tables, kPairSpans of them.
+constexpr int kPairSpans = 10;
+static void pair_spans(const lora_pool_t *pools, span *out) {
+    for (int m = 0; m < 2; ++m, out += kPairSpans / 2) {
+        const lora_pool_t &p = pools[m];
+        const size_t rows = p.row0_host ? (size_t)p.row0_host[p.n_slots] : (size_t)p.n_slots * p.max_rank;
+        const size_t eb = dtype_bytes(p.dtype), table = 4 * (size_t)p.n_slots;
+        out[0] = span{p.a, rows * p.d_in * eb};
+        out[1] = span{p.b, rows * p.d_out * eb};
+        out[2] = span{p.scale, table};
+        out[3] = span{p.rank, table};
+        out[4] = span{p.row0, table + 4};
+    }
+}
+
 // Segments (where the mode uses them) and both slices' rank vectors, then the
 // pair.  c holds everything but ids' order, v and the partials.
 static lora_status_t run_gated(gated_call &c, lora_mode_t mode, uint32_t flags, const ws_layout &L, void *ws,
@@ -744,10 +782,15 @@ lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void 
         }
         return st;
     }
-    if (dx && (dx == x || dx == gate || dx == up || dx == dh)) return LORA_ERR_INVALID_ARGUMENT;
-    if (dA && (dA[0] == dA[1] || dB[0] == dB[1] || dA[0] == dB[0] || dA[0] == dB[1] || dA[1] == dB[0] ||
-               dA[1] == dB[1] || dx == dA[0] || dx == dA[1] || dx == dB[0] || dx == dB[1]))
-        return LORA_ERR_INVALID_ARGUMENT;
+    const size_t eb = dtype_bytes(p.dtype), in = (size_t)T * p.d_in * eb, rows = (size_t)T * p.d_out * eb,
+                 weight = (size_t)p.d_in * p.d_out * eb, da = (size_t)p.n_slots * p.d_in * p.max_rank * eb,
+                 db = (size_t)p.n_slots * p.max_rank * p.d_out * eb;
+    const span out[] = {{dx, in}, {ws, ws_bytes}, {dA ? dA[0] : nullptr, da}, {dA ? dA[1] : nullptr, da},
+                        {dB ? dB[0] : nullptr, db}, {dB ? dB[1] : nullptr, db}};
+    span read[7 + kPairSpans] = {{x, in}, {W_gate, weight}, {W_up, weight}, {ids, 4 * (size_t)T},
+                                 {gate, rows}, {up, rows}, {dh, rows}};
+    pair_spans(pools, read + 7);
+    if (!outputs_clear(out, 6, read, 7 + kPairSpans)) return LORA_ERR_INVALID_ARGUMENT;
     gated_bwd_call c{x, {W_gate, W_up}, gate, up, dh, dx, {nullptr, nullptr}, {nullptr, nullptr}, T, (int32_t)act,
                      pools, ids, ws, ws_bytes};
     for (int i = 0; i < 2 && dA; ++i) {
