@@ -557,7 +557,8 @@ size_t lora_workspace_bytes_gated_fp8(int32_t T, int32_t n_slots, int32_t max_ra
  * of the pools' dtype; pools HOST [2] (gate, up) with the conditions of
  * lora_linear_forward_sliced and one d_out.  gate and up DEVICE [T, d_out]
  * keep g and u, each rounded once, for lora_gated_backward; both may be NULL.
- * No output is another's buffer, or x's.
+ * h, gate, up and ws share no byte with each other or with anything the call
+ * reads (T > 0; else LORA_ERR_INVALID_ARGUMENT).
  * mode, ids and bad ids as in lora_linear_forward; a row whose slot is empty
  * in one pool has only the other's term (and is recorded).  flags: 0 or
  * LORA_FLAG_SEGMENTS_READY (segments built by lora_build_segments, by this

@@ -597,12 +597,6 @@ static lora_status_t check_pair(const lora_pool_t *pools) {
 
 static inline bool valid_act(int32_t a) { return a == LORA_ACT_SILU || a == LORA_ACT_GELU || a == LORA_ACT_GELU_TANH; }
 
-// No output of the pair is another's buffer, or x's (tiles of x are read while
-// others' outputs are written).
-static bool apart(const void *x, const void *h, const void *gate, const void *up) {
-    return h != x && !(gate && (gate == up || gate == x || up == x || gate == h || up == h));
-}
-
 // Bytes that a call reads or writes; p null: none.
 struct span {
     const void *p;
@@ -687,7 +681,13 @@ lora_status_t lora_gated_forward(const void *x, const void *W_gate, const void *
     ws_layout L;
     st = check_ws(ws, ws_bytes, T, pools[0].n_slots, 2 * pools[0].max_rank, &L);
     if (st != LORA_OK || T == 0) return st;
-    if (!apart(x, h, gate, up)) return LORA_ERR_INVALID_ARGUMENT;
+    const size_t eb = dtype_bytes(pools[0].dtype), rows = (size_t)T * pools[0].d_out * eb,
+                 weight = (size_t)pools[0].d_in * pools[0].d_out * eb;
+    const span out[] = {{h, rows}, {gate, rows}, {up, rows}, {ws, ws_bytes}};
+    span read[4 + kPairSpans] = {{x, (size_t)T * pools[0].d_in * eb}, {W_gate, weight}, {W_up, weight},
+                                 {ids, 4 * (size_t)T}};
+    pair_spans(pools, read + 4);
+    if (!outputs_clear(out, 4, read, 4 + kPairSpans)) return LORA_ERR_INVALID_ARGUMENT;
     gated_call c{};
     c.x = x;
     c.W[0] = W_gate;
@@ -720,7 +720,12 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
     ws_layout L;
     st = check_ws_fp8(ws, ws_bytes, T, pools[0].n_slots, 2 * pools[0].max_rank, xq ? 0 : pools[0].d_in, &L);
     if (st != LORA_OK || T == 0) return st;
-    if (!apart(x, h, gate, up)) return LORA_ERR_INVALID_ARGUMENT;
+    const size_t K = pools[0].d_in, N = pools[0].d_out, rows = 2 * N * T;
+    const span out[] = {{h, rows}, {gate, rows}, {up, rows}, {ws, ws_bytes}};
+    span read[8 + kPairSpans] = {{x, 2 * K * T}, {xq, K * T}, {x_scale, 4 * (size_t)T}, {wq_gate, K * N}, {wq_up, K * N},
+                                 {w_scale_gate, 4 * N}, {w_scale_up, 4 * N}, {ids, 4 * (size_t)T}};
+    pair_spans(pools, read + 8);
+    if (!outputs_clear(out, 4, read, 8 + kPairSpans)) return LORA_ERR_INVALID_ARGUMENT;
     const hipStream_t s = hs(stream);
     if (!xq) {
         uint8_t *q = ws_ptr<uint8_t>(ws, L.xq);

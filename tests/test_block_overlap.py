@@ -66,3 +66,38 @@ def test_backward(lib):
 
     for o, other, by in meetings(size, ["dx", "dA0", "dA1", "dB0", "dB1", "ws"], ["x", "wg", "wu", "ids", "gate", "up", "dh"] + POOLS):
         assert call(dict(base, **{o: base[other] + by})) == INVALID, (o, other, by)
+
+
+def pair_buffers(n):
+    names = ["x", "xq", "xs", "wg", "sg", "wu", "su", "ids"] + POOLS + ["h", "gate", "up", "ws"]
+    size = dict(x=T * K * 2, xq=T * K, xs=4 * T, wg=K * N * 2, sg=4 * N, wu=K * N * 2, su=4 * N, ids=4 * T,
+                h=T * N * 2, gate=T * N * 2, up=T * N * 2, ws=n, **POOL_BYTES)
+    return places(names, size), size
+
+
+def test_gated_forward(lib):
+    n = L.lora_workspace_bytes_gated(T, S, R, N)
+    base, size = pair_buffers(n)
+
+    def call(at):
+        return lib.lora_gated_forward(at["x"], at["wg"], at["wu"], at["h"], at["gate"], at["up"], T, pools(at),
+                                      at["ids"], 0, 0, 0, at["ws"], n, None)
+
+    for o, other, by in meetings(size, ["h", "gate", "up", "ws"], ["x", "wg", "wu", "ids"] + POOLS):
+        assert call(dict(base, **{o: base[other] + by})) == INVALID, (o, other, by)
+
+
+def test_gated_forward_fp8(lib):
+    n = L.lora_workspace_bytes_gated_fp8(T, S, R, K, N)
+    base, size = pair_buffers(n)
+    size.update(wg=K * N, wu=K * N)
+
+    def call(at):
+        return lib.lora_gated_forward_fp8(at["x"], at["xq"], at["xs"], at["wg"], at["sg"], at["wu"], at["su"], at["h"],
+                                          at["gate"], at["up"], T, pools(at), at["ids"], 0, 0, 0, at["ws"], n, None)
+
+    ins = ["x", "xq", "xs", "wg", "sg", "wu", "su", "ids"] + POOLS
+    for o, other, by in meetings(size, ["h", "gate", "up", "ws"], ins):
+        assert call(dict(base, **{o: base[other] + by})) == INVALID, (o, other, by)
+    no_codes = dict(base, xq=None, xs=None)
+    assert call(dict(no_codes, h=base["x"])) == INVALID
