@@ -517,9 +517,11 @@ lora_status_t lora_linear_forward_fp8(const void *x, const uint8_t *wq, const fl
  * norm is of the unrounded z).  All of `dtype`: x, residual, residual_out, y
  * DEVICE [T, d], weight DEVICE [d].  residual may be NULL (z = x);
  * residual_out may be NULL (z not stored).  residual_out may be residual's
- * or x's own buffer and y may be x's or residual's (the same address;
- * residual_out and y differ).  d a positive multiple of 8; eps finite and
- * positive. */
+ * or x's own buffer and y may be x's or residual's (the same address); beyond
+ * that an output that shares a byte with another output or with an input is
+ * refused (LORA_ERR_INVALID_ARGUMENT).  The squares are summed in fp32: a row
+ * whose sum passes 3.4e38 gives y = 0.  d a positive multiple of 8; eps finite
+ * and positive. */
 lora_status_t lora_add_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int32_t T,
                                int32_t d, lora_dtype_t dtype, void *residual_out, void *y,
                                lora_stream_t stream);

@@ -805,18 +805,33 @@ lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void 
     return launch_gated_backward(c, B, s);
 }
 
-// What both norms ask of their arguments (T > 0: the pointers too).
+// What both norms ask of their arguments (T > 0: the pointers too).  z's and
+// y's rows may be x's or the residual's own (a thread reads its part of a row
+// before it writes there); a buffer that only partly is one is refused.
 static bool valid_norm(const void *x, const void *residual, const void *weight, float eps, int32_t T, int32_t d,
-                       int32_t d_step, const void *residual_out, const void *y) {
+                       int32_t d_step, int32_t dtype, const void *residual_out, const void *y, const void *yq,
+                       const void *ys) {
     if (T < 0 || d <= 0 || (d % d_step) || !(eps > 0.0f) || !(eps < __builtin_inff())) return false;
     if (T == 0) return true;
-    return x && weight && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(residual_out) &&
-           aligned16(y) && !(y && residual_out == y);
+    if (!x || !weight || !aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
+        !aligned16(y))
+        return false;
+    const size_t n = (size_t)T * d, rows = n * dtype_bytes(dtype);
+    const span out[] = {{residual_out, rows}, {y, rows}, {yq, n}, {ys, 4 * (size_t)T}};
+    const span w = {weight, (size_t)d * dtype_bytes(dtype)};
+    if (!outputs_clear(out, 4, &w, 1)) return false;
+    for (const void *in : {x, residual})
+        for (int i = 0; i < 4; ++i) {
+            const span read = {in, rows};
+            if (!(i < 2 && out[i].p == in) && !outputs_clear(out + i, 1, &read, 1)) return false;
+        }
+    return true;
 }
 
 lora_status_t lora_add_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int32_t T,
                                int32_t d, lora_dtype_t dtype, void *residual_out, void *y, lora_stream_t stream) {
-    if (!valid_dtype(dtype) || !valid_norm(x, residual, weight, eps, T, d, 8, residual_out, y) || (T > 0 && !y))
+    if (!valid_dtype(dtype) || !valid_norm(x, residual, weight, eps, T, d, 8, dtype, residual_out, y, nullptr, nullptr) ||
+        (T > 0 && !y))
         return LORA_ERR_INVALID_ARGUMENT;
     return launch_add_rmsnorm(x, residual, weight, eps, T, d, dtype, residual_out, y, nullptr, nullptr, hs(stream));
 }
@@ -824,7 +839,7 @@ lora_status_t lora_add_rmsnorm(const void *x, const void *residual, const void *
 lora_status_t lora_add_rmsnorm_fp8(const void *x, const void *residual, const void *weight, float eps, int32_t T,
                                    int32_t d, void *residual_out, void *y, uint8_t *yq, float *y_scale,
                                    lora_stream_t stream) {
-    if (!valid_norm(x, residual, weight, eps, T, d, 16, residual_out, y) ||
+    if (!valid_norm(x, residual, weight, eps, T, d, 16, LORA_BF16, residual_out, y, yq, y_scale) ||
         (T > 0 && (!yq || !y_scale || !aligned16(yq) || !aligned16(y_scale))))
         return LORA_ERR_INVALID_ARGUMENT;
     return launch_add_rmsnorm(x, residual, weight, eps, T, d, LORA_BF16, residual_out, y, yq, y_scale, hs(stream));

@@ -23,7 +23,7 @@ def lib():
 
 def places(names, size):
     """Names -> addresses far apart."""
-    assert max(size.values()) < STEP
+    assert max(size.values(), default=0) < STEP
     return {n: (1 << 40) + i * STEP for i, n in enumerate(names)}
 
 
@@ -101,3 +101,38 @@ def test_gated_forward_fp8(lib):
         assert call(dict(base, **{o: base[other] + by})) == INVALID, (o, other, by)
     no_codes = dict(base, xq=None, xs=None)
     assert call(dict(no_codes, h=base["x"])) == INVALID
+
+
+def norm_buffers(d, T=T):
+    names = ["x", "r", "w", "z", "y", "q", "s"]
+    return places(names, {}), dict(x=T * d * 2, r=T * d * 2, w=d * 2, z=T * d * 2, y=T * d * 2, q=T * d, s=4 * T)
+
+
+def test_norm(lib):
+    """z and y may be x's or the residual's own buffers, row for row, and nothing else."""
+    base, size = norm_buffers(K)
+    size.pop("q"), size.pop("s")
+
+    def call(at):
+        return lib.lora_add_rmsnorm(at["x"], at["r"], at["w"], 1e-6, T, K, L.LORA_BF16, at["z"], at["y"], None)
+
+    for o, other, by in meetings(size, ["z", "y"], ["x", "r", "w"]):
+        if by == 0 and other in ("x", "r"):
+            continue
+        assert call(dict(base, **{o: base[other] + by})) == INVALID, (o, other, by)
+    # in place on rows that the other input is half a buffer into
+    assert call(dict(base, z=base["x"], r=base["x"] + size["x"] // 2)) == INVALID
+
+
+def test_norm_fp8(lib):
+    base, size = norm_buffers(K)
+
+    def call(at):
+        return lib.lora_add_rmsnorm_fp8(at["x"], at["r"], at["w"], 1e-6, T, K, at["z"], at["y"], at["q"], at["s"], None)
+
+    for o, other, by in meetings(size, ["z", "y", "q", "s"], ["x", "r", "w"]):
+        if by == 0 and o in ("z", "y") and other in ("x", "r"):
+            continue
+        assert call(dict(base, **{o: base[other] + by})) == INVALID, (o, other, by)
+    assert call(dict(base, y=None, q=base["x"])) == INVALID
+    assert call(dict(base, r=None, z=None, s=base["w"])) == INVALID
