@@ -33,8 +33,8 @@ def sorted_ids(T, lengths):
 
 # ---- backward: dx's plans ----------------------------------------------------
 # T, d, f: 256 x 256 tiles in pieces of K (f past 4096, its own odd end), whole 256 x 256 tiles, these with a
-# last round in pieces, 256 x 128 tiles whole, and with a last round in pieces
-DX = [(1797, 1800, 4104), (3500, 3800, 72), (4000, 4296, 520), (2000, 3496, 136), (1990, 4104, 520)]
+# last round in pieces, 256 x 128 tiles whole, and with a last round in pieces, 128 x 64 tiles with one
+DX = [(1797, 1800, 4104), (3500, 3800, 72), (4000, 4296, 520), (2000, 3496, 136), (1990, 4104, 520), (2000, 1080, 520)]
 
 
 @pytest.mark.parametrize("T,d,f", DX)
