@@ -542,6 +542,8 @@ def lora_gated_backward(x, W_gate, W_up, T, pools, ids, act, gate, up, dh, dx, d
     pair, p = _pool_pair(pools), pools[0]
     dt, n, nw, nr = _TORCH_TYPES.get(p.dtype), T * p.d_out, p.d_in * p.d_out, p.n_slots * p.max_rank
     nbytes = _ws_bytes(ws)
+    if (dA is None) != (dB is None) or dA is not None and (len(dA) != 2 or len(dB) != 2):
+        raise LoraError(LORA_ERR_INVALID_ARGUMENT, "gate's and up's gradients of A and of B, or none")
     grads = [None, None] if dA is None else list(dA), [None, None] if dB is None else list(dB)
     x, W_gate, W_up, ids, gate, up, dh, dx, ws, a0, a1, b0, b1 = _checked(
         "lora_gated_backward", (x, dt, T * p.d_in), (W_gate, dt, nw), (W_up, dt, nw), (ids, torch.int32, T),
