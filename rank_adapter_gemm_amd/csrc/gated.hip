@@ -95,7 +95,9 @@ template <bool SPLIT> __global__ void __launch_bounds__(256, 2) k_gated_f32(gate
     static_assert(32 * WS <= NS * STAGE, "the sums fit the stages' LDS");
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     int tm, tn, split;
-    f32_tile(blockIdx.x, gridDim.x, g.n_tiles_m, SPLIT ? g.splits : 1, tm, tn, split);
+    const int total = g.n_tiles_m * g.n_tiles_n * (SPLIT ? g.splits : 1);
+    if (grid_index() >= total) return;
+    f32_tile((int)grid_index(), total, g.n_tiles_m, SPLIT ? g.splits : 1, tm, tn, split);
     const int tile = tm * g.n_tiles_n + tn, m0 = tm * 32, n0 = tn * 64;
     const int N = g.N, T = g.T, k_begin = split * g.k_chunk, k_end = min(g.K, k_begin + g.k_chunk);
     __shared__ row_slot s_slot[SPLIT ? 1 : 32];
@@ -326,7 +328,7 @@ lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {
         const int tiles = g.n_tiles_m * g.n_tiles_n;
         g.splits = f32_splits(tiles, g.K, 32 * 128, c.partial_bytes, g.k_chunk);
         if (g.splits == 1) {
-            hipLaunchKernelGGL(k_gated_f32<false>, dim3(tiles), dim3(256), 0, s, g);
+            hipLaunchKernelGGL(k_gated_f32<false>, grid_of(tiles), dim3(256), 0, s, g);
         } else {
             hipLaunchKernelGGL(k_gated_f32<true>, dim3(tiles * g.splits), dim3(256), 0, s, g);
             hipLaunchKernelGGL(k_gated_reduce_f32, dim3(tiles * 2), dim3(256), 0, s, g);
