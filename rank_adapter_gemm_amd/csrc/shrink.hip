@@ -200,7 +200,7 @@ __device__ __forceinline__ void shrink_row(const typename elem<DT>::T *__restric
     }
 }
 
-// BGMV: one workgroup per row (position blockIdx.x through perm).
+// BGMV: one workgroup per row (position grid_index() through perm).
 template <int DT, int RM, bool Q8 = false>
 __global__ void __launch_bounds__(512) k_shrink_rows(const typename elem<DT>::T *__restrict__ x,
                                                      int32_t T, int32_t d_in, slice_set ss,
@@ -209,7 +209,9 @@ __global__ void __launch_bounds__(512) k_shrink_rows(const typename elem<DT>::T 
                                                      const int32_t *__restrict__ perm,
                                                      float *__restrict__ v, int32_t *err,
                                                      uint8_t *__restrict__ xq, float *__restrict__ xs) {
-    shrink_row<DT, RM, Q8>(x, T, d_in, ss, n_slots, max_rank, ids, perm, v, err, xq, xs, blockIdx.x);
+    const int64_t p = grid_index();
+    if (p >= T) return;
+    shrink_row<DT, RM, Q8>(x, T, d_in, ss, n_slots, max_rank, ids, perm, v, err, xq, xs, (int)p);
 }
 
 
@@ -447,7 +449,7 @@ static void launch_rows(const void *x, int32_t T, const lora_pool_t &p, const sl
     typedef typename elem<DT>::T E;
     const E *xe = (const E *)x;
 #define LORA_SHRINK_ROWS(RMV)                                                                   \
-    hipLaunchKernelGGL((k_shrink_rows<DT, RMV>), dim3(T), dim3(512), 0, s, xe, T, p.d_in, ss,   \
+    hipLaunchKernelGGL((k_shrink_rows<DT, RMV>), grid_of(T), dim3(512), 0, s, xe, T, p.d_in, ss, \
                        p.n_slots, p.max_rank, ids, perm, v, err, nullptr, nullptr)
     if (p.max_rank <= 8) LORA_SHRINK_ROWS(8);
     else if (p.max_rank <= 16) LORA_SHRINK_ROWS(16);
@@ -469,7 +471,7 @@ lora_status_t launch_quant_shrink_rows(const void *x, int32_t T, const lora_pool
     }
     const uint16_t *xe = (const uint16_t *)x;
 #define LORA_QSHRINK_ROWS(RMV)                                                                            \
-    hipLaunchKernelGGL((k_shrink_rows<LORA_BF16, RMV, true>), dim3(T), dim3(512), 0, s, xe, T, pool->d_in, ss, \
+    hipLaunchKernelGGL((k_shrink_rows<LORA_BF16, RMV, true>), grid_of(T), dim3(512), 0, s, xe, T, pool->d_in, ss, \
                        pool->n_slots, pool->max_rank, ids, nullptr, v, err, xq, xs)
     if (pool->max_rank <= 8) LORA_QSHRINK_ROWS(8);
     else if (pool->max_rank <= 16) LORA_QSHRINK_ROWS(16);

@@ -1,0 +1,85 @@
+"""Batches whose rows need more than 2^32 threads in one grid dimension (a
+launch of that size runs a part of its workgroups without an error).  Small
+whole numbers, so every sum is exact and every row is compared."""
+import numpy as np
+import pytest
+import torch
+
+from rank_adapter_gemm_amd import lora as L
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    L.load()
+    torch.cuda.empty_cache()
+
+
+def needs(gb):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gb * 1e9:
+        pytest.skip("not enough free memory")
+
+
+def whole(*shape, dtype=BF16, most=3, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda", dtype=torch.int8).to(dtype)
+
+
+def two_slots(T, d, f, dtype):
+    """A pool of two adapters of rank 8 (scale 1), and ids -1, 0, 1 in turn."""
+    pool = L.AdapterPool(2, d, f, 8, dtype)
+    A, B = whole(2, d, 8, dtype=dtype, seed=1), whole(2, 8, f, dtype=dtype, seed=2)
+    for s in range(2):
+        pool.upload(s, A[s], B[s], 8, 8.0)
+    ids = (torch.arange(T, device="cuda", dtype=torch.int32) % 3) - 1
+    return pool, A, B, ids
+
+
+def rank_vectors(x, A, ids, a=0, b=None):
+    """x A of every row's own adapter, rows a to b."""
+    xs, ix = x[a:b].float(), ids[a:b]
+    return sum((xs @ A[s].float()) * (ix == s)[:, None] for s in range(2))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_shrink_by_rows(dtype):
+    T = (1 << 23) + 700                                    # 512 threads a row
+    pool, A, _, ids = two_slots(T, 8, 8, dtype)
+    x = whole(T, 8, dtype=dtype)
+    ws = L.Workspace(T, 2, 8)
+    v = torch.full((T, 8), 7.5, device="cuda")
+    L.lora_shrink(x, T, pool.pool, ids, L.LORA_MODE_BGMV, v, ws.buf)
+    assert torch.equal(v, rank_vectors(x, A, ids))
+
+
+def test_f32_pair_in_adapter_order():
+    """AUTO on this many rows: the rank vectors by rows, through the segments' order."""
+    T = (1 << 23) + 700
+    pool, A, B, ids = two_slots(T, 8, 8, F32)
+    x, W = whole(T, 8, dtype=F32), [whole(8, 8, dtype=F32, seed=3 + i) for i in range(2)]
+    h, g, u = (torch.full((T, 8), 7.5, device="cuda") for _ in range(3))
+    ws = L.Workspace(T, 2, 8, gated=True)
+    L.lora_gated_forward(x, W[0], W[1], h, T, [pool.pool, pool.pool], ids, L.LORA_ACT_SILU, L.LORA_MODE_AUTO, 0, ws.buf,
+                         gate=g, up=u)
+    delta = sum((rank_vectors(x, A, ids) @ B[s]) * (ids == s)[:, None] for s in range(2))
+    assert torch.equal(g, x @ W[0] + delta) and torch.equal(u, x @ W[1] + delta)
+
+
+def test_fp8_layer_by_rows():
+    """The FP8 layer's rank vectors and codes in one launch (512 threads a row)."""
+    T, d = (1 << 23) + 700, 16
+    pool, A, B, ids = two_slots(T, d, 8, BF16)
+    x = whole(T, d, most=3)
+    W = torch.zeros(d, 8, dtype=BF16, device="cuda")
+    w = L.Fp8Weight(W)
+    y = torch.full((T, 8), 7.5, dtype=BF16, device="cuda")
+    ws = L.Workspace(T, 2, 8, 8, fp8_d_in=d)
+    L.lora_linear_forward_fp8(x, w.codes, w.scale, y, T, pool.pool, ids, L.LORA_MODE_BGMV, 0, ws.buf)
+    v = rank_vectors(x, A, ids)
+    assert torch.equal(y, sum((v @ B[s].float()) * (ids == s)[:, None] for s in range(2)).to(BF16))
