@@ -51,9 +51,10 @@ __device__ __forceinline__ float block_max256(float m, float *red) {
 
 // One token row per workgroup: amax over the row, then the codes (second
 // read of the row, from cache).  x bf16 [T][K], K % 16 == 0; xs[t] = 2^e.
-__global__ void __launch_bounds__(256) k_quant_rows_fp8(const uint16_t *x, int32_t K, uint8_t *xq, float *xs) {
+__global__ void __launch_bounds__(256) k_quant_rows_fp8(const uint16_t *x, int32_t T, int32_t K, uint8_t *xq, float *xs) {
     __shared__ float red[4];
-    const int64_t t = blockIdx.x;
+    const int64_t t = grid_index();
+    if (t >= T) return;
     const uint16_t *row = x + t * K;
     const int nch = K / 8;
     float m = 0.0f;
@@ -401,7 +402,7 @@ static void launch_fp8_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStrea
 
 lora_status_t launch_quant_rows_fp8(const void *x, int32_t T, int32_t K, uint8_t *xq, float *xs, hipStream_t s) {
     if (T <= 0) return LORA_OK;
-    hipLaunchKernelGGL(k_quant_rows_fp8, dim3(T), dim3(256), 0, s, (const uint16_t *)x, K, xq, xs);
+    hipLaunchKernelGGL(k_quant_rows_fp8, grid_of(T), dim3(256), 0, s, (const uint16_t *)x, T, K, xq, xs);
     return hip_status(hipGetLastError());
 }
 

@@ -83,3 +83,15 @@ def test_fp8_layer_by_rows():
     L.lora_linear_forward_fp8(x, w.codes, w.scale, y, T, pool.pool, ids, L.LORA_MODE_BGMV, 0, ws.buf)
     v = rank_vectors(x, A, ids)
     assert torch.equal(y, sum((v @ B[s].float()) * (ids == s)[:, None] for s in range(2)).to(BF16))
+
+
+def test_fp8_rows():
+    """Codes and scales of rows (256 threads each), alone and within the pair."""
+    T, d = (1 << 24) + 300, 16
+    x = whole(T, d, most=100)
+    q, s = torch.full((T, d), 99, dtype=torch.uint8, device="cuda"), torch.full((T,), 7.5, device="cuda")
+    L.lora_quantize_rows_fp8(x, T, d, q, s)
+    m, e = torch.frexp(x.float().abs().amax(1))            # the smallest 2^e with amax <= 448 2^e = 0.875 2^(e + 9)
+    want = torch.ldexp(torch.ones_like(m), e - 9 + (m > 0.875).int())
+    assert torch.equal(s, torch.where(m > 0, want, s)) and float(s.max()) < 1
+    assert torch.equal(q.view(torch.float8_e4m3fn).float(), (x.float() / s[:, None]).to(torch.float8_e4m3fn).float())
