@@ -93,7 +93,9 @@ __global__ void __launch_bounds__(256) k_expand_rows(const float *__restrict__ v
                                                      const int32_t *__restrict__ ids,
                                                      const int32_t *__restrict__ perm,
                                                      typename elem<DT>::T *__restrict__ y) {
-    expand_row<DT>(v, T, d_out, b, scale, rank, row0, n_slots, max_rank, v_stride, ids, perm, y, blockIdx.x);
+    const int64_t p = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+    if (p >= T) return;
+    expand_row<DT>(v, T, d_out, b, scale, rank, row0, n_slots, max_rank, v_stride, ids, perm, y, (int)p);
 }
 
 // Expand of rows that share one adapter: y[t] += s_a (v[t, 0:r] B_a) for
@@ -263,7 +265,7 @@ lora_status_t launch_expand(const float *v, int32_t v_stride, int32_t T, const l
         if (st == LORA_OK) st = launch_expand_short(v, v_stride, T, p, y, L, ws, s);
         return st;
     }
-    const dim3 grid(T, (p.d_out + 2047) / 2048);
+    const dim3 rows = grid_of(T), grid(rows.x, (p.d_out + 2047) / 2048, rows.y);
     if (p.dtype == LORA_F32)
         hipLaunchKernelGGL(k_expand_rows<LORA_F32>, grid, dim3(256), 0, s, v, T, p.d_out,
                            (const float *)p.b, p.scale, p.rank, p.row0, p.n_slots, p.max_rank, v_stride, ids, perm,

@@ -95,3 +95,14 @@ def test_fp8_rows():
     want = torch.ldexp(torch.ones_like(m), e - 9 + (m > 0.875).int())
     assert torch.equal(s, torch.where(m > 0, want, s)) and float(s.max()) < 1
     assert torch.equal(q.view(torch.float8_e4m3fn).float(), (x.float() / s[:, None]).to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_expand_by_rows(dtype):
+    T = (1 << 24) + 300                                    # 256 threads a row
+    pool, _, B, ids = two_slots(T, 8, 8, dtype)
+    v = whole(T, 8, dtype=F32)
+    y = torch.zeros(T, 8, dtype=dtype, device="cuda")
+    ws = L.Workspace(T, 2, 8)
+    L.lora_expand(v, T, pool.pool, ids, L.LORA_MODE_BGMV, y, ws.buf)
+    assert torch.equal(y, sum((v @ B[s].float()) * (ids == s)[:, None] for s in range(2)).to(dtype))
