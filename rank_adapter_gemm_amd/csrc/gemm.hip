@@ -390,7 +390,9 @@ __global__ void __launch_bounds__(256) k_gemm_f32(gemm_f32_args g) {
     __shared__ float As[16][64 + 4];
     __shared__ float Bs[16][64 + 4];
     const int tid = threadIdx.x;
-    const int tm = blockIdx.x / g.n_tiles_n, tn = blockIdx.x % g.n_tiles_n;
+    const uint32_t wg = (uint32_t)grid_index();           // fewer than 2^32 tiles of 64 x 64 fit any memory
+    const int tm = (int)(wg / (uint32_t)g.n_tiles_n), tn = (int)(wg % (uint32_t)g.n_tiles_n);
+    if (tm >= (g.T + 63ll) / 64) return;
     const int m0 = tm * 64, n0 = tn * 64;
     const int K = g.K, N = g.N, T = g.T;
     const int lr = tid >> 2, lk = (tid & 3) * 4;          // x tile loader
@@ -720,11 +722,11 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
         g.v = v;
         g.v_stride = v_stride;
         g.n_tiles_n = (d_out + 63) / 64;
-        const int tiles = ((T + 63) / 64) * g.n_tiles_n;
+        const dim3 grid = grid_of((T + 63ll) / 64 * g.n_tiles_n);
         if (pool)
-            hipLaunchKernelGGL(k_gemm_f32<true>, dim3(tiles), dim3(256), 0, s, g);
+            hipLaunchKernelGGL(k_gemm_f32<true>, grid, dim3(256), 0, s, g);
         else
-            hipLaunchKernelGGL(k_gemm_f32<false>, dim3(tiles), dim3(256), 0, s, g);
+            hipLaunchKernelGGL(k_gemm_f32<false>, grid, dim3(256), 0, s, g);
     }
     return hip_status(hipGetLastError());
 }

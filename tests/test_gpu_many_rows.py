@@ -106,3 +106,20 @@ def test_expand_by_rows(dtype):
     ws = L.Workspace(T, 2, 8)
     L.lora_expand(v, T, pool.pool, ids, L.LORA_MODE_BGMV, y, ws.buf)
     assert torch.equal(y, sum((v @ B[s].float()) * (ids == s)[:, None] for s in range(2)).to(dtype))
+
+
+def test_f32_gemm():
+    """2^30 rows: 256 threads for every 64 rows."""
+    needs(85)
+    T = (1 << 30) + 192
+    x, W = torch.zeros(T, 8, device="cuda"), whole(8, 8, dtype=F32, seed=3)
+    near = [slice(0, 999), slice(T // 2, T // 2 + 999), slice(T - 4000, T)]
+    for i, n in enumerate(near):
+        x[n] = whole(x[n].shape[0], 8, dtype=F32, seed=10 + i)
+    y = torch.full((T, 8), 7.5, device="cuda")
+    L.lora_gemm(x, W, y, T, 8, 8, L.LORA_F32)
+    for n in near:
+        assert torch.equal(y[n], x[n] @ W)
+    assert float(y[T // 4:T // 4 + 1000].abs().max()) == 0
+    del x, y
+    torch.cuda.empty_cache()
