@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(256) k_shrink_grouped(
     constexpr int RBN = BR / 16;                         // 16-row MFMA blocks
     __shared__ __attribute__((aligned(1024))) uint16_t smem[C::LDS_BYTES / 2];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wid = blockIdx.x;
+    // grid.z: rows past what grid.x holds
+    const int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+    if (wg >= n_work_upper + ((int64_t)T + BR - 1) / BR) return;
+    const int wid = (int)wg;
     const int VS = ss.n * max_rank;                      // v row stride: all slices
     if (wid >= n_work_upper) {
         // base-only block: sorted positions [0, offsets[1]) get v = 0
@@ -504,7 +507,7 @@ lora_status_t launch_shrink(const void *x, int32_t T, const lora_pool_t *pools, 
     }
     // SGMV bf16: grouped over segment blocks; split K so that about 512
     // workgroups have work.
-    const int32_t row_blocks = (T + kShrinkRows - 1) / kShrinkRows;
+    const int32_t row_blocks = (int32_t)((T + (int64_t)kShrinkRows - 1) / kShrinkRows);
     const int32_t n_work_upper = row_blocks + (T < p.n_slots ? T : p.n_slots);
     int32_t split = (512 + row_blocks) / (row_blocks + 1);
     if (split > kMaxKSplit) split = kMaxKSplit;
@@ -516,7 +519,7 @@ lora_status_t launch_shrink(const void *x, int32_t T, const lora_pool_t *pools, 
     const uint16_t *xe = (const uint16_t *)x;
     const int rc = (VS + 15) / 16;
     const int32_t *offsets = ws_ptr<int32_t>(ws, L.offsets);
-    const dim3 grid(n_work_upper + row_blocks, split);
+    const dim3 blocks = grid_of(n_work_upper + row_blocks), grid(blocks.x, split, blocks.y);
     // Stages: 3 for narrow rank sets streaming long K ranges (more bytes in
     // flight per workgroup), else 2 (more workgroups resident per CU, which
     // serves short K ranges and wide rank sets better).

@@ -123,3 +123,23 @@ def test_f32_gemm():
     assert float(y[T // 4:T // 4 + 1000].abs().max()) == 0
     del x, y
     torch.cuda.empty_cache()
+
+
+def test_grouped_shrink():
+    """2^28 rows: 256 threads for every 16 rows."""
+    needs(185)
+    T = (1 << 28) + 64
+    pool, A, _, ids = two_slots(T, 8, 8, BF16)
+    x = torch.zeros(T, 8, dtype=BF16, device="cuda")
+    near = [slice(0, 999), slice(T // 2, T // 2 + 999), slice(T - 4000, T)]
+    for i, n in enumerate(near):
+        x[n] = whole(x[n].shape[0], 8, seed=10 + i)
+    ws = L.Workspace(T, 2, 8)
+    L.lora_build_segments(ids, T, 2, 8, ws.buf)
+    v = torch.full((T, 8), 7.5, device="cuda")
+    L.lora_shrink(x, T, pool.pool, ids, L.LORA_MODE_SGMV, v, ws.buf)
+    for n in near:
+        assert torch.equal(v[n], rank_vectors(x, A, ids, n.start, n.stop))
+    assert int((v == 7.5).sum()) == 0
+    del v, ws, x
+    torch.cuda.empty_cache()
