@@ -132,3 +132,13 @@ def test_64_rows(T):
         p = Pair(T, d, f, [16, 3, 8, 0, 13], 16, BF16, seed=T)
         for mode in (L.LORA_MODE_BGMV, L.LORA_MODE_SGMV):
             check_forward(p, "gelu_tanh", run_forward(p, "gelu_tanh", mode, keep=True), "64 rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_than_2_20_workgroups_of_rows(dtype):
+    """Rows past one grid dimension of the row kernels, and adapters of 200000 rows."""
+    p = Pair(600011, 16, 24, [8, 3, 5], 8, dtype, seed=51)
+    for mode in (L.LORA_MODE_BGMV, L.LORA_MODE_SGMV):
+        check_forward(p, "silu", run_forward(p, "silu", mode, keep=True), "forward")
+    k = kept(p)
+    check_backward(p, "silu", *k, run_backward(p, "silu", *k), "backward")
