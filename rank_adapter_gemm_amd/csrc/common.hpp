@@ -120,6 +120,16 @@ __device__ __forceinline__ void flag_bad_row(int32_t *err, int32_t row) {
     if (err) atomicMin(err, row);
 }
 
+// A grid of n workgroups, and a workgroup's number in it (past n in the last
+// row of a grid of two dimensions), for counts whose threads may pass 2^32 in
+// one dimension: the runtime launches a part of such a grid and reports no
+// error.
+inline dim3 grid_of(int64_t n) {
+    const int64_t w = 1 << 20;
+    return n <= w ? dim3((uint32_t)n) : dim3((uint32_t)w, (uint32_t)((n + w - 1) / w));
+}
+__device__ __forceinline__ int64_t grid_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // ---------------------------------------------------------------------------
 // Workspace layout (host side).  Regions are 256-byte aligned.
 // ---------------------------------------------------------------------------
@@ -132,14 +142,6 @@ constexpr int32_t kShortSegDefault = 16;
 // low-rank term is fused into the GEMM (those before the short-segment rows
 // in the GEMM's row order), the short-segment threshold of the build and the
 // number of short segments.
-// A grid of n workgroups, and a workgroup's number in it, for counts whose
-// threads may pass the runtime's 2^32 per grid dimension.
-inline dim3 grid_of(int64_t n) {
-    const int64_t w = 1 << 20;
-    return n <= w ? dim3((uint32_t)n) : dim3((uint32_t)w, (uint32_t)((n + w - 1) / w));
-}
-__device__ __forceinline__ int64_t grid_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
-
 constexpr int32_t kHdrErr = 0, kHdrNLong = 1, kHdrShortLen = 2, kHdrNShort = 3;
 constexpr int32_t kShrinkRows = 32;    // rows of one segment per grouped-shrink work block
 constexpr int32_t kMaxKSplit = 16;     // shrink k-split factor bound

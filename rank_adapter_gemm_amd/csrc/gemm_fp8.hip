@@ -295,10 +295,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     const int nk = (k_end - k_begin + BK - 1) / BK;
     constexpr int PER = XI + WI;                          // DMA instructions per stage per wave
     auto wait_stage = [&](int ahead) {                    // later stages still in flight
-        constexpr int V5 = 5 * PER > 63 ? 63 : 5 * PER, V4 = 4 * PER > 63 ? 63 : 4 * PER;
-        if (NS > 5 && ahead >= 5) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(V5) : "memory");
-        else if (NS > 4 && ahead >= 4) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(V4) : "memory");
-        else if (ahead >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER) : "memory");
+        if (ahead >= 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * PER) : "memory");
         else if (ahead == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PER) : "memory");
         else if (ahead == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER) : "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

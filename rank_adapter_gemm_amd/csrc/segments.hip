@@ -23,8 +23,7 @@
 //      same key (stable), perm[base + rank] = t, and its place in the GEMM
 //      order.
 // A batch of one tile takes one launch of one workgroup (k_seg_one): all of it
-// is latency, and two launches fewer save most of it (190 rows of 6 slots: 6 us
-// against 27 in three).
+// is latency (64 slots, rows at random: 1024 rows 9.7 us, 1025 in three launches 13).
 #include "common.hpp"
 
 namespace lora {
