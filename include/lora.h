@@ -583,7 +583,7 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
 /* Backward pass of the pair, the base weights frozen: from dh DEVICE
  * [T, d_out], the gradient of h, and gate and up as lora_gated_forward kept
  * them for the same x, ids and adapters, with s = scale[a], a = ids[t]:
- *     dg = dh u act'(g),   du = dh act(g)        (bf16 pools: rounded once)
+ *     dg = dh u act'(g),   du = dh act(g)
  *     dx = dg W_gate^T + du W_up^T + dv_g A_a^T + dv_u A_a^T,   dv = s d{g,u} B_a^T
  *     dA_a = sum over a's rows of x^T dv,        dB_a = s sum of (x A_a)^T d{g,u}
  * dx DEVICE [T, d_in], overwritten (NULL: not computed).  dA and dB HOST
@@ -592,8 +592,9 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
  * one slot's (lda = max_rank, ldb = d_out); padded so for packed pools too.
  * All of them are overwritten: a slot with no row in the batch, and ranks at
  * and past a slot's, get zeros (T == 0 too).  Both NULL: not computed.  All of
- * the pools' dtype, sums in fp32.  Rows without a usable adapter have only the base
- * term.  The sums over an adapter's rows are in batch order: the same inputs
+ * the pools' dtype, sums in fp32.  bf16 pools: dg and du are rounded once to
+ * bf16 in dx's base term, and kept to 2^-17 (two bf16 parts) in all others.
+ * Rows without a usable adapter have only the base term.  The sums over an adapter's rows are in batch order: the same inputs
  * give bitwise the same gradients.  dx, dA's and dB's buffers and ws share no
  * byte with each other or with anything the call reads (T > 0; else
  * LORA_ERR_INVALID_ARGUMENT).  ws: lora_workspace_bytes_gated_backward,

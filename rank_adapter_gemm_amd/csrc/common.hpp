@@ -327,7 +327,7 @@ lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *po
 // partials for 2 max_rank columns) and what follows it.
 struct bwd_layout {
     ws_layout L;
-    size_t dy;          // dg, du: [2][T][d_out], the pools' dtype
+    size_t dy;          // dg, du: [2][T][d_out], the pools' dtype; bf16: first parts, then second parts
     size_t dv;          // fp32 [T][2 max_rank]
     size_t vt;          // bf16 parts of s v and dv, transposed (see k_rank_finish)
     size_t oct;         // bf16: both slices' A in rank octets, one set per segment

@@ -11,6 +11,12 @@
 
 namespace lora {
 
+// What is left of a value beside its first bf16 part; an infinite or NaN value
+// has no second part.
+__device__ __forceinline__ float second_part(float rest) {
+    return fabsf(rest) < __builtin_inff() ? rest : 0.0f;
+}
+
 // act and its derivative at x.
 template <bool FINE> __device__ __forceinline__ void act_both(int act, float x, float &a, float &da) {
     if (act == LORA_ACT_SILU) {
@@ -30,14 +36,18 @@ template <bool FINE> __device__ __forceinline__ void act_both(int act, float x, 
     }
 }
 
-// dg and du of 16 bytes of values per thread.  For bf16 they are rounded
-// once: they are operands of bf16 matrix products, and their rounding enters
-// each sum as one more rounding of an input would.  Bound by its bytes: 2048 x
-// 14336, 45 us, 6.5 TB/s.
+// dg and du of 16 bytes of values per thread.  bf16: two bf16 parts each, hi =
+// bf16(f) and, `lo` values on, bf16(f - hi), together within 2^-17 of f.  The
+// adapters' gradients take both (a sum over an adapter's few rows shows a
+// rounding of dg: with hi alone their error against 64 bits was 1.3 to 1.8 times
+// that of 32-bit products); dx, a sum over 2 d_out terms, takes hi, one more
+// rounding of an operand, for half the matrix products (its error is 1.41 times
+// that of 32-bit products at every size).
+// Bound by its bytes: 2048 x 14336, 62 us, 6.6 TB/s.
 template <int DT>
 __global__ void __launch_bounds__(256) k_gated_dact(const typename elem<DT>::T *gate, const typename elem<DT>::T *up,
                                                     const typename elem<DT>::T *dh, typename elem<DT>::T *dg,
-                                                    typename elem<DT>::T *du, int64_t n_vec, int act) {
+                                                    typename elem<DT>::T *du, int64_t lo, int64_t n_vec, int act) {
     constexpr int VN = vec16<DT>::n;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n_vec; i += gridDim.x * 256ll) {
         float g[VN], u[VN], h[VN];
@@ -51,8 +61,21 @@ __global__ void __launch_bounds__(256) k_gated_dact(const typename elem<DT>::T *
             g[e] = h[e] * u[e] * da;
             u[e] = h[e] * a;
         }
-        stg16(dg + i * VN, vec16<DT>::narrow(g));
-        stg16(du + i * VN, vec16<DT>::narrow(u));
+        const uint4 gq = vec16<DT>::narrow(g), uq = vec16<DT>::narrow(u);
+        stg16(dg + i * VN, gq);
+        stg16(du + i * VN, uq);
+        if constexpr (DT == LORA_BF16) {
+            float gh[VN], uh[VN];
+            vec16<DT>::widen(gq, gh);
+            vec16<DT>::widen(uq, uh);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                g[e] = second_part(g[e] - gh[e]);
+                u[e] = second_part(u[e] - uh[e]);
+            }
+            stg16(dg + lo + i * VN, vec16<DT>::narrow(g));
+            stg16(du + lo + i * VN, vec16<DT>::narrow(u));
+        }
     }
 }
 
@@ -107,18 +130,18 @@ __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>:
 // (ds_read_b64_tr_b16: 4 n of 16 ranks per instruction).  Each of the 4
 // wavefronts takes a 32-n quarter of every stage; N is split over blockIdx.y.
 // Partial sums go to part[m][split][sorted position][R].  Bound by the bytes of
-// dg and du (2048 rows of 14336: 24 us, 5 TB/s).
+// dg's and du's parts (2048 rows of 14336: 43 us, 5.5 TB/s).
 template <int RCH> struct rank_grad_cfg {
     static constexpr int BR = kShrinkRows, NR = RCH * 16, BK = 128, CH = BK / 8, NS = 3;
     static constexpr int OCT = BK * 8 + 16;              // elements between octets (32 bytes apart in the banks)
-    static constexpr int YST = BR * BK, STAGE = YST + (NR / 8) * OCT;
+    static constexpr int YST = BR * BK, STAGE = 2 * YST + (NR / 8) * OCT;   // dy's two parts, B
     static constexpr int YI = BR * CH / 256, BI = NR / 8 * BK / 256;   // DMA instructions per wave per stage
     static constexpr int RED = 4 * BR * (NR + 1);
     static constexpr int LDS_BYTES = NS * STAGE * 2 > RED * 4 ? NS * STAGE * 2 : RED * 4;
 };
 
 struct rank_grad_args {
-    const uint16_t *dy;                // [2][T][N]
+    const uint16_t *dy;                // first and second parts: [2][2][T][N]
     int32_t T, N, R, n_slots, n_chunk;
     const int32_t *perm, *seg_id, *seg_start, *n_seg, *blk_start, *blk_seg;
     float *part;
@@ -126,7 +149,7 @@ struct rank_grad_args {
 
 template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_args g, pair_pools pp) {
     typedef rank_grad_cfg<RCH> C;
-    constexpr int BR = C::BR, NR = C::NR, BK = C::BK, CH = C::CH, NS = C::NS, PER = C::YI + C::BI;
+    constexpr int BR = C::BR, NR = C::NR, BK = C::BK, CH = C::CH, NS = C::NS, PER = 2 * C::YI + C::BI;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[C::LDS_BYTES / 2];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = blockIdx.z;
     const int nseg = min(*g.n_seg, g.n_slots);
@@ -141,6 +164,7 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
     const int p0 = (int)q0, pend = (int)(s1 < q0 + BR ? s1 : q0 + BR);
     const int32_t rk = min(pp.rank[m][id], g.R);
     const int n_begin = blockIdx.y * g.n_chunk, n_end = min(g.N, n_begin + g.n_chunk);
+    const int64_t lo = 2ll * g.T * g.N;
     const uint16_t *dy = g.dy + (int64_t)m * g.T * g.N;
     const uint16_t *b = (const uint16_t *)pp.b[m] + slot_row0(pp.row0[m], id, g.R) * g.N;
 
@@ -154,14 +178,16 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
         ycol[j] = 8 * ((c % CH) ^ (r % CH));
     }
     auto dma_stage = [&](int kt, int buf) {
-        uint16_t *ys = smem + buf * C::STAGE, *bs = ys + C::YST;
+        uint16_t *ys = smem + buf * C::STAGE, *bs = ys + 2 * C::YST;
         const int k0 = n_begin + kt * BK;
 #pragma unroll
-        for (int j = 0; j < C::YI; ++j) {
-            const int n = k0 + ycol[j];
-            dma16(yrow[j] >= 0 && n < n_end ? (const void *)(dy + yrow[j] + n) : (const void *)g_zero16,
-                  ys + (wave * C::YI + j) * 64 * 8);
-        }
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int j = 0; j < C::YI; ++j) {
+                const int n = k0 + ycol[j];
+                dma16(yrow[j] >= 0 && n < n_end ? (const void *)(dy + part * lo + yrow[j] + n) : (const void *)g_zero16,
+                      ys + part * C::YST + (wave * C::YI + j) * 64 * 8);
+            }
 #pragma unroll
         for (int j = 0; j < C::BI; ++j) {                 // half an octet's 128 columns per instruction
             const int i = wave * C::BI + j, o = i >> 1, n = k0 + (i & 1) * 64 + lane;
@@ -191,13 +217,16 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
-        const uint16_t *ys = smem + (kt % NS) * C::STAGE, *bs = ys + C::YST;
-        uint4 yq[2];
+        const uint16_t *ys = smem + (kt % NS) * C::STAGE, *bs = ys + 2 * C::YST;
+        uint4 yq[2][2];
         bf16x8_t bq[RCH];
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb) {
             const int r = rb * 16 + l16;
-            yq[rb] = *reinterpret_cast<const uint4 *>(ys + r * BK + 8 * ((4 * wave + kg) ^ (r % CH)));
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+                yq[part][rb] = *reinterpret_cast<const uint4 *>(ys + part * C::YST + r * BK +
+                                                                8 * ((4 * wave + kg) ^ (r % CH)));
         }
 #pragma unroll
         for (int rc = 0; rc < RCH; ++rc) {
@@ -213,11 +242,13 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
             bq[rc] = __builtin_bit_cast(bf16x8_t, hv);
         }
 #pragma unroll
-        for (int rb = 0; rb < 2; ++rb)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int rc = 0; rc < RCH; ++rc)
-                acc[rb][rc] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, yq[rb]), bq[rc],
-                                                                      acc[rb][rc], 0, 0, 0);
+            for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+                for (int rc = 0; rc < RCH; ++rc)
+                    acc[rb][rc] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, yq[part][rb]),
+                                                                          bq[rc], acc[rb][rc], 0, 0, 0);
     }
     __syncthreads();                                      // all waves done with the stages
     float (*red)[BR][NR + 1] = reinterpret_cast<float (*)[BR][NR + 1]>(smem);
@@ -334,11 +365,10 @@ __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, a_octet
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             const uint32_t hi = f32_to_bf16_bits(f[w]);
-            // an infinite or NaN value has no second part
-            const float rest = f[w] - __uint_as_float(hi << 16);
+            const float rest = second_part(f[w] - __uint_as_float(hi << 16));
             uint16_t *o = g.vt + (int64_t)w * 2 * R2 * g.Tp + (int64_t)j * g.Tp + at;
             o[0] = (uint16_t)hi;
-            o[(int64_t)R2 * g.Tp] = (uint16_t)f32_to_bf16_bits(rest == rest ? rest : 0.0f);
+            o[(int64_t)R2 * g.Tp] = (uint16_t)f32_to_bf16_bits(rest);
         }
     }
 }
@@ -843,41 +873,45 @@ __global__ void __launch_bounds__(256, 2) k_dx_outer_f32(dx_f32_args d, outer_f3
 // vt's rows are DMA'd into a ring of stages, q read transposed as the base
 // GEMM reads W.  One launch holds both gradients: the workgroups of dA (both
 // projections' ranks at once, so x is read once) come first, then dB's.  Bound
-// by the bytes of x, dg and du (2048 rows of 4 slots, 4096 and 14336 wide: 30
-// us, 4.5 TB/s).
+// by the bytes of x and of dg's and du's parts (2048 rows of 4 slots, 4096 and
+// 14336 wide: 43 us, 5.9 TB/s).
 constexpr int kOuterCols = 128, kOuterRows = 1024;
 struct seg_outer_args {
-    const uint16_t *x, *dy, *vt;       // [T][K], [2][T][N], see k_rank_finish
+    const uint16_t *x, *dy, *vt;       // [T][K], [2][2][T][N] (both first parts, both second), see k_rank_finish
     uint16_t *dA[2], *dB[2];
     int32_t T, K, N, R, n_slots, Tp;
     const int32_t *perm, *offsets, *rank[2], *slot_blk;
     int32_t tiles_k, tiles_n;          // column tiles of x and of dy
 };
 
-template <int MB> struct outer_cfg {
-    static constexpr int BT = 32, NS = MB > 2 ? 3 : 4;
-    static constexpr int QST = BT * kOuterCols, PST = 32 * MB * BT, STAGE = QST + 2 * PST;
+template <int MB, int QP> struct outer_cfg {              // QP: parts of q
+    static constexpr int BT = 32, NS = MB > 2 || QP > 1 ? 3 : 4;
+    static constexpr int QST = BT * kOuterCols, PST = 32 * MB * BT, STAGE = QP * QST + 2 * PST;
     static constexpr int QI = QST / 8 / 256, PI = 2 * PST / 8 / 256;   // DMA instructions per wave per stage
 };
 
 // rank rows [0, nj) at vt + j Tp (and, 2 R Tp on, their second parts), rows p0..p1 of
-// perm at places b0.., columns [n0, n0 + 128) of q [T][N].
-template <int MB>
+// perm at places b0.., columns [n0, n0 + 128) of q [T][N] (QP = 2: and of its
+// second part, q_lo on; the product of the second parts, 2^-16 of the whole, is
+// left out).
+template <int MB, int QP>
 __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *smem, int32_t *s_row,
                                               const seg_outer_args &g,
-                                              const uint16_t *q, int N, int n0, const uint16_t *vt, int nj, int p0,
-                                              int p1, int64_t b0) {
-    typedef outer_cfg<MB> C;
-    constexpr int BT = C::BT, NS = C::NS, QI = C::QI, PI = C::PI, PER = QI + PI;
+                                              const uint16_t *q, int64_t q_lo, int N, int n0, const uint16_t *vt, int nj,
+                                              int p0, int p1, int64_t b0) {
+    typedef outer_cfg<MB, QP> C;
+    constexpr int BT = C::BT, NS = C::NS, QI = C::QI, PI = C::PI, PER = QP * QI + PI;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     auto dma_stage = [&](int kt, int buf) {
-        uint16_t *qs = smem + buf * C::STAGE, *ps = qs + C::QST;
+        uint16_t *qs = smem + buf * C::STAGE, *ps = qs + QP * C::QST;
 #pragma unroll
         for (int j = 0; j < QI; ++j) {
             const int c = (wave * QI + j) * 64 + lane, r = c >> 4, col = n0 + 8 * ((c & 15) ^ swz_w<kOuterCols>(r));
             const int32_t t = s_row[kt * BT + r];
-            dma16(t >= 0 && col < N ? (const void *)(q + (int64_t)t * N + col) : (const void *)g_zero16,
-                  qs + (wave * QI + j) * 64 * 8);
+#pragma unroll
+            for (int part = 0; part < QP; ++part)
+                dma16(t >= 0 && col < N ? (const void *)(q + part * q_lo + (int64_t)t * N + col) : (const void *)g_zero16,
+                      qs + part * C::QST + (wave * QI + j) * 64 * 8);
         }
 #pragma unroll
         for (int j = 0; j < PI; ++j) {                    // rank rows of 4 chunks: first parts, then second parts
@@ -913,25 +947,32 @@ __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *sme
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
-        const uint16_t *qs = smem + (kt % NS) * C::STAGE, *ps = qs + C::QST;
+        const uint16_t *qs = smem + (kt % NS) * C::STAGE, *ps = qs + QP * C::QST;
 #pragma unroll
         for (int ks = 0; ks < BT / 16; ++ks) {
-            short4_t h[2];
+            bf16x8_t bq[QP];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = 16 * ks + 4 * i + b_kofs;
-                const uint16_t *at = qs + k * kOuterCols + 8 * ((b_col >> 3) ^ swz_w<kOuterCols>(k)) + (b_col & 7);
-                h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t *)(reinterpret_cast<uintptr_t>(at)));
+            for (int part = 0; part < QP; ++part) {
+                short4_t h[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int k = 16 * ks + 4 * i + b_kofs;
+                    const uint16_t *at = qs + part * C::QST + k * kOuterCols + 8 * ((b_col >> 3) ^ swz_w<kOuterCols>(k)) +
+                                         (b_col & 7);
+                    h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t *)(reinterpret_cast<uintptr_t>(at)));
+                }
+                const short8_t hv = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
+                bq[part] = __builtin_bit_cast(bf16x8_t, hv);
             }
-            const short8_t hv = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
-            const bf16x8_t bq = __builtin_bit_cast(bf16x8_t, hv);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
                     const int r = mb * 32 + fr, ch = (2 * ks + fk) ^ ((r >> 1) & 3);
                     const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(ps + part * C::PST + r * BT + 8 * ch);
-                    acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, bq, acc[mb], 0, 0, 0);
+                    acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, bq[0], acc[mb], 0, 0, 0);
+                    if constexpr (QP > 1)
+                        if (part == 0) acc[mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, bq[QP - 1], acc[mb], 0, 0, 0);
                 }
         }
     }
@@ -939,7 +980,8 @@ __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *sme
 }
 
 template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
-    constexpr int LA = outer_cfg<MBA>::NS * outer_cfg<MBA>::STAGE, LB = outer_cfg<MBB>::NS * outer_cfg<MBB>::STAGE;
+    constexpr int LA = outer_cfg<MBA, 1>::NS * outer_cfg<MBA, 1>::STAGE;
+    constexpr int LB = outer_cfg<MBB, 2>::NS * outer_cfg<MBB, 2>::STAGE;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[LA > LB ? LA : LB];
     __shared__ int32_t s_row[kOuterRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -963,7 +1005,7 @@ template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_m
         for (int mb = 0; mb < MBA; ++mb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
-        seg_outer_sum<MBA>(acc, smem, s_row, g, g.x, N, n0, g.vt + (int64_t)2 * 2 * R * g.Tp, 2 * R, p0, p1, b0);
+        seg_outer_sum<MBA, 1>(acc, smem, s_row, g, g.x, 0, N, n0, g.vt + (int64_t)2 * 2 * R * g.Tp, 2 * R, p0, p1, b0);
         if (col >= N) return;
         // [slot][k][j]: a lane's accumulators hold groups of 4 neighbouring ranks of its k
 #pragma unroll
@@ -985,8 +1027,8 @@ template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_m
         for (int mb = 0; mb < MBB; ++mb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
-        seg_outer_sum<MBB>(acc, smem, s_row, g, g.dy + (int64_t)m * g.T * N, N, n0, g.vt + (int64_t)m * R * g.Tp, R, p0, p1,
-                           b0);
+        seg_outer_sum<MBB, 2>(acc, smem, s_row, g, g.dy + (int64_t)m * g.T * N, 2ll * g.T * N, N, n0,
+                              g.vt + (int64_t)m * R * g.Tp, R, p0, p1, b0);
         if (col >= N) return;
         uint16_t *out = (m ? g.dB[1] : g.dB[0]) + (int64_t)slot * R * N + col;
 #pragma unroll
@@ -1010,7 +1052,7 @@ bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t R, int32_t d_in, 
     const size_t t = (size_t)(T > 0 ? T : 1), eb = dtype == LORA_F32 ? 4 : 2;
     const size_t segs = (size_t)n_slots < t ? (size_t)n_slots : t;
     size_t o = B.L.total;
-    B.dy = o;      o = align256(o + 2 * t * (size_t)d_out * eb);
+    B.dy = o;      o = align256(o + (dtype == LORA_BF16 ? 4 : 2) * t * (size_t)d_out * eb);
     B.dv = o;      o = align256(o + 4 * t * 2 * (size_t)R);
     // transposed bf16 parts of s v and dv, every segment from a work block on
     B.vt = o;      o = align256(o + (dtype == LORA_BF16 ? 16 * (size_t)R * 32 * ((t + 31) / 32 + segs) : 0));
@@ -1048,7 +1090,8 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     const pair_pools pp = make_pair_pools(p);
     const int64_t n_vec = (int64_t)T * F / vec16<DT>::n;
     hipLaunchKernelGGL(k_gated_dact<DT>, dim3((uint32_t)(n_vec < (1 << 24) ? (n_vec + 255) / 256 : 1 << 16)),
-                       dim3(256), 0, s, (const E *)c.gate, (const E *)c.up, (const E *)c.dh, dg, du, n_vec, c.act);
+                       dim3(256), 0, s, (const E *)c.gate, (const E *)c.up, (const E *)c.dh, dg, du, 2ll * T * F, n_vec,
+                       c.act);
     // v = x A (also records the bad ids); dv
     st = DT == LORA_F32 ? launch_shrink_pair(c.x, T, p, c.ids, v, ws_ptr<int32_t>(ws, L.header), s)
                         : launch_shrink(c.x, T, p, 2, c.ids, true, v, L, ws, s);
