@@ -573,7 +573,9 @@ lora_status_t lora_gated_forward(const void *x, const void *W_gate, const void *
 /* The same on FP8 base weights (bf16 x, h and pools; d_in a multiple of 16):
  * wq_* and w_scale_* from lora_quantize_weight_fp8.  xq and x_scale are the
  * codes and scales of x's rows (lora_add_rmsnorm_fp8, lora_quantize_rows_fp8;
- * DEVICE uint8 [T, d_in] and fp32 [T]); both NULL: x is quantized into ws. */
+ * DEVICE uint8 [T, d_in] and fp32 [T]); both NULL: x is quantized into ws.
+ * There is no backward pass on FP8 base weights: lora_gated_backward takes gate
+ * and up kept here with the weights in bf16. */
 lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const float *x_scale, const uint8_t *wq_gate,
                                      const float *w_scale_gate, const uint8_t *wq_up, const float *w_scale_up,
                                      void *h, void *gate, void *up, int32_t T, const lora_pool_t *pools,
