@@ -61,7 +61,7 @@ typedef struct ihipStream_t *lora_stream_t; /* a hipStream_t; NULL = the null st
 
 typedef enum {
     LORA_OK = 0,
-    LORA_ERR_INVALID_ARGUMENT = 1,   /* null pointer, bad size, bad dtype, misaligned pointer */
+    LORA_ERR_INVALID_ARGUMENT = 1,   /* null pointer, bad size, bad dtype, misaligned pointer, an output over another buffer */
     LORA_ERR_RANK_EXCEEDS_MAX = 2,   /* upload with r > max_rank ("Serving LoRA adapters ...", Step 3: the rank check against the maximum LoRA rank) */
     LORA_ERR_SLOT_OUT_OF_RANGE = 3,  /* slot outside [0, n_slots) */
     LORA_ERR_WORKSPACE_TOO_SMALL = 4,
