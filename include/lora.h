@@ -600,7 +600,8 @@ lora_status_t lora_gated_forward_fp8(const void *x, const uint8_t *xq, const flo
  * give bitwise the same gradients.  dx, dA's and dB's buffers and ws share no
  * byte with each other or with anything the call reads (T > 0; else
  * LORA_ERR_INVALID_ARGUMENT).  ws: lora_workspace_bytes_gated_backward,
- * cleared by lora_workspace_init. */
+ * cleared by lora_workspace_init.  bf16 pools with dx: min(n_slots, T) * d_in
+ * below 2^32 (LORA_ERR_UNSUPPORTED from about there on). */
 size_t lora_workspace_bytes_gated_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out,
                                            lora_dtype_t dtype);
 lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void *W_up, int32_t T,

@@ -1082,6 +1082,9 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     const int32_t T = c.T, K = p[0].d_in, F = p[0].d_out, R = p[0].max_rank, S = p[0].n_slots;
     const ws_layout &L = B.L;
     void *ws = c.ws;
+    // k_rank_finish has its workgroups in one grid dimension, which holds fewer than 2^32 threads
+    const int64_t finish = 2 * ceil_div(T, kShrinkRows) + (S < T ? S : T) * (1ll + (c.dx ? ceil_div(K, 256) : 0));
+    if (DT == LORA_BF16 && finish * 256 >= 1ll << 32) return LORA_ERR_UNSUPPORTED;
     lora_status_t st = launch_segments(c.ids, T, S, L, ws, s, 1);
     if (st != LORA_OK) return st;
     const int32_t *perm = ws_ptr<int32_t>(ws, L.perm), *offsets = ws_ptr<int32_t>(ws, L.offsets);
