@@ -129,10 +129,12 @@ __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>:
 // a column) lie in LDS as in memory and are read transposed
 // (ds_read_b64_tr_b16: 4 n of 16 ranks per instruction).  Each of the 4
 // wavefronts takes a 32-n quarter of every stage; N is split over blockIdx.y.
+// Two stages for wide ranks, so that two workgroups fit a CU (64 ranks, 2048 rows
+// of 14336: 57 us, with three stages 64; 16 ranks 46 and 40).
 // Partial sums go to part[m][split][sorted position][R].  Bound by the bytes of
 // dg's and du's parts (2048 rows of 14336: 43 us, 5.5 TB/s).
 template <int RCH> struct rank_grad_cfg {
-    static constexpr int BR = kShrinkRows, NR = RCH * 16, BK = 128, CH = BK / 8, NS = 3;
+    static constexpr int BR = kShrinkRows, NR = RCH * 16, BK = 128, CH = BK / 8, NS = RCH > 2 ? 2 : 3;
     static constexpr int OCT = BK * 8 + 16;              // elements between octets (32 bytes apart in the banks)
     static constexpr int YST = BR * BK, STAGE = 2 * YST + (NR / 8) * OCT;   // dy's two parts, B
     static constexpr int YI = BR * CH / 256, BI = NR / 8 * BK / 256;   // DMA instructions per wave per stage
