@@ -535,6 +535,43 @@ lora_status_t lora_add_rmsnorm_fp8(const void *x, const void *residual, const vo
                                    int32_t d, void *residual_out, void *y, uint8_t *yq, float *y_scale,
                                    lora_stream_t stream);
 
+/* ---- layer norm, and its backward pass --------------------------------------------- */
+
+/* As lora_add_rmsnorm, with the mean taken out and a bias: for every row t
+ *     z = x[t,:] + residual[t,:],   y = (z - mean(z)) / sqrt(var(z) + eps) * weight + bias
+ * var(z) = mean((z - mean(z))^2), in fp32.  bias DEVICE [d], may be NULL (none).
+ * mean and rstd DEVICE fp32 [T] keep mean(z) and 1 / sqrt(var(z) + eps) for the
+ * backward pass; both may be NULL.  Everything else as lora_add_rmsnorm: z's and
+ * y's buffers may be x's or the residual's own, no output meets another. */
+lora_status_t lora_add_layernorm(const void *x, const void *residual, const void *weight, const void *bias, float eps,
+                                 int32_t T, int32_t d, lora_dtype_t dtype, void *residual_out, void *y, float *mean,
+                                 float *rstd, lora_stream_t stream);
+
+/* The same for bf16 rows that feed an FP8 base weight, as lora_add_rmsnorm_fp8. */
+lora_status_t lora_add_layernorm_fp8(const void *x, const void *residual, const void *weight, const void *bias,
+                                     float eps, int32_t T, int32_t d, void *residual_out, void *y, uint8_t *yq,
+                                     float *y_scale, float *mean, float *rstd, lora_stream_t stream);
+
+/* Backward pass, from dy (the gradient of y), z as residual_out kept it (x itself
+ * where there was no residual), and the mean and rstd kept.  With h = (z - mean) rstd
+ * and a = dy * weight, per row:
+ *     dx = rstd (a - mean(a) - h mean(a h)) + dresidual
+ *     dweight = sum over the rows of dy h,   dbias = sum of dy
+ * dx is the gradient of x and of residual alike; dresidual DEVICE [T, d], may be
+ * NULL, is what reached residual_out from after this norm.  dweight and dbias
+ * DEVICE [d], overwritten (zeros for T == 0); each may be NULL (not computed).  All
+ * but mean and rstd (fp32 [T]) of `dtype`, each output rounded once from fp32
+ * sums, whose order is fixed: the same inputs give bitwise the same gradients.  dx
+ * may be dy's, z's or dresidual's own buffer; beyond that an output that shares a byte
+ * with another buffer is refused.  ws DEVICE, ws_bytes at least
+ * lora_workspace_bytes_layernorm_backward (0 on bad arguments); it needs no
+ * lora_workspace_init, and may be NULL where neither dweight nor dbias is asked for. */
+size_t lora_workspace_bytes_layernorm_backward(int32_t T, int32_t d);
+lora_status_t lora_add_layernorm_backward(const void *dy, const void *dresidual, const void *z, const void *weight,
+                                          const float *mean, const float *rstd, int32_t T, int32_t d,
+                                          lora_dtype_t dtype, void *dx, void *dweight, void *dbias, void *ws,
+                                          size_t ws_bytes, lora_stream_t stream);
+
 /* ---- the gated feed-forward pair --------------------------------------------------- */
 
 /* Gate and up of a feed-forward block, each with its own pool, and what is
@@ -608,6 +645,31 @@ lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void 
                                   const lora_pool_t *pools, const int32_t *ids, lora_act_t act, const void *gate,
                                   const void *up, const void *dh, void *dx, void *const *dA, void *const *dB,
                                   void *ws, size_t ws_bytes, lora_stream_t stream);
+
+/* ---- orthogonalised updates ---------------------------------------------------------- */
+
+/* What an orthogonalising optimiser makes of a gradient (or of its momentum): for
+ * each of n matrices g[i] [rows, cols], row-major one after the other -- the
+ * gradients dA [n_slots, d_in, max_rank] or dB [n_slots, max_rank, d_out] of a
+ * pool's adapters --
+ *     X = g[i] / (|g[i]| + eps),   |.| the square root of the sum of squares;
+ *     X <- c0 X + c1 (X X^T) X + c2 (X X^T)^2 X   for the steps in turn;   out[i] = scale X
+ * (Newton-Schulz products, which bring the singular values near 1 and keep the
+ * singular vectors).  coef HOST fp32 [steps][3] (c0, c1, c2 of each step), 1 <= steps
+ * <= LORA_MAX_ORTHO_STEPS.  g and out DEVICE of `dtype`; out may be g's own buffer,
+ * else it shares no byte with it or ws.  rows and cols positive multiples of 8, the
+ * smaller at most LORA_MAX_ORTHO_SIDE, the larger below 2^28 (LORA_ERR_UNSUPPORTED
+ * past these).  Zero rows and columns (ranks past an adapter's) and zero matrices
+ * stay zero; a matrix with infinite or NaN values gives NaN, and leaves the others as
+ * they are.  eps finite and positive, scale finite.  Sums of products of g and the steps are in 64 bits, and
+ * for fp32 also the last product; the order of the sums is fixed.  ws DEVICE, ws_bytes at least
+ * lora_workspace_bytes_orthogonalize (0 on bad arguments); it needs no lora_workspace_init. */
+#define LORA_MAX_ORTHO_SIDE 128
+#define LORA_MAX_ORTHO_STEPS 16
+size_t lora_workspace_bytes_orthogonalize(int32_t n, int32_t rows, int32_t cols);
+lora_status_t lora_orthogonalize(const void *g, int32_t n, int32_t rows, int32_t cols, lora_dtype_t dtype,
+                                 const float *coef, int32_t steps, float eps, float scale, void *out, void *ws,
+                                 size_t ws_bytes, lora_stream_t stream);
 
 /* ---- the layer without a caller workspace ---------------------------------------- */
 

@@ -845,6 +845,115 @@ lora_status_t lora_add_rmsnorm_fp8(const void *x, const void *residual, const vo
     return launch_add_rmsnorm(x, residual, weight, eps, T, d, LORA_BF16, residual_out, y, yq, y_scale, hs(stream));
 }
 
+// The layer norms': as valid_norm, with a bias and the kept statistics.
+static bool valid_layernorm(const void *x, const void *residual, const void *weight, const void *bias, float eps,
+                            int32_t T, int32_t d, int32_t d_step, int32_t dtype, const void *residual_out, const void *y,
+                            const void *yq, const void *ys, const float *mean, const float *rstd) {
+    if (!valid_norm(x, residual, weight, eps, T, d, d_step, dtype, residual_out, y, yq, ys) || !mean != !rstd) return false;
+    if (T == 0) return true;
+    if (!aligned16(bias) || !aligned16(mean) || !aligned16(rstd)) return false;
+    const size_t n = (size_t)T * d, eb = dtype_bytes(dtype), t4 = 4 * (size_t)T;
+    const span stats[] = {{mean, t4}, {rstd, t4}};
+    const span other[] = {{x, n * eb}, {residual, n * eb}, {weight, d * eb}, {bias, d * eb}, {residual_out, n * eb},
+                          {y, n * eb}, {yq, n}, {ys, t4}};
+    const span b = {bias, d * eb};
+    return outputs_clear(stats, 2, other, 8) && outputs_clear(other + 4, 1, &b, 1) && outputs_clear(other + 5, 1, &b, 1) &&
+           outputs_clear(other + 6, 2, &b, 1);
+}
+
+lora_status_t lora_add_layernorm(const void *x, const void *residual, const void *weight, const void *bias, float eps,
+                                 int32_t T, int32_t d, lora_dtype_t dtype, void *residual_out, void *y, float *mean,
+                                 float *rstd, lora_stream_t stream) {
+    if (!valid_dtype(dtype) ||
+        !valid_layernorm(x, residual, weight, bias, eps, T, d, 8, dtype, residual_out, y, nullptr, nullptr, mean, rstd) ||
+        (T > 0 && !y))
+        return LORA_ERR_INVALID_ARGUMENT;
+    return launch_add_layernorm(x, residual, weight, bias, eps, T, d, dtype, residual_out, y, nullptr, nullptr, mean,
+                                rstd, hs(stream));
+}
+
+lora_status_t lora_add_layernorm_fp8(const void *x, const void *residual, const void *weight, const void *bias,
+                                     float eps, int32_t T, int32_t d, void *residual_out, void *y, uint8_t *yq,
+                                     float *y_scale, float *mean, float *rstd, lora_stream_t stream) {
+    if (!valid_layernorm(x, residual, weight, bias, eps, T, d, 16, LORA_BF16, residual_out, y, yq, y_scale, mean, rstd) ||
+        (T > 0 && (!yq || !y_scale || !aligned16(yq) || !aligned16(y_scale))))
+        return LORA_ERR_INVALID_ARGUMENT;
+    return launch_add_layernorm(x, residual, weight, bias, eps, T, d, LORA_BF16, residual_out, y, yq, y_scale, mean,
+                                rstd, hs(stream));
+}
+
+size_t lora_workspace_bytes_layernorm_backward(int32_t T, int32_t d) {
+    if (T < 0 || d <= 0 || (d % 8)) return 0;
+    return layernorm_partial_bytes(T, d);
+}
+
+lora_status_t lora_add_layernorm_backward(const void *dy, const void *dresidual, const void *z, const void *weight,
+                                          const float *mean, const float *rstd, int32_t T, int32_t d,
+                                          lora_dtype_t dtype, void *dx, void *dweight, void *dbias, void *ws,
+                                          size_t ws_bytes, lora_stream_t stream) {
+    if (!valid_dtype(dtype) || T < 0 || d <= 0 || (d % 8) || !aligned16(dweight) || !aligned16(dbias))
+        return LORA_ERR_INVALID_ARGUMENT;
+    const hipStream_t s = hs(stream);
+    const size_t eb = dtype_bytes(dtype), row = (size_t)d * eb;
+    if (T == 0) {
+        const span out[] = {{dweight, row}, {dbias, row}};
+        if (!outputs_clear(out, 2, nullptr, 0)) return LORA_ERR_INVALID_ARGUMENT;
+        lora_status_t st = dweight ? launch_zero(dweight, row, s) : LORA_OK;
+        if (st == LORA_OK && dbias) st = launch_zero(dbias, row, s);
+        return st;
+    }
+    if (!dy || !z || !weight || !mean || !rstd || !dx || !aligned16(dy) || !aligned16(dresidual) || !aligned16(z) ||
+        !aligned16(weight) || !aligned16(mean) || !aligned16(rstd) || !aligned16(dx))
+        return LORA_ERR_INVALID_ARGUMENT;
+    const bool sums = dweight || dbias;
+    if (sums && (!ws || !aligned16(ws))) return LORA_ERR_INVALID_ARGUMENT;
+    if (sums && ws_bytes < layernorm_partial_bytes(T, d)) return LORA_ERR_WORKSPACE_TOO_SMALL;
+    const size_t rows = (size_t)T * row, t4 = 4 * (size_t)T;
+    const span out[] = {{dx, rows}, {dweight, row}, {dbias, row}, {sums ? ws : nullptr, ws_bytes}};
+    const span small[] = {{weight, row}, {mean, t4}, {rstd, t4}};
+    if (!outputs_clear(out, 4, small, 3)) return LORA_ERR_INVALID_ARGUMENT;
+    for (const void *in : {dy, dresidual, z}) {
+        const span read = {in, rows};
+        if (!outputs_clear(out + 1, 3, &read, 1) || (in != dx && !outputs_clear(out, 1, &read, 1)))
+            return LORA_ERR_INVALID_ARGUMENT;
+    }
+    return launch_layernorm_backward(dy, dresidual, z, weight, mean, rstd, T, d, dtype, dx, dweight, dbias,
+                                     static_cast<float *>(ws), s);
+}
+
+static_assert(LORA_MAX_ORTHO_SIDE == kMaxOrthoSide && LORA_MAX_ORTHO_STEPS == kMaxOrthoSteps, "as the header says");
+
+static lora_status_t check_ortho(int32_t n, int32_t rows, int32_t cols) {
+    if (n < 0 || rows <= 0 || cols <= 0 || (rows % 8) || (cols % 8)) return LORA_ERR_INVALID_ARGUMENT;
+    return (rows < cols ? rows : cols) > kMaxOrthoSide || rows >= 1 << 28 || cols >= 1 << 28 ? LORA_ERR_UNSUPPORTED : LORA_OK;
+}
+
+size_t lora_workspace_bytes_orthogonalize(int32_t n, int32_t rows, int32_t cols) {
+    return check_ortho(n, rows, cols) == LORA_OK ? ortho_workspace_bytes(n > 0 ? n : 1, rows, cols) : 0;
+}
+
+lora_status_t lora_orthogonalize(const void *g, int32_t n, int32_t rows, int32_t cols, lora_dtype_t dtype,
+                                 const float *coef, int32_t steps, float eps, float scale, void *out, void *ws,
+                                 size_t ws_bytes, lora_stream_t stream) {
+    const lora_status_t st = check_ortho(n, rows, cols);
+    if (st != LORA_OK) return st;
+    const float inf = __builtin_inff();
+    if (!valid_dtype(dtype) || !coef || steps < 1 || steps > kMaxOrthoSteps || !(eps > 0.0f) || !(eps < inf) ||
+        !(scale < inf) || !(scale > -inf))
+        return LORA_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!(coef[i] < inf) || !(coef[i] > -inf)) return LORA_ERR_INVALID_ARGUMENT;
+    if (n == 0) return LORA_OK;
+    if (!g || !out || !ws || !aligned16(g) || !aligned16(out) || !aligned16(ws)) return LORA_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < ortho_workspace_bytes(n, rows, cols)) return LORA_ERR_WORKSPACE_TOO_SMALL;
+    const size_t all = (size_t)n * rows * cols * dtype_bytes(dtype);
+    const span spans[] = {{ws, ws_bytes}, {out, all}}, read = {g, all};
+    if (!outputs_clear(spans, 1, &read, 1) || !outputs_clear(spans, 2, nullptr, 0) ||
+        (out != g && !outputs_clear(spans + 1, 1, &read, 1)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    return launch_orthogonalize(g, n, rows, cols, dtype, coef, steps, eps, scale, out, ws, hs(stream));
+}
+
 lora_status_t lora_linear_forward_noalloc(const void *x, const void *W, void *y, int32_t T,
                                           const lora_pool_t *pool, const int32_t *ids, lora_mode_t mode,
                                           uint32_t flags, int32_t *err_out, lora_stream_t stream) {

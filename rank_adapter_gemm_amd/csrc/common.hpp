@@ -356,4 +356,27 @@ lora_status_t launch_add_rmsnorm(const void *x, const void *residual, const void
                                  int32_t d, int32_t dtype, void *residual_out, void *y, uint8_t *yq, float *ys,
                                  hipStream_t s);
 
+// The layer norm of z = x + residual (residual, bias, residual_out, y, codes and
+// statistics may be null), and its backward pass: dx, and where part
+// (layernorm_partial_bytes) and an output for them are given, dweight and dbias.
+lora_status_t launch_add_layernorm(const void *x, const void *residual, const void *weight, const void *bias, float eps,
+                                   int32_t T, int32_t d, int32_t dtype, void *residual_out, void *y, uint8_t *yq,
+                                   float *ys, float *mean, float *rstd, hipStream_t s);
+size_t layernorm_partial_bytes(int32_t T, int32_t d);
+lora_status_t launch_layernorm_backward(const void *dy, const void *dres, const void *z, const void *weight,
+                                        const float *mean, const float *rstd, int32_t T, int32_t d, int32_t dtype,
+                                        void *dx, void *dweight, void *dbias, float *part, hipStream_t s);
+// part fp32 [groups][n], its columns added up in a fixed order: the first d into
+// out0, the rest into out1 (either may be null), of dtype.
+lora_status_t launch_column_sums(const float *part, int32_t groups, int32_t n, int32_t d, int32_t dtype, void *out0,
+                                 void *out1, hipStream_t s);
+
+// out = scale times the Newton-Schulz steps (coef [steps][3], host) on each of n
+// matrices [rows][cols], the shorter side at most kMaxOrthoSide.
+constexpr int32_t kMaxOrthoSteps = 16, kMaxOrthoSide = 128;
+size_t ortho_workspace_bytes(int32_t n, int32_t rows, int32_t cols);
+lora_status_t launch_orthogonalize(const void *in, int32_t n, int32_t rows, int32_t cols, int32_t dtype,
+                                   const float *coef, int32_t steps, float eps, float scale, void *out, void *ws,
+                                   hipStream_t s);
+
 }  // namespace lora

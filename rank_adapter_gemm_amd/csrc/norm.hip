@@ -14,8 +14,7 @@
 // than a plain copy of 1 GiB reaches) and, for few rows, by one trip to memory
 // and back: a row has as many threads as give each one or two of its 16-byte
 // vectors, so that all of it is in flight at once (one row of 4096: 2.2 us).
-#include "common.hpp"
-#include "fp8_common.hpp"
+#include "norm_common.hpp"
 
 namespace lora {
 
@@ -28,38 +27,6 @@ struct norm_args {
     int32_t T, d;
 };
 
-// Reductions over the NT threads of one row (rows of 64 threads need no LDS).
-// `slot` keeps two reductions of one row apart in LDS.
-template <int NT, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float (*red)[NT / 64], int slot, int lane, int wave) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const float w = __shfl_xor(v, o, 64);
-        v = MAX ? fmaxf(v, w) : v + w;
-    }
-    if constexpr (NT > 64) {
-        if (lane == 0) red[slot][wave] = v;
-        __syncthreads();
-        v = red[slot][0];
-#pragma unroll
-        for (int i = 1; i < NT / 64; ++i) v = MAX ? fmaxf(v, red[slot][i]) : v + red[slot][i];
-    }
-    return v;
-}
-
-template <int DT>
-__device__ __forceinline__ void load_z(const norm_args &a, int64_t at, float *z) {
-    constexpr int VN = vec16<DT>::n;
-    typedef typename elem<DT>::T E;
-    vec16<DT>::widen(ldg16((const E *)a.x + at), z);
-    if (a.residual) {
-        float r[VN];
-        vec16<DT>::widen(ldg16((const E *)a.residual + at), r);
-#pragma unroll
-        for (int i = 0; i < VN; ++i) z[i] += r[i];
-    }
-}
-
 // The rounded y of one vector, as stored (and back in fp32 for the codes).
 template <int DT>
 __device__ __forceinline__ uint4 norm_vec(const float *z, float inv, const uint4 &wq, float *yr) {
@@ -71,11 +38,6 @@ __device__ __forceinline__ uint4 norm_vec(const float *z, float inv, const uint4
     const uint4 q = vec16<DT>::narrow(o);
     vec16<DT>::widen(q, yr);
     return q;
-}
-
-__device__ __forceinline__ uint2 codes_of(const float *yr, float inv) {
-    return make_uint2(e4m3x4(yr[0] * inv, yr[1] * inv, yr[2] * inv, yr[3] * inv),
-                      e4m3x4(yr[4] * inv, yr[5] * inv, yr[6] * inv, yr[7] * inv));
 }
 
 // NT threads per row, VPT 16-byte vectors of the row in each thread's
@@ -102,7 +64,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_add_rmsnorm(norm_args a
             for (int v = 0; v < VPT; ++v) {
                 const int c = tid + v * NT;
                 if (c < nvec) {
-                    load_z<DT>(a, row + (int64_t)c * VN, z[v]);
+                    load_z<DT>(a.x, a.residual, row + (int64_t)c * VN, z[v]);
                     wq[v] = ldg16((const E *)a.weight + c * VN);
                 }
             }
@@ -140,7 +102,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_add_rmsnorm(norm_args a
         } else {
             float z[VN];
             for (int c = tid; c < nvec; c += NT) {
-                load_z<DT>(a, row + (int64_t)c * VN, z);
+                load_z<DT>(a.x, a.residual, row + (int64_t)c * VN, z);
 #pragma unroll
                 for (int i = 0; i < VN; ++i) ss = fmaf(z[i], z[i], ss);
             }
@@ -149,7 +111,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_add_rmsnorm(norm_args a
             if constexpr (Q8) {
                 float m = 0.0f;
                 for (int c = tid; c < nvec; c += NT) {
-                    load_z<DT>(a, row + (int64_t)c * VN, z);
+                    load_z<DT>(a.x, a.residual, row + (int64_t)c * VN, z);
                     norm_vec<DT>(z, inv, ldg16((const E *)a.weight + c * VN), z);
 #pragma unroll
                     for (int i = 0; i < VN; ++i) m = fmaxf(m, fabsf(z[i]));
@@ -159,7 +121,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_add_rmsnorm(norm_args a
                 if (tid == 0) a.ys[t] = exp2i(e);
             }
             for (int c = tid; c < nvec; c += NT) {
-                load_z<DT>(a, row + (int64_t)c * VN, z);
+                load_z<DT>(a.x, a.residual, row + (int64_t)c * VN, z);
                 if (a.residual_out) stg16((E *)a.residual_out + row + (int64_t)c * VN, vec16<DT>::narrow(z));
                 const uint4 q = norm_vec<DT>(z, inv, ldg16((const E *)a.weight + c * VN), z);
                 if (a.y) stg16((E *)a.y + row + (int64_t)c * VN, q);

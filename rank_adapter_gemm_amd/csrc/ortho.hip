@@ -1,0 +1,569 @@
+// Orthogonalised updates: for each of n matrices G (an adapter slot's gradient of
+// A, [d_in][r], or of B, [r][d_out])
+//   X = G / (|G|_F + eps);  X <- c0 X + c1 (X X^T) X + c2 (X X^T)^2 X,  step by step
+// (Newton-Schulz products: an odd polynomial of every singular value, the singular
+// vectors kept).  The short side r is at most 128, so X is never formed: with M =
+// X^T X (r x r, X taken with its long side down) a step is X <- X Q with Q = c0 I +
+// c1 M + c2 M^2, and M <- M Q^2.  All are polynomials of the first M, so they
+// commute, and the last X is G times one r x r matrix P:
+//   k_ortho_gram    G^T G, split over the long side                 one read of G
+//   k_ortho_poly    the pieces' sum, and the steps on r x r         a workgroup a matrix
+//   k_ortho_apply   G P                                     one more read, one write
+//
+// 64 bits: small singular values are amplified, by c0 at every step (485-fold in 5
+// steps of 3.4445), and an error e of M by up to 3e4 e relative to what those
+// directions get.  32-bit sums of M (6e-8) would show in the result; 64-bit ones
+// (v_mfma_f64_16x16x4_f64) do not.  So M, the steps and P are 64-bit; G P is 64-bit
+// products for fp32 G, and exact bf16 products of P in three parts, summed in fp32,
+// for bf16 G, whose result is rounded to bf16.
+//
+// Tiles: W tiles of 16 indices of the short side hold it (W = 1, 2, 4, 8); only those
+// on and under the diagonal are computed.  G goes from memory to the products
+// without LDS: a lane reads neighbouring values of one row of G, and which index of
+// the short side (or of the long one) stands at which place of a product is chosen
+// to fit.  G [D][r] ("tall"): place p of tile s is index W p + s; G [r][D]: 16 s + p.
+#include "gemm_common.hpp"
+
+namespace lora {
+
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+
+// v_mfma_f64_16x16x4_f64, lane l: A row l % 16, B column l % 16, both k = l / 16;
+// element e of the result is row 4 e + l / 16, column l % 16 (checked on the GPU).
+__device__ __forceinline__ f64x4_t mfma64(double a, double b, f64x4_t c) {
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ int mfma64_row(int e, int lane) { return 4 * e + (lane >> 4); }
+
+constexpr int ortho_tiles(int W) { return W * (W + 1) / 2; }
+// Number of tile (a, b), a >= b.
+__device__ __forceinline__ constexpr int ortho_tile(int a, int b) { return a * (a + 1) / 2 + b; }
+// The short-side index at place p of tile s.
+template <int W, bool TALL> __device__ __forceinline__ int ortho_index(int s, int p) {
+    return TALL ? W * p + s : 16 * s + p;
+}
+
+struct ortho_args {
+    const void *g;
+    void *out;
+    double *part;                      // [n][splits][tiles][256]: a tile's sums, element by element
+    double *poly;                      // [n][r][r]
+    double *factor;                    // [n]: scale / (|G| + eps)
+    int32_t D, n, r, splits, chunk;    // chunk: long-side indices per split, a multiple of 64
+    int32_t rows, blocks;              // k_ortho_apply: long-side indices per workgroup, workgroups per matrix
+    int32_t steps;
+    float eps, scale;
+    float coef[kMaxOrthoSteps][3];
+};
+
+// ---------------------------------------------------------------------------
+// G^T G.  Four wavefronts share a split's long side and add their sums through
+// LDS in a fixed order.  Of 8 tiles a side a wavefront holds half the rows of
+// tiles (0, 3, 4, 7 or 1, 2, 5, 6: 18 tiles each), and two share a part.
+// ---------------------------------------------------------------------------
+template <int W> __device__ __forceinline__ constexpr bool gram_owns(int half, int a) {
+    return W < 8 || (((a + 1) >> 1) & 1) == half;
+}
+template <int W> __device__ __forceinline__ constexpr int gram_at(int half, int a, int b) {
+    int n = 0;
+    for (int i = 0; i < a; ++i) n += gram_owns<W>(half, i) ? i + 1 : 0;
+    return n + b;
+}
+
+// 16-byte vector (or W * 2 or W * 4 bytes) of G, zeros where not ok.
+template <int BYTES> __device__ __forceinline__ void load_bytes(const void *p, bool ok, uint32_t *q) {
+    if constexpr (BYTES == 2) {
+        q[0] = ok ? *(const uint16_t *)p : 0u;
+    } else if constexpr (BYTES == 4) {
+        q[0] = ok ? *(const uint32_t *)p : 0u;
+    } else if constexpr (BYTES == 8) {
+        const uint2 v = ok ? *(const uint2 *)p : make_uint2(0u, 0u);
+        q[0] = v.x; q[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const uint4 v = ok ? ldg16((const char *)p + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+            q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
+        }
+    }
+}
+// Value i of such a vector.
+template <int DT> __device__ __forceinline__ float value_of(const uint32_t *q, int i) {
+    if (DT == LORA_F32) return __uint_as_float(q[i]);
+    return (i & 1) ? bf16_hi(q[i >> 1]) : bf16_lo(q[i >> 1]);
+}
+
+template <int DT, int W, bool TALL, int HALF, int N>
+__device__ __forceinline__ void gram_wave(const ortho_args &g, const typename elem<DT>::T *base, int begin, int end,
+                                          int kw, int lane, f64x4_t (&acc)[N]) {
+    constexpr int VN = vec16<DT>::n, KW = W == 8 ? 2 : 4, EB = elem<DT>::bytes;
+    // a wavefront reads U groups of STEP long-side indices at once: a value of W
+    // short-side indices for each of 4 (tall), or 16 bytes of each tile's 16 rows
+    constexpr int STEP = TALL ? 4 : 4 * VN, U = TALL ? 16 / W : 1;
+    constexpr int WORDS = TALL ? (W * EB + 3) / 4 : 4 * W;
+    const int p = lane & 15, kg = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    uint32_t q[2][U][WORDS];
+    auto load = [&](int i0, uint32_t (&to)[U][WORDS]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (TALL) {
+                const int i = i0 + 4 * u + kg;
+                load_bytes<W * EB>(base + (int64_t)i * g.r + W * p, i < end && W * p < g.r, to[u]);
+            } else {
+                const int i = i0 + STEP * u + VN * kg;
+#pragma unroll
+                for (int s = 0; s < W; ++s)
+                    load_bytes<16>(base + (int64_t)(16 * s + p) * g.D + i, i < end && 16 * s + p < g.r, to[u] + 4 * s);
+            }
+        }
+    };
+    auto products = [&](const uint32_t (&from)[U][WORDS]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < (TALL ? 1 : VN); ++k) {
+                double x[W];
+#pragma unroll
+                for (int s = 0; s < W; ++s) x[s] = (double)value_of<DT>(TALL ? from[u] : from[u] + 4 * s, TALL ? s : k);
+#pragma unroll
+                for (int a = 0; a < W; ++a)
+                    if (gram_owns<W>(HALF, a))
+#pragma unroll
+                        for (int b = 0; b <= a; ++b)
+                            acc[gram_at<W>(HALF, a, b)] = mfma64(x[a], x[b], acc[gram_at<W>(HALF, a, b)]);
+            }
+    };
+    constexpr int STRIDE = KW * STEP * U;
+    int i = begin + kw * STEP * U;
+    load(i, q[0]);
+    for (; i < end; i += 2 * STRIDE) {
+        load(i + STRIDE, q[1]);
+        products(q[0]);
+        load(i + 2 * STRIDE, q[0]);
+        products(q[1]);
+    }
+}
+
+template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ortho_gram(ortho_args g) {
+    constexpr int NT = ortho_tiles(W), KW = W == 8 ? 2 : 4, HALVES = 4 / KW, N = NT / HALVES;
+    __shared__ double s_sum[KW - 1][NT][256];
+    const int64_t item = grid_index();
+    if (item >= (int64_t)g.n * g.splits) return;
+    const int64_t mat = item / g.splits;
+    const int split = (int)(item - mat * g.splits), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int kw = wave / HALVES, half = wave % HALVES;
+    const typename elem<DT>::T *base = (const typename elem<DT>::T *)g.g + mat * g.D * g.r;
+    const int begin = split * g.chunk, end = min(g.D, begin + g.chunk);
+    f64x4_t acc[N];
+    if (half) gram_wave<DT, W, TALL, 1>(g, base, begin, end, kw, lane, acc);
+    else gram_wave<DT, W, TALL, 0>(g, base, begin, end, kw, lane, acc);
+    auto each = [&](auto &&f) {
+#pragma unroll
+        for (int a = 0; a < W; ++a)
+#pragma unroll
+            for (int b = 0; b <= a; ++b) {
+                if (gram_owns<W>(0, a) && half == 0) f(ortho_tile(a, b), acc[gram_at<W>(0, a, b) < N ? gram_at<W>(0, a, b) : 0]);
+                if (W == 8 && gram_owns<W>(1, a) && half == 1) f(ortho_tile(a, b), acc[gram_at<W>(1, a, b) < N ? gram_at<W>(1, a, b) : 0]);
+            }
+    };
+    if (kw > 0)
+        each([&](int tile, const f64x4_t &c) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s_sum[kw - 1][tile][64 * e + lane] = c[e];
+        });
+    __syncthreads();
+    if (kw > 0) return;
+    double *part = g.part + item * NT * 256;
+    each([&](int tile, f64x4_t &c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int k = 0; k < KW - 1; ++k) c[e] += s_sum[k][tile][64 * e + lane];
+            part[tile * 256 + 64 * e + lane] = c[e];
+        }
+    });
+}
+
+// ---------------------------------------------------------------------------
+// The steps on the r x r matrices, one workgroup a matrix: a wavefront holds one
+// tile (three of 8 a side) of M, P and what is made of them; the two factors of a
+// product lie in LDS, the tiles on and under the diagonal, in rows of 17 values
+// (both ways of reading a tile then spread over the banks).  Bound by the chain of
+// 4 products a step.
+// ---------------------------------------------------------------------------
+template <int W> struct poly_cfg {
+    static constexpr int NT = ortho_tiles(W), OWN = W == 8 ? 3 : 1, WAVES = NT / OWN, TILE = 16 * 17;
+};
+
+template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES * 64) k_ortho_poly(ortho_args g) {
+    typedef poly_cfg<W> C;
+    constexpr int NT = C::NT, OWN = C::OWN, TILE = C::TILE;
+    __shared__ double s_x[NT * TILE], s_y[NT * TILE];
+    __shared__ double s_trace;
+    const int64_t mat = grid_index();
+    if (mat >= g.n) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, p = lane & 15, kg = lane >> 4;
+    int ta[OWN], tb[OWN], tt[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        tt[o] = wave * OWN + o;
+        int a = 0;
+        while ((a + 1) * (a + 2) / 2 <= tt[o]) ++a;
+        ta[o] = a;
+        tb[o] = tt[o] - a * (a + 1) / 2;
+    }
+    f64x4_t m[OWN], pr[OWN], q[OWN], t[OWN];
+    auto put = [&](double *s, const f64x4_t (&v)[OWN]) {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[tt[o] * TILE + mfma64_row(e, lane) * 17 + p] = v[o][e];
+    };
+    // own tiles of x y, both symmetric and commuting, so their product is too
+    auto product = [&](const double *x, const double *y, f64x4_t (&to)[OWN]) {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            f64x4_t c = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll(OWN > 1 ? 1 : W)
+            for (int k = 0; k < W; ++k) {
+                const double *xt = x + (ta[o] >= k ? ortho_tile(ta[o], k) : ortho_tile(k, ta[o])) * TILE;
+                const double *yt = y + (k >= tb[o] ? ortho_tile(k, tb[o]) : ortho_tile(tb[o], k)) * TILE;
+                const int xs = ta[o] >= k ? 17 : 1, xk = ta[o] >= k ? 1 : 17;   // strides of its row, of k
+                const int ys = k >= tb[o] ? 1 : 17, yk = k >= tb[o] ? 17 : 1;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    c = mfma64(xt[p * xs + (4 * s + kg) * xk], yt[p * ys + (4 * s + kg) * yk], c);
+            }
+            to[o] = c;
+        }
+    };
+    auto one = [&](int o, int e) { return ta[o] == tb[o] && mfma64_row(e, lane) == p ? 1.0 : 0.0; };
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) m[o] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    const double *part = g.part + mat * g.splits * NT * 256 + lane;
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s, part += NT * 256)
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[o][e] += part[tt[o] * 256 + 64 * e];
+    put(s_x, m);
+    __syncthreads();
+    if (wave == 0) {
+        double d = 0.0;
+        for (int i = lane; i < 16 * W; i += 64) d += s_x[ortho_tile(i >> 4, i >> 4) * TILE + (i & 15) * 18];
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
+        if (lane == 0) s_trace = d;
+    }
+    __syncthreads();
+    const double inv = 1.0 / (sqrt(s_trace) + (double)g.eps);
+    if (threadIdx.x == 0) g.factor[mat] = (double)g.scale * inv;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[o][e] *= inv * inv;
+    for (int step = 0; step < g.steps; ++step) {
+        const double c0 = g.coef[step][0], c1 = g.coef[step][1], c2 = g.coef[step][2];
+        const bool last = step + 1 == g.steps;
+        put(s_x, m);
+        __syncthreads();
+        product(s_x, s_x, t);
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[o][e] = c0 * one(o, e) + c1 * m[o][e] + c2 * t[o][e];
+        put(s_y, q);
+        __syncthreads();
+        if (!last) product(s_x, s_y, t);                  // M Q
+        __syncthreads();
+        if (step == 0) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) pr[o] = q[o];
+        } else {
+            put(s_x, pr);
+            __syncthreads();
+            product(s_x, s_y, pr);                        // P Q
+            __syncthreads();
+        }
+        if (!last) {
+            put(s_x, t);
+            __syncthreads();
+            product(s_x, s_y, m);                         // M Q Q
+            __syncthreads();
+        }
+    }
+    double *poly = g.poly + mat * g.r * g.r;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = ortho_index<W, TALL>(ta[o], mfma64_row(e, lane)), j = ortho_index<W, TALL>(tb[o], p);
+            if (i >= g.r || j >= g.r) continue;
+            poly[i * g.r + j] = pr[o][e];
+            if (ta[o] != tb[o]) poly[j * g.r + i] = pr[o][e];
+        }
+}
+
+// ---------------------------------------------------------------------------
+// G P.  P lies in LDS (bf16: in three parts); the result's rows are P's, its
+// columns long-side indices, so that a lane holds neighbouring values of the
+// result in either layout.
+// ---------------------------------------------------------------------------
+// fp32: 64-bit products.  tall: a block is 16 rows i of G, and a lane reads 4
+// neighbouring values j of one; wide: 64 columns i, and a lane reads 4
+// neighbouring ones of row j.
+template <int W, bool TALL>
+__device__ __forceinline__ void apply_f32(const ortho_args &g, const float *in, float *out, const double *s_p,
+                                          double factor, int i0, int lane) {
+    constexpr int LD = 16 * W + 4, CB = W < 2 ? W : 2, R4 = TALL ? W : 4 * W, S = TALL ? 1 : 4;
+    const int p = lane & 15, kg = lane >> 4, r = g.r;
+    f32x4_t x[R4];
+#pragma unroll
+    for (int k = 0; k < R4; ++k) {
+        // tall: j = 16 k + 4 kg + (0..3) of row i0 + p; wide: row j = 4 k + kg, columns i0 + 4 p + (0..3)
+        const int j = TALL ? 16 * k + 4 * kg : 4 * k + kg, i = TALL ? i0 + p : i0 + 4 * p;
+        x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (j < r && i < g.D) x[k] = *reinterpret_cast<const f32x4_t *>(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
+    }
+#pragma unroll 1                                           // (unrolled, the wide ones spill)
+    for (int c0 = 0; c0 < W; c0 += CB) {
+        f64x4_t acc[CB][S];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int s = 0; s < S; ++s) acc[cb][s] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+        for (int k = 0; k < 4 * W; ++k)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                // the result's row 4 e + kg is the tile's column 4 kg + e where lanes store along it (tall)
+                const int c = 16 * (c0 + cb) + (TALL ? 4 * (p & 3) + (p >> 2) : p);
+                const double a = s_p[c * LD + 4 * k + kg];
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    acc[cb][s] = mfma64(a, (double)(TALL ? x[k >> 2][k & 3] : x[k][s]), acc[cb][s]);
+            }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            if constexpr (TALL) {
+                const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
+                if (c < r && i < g.D)
+                    *reinterpret_cast<f32x4_t *>(out + (int64_t)i * r + c) =
+                        f32x4_t{(float)(factor * acc[cb][0][0]), (float)(factor * acc[cb][0][1]),
+                                (float)(factor * acc[cb][0][2]), (float)(factor * acc[cb][0][3])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 16 * (c0 + cb) + mfma64_row(e, lane), i = i0 + 4 * p;
+                    if (c < r && i < g.D)
+                        *reinterpret_cast<f32x4_t *>(out + (int64_t)c * g.D + i) =
+                            f32x4_t{(float)(factor * acc[cb][0][e]), (float)(factor * acc[cb][S > 1 ? 1 : 0][e]),
+                                    (float)(factor * acc[cb][S > 2 ? 2 : 0][e]), (float)(factor * acc[cb][S > 3 ? 3 : 0][e])};
+                }
+            }
+        }
+    }
+}
+
+// bf16: v_mfma_f32_16x16x32_bf16 (lane l: A row and B column l % 16, k = 8 (l / 16)
+// + (0..7); the result's row 4 (l / 16) + e, column l % 16).  tall: a block is 16
+// rows i, and a lane reads 8 neighbouring values of one; wide: 128 columns, and a
+// lane reads 8 neighbouring columns of each of 8 rows j, and exchanges rows for
+// columns in its registers.
+template <int W, bool TALL>
+__device__ __forceinline__ void apply_bf16(const ortho_args &g, const uint16_t *in, uint16_t *out, const uint16_t *s_p,
+                                           float factor, int i0, int lane) {
+    constexpr int RP = W < 2 ? 32 : 16 * W, LD = RP + 8, PART = 16 * W * LD, KT = RP / 32, CB = W < 2 ? W : 2, S = TALL ? 1 : 8;
+    const int p = lane & 15, kg = lane >> 4, r = g.r;
+    uint4 x[KT][S];
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        if constexpr (TALL) {
+            const int j = 32 * k + 8 * kg, i = i0 + p;
+            x[k][0] = j < r && i < g.D ? ldg16(in + (int64_t)i * r + j) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            uint32_t w[8][4];                             // rows j = 32 k + 8 kg + (0..7), columns i0 + 8 p + (0..7)
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const int j = 32 * k + 8 * kg + h, i = i0 + 8 * p;
+                const uint4 v = j < r && i < g.D ? ldg16(in + (int64_t)j * g.D + i) : make_uint4(0u, 0u, 0u, 0u);
+                w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
+            }
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {                 // column s of the 8: its values of the 8 rows
+                uint32_t o[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    o[h] = __builtin_amdgcn_perm(w[2 * h + 1][s >> 1], w[2 * h][s >> 1], (s & 1) ? 0x07060302u : 0x05040100u);
+                x[k][S > 1 ? s : 0] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+#pragma unroll 1                                           // (unrolled, the wide ones spill)
+    for (int c0 = 0; c0 < W; c0 += CB) {
+        f32x4_t acc[CB][S];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int s = 0; s < S; ++s) acc[cb][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                for (int part = 2; part >= 0; --part) {   // the small parts first
+                    const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(s_p + part * PART + (16 * (c0 + cb) + p) * LD +
+                                                                           32 * k + 8 * kg);
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        acc[cb][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[k][s]),
+                                                                             acc[cb][s], 0, 0, 0);
+                }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            if constexpr (TALL) {
+                const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
+                if (c < r && i < g.D)
+                    *reinterpret_cast<uint2 *>(out + (int64_t)i * r + c) =
+                        make_uint2(pack_bf16x2(factor * acc[cb][0][0], factor * acc[cb][0][1]),
+                                   pack_bf16x2(factor * acc[cb][0][2], factor * acc[cb][0][3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 16 * (c0 + cb) + 4 * kg + e, i = i0 + 8 * p;
+                    if (c >= r || i >= g.D) continue;
+                    float f[8];
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) f[s] = factor * acc[cb][S > 1 ? s : 0][e];
+                    stg16(out + (int64_t)c * g.D + i, vec16<LORA_BF16>::narrow(f));
+                }
+            }
+        }
+    }
+}
+
+template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ortho_apply(ortho_args g) {
+    typedef typename elem<DT>::T E;
+    constexpr bool F32 = DT == LORA_F32;
+    constexpr int RP = W < 2 ? 32 : 16 * W, BLOCK = TALL ? 16 : F32 ? 64 : 128;
+    __shared__ __attribute__((aligned(16))) char s_p[F32 ? 16 * W * (16 * W + 4) * 8 : 3 * 16 * W * (RP + 8) * 2];
+    const int64_t item = grid_index();
+    if (item >= (int64_t)g.n * g.blocks) return;
+    const int64_t mat = item / g.blocks;
+    const int begin = (int)(item - mat * g.blocks) * g.rows, end = min(g.D, begin + g.rows);
+    const double *poly = g.poly + mat * g.r * g.r;
+    const double factor = g.factor[mat];
+    if constexpr (F32) {
+        double *s = reinterpret_cast<double *>(s_p);
+        for (int i = threadIdx.x; i < 16 * W * 16 * W; i += 256) {
+            const int c = i / (16 * W), j = i % (16 * W);
+            // tall: products take j = 16 k + 4 kg + s in the order of s, then kg
+            const int at = TALL ? (j & ~15) + 4 * (j & 3) + ((j >> 2) & 3) : j;
+            s[c * (16 * W + 4) + at] = c < g.r && j < g.r ? poly[c * g.r + j] : 0.0;
+        }
+    } else {
+        uint16_t *s = reinterpret_cast<uint16_t *>(s_p);
+        for (int i = threadIdx.x; i < 16 * W * RP; i += 256) {
+            const int c = i / RP, j = i % RP;
+            // three bf16 parts carry the value to 2^-27: hi = bf16(f), then what is left
+            const float f = c < g.r && j < g.r ? (float)poly[c * g.r + j] : 0.0f;
+            const uint32_t hi = f32_to_bf16_bits(f);
+            const float r1 = f - __uint_as_float(hi << 16);
+            const uint32_t mid = f32_to_bf16_bits(r1);
+            uint16_t *at = s + c * (RP + 8) + j;
+            at[0] = (uint16_t)hi;
+            at[16 * W * (RP + 8)] = (uint16_t)mid;
+            at[2 * 16 * W * (RP + 8)] = (uint16_t)f32_to_bf16_bits(r1 - __uint_as_float(mid << 16));
+        }
+    }
+    __syncthreads();
+    const E *in = (const E *)g.g + mat * g.D * g.r;
+    E *out = (E *)g.out + mat * g.D * g.r;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int i0 = begin + wave * BLOCK; i0 < end; i0 += 4 * BLOCK) {
+        if constexpr (F32) apply_f32<W, TALL>(g, in, out, reinterpret_cast<const double *>(s_p), factor, i0, lane);
+        else apply_bf16<W, TALL>(g, in, out, reinterpret_cast<const uint16_t *>(s_p), (float)factor, i0, lane);
+    }
+}
+
+// ---------------------------------------------------------------------------
+struct ortho_layout {
+    int32_t r, D, W, splits, chunk;
+    size_t part, poly, factor, total;
+};
+
+static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
+    ortho_layout L{};
+    L.r = rows < cols ? rows : cols;
+    L.D = rows < cols ? cols : rows;
+    L.W = L.r <= 16 ? 1 : L.r <= 32 ? 2 : L.r <= 64 ? 4 : 8;
+    // about two workgroups a CU over all matrices, of at least 256 indices
+    int splits = ceil_div(512, n > 0 ? n : 1);
+    if (splits > 32) splits = 32;
+    if (splits > ceil_div(L.D, 256)) splits = ceil_div(L.D, 256);
+    L.chunk = ceil_div(ceil_div(L.D, splits), 64) * 64;
+    L.splits = ceil_div(L.D, L.chunk);
+    size_t o = 0;
+    L.part = o;   o = align256(o + (size_t)n * L.splits * ortho_tiles(L.W) * 256 * 8);
+    L.poly = o;   o = align256(o + (size_t)n * L.r * L.r * 8);
+    L.factor = o; o = align256(o + (size_t)n * 8);
+    L.total = o;
+    return L;
+}
+
+size_t ortho_workspace_bytes(int32_t n, int32_t rows, int32_t cols) { return make_ortho_layout(n, rows, cols).total; }
+
+template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, hipStream_t s) {
+    hipLaunchKernelGGL((k_ortho_gram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits), dim3(256), 0, s, g);
+    hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
+    // about three workgroups a CU, of whole rounds of their wavefronts' blocks
+    constexpr int ROUND = 4 * (TALL ? 16 : DT == LORA_F32 ? 64 : 128);
+    int blocks = ceil_div(768, g.n);
+    if (blocks > ceil_div(g.D, ROUND)) blocks = ceil_div(g.D, ROUND);
+    g.rows = ceil_div(ceil_div(g.D, blocks), ROUND) * ROUND;
+    g.blocks = ceil_div(g.D, g.rows);
+    hipLaunchKernelGGL((k_ortho_apply<DT, W, TALL>), grid_of((int64_t)g.n * g.blocks), dim3(256), 0, s, g);
+}
+
+template <int DT, bool TALL> static void launch_ortho_w(ortho_args &g, int W, hipStream_t s) {
+    if (W == 1) launch_ortho_cfg<DT, 1, TALL>(g, s);
+    else if (W == 2) launch_ortho_cfg<DT, 2, TALL>(g, s);
+    else if (W == 4) launch_ortho_cfg<DT, 4, TALL>(g, s);
+    else launch_ortho_cfg<DT, 8, TALL>(g, s);
+}
+
+lora_status_t launch_orthogonalize(const void *in, int32_t n, int32_t rows, int32_t cols, int32_t dtype,
+                                   const float *coef, int32_t steps, float eps, float scale, void *out, void *ws,
+                                   hipStream_t s) {
+    const ortho_layout L = make_ortho_layout(n, rows, cols);
+    ortho_args g{};
+    g.g = in;
+    g.out = out;
+    g.part = ws_ptr<double>(ws, L.part);
+    g.poly = ws_ptr<double>(ws, L.poly);
+    g.factor = ws_ptr<double>(ws, L.factor);
+    g.D = L.D;
+    g.n = n;
+    g.r = L.r;
+    g.splits = L.splits;
+    g.chunk = L.chunk;
+    g.steps = steps;
+    g.eps = eps;
+    g.scale = scale;
+    for (int i = 0; i < steps; ++i)
+        for (int j = 0; j < 3; ++j) g.coef[i][j] = coef[3 * i + j];
+    const bool tall = rows >= cols;
+    if (dtype == LORA_F32) {
+        if (tall) launch_ortho_w<LORA_F32, true>(g, L.W, s);
+        else launch_ortho_w<LORA_F32, false>(g, L.W, s);
+    } else {
+        if (tall) launch_ortho_w<LORA_BF16, true>(g, L.W, s);
+        else launch_ortho_w<LORA_BF16, false>(g, L.W, s);
+    }
+    return hip_status(hipGetLastError());
+}
+
+}  // namespace lora

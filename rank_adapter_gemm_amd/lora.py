@@ -54,6 +54,9 @@ EXPORTED = (
     "lora_quantize_rows_fp8", "lora_quantize_weight_fp8", "lora_gemm_fp8", "lora_workspace_bytes_fp8",
     "lora_linear_forward_fp8",
     "lora_add_rmsnorm", "lora_add_rmsnorm_fp8",
+    "lora_add_layernorm", "lora_add_layernorm_fp8", "lora_workspace_bytes_layernorm_backward",
+    "lora_add_layernorm_backward",
+    "lora_workspace_bytes_orthogonalize", "lora_orthogonalize",
     "lora_workspace_bytes_gated", "lora_workspace_bytes_gated_fp8", "lora_gated_forward", "lora_gated_forward_fp8",
     "lora_workspace_bytes_gated_backward", "lora_gated_backward",
     "lora_linear_forward_noalloc",
@@ -152,6 +155,15 @@ def load(path: str = LIB_PATH):
                                             c_vp, c_sz, c_vp]),
         "lora_add_rmsnorm": (c_i32, [c_vp, c_vp, c_vp, c_f, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
         "lora_add_rmsnorm_fp8": (c_i32, [c_vp, c_vp, c_vp, c_f, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "lora_add_layernorm": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_f, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "lora_add_layernorm_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_f, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                           c_vp, c_vp]),
+        "lora_workspace_bytes_layernorm_backward": (c_sz, [c_i32, c_i32]),
+        "lora_add_layernorm_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp,
+                                                c_vp, c_vp, c_sz, c_vp]),
+        "lora_workspace_bytes_orthogonalize": (c_sz, [c_i32, c_i32, c_i32]),
+        "lora_orthogonalize": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, P(c_f), c_i32, c_f, c_f, c_vp, c_vp, c_sz,
+                                       c_vp]),
         "lora_workspace_bytes_gated": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
         "lora_workspace_bytes_gated_fp8": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
         "lora_gated_forward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_i32,
@@ -491,6 +503,62 @@ def lora_add_rmsnorm_fp8(x, residual, weight, eps, T, d, residual_out, y, yq, y_
         (yq, _CODES, n), (y_scale, torch.float32, T))
     _ok(load().lora_add_rmsnorm_fp8(x, residual, weight, eps, T, d, residual_out, y, yq, y_scale, _stream(stream)),
         "lora_add_rmsnorm_fp8")
+
+
+def lora_add_layernorm(x, residual, weight, bias, eps, T, d, dtype, residual_out, y, mean=None, rstd=None, stream=None):
+    """z = x + residual; y = (z - mean) / sqrt(var + eps) * weight + bias.  residual, bias, residual_out, and mean and
+    rstd (fp32, for the backward pass): tensors or None."""
+    dt, n, f32 = _TORCH_TYPES.get(dtype), T * d, torch.float32
+    x, residual, weight, bias, residual_out, y, mean, rstd = _checked(
+        "lora_add_layernorm", (x, dt, n), (residual, dt, n), (weight, dt, d), (bias, dt, d), (residual_out, dt, n),
+        (y, dt, n), (mean, f32, T), (rstd, f32, T))
+    _ok(load().lora_add_layernorm(x, residual, weight, bias, eps, T, d, dtype, residual_out, y, mean, rstd,
+                                  _stream(stream)), "lora_add_layernorm")
+
+
+def lora_add_layernorm_fp8(x, residual, weight, bias, eps, T, d, residual_out, y, yq, y_scale, mean=None, rstd=None,
+                           stream=None):
+    """The same on bf16 rows, with the E4M3 codes and scales of y's rows; y may be None."""
+    dt, n, f32 = torch.bfloat16, T * d, torch.float32
+    x, residual, weight, bias, residual_out, y, yq, y_scale, mean, rstd = _checked(
+        "lora_add_layernorm_fp8", (x, dt, n), (residual, dt, n), (weight, dt, d), (bias, dt, d), (residual_out, dt, n),
+        (y, dt, n), (yq, _CODES, n), (y_scale, f32, T), (mean, f32, T), (rstd, f32, T))
+    _ok(load().lora_add_layernorm_fp8(x, residual, weight, bias, eps, T, d, residual_out, y, yq, y_scale, mean, rstd,
+                                      _stream(stream)), "lora_add_layernorm_fp8")
+
+
+def lora_workspace_bytes_layernorm_backward(T, d) -> int:
+    return int(load().lora_workspace_bytes_layernorm_backward(T, d))
+
+
+def lora_add_layernorm_backward(dy, dresidual, z, weight, mean, rstd, T, d, dtype, dx, dweight, dbias, ws,
+                                stream=None):
+    """Gradients of lora_add_layernorm: dx (of x and of residual), dweight and dbias (each may be None); z, mean and
+    rstd as the forward pass kept them; dresidual: the gradient of residual_out, or None."""
+    dt, n, f32 = _TORCH_TYPES.get(dtype), T * d, torch.float32
+    nbytes = _ws_bytes(ws)
+    dy, dresidual, z, weight, mean, rstd, dx, dweight, dbias, ws = _checked(
+        "lora_add_layernorm_backward", (dy, dt, n), (dresidual, dt, n), (z, dt, n), (weight, dt, d), (mean, f32, T),
+        (rstd, f32, T), (dx, dt, n), (dweight, dt, d), (dbias, dt, d), (ws, torch.uint8, 0))
+    _ok(load().lora_add_layernorm_backward(dy, dresidual, z, weight, mean, rstd, T, d, dtype, dx, dweight, dbias, ws,
+                                           nbytes, _stream(stream)), "lora_add_layernorm_backward")
+
+
+def lora_workspace_bytes_orthogonalize(n, rows, cols) -> int:
+    return int(load().lora_workspace_bytes_orthogonalize(n, rows, cols))
+
+
+def lora_orthogonalize(g, n, rows, cols, dtype, coefficients, eps, scale, out, ws, stream=None):
+    """out = scale times the Newton-Schulz steps on each of the n matrices g [n, rows, cols]; coefficients: (c0, c1, c2)
+    of each step; out may be g."""
+    dt, size, steps = _TORCH_TYPES.get(dtype), n * rows * cols, len(coefficients)
+    if any(len(c) != 3 for c in coefficients):
+        raise LoraError(LORA_ERR_INVALID_ARGUMENT, "lora_orthogonalize: three coefficients a step")
+    coef = (ctypes.c_float * (3 * max(steps, 1)))(*[float(c) for step in coefficients for c in step])
+    nbytes = _ws_bytes(ws)
+    g, out, ws = _checked("lora_orthogonalize", (g, dt, size), (out, dt, size), (ws, torch.uint8, 0))
+    _ok(load().lora_orthogonalize(g, n, rows, cols, dtype, coef, steps, eps, scale, out, ws, nbytes, _stream(stream)),
+        "lora_orthogonalize")
 
 
 def lora_workspace_bytes_gated(T, n_slots, max_rank, d_out=0) -> int:
