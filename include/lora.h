@@ -582,7 +582,8 @@ lora_status_t lora_add_layernorm_backward(const void *dy, const void *dresidual,
 typedef enum {
     LORA_ACT_SILU = 0,      /* x / (1 + exp(-x)) */
     LORA_ACT_GELU = 1,      /* x times the normal distribution's cdf */
-    LORA_ACT_GELU_TANH = 2  /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    LORA_ACT_GELU_TANH = 2, /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    LORA_ACT_NONE = 3       /* x: lora_linear_act_forward and _backward only */
 } lora_act_t;
 
 /* Workspace bytes for the two forwards below on batches of up to T rows and
@@ -645,6 +646,36 @@ lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void 
                                   const lora_pool_t *pools, const int32_t *ids, lora_act_t act, const void *gate,
                                   const void *up, const void *dh, void *dx, void *const *dA, void *const *dB,
                                   void *ws, size_t ws_bytes, lora_stream_t stream);
+
+/* ---- the linear layer with bias, activation and residual ------------------------------- */
+
+/* lora_linear_forward and what follows it in a block, in one kernel's epilogue: for
+ * every row t, a = ids[t],
+ *     p = x W + s_a (x A_a) B_a + bias,      y = act(p) + residual
+ * with y rounded once from fp32.  x DEVICE [T, d_in], W DEVICE [d_in, d_out], bias
+ * DEVICE [d_out] or NULL, residual DEVICE [T, d_out] or NULL, y DEVICE [T, d_out], all
+ * of the pool's dtype; act may be LORA_ACT_NONE.  pre DEVICE [T, d_out] keeps p,
+ * rounded once, for lora_linear_act_backward; may be NULL.  residual may be y's own
+ * buffer; beyond that y, pre and ws share no byte with each other or with anything
+ * the call reads (T > 0; else LORA_ERR_INVALID_ARGUMENT).  mode, ids and bad ids as in
+ * lora_linear_forward.  flags: 0 or LORA_FLAG_SEGMENTS_READY (segments built by
+ * lora_build_segments, by this function or by an SGMV-mode forward in this workspace
+ * for these ids).  ws: lora_workspace_bytes. */
+lora_status_t lora_linear_act_forward(const void *x, const void *W, const void *bias, const void *residual, void *y,
+                                      void *pre, int32_t T, const lora_pool_t *pool, const int32_t *ids,
+                                      lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
+                                      lora_stream_t stream);
+
+/* The same on an FP8 base weight (bf16 x, bias, residual, y, pre and pool; d_in a
+ * multiple of 16): wq and w_scale from lora_quantize_weight_fp8.  xq and x_scale are the
+ * codes and scales of x's rows (lora_add_layernorm_fp8, lora_add_rmsnorm_fp8,
+ * lora_quantize_rows_fp8); both NULL: x is quantized into ws.  ws:
+ * lora_workspace_bytes_fp8, or lora_workspace_bytes where xq and x_scale are given. */
+lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, const float *x_scale, const uint8_t *wq,
+                                          const float *w_scale, const void *bias, const void *residual, void *y,
+                                          void *pre, int32_t T, const lora_pool_t *pool, const int32_t *ids,
+                                          lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
+                                          lora_stream_t stream);
 
 /* ---- orthogonalised updates ---------------------------------------------------------- */
 

@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "liblora.so")
 SOURCES = ["api.hip", "pool.hip", "segments.hip", "shrink.hip", "expand.hip", "gemm.hip", "gemm_fp8.hip", "cache.hip",
-           "norm.hip", "layernorm.hip", "ortho.hip", "gated.hip", "gated_bwd.hip"]
+           "norm.hip", "layernorm.hip", "linear_act.hip", "ortho.hip",
+           "gated.hip", "gated_bwd.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 instructions.

@@ -845,6 +845,120 @@ lora_status_t lora_add_rmsnorm_fp8(const void *x, const void *residual, const vo
     return launch_add_rmsnorm(x, residual, weight, eps, T, d, LORA_BF16, residual_out, y, yq, y_scale, hs(stream));
 }
 
+// What a call reads of one pool, as pair_spans.
+static void pool_spans(const lora_pool_t &p, span *out) {
+    const lora_pool_t two[2] = {p, p};
+    span both[kPairSpans];
+    pair_spans(two, both);
+    for (int i = 0; i < kPairSpans / 2; ++i) out[i] = both[i];
+}
+constexpr int kPoolSpans = kPairSpans / 2;
+
+static bool valid_act_or_none(int32_t a) { return valid_act(a) || a == LORA_ACT_NONE; }
+
+// Whole tiles of 256 x 256 whose threads fit one grid dimension (a longer grid
+// would be cut short without an error).
+static bool tiles_fit(int32_t T, int32_t N) {
+    return ((T + 255ll) / 256) * ((N + 255ll) / 256) * 512 < 1ll << 32;
+}
+
+// The buffers of the layer with its epilogue: read holds what is read but the
+// residual, which may be y's own.
+static bool act_buffers_clear(const void *y, const void *pre, const void *ws, size_t ws_bytes, const void *residual,
+                              size_t rows, const span *read, int n_read) {
+    const span out[] = {{y, rows}, {pre, rows}, {ws, ws_bytes}}, res = {residual, rows};
+    return outputs_clear(out, 3, read, n_read) && outputs_clear(out + 1, 2, &res, 1) &&
+           (y == residual || outputs_clear(out, 1, &res, 1));
+}
+
+lora_status_t lora_linear_act_forward(const void *x, const void *W, const void *bias, const void *residual, void *y,
+                                      void *pre, int32_t T, const lora_pool_t *pool, const int32_t *ids,
+                                      lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
+                                      lora_stream_t stream) {
+    if (!valid_pool(pool) || T < 0 || !valid_mode(mode) || !valid_act_or_none(act) || (flags & ~LORA_FLAG_SEGMENTS_READY))
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!x || !W || !y || !ids || !aligned16(x) || !aligned16(W) || !aligned16(bias) || !aligned16(residual) ||
+                  !aligned16(y) || !aligned16(pre)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    ws_layout L;
+    lora_status_t st = check_ws(ws, ws_bytes, T, pool->n_slots, pool->max_rank, &L);
+    if (st != LORA_OK || T == 0) return st;
+    const size_t eb = dtype_bytes(pool->dtype), K = pool->d_in, N = pool->d_out;
+    span read[4 + kPoolSpans] = {{x, T * K * eb}, {W, K * N * eb}, {bias, N * eb}, {ids, 4 * (size_t)T}};
+    pool_spans(*pool, read + 4);
+    if (!act_buffers_clear(y, pre, ws, ws_bytes, residual, T * N * eb, read, 4 + kPoolSpans))
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (!tiles_fit(T, pool->d_out)) return LORA_ERR_UNSUPPORTED;
+    const hipStream_t s = hs(stream);
+    const bool sgmv = use_sgmv(mode, T);
+    if (sgmv && !(flags & LORA_FLAG_SEGMENTS_READY)) {
+        // act is not linear: every row's term goes into its sums, none to a separate expand
+        st = launch_segments(ids, T, pool->n_slots, L, ws, s, 1);
+        if (st != LORA_OK) return st;
+    }
+    const epilogue epi{bias, residual, pre, (int32_t)act};
+    float *partial = ws_ptr<float>(ws, L.gemm_partial);
+    const size_t partial_bytes = ws_bytes - L.gemm_partial;
+    if (!sgmv && pool->dtype == LORA_BF16 &&
+        gemm_fused_shrink_ok(T, pool->d_in, pool->d_out, pool->max_rank, partial_bytes))
+        return launch_gemm_fused_shrink(x, W, y, T, pool, ids, ws_ptr<float>(ws, L.partial),
+                                        ws_ptr<int32_t>(ws, L.header), partial, partial_bytes, s, &epi);
+    float *v = ws_ptr<float>(ws, L.v);
+    st = launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s);
+    if (st != LORA_OK) return st;
+    return launch_gemm(x, W, y, T, pool->d_in, pool->d_out, pool->dtype, pool, ids, v, pool->max_rank,
+                       sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr, partial, partial_bytes, s, nullptr, &epi);
+}
+
+lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, const float *x_scale, const uint8_t *wq,
+                                          const float *w_scale, const void *bias, const void *residual, void *y,
+                                          void *pre, int32_t T, const lora_pool_t *pool, const int32_t *ids,
+                                          lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
+                                          lora_stream_t stream) {
+    if (!valid_pool(pool) || pool->dtype != LORA_BF16 || (pool->d_in % 16) || T < 0 || !valid_mode(mode) ||
+        !valid_act_or_none(act) || (flags & ~LORA_FLAG_SEGMENTS_READY) || !xq != !x_scale)
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!x || !wq || !w_scale || !y || !ids || !aligned16(x) || !aligned16(xq) || !aligned16(x_scale) ||
+                  !aligned16(wq) || !aligned16(w_scale) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) ||
+                  !aligned16(pre)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    ws_layout L;
+    lora_status_t st = check_ws_fp8(ws, ws_bytes, T, pool->n_slots, pool->max_rank, xq ? 0 : pool->d_in, &L);
+    if (st != LORA_OK || T == 0) return st;
+    const size_t K = pool->d_in, N = pool->d_out;
+    span read[7 + kPoolSpans] = {{x, 2 * K * T}, {xq, K * T}, {x_scale, 4 * (size_t)T}, {wq, K * N}, {w_scale, 4 * N},
+                                 {bias, 2 * N}, {ids, 4 * (size_t)T}};
+    pool_spans(*pool, read + 7);
+    if (!act_buffers_clear(y, pre, ws, ws_bytes, residual, 2 * N * T, read, 7 + kPoolSpans))
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (!tiles_fit(T, pool->d_out)) return LORA_ERR_UNSUPPORTED;
+    const hipStream_t s = hs(stream);
+    const bool sgmv = use_sgmv(mode, T);
+    if (sgmv && !(flags & LORA_FLAG_SEGMENTS_READY)) {
+        st = launch_segments(ids, T, pool->n_slots, L, ws, s, 1);
+        if (st != LORA_OK) return st;
+    }
+    float *v = ws_ptr<float>(ws, L.v);
+    if (!xq) {
+        uint8_t *q = ws_ptr<uint8_t>(ws, L.xq);
+        float *qs = ws_ptr<float>(ws, L.xs);
+        // decode rows: quantized by the workgroup that shrinks them
+        st = sgmv ? launch_quant_rows_fp8(x, T, pool->d_in, q, qs, s)
+                  : launch_quant_shrink_rows(x, T, pool, ids, v, q, qs, ws_ptr<int32_t>(ws, L.header), s);
+        if (st != LORA_OK) return st;
+        if (sgmv) st = launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s);
+        xq = q;
+        x_scale = qs;
+    } else {
+        st = launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s);
+    }
+    if (st != LORA_OK) return st;
+    const epilogue epi{bias, residual, pre, (int32_t)act};
+    return launch_gemm_fp8(xq, x_scale, wq, w_scale, y, T, pool->d_in, pool->d_out, pool, ids, v, pool->max_rank,
+                           sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr, ws_ptr<float>(ws, L.gemm_partial),
+                           ws_bytes - L.gemm_partial, s, nullptr, &epi);
+}
+
 // The layer norms': as valid_norm, with a bias and the kept statistics.
 static bool valid_layernorm(const void *x, const void *residual, const void *weight, const void *bias, float eps,
                             int32_t T, int32_t d, int32_t d_step, int32_t dtype, const void *residual_out, const void *y,

@@ -220,6 +220,14 @@ template <typename T> inline T *ws_ptr(void *ws, size_t off) {
 
 inline lora_status_t hip_status(hipError_t e) { return e == hipSuccess ? LORA_OK : LORA_ERR_HIP; }
 
+// The linear layer's epilogue: y = act(sums + bias) + residual, the argument of act
+// kept in pre; bias, residual and pre may be null.
+struct epilogue {
+    const void *bias, *residual;
+    void *pre;
+    int32_t act;
+};
+
 // Launchers (one per kernel family), implemented in the matching .hip file.
 lora_status_t launch_pool_fill(void *a, size_t a_bytes, void *b, size_t b_bytes, float *scale,
                                int32_t *rank, int32_t n_slots, hipStream_t s);
@@ -277,7 +285,7 @@ bool gemm_fused_shrink_ok(int32_t T, int32_t d_in, int32_t d_out, int32_t max_ra
 lora_status_t launch_gemm_fused_shrink(const void *x, const void *W, void *y, int32_t T,
                                        const lora_pool_t *pool, const int32_t *ids, float *vpart,
                                        int32_t *err, float *partial, size_t partial_bytes,
-                                       hipStream_t s);
+                                       hipStream_t s, const epilogue *epi = nullptr);
 bool gemm_grouping_pays(int32_t T, int32_t K, const int32_t *Ns, int32_t n, size_t partial_bytes);
 // n_fused (device, may be null): rows at GEMM positions >= *n_fused get no
 // low-rank term here (the short-segment rows; their expand is separate).
@@ -289,7 +297,11 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
                           int32_t d_out, int32_t dtype, const lora_pool_t *pool,
                           const int32_t *ids, const float *v, int32_t v_stride,
                           const int32_t *perm, float *partial, size_t partial_bytes, hipStream_t s,
-                          const int32_t *n_fused = nullptr);
+                          const int32_t *n_fused = nullptr, const epilogue *epi = nullptr);
+// The fp32 layer with its epilogue.
+lora_status_t launch_linear_f32(const void *x, const void *W, void *y, int32_t T, const lora_pool_t &p,
+                                const int32_t *ids, const float *v, int32_t v_stride, const int32_t *perm,
+                                float *partial, size_t partial_bytes, const epilogue &epi, hipStream_t s);
 // FP8 base (E4M3 codes, fp32 scales): per-row and per-column quantizers and
 // y = s_x s_w (xq wq^T) (+ s v B when pool != nullptr), bf16 y.
 lora_status_t launch_quant_rows_fp8(const void *x, int32_t T, int32_t K, uint8_t *xq, float *xs, hipStream_t s);
@@ -300,7 +312,8 @@ lora_status_t launch_quant_cols_fp8(const void *W, int32_t K, int32_t N, uint8_t
 lora_status_t launch_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t *wq, const float *wsc, void *y,
                               int32_t T, int32_t d_in, int32_t d_out, const lora_pool_t *pool,
                               const int32_t *ids, const float *v, int32_t v_stride, const int32_t *perm,
-                              float *partial, size_t partial_bytes, hipStream_t s, const int32_t *n_fused = nullptr);
+                              float *partial, size_t partial_bytes, hipStream_t s, const int32_t *n_fused = nullptr,
+                              const epilogue *epi = nullptr);
 
 // The gated pair h = act(g) * u of two projections of x with their pools (bf16
 // or fp32; wq, wsc: FP8 base codes and column scales instead of W, with the

@@ -23,7 +23,7 @@
 //   * Split-K (small grids): each workgroup sums a K range and writes fp32
 //     partials in sorted-row order; k_splitk_reduce adds them in split order
 //     (deterministic, no atomics) and applies the same epilogue.
-#include "gated_common.hpp"
+#include "act_common.hpp"
 
 namespace lora {
 
@@ -46,7 +46,10 @@ template <int BM, int BN, int BK, int NS, bool SH, int WV = 4, int WR = 2> struc
 //   * GATED: the tile's columns are pairs of 32 gate and 32 up columns (see
 //     gated_col), each with its own weight and adapter pool; the epilogue
 //     writes h = act(gate) * up, so gate and up need not leave the chip.
+//   * EPI: whole tiles of the linear layer with bias, activation and residual
+//     (its split pieces are the plain ones; k_splitk_reduce finishes them).
 template <bool LORA, int BM, int BN, int BK, int NS, bool SPLIT, bool SH = false, int WV = 4, int WR = 2,
+          bool EPI = false,
           bool GATED = false>   // GATED without LORA: the rows' terms are added in the store, row by row
 __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     static_assert(!SH || SPLIT, "the fused shrink runs in split-K mode");
@@ -56,7 +59,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     constexpr bool ADD = LORA && !SPLIT && NS == 1;
     static_assert(!GATED || (!SH && !ADD), "the gated pair has its own shrink and epilogue");
     typedef gemm_cfg<BM, BN, BK, NS, SH, WV, WR> C;
-    static_assert(!GATED || WR * 32 * (BN + 4) * 4 <= C::LDS, "the gated store fits the stages' LDS");
+    static_assert(!(GATED || EPI) || WR * 32 * (BN + 4) * 4 <= C::LDS, "the store fits the stages' LDS");
+    static_assert(!EPI || (LORA && !SPLIT && !ADD && !GATED), "whole tiles of the layer with its adapters");
     constexpr int WM = C::WM, WN = C::WN, RB = C::RB, CB = C::CB;
     constexpr int XCH = C::XCH, WCH = C::WCH, XSTAGE = C::XSTAGE, WSTAGE = C::WSTAGE;
     constexpr int XI = C::XI, WI = C::WI, AI = C::AI, ACH = C::ACH, STAGE = C::STAGE;
@@ -223,6 +227,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     int32_t *s_meta_t = nullptr, *s_meta_id = nullptr;
     constexpr bool SLOTS = GATED && !SPLIT;
     __shared__ row_slot s_slot[SLOTS ? BM : 1];
+    __shared__ row_term s_term[EPI ? BM : 1];
     if constexpr (!SPLIT) {
         __shared__ int32_t s_meta_t_buf[BM], s_meta_id_buf[BM];
         s_meta_t = s_meta_t_buf;
@@ -236,10 +241,11 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
             int32_t id = -1;
             if ((LORA || GATED) && t >= 0 && (!g.n_fused || p < n_fused)) {
                 const int32_t raw = g.ids[t];
-                if (raw >= 0 && raw < g.n_slots && (GATED || g.rank[raw] > 0)) id = raw;
+                if (raw >= 0 && raw < g.n_slots && (GATED || EPI || g.rank[raw] > 0)) id = raw;
             }
             s_meta_t[i] = (ADD && id < 0) ? -1 : t;   // adding: rows without a term stay untouched
-            if constexpr (SLOTS) set_row(g, id, !LORA, s_meta_id[i], s_slot[i]);
+            if constexpr (EPI) set_row_term(g, id, s_meta_id[i], s_term[i]);
+            else if constexpr (SLOTS) set_row(g, id, !LORA, s_meta_id[i], s_slot[i]);
             else s_meta_id[i] = id;
         }
     }
@@ -304,6 +310,9 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
     if constexpr (GATED && LORA && !SPLIT)
         gated_lora_pass<RB, CB, (RB >= 4 ? 2 : 1), 1, (RB >= 4 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, wm * WM,
                                                                        gated_col(n0 + wn * WN), lane);
+    else if constexpr (EPI)
+        lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1), 1, 0, true>(g, acc, s_meta_t, s_meta_id, n0, wm * WM,
+                                                                                    n0 + wn * WN, lane);
     else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 2 ? 2 : 1), 1, (RB >= 2 ? 2 : 1)>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN,
                                                     lane);
@@ -358,7 +367,9 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_bf16(gemm_args g) {
             flag_bad_row(g.err, fl_t);
     }
 
-    if constexpr (GATED && !SPLIT)
+    if constexpr (EPI)
+        act_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_meta_id, s_term, n0);
+    else if constexpr (GATED && !SPLIT)
         gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_meta_id, s_slot, n0, w,
                                          lane);
     else if constexpr (GATED)
@@ -463,13 +474,16 @@ __global__ void __launch_bounds__(256) k_gemm_f32(gemm_f32_args g) {
 // NST, WVT: stages and wavefronts of the split-K pieces (their LDS holds no
 // row tables).
 template <int BM, int BN, int NS = 2, int WV = 4, int WR = 2, int BK = 64, int NST = NS, int WVT = WV>
-static void launch_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t s) {
+static void launch_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t s, bool epi = false) {
     if (pl.n_dp > 0) {
         g.tile_base = 0;
         g.n_tiles = pl.n_dp;
         g.splits = 1;
         g.k_chunk = g.K;
-        if (lora)
+        if (epi)
+            hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, BK, NS, false, false, WV, WR, true>), dim3(pl.n_dp),
+                               dim3(WV * 64), 0, s, g);
+        else if (lora)
             hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, BK, NS, false, false, WV, WR>), dim3(pl.n_dp), dim3(WV * 64),
                                0, s, g);
         else
@@ -484,7 +498,9 @@ static void launch_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t 
         hipLaunchKernelGGL((k_gemm_bf16<false, BM, BN, BK, NST, true, false, WVT, WR>), dim3(pl.tail * pl.splits),
                            dim3(WVT * 64), 0, s, g);
         const dim3 rgrid(pl.tail * (BM / (2048 / BN)));
-        if (lora)
+        if (epi)
+            hipLaunchKernelGGL((k_splitk_reduce<true, false, BM, BN, true>), rgrid, dim3(256), 0, s, g);
+        else if (lora)
             hipLaunchKernelGGL((k_splitk_reduce<true, false, BM, BN>), rgrid, dim3(256), 0, s, g);
         else
             hipLaunchKernelGGL((k_splitk_reduce<false, false, BM, BN>), rgrid, dim3(256), 0, s, g);
@@ -518,8 +534,9 @@ bool gemm_fused_shrink_ok(int32_t T, int32_t d_in, int32_t d_out, int32_t max_ra
 lora_status_t launch_gemm_fused_shrink(const void *x, const void *W, void *y, int32_t T,
                                        const lora_pool_t *pool, const int32_t *ids, float *vpart,
                                        int32_t *err, float *partial, size_t partial_bytes,
-                                       hipStream_t s) {
+                                       hipStream_t s, const epilogue *epi) {
     gemm_args g{};
+    set_epilogue(g, epi);
     g.x = (const uint16_t *)x;
     g.W = (const uint16_t *)W;
     g.y = (uint16_t *)y;
@@ -551,13 +568,21 @@ lora_status_t launch_gemm_fused_shrink(const void *x, const void *W, void *y, in
     if (pl.bm == 128) {
         hipLaunchKernelGGL((k_gemm_bf16<false, 128, 128, 64, 4, true, true, 8, 2>), dim3(pl.tail * pl.splits),
                            dim3(512), 0, s, g);
-        hipLaunchKernelGGL((k_splitk_reduce<true, true, 128, 128>), dim3(pl.tail * (128 / 16)), dim3(256), 0, s,
-                           g);
+        if (epi)
+            hipLaunchKernelGGL((k_splitk_reduce<true, true, 128, 128, true>), dim3(pl.tail * (128 / 16)), dim3(256), 0,
+                               s, g);
+        else
+            hipLaunchKernelGGL((k_splitk_reduce<true, true, 128, 128>), dim3(pl.tail * (128 / 16)), dim3(256), 0, s,
+                               g);
     } else {
         hipLaunchKernelGGL((k_gemm_bf16<false, 256, 64, 64, 3, true, true>), dim3(pl.tail * pl.splits),
                            dim3(256), 0, s, g);
-        hipLaunchKernelGGL((k_splitk_reduce<true, true, 256, 64>), dim3(pl.tail * (256 / 32)), dim3(256), 0, s,
-                           g);
+        if (epi)
+            hipLaunchKernelGGL((k_splitk_reduce<true, true, 256, 64, true>), dim3(pl.tail * (256 / 32)), dim3(256), 0, s,
+                               g);
+        else
+            hipLaunchKernelGGL((k_splitk_reduce<true, true, 256, 64>), dim3(pl.tail * (256 / 32)), dim3(256), 0, s,
+                               g);
     }
     return hip_status(hipGetLastError());
 }
@@ -667,9 +692,11 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
                           int32_t d_out, int32_t dtype, const lora_pool_t *pool,
                           const int32_t *ids, const float *v, int32_t v_stride,
                           const int32_t *perm, float *partial, size_t partial_bytes, hipStream_t s,
-                          const int32_t *n_fused) {
+                          const int32_t *n_fused, const epilogue *epi) {
+    if (epi && !pool) return LORA_ERR_INVALID_ARGUMENT;
     if (dtype == LORA_BF16) {
         gemm_args g{};
+        set_epilogue(g, epi);
         g.x = (const uint16_t *)x;
         g.W = (const uint16_t *)W;
         g.y = (uint16_t *)y;
@@ -699,10 +726,12 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
         // 256-row tiles and the 128 x 128 split pieces run 8 wavefronts (two
         // per SIMD: one issues MFMAs while the other waits on LDS or the
         // barrier); other tiles 4.
-        if (pl.bm == 256 && pl.bn == 256) launch_cfg<256, 256, 2, 8>(g, pl, lora, s);
-        else if (pl.bm == 256 && pl.bn == 128) launch_cfg<256, 128, 2, 8>(g, pl, lora, s);
-        else if (pl.bn == 128) launch_cfg<128, 128, 2, 4, 2, 64, 4, 8>(g, pl, lora, s);
-        else launch_cfg<128, 64>(g, pl, lora, s);
+        if (pl.bm == 256 && pl.bn == 256) launch_cfg<256, 256, 2, 8>(g, pl, lora, s, epi != nullptr);
+        else if (pl.bm == 256 && pl.bn == 128) launch_cfg<256, 128, 2, 8>(g, pl, lora, s, epi != nullptr);
+        else if (pl.bn == 128) launch_cfg<128, 128, 2, 4, 2, 64, 4, 8>(g, pl, lora, s, epi != nullptr);
+        else launch_cfg<128, 64>(g, pl, lora, s, epi != nullptr);
+    } else if (epi) {
+        return launch_linear_f32(x, W, y, T, *pool, ids, v, v_stride, perm, partial, partial ? partial_bytes : 0, *epi, s);
     } else {
         gemm_f32_args g;
         g.x = (const float *)x;
@@ -738,7 +767,7 @@ static void launch_gated_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s) {
         g.n_tiles = pl.n_dp;
         g.splits = 1;
         g.k_chunk = g.K;
-        hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, 64, NS, false, false, WV, WR, true>), dim3(pl.n_dp),
+        hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, 64, NS, false, false, WV, WR, false, true>), dim3(pl.n_dp),
                            dim3(WV * 64), 0, s, g);
     }
     if (pl.tail > 0) {
@@ -746,7 +775,7 @@ static void launch_gated_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s) {
         g.n_tiles = pl.tail;
         g.splits = pl.splits;
         g.k_chunk = pl.k_chunk;
-        hipLaunchKernelGGL((k_gemm_bf16<false, BM, BN, 64, NST, true, false, WVT, WRT, true>),
+        hipLaunchKernelGGL((k_gemm_bf16<false, BM, BN, 64, NST, true, false, WVT, WRT, false, true>),
                            dim3(pl.tail * pl.splits), dim3(WVT * 64), 0, s, g);
         launch_gated_reduce<BM, BN>(g, s);
     }
@@ -759,10 +788,10 @@ static void launch_gated_few(gemm_args g, const gemm_plan &pl, hipStream_t s) {
     g.splits = pl.splits;
     g.k_chunk = pl.k_chunk;
     if (pl.splits == 1)
-        hipLaunchKernelGGL((k_gemm_bf16<false, 32, 128, 64, 3, false, false, 4, 1, true>), dim3(g.n_tiles), dim3(256),
+        hipLaunchKernelGGL((k_gemm_bf16<false, 32, 128, 64, 3, false, false, 4, 1, false, true>), dim3(g.n_tiles), dim3(256),
                            0, s, g);
     else {
-        hipLaunchKernelGGL((k_gemm_bf16<false, 32, 128, 64, 3, true, false, 4, 1, true>), dim3(g.n_tiles * pl.splits),
+        hipLaunchKernelGGL((k_gemm_bf16<false, 32, 128, 64, 3, true, false, 4, 1, false, true>), dim3(g.n_tiles * pl.splits),
                            dim3(256), 0, s, g);
         launch_gated_reduce<32, 128>(g, s);
     }

@@ -3,7 +3,7 @@
 // the tile store, the split-K reduction and the tile/split planner.
 #pragma once
 
-#include "common.hpp"
+#include "act.hpp"
 
 namespace lora {
 
@@ -53,7 +53,45 @@ struct gemm_args {
     int32_t n_slices;              // grouped launch: 0 (one output), else slices sl[0..n_slices)
     gemm_slice sl[kMaxSlices];     // column tiles numbered slice after slice
     int32_t act;                   // gated pair: the activation (sl[0] gate, sl[1] up, y = h, N = h's width)
+    const uint16_t *bias, *residual;   // the linear layer's epilogue: y = act(sum + bias) + residual, the argument of
+    uint16_t *pre;                     // act kept in pre; each may be null
 };
+
+inline void set_epilogue(gemm_args &g, const epilogue *epi) {
+    if (!epi) return;
+    g.bias = (const uint16_t *)epi->bias;
+    g.residual = (const uint16_t *)epi->residual;
+    g.pre = (uint16_t *)epi->pre;
+    g.act = epi->act;
+}
+
+// The epilogue of 8 neighbouring columns n.. of row t: o holds the sums.  bq and
+// rq: the columns' bias and residual, loaded ahead (not looked at where there is none).
+__device__ __forceinline__ void epilogue8(const gemm_args &g, int64_t t, int n, float (&o)[8], const uint4 &bq,
+                                          const uint4 &rq) {
+    const int64_t at = t * g.N + n;
+    float f[8];
+    if (g.bias) {
+        vec16<LORA_BF16>::widen(bq, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += f[e];
+    }
+    if (g.pre) stg16(g.pre + at, vec16<LORA_BF16>::narrow(o));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = act_or_none<false>(g.act, o[e]);
+    if (g.residual) {
+        vec16<LORA_BF16>::widen(rq, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += f[e];
+    }
+    stg16(g.y + at, vec16<LORA_BF16>::narrow(o));
+}
+__device__ __forceinline__ uint4 load_bias8(const gemm_args &g, int n) {
+    return g.bias ? ldg16(g.bias + n) : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ uint4 load_residual8(const gemm_args &g, int64_t t, int n) {
+    return g.residual ? ldg16(g.residual + t * g.N + n) : make_uint4(0u, 0u, 0u, 0u);
+}
 
 // Grouped launch: point g at the slice that owns global column tile tn and
 // return the tile's index within that slice (identity without slices).  The
@@ -472,7 +510,8 @@ __device__ __forceinline__ void gemm_store_tile(const gemm_args &g, f32x16_t (&a
 // The partials of an element are summed in split order (deterministic).
 // With VP (fused shrink) the rows' v are first summed from the K-range rank
 // partials (in range order) into LDS (the GEMM has flagged bad ids).
-template <bool LORA, bool VP, int BM, int BN>
+// EPI: the linear layer's epilogue on the sums.
+template <bool LORA, bool VP, int BM, int BN, bool EPI = false>
 __global__ void __launch_bounds__(256) k_splitk_reduce(gemm_args g0) {
     constexpr int RW = 2048 / BN, CPR = BN / 8, CHUNKS = BM / RW;
     constexpr int SP = 4;                                 // split partials loaded ahead
@@ -505,6 +544,7 @@ __global__ void __launch_bounds__(256) k_splitk_reduce(gemm_args g0) {
     const bool slot_ok = raw >= 0 && raw < g.n_slots;
     float4 pa[SP], pb[SP];
     uint4 bq[GP][8];
+    uint4 bias, res;
     // B of a padded slot is prefetched from its first GP octets (at most
     // max_rank ranks, all inside the slot, zero past its rank); a packed
     // slot's octets past its capacity belong to the next slot, so there only
@@ -512,6 +552,10 @@ __global__ void __launch_bounds__(256) k_splitk_reduce(gemm_args g0) {
     const int gp_pre = g.row0 ? 1 : GP;
     int64_t bbase = 0;
     if (t >= 0) {
+        if (EPI) {
+            bias = load_bias8(g, n);
+            res = load_residual8(g, t, n);
+        }
 #pragma unroll
         for (int sidx = 0; sidx < SP; ++sidx)
             if (sidx < g.splits) {
@@ -599,7 +643,8 @@ __global__ void __launch_bounds__(256) k_splitk_reduce(gemm_args g0) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) o[q] = fmaf(sc, d[q], o[q]);
     }
-    stg16(g.y + (int64_t)t * N + n, vec16<LORA_BF16>::narrow(o));
+    if constexpr (EPI) epilogue8(g, t, n, o, bias, res);
+    else stg16(g.y + (int64_t)t * N + n, vec16<LORA_BF16>::narrow(o));
 }
 
 // Column bands per XCD (col_strips) for wide grids whose x is the smaller

@@ -29,7 +29,7 @@
 // scale operand of lane l applies to row (column) l % 32 in K-block l / 32 --
 // with one scale per row and column, lanes l and l + 32 pass the same one.
 // The output layout is that of the bf16 32x32 MFMAs.
-#include "gated_common.hpp"
+#include "act_common.hpp"
 #include "fp8_common.hpp"
 
 namespace lora {
@@ -161,13 +161,15 @@ template <int BM, int BN, int NS, int WV, int WR> struct fp8_cfg {
     static_assert(XI * 64 * WV == BM * CH && WI * 64 * WV == BN * CH, "DMA plan must cover the tiles");
 };
 
-// GATED: pairs of 32 gate and 32 up columns, as in the bf16 kernel.
-template <bool LORA, int BM, int BN, int NS, bool SPLIT, int WV = 4, int WR = 2, bool GATED = false>
+// GATED: pairs of 32 gate and 32 up columns, EPI: the layer with its epilogue, as
+// in the bf16 kernel.
+template <bool LORA, int BM, int BN, int NS, bool SPLIT, int WV = 4, int WR = 2, bool EPI = false, bool GATED = false>
 __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     typedef fp8_cfg<BM, BN, NS, WV, WR> C;
     constexpr int BK = C::BK, CH = C::CH, WM = C::WM, WN = C::WN, RB = C::RB, CB = C::CB;
     constexpr int XI = C::XI, WI = C::WI, XSTAGE = C::XSTAGE, STAGE = C::STAGE;
-    static_assert(!GATED || WR * 32 * (BN + 4) * 4 <= C::LDS, "the gated store fits the stages' LDS");
+    static_assert(!(GATED || EPI) || WR * 32 * (BN + 4) * 4 <= C::LDS, "the store fits the stages' LDS");
+    static_assert(!EPI || (LORA && !SPLIT && !GATED), "whole tiles of the layer with its adapters");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int wm = w / (WV / WR), wn = w % (WV / WR);
@@ -204,18 +206,19 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
         uint8_t *xs = smem + buf * STAGE;
         uint8_t *wsm = xs + XSTAGE;
         const int k0 = k_begin + kt * BK;
-        // Gated: only a last, partial stage looks at its chunks' columns, which
+        // Gated, EPI: only a last, partial stage looks at its chunks' columns, which
         // it makes anew (the asm): the 256 x 256 tiles hold no register for them.
+        constexpr bool LEAN = GATED || EPI;
         const bool whole = k0 + BK <= k_end;
         int ln = lane;
-        if (GATED && !whole) asm volatile("" : "+v"(ln));
+        if (LEAN && !whole) asm volatile("" : "+v"(ln));
         auto in_k = [&](int j, int per) {
             return whole || k0 + 16 * ((ln ^ (ln >> 3) ^ (wu * per + j)) & (CH - 1)) < k_end;
         };
 #pragma unroll
         for (int j = 0; j < XI; ++j) {
             const int kk = k0 + xcol[j];
-            const bool in = GATED ? in_k(j, XI) : kk < k_end;
+            const bool in = LEAN ? in_k(j, XI) : kk < k_end;
             const void *src = (xrow[j] >= 0 && in) ? (const void *)(g.xq + xrow[j] + kk) : (const void *)g_zero16;
             dma16(src, xs + (w * XI + j) * 64 * 16);
         }
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
             const int kk = k0 + wcol[j];
             // gated: an instruction's 64 / CH rows are one projection's (a scalar choice)
             const uint8_t *wq = !GATED ? g.wq : (gated_up((wu * WI + j) * (64 / CH)) ? g.sl[1].wq : g.sl[0].wq);
-            const bool in = GATED ? in_k(j, WI) : kk < k_end;
+            const bool in = LEAN ? in_k(j, WI) : kk < k_end;
             const void *src = (wrow[j] >= 0 && in) ? (const void *)(wq + wrow[j] + kk) : (const void *)g_zero16;
             dma16(src, wsm + (w * WI + j) * 64 * 16);
         }
@@ -276,6 +279,7 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     // the row scale (1.0 for rows past T).
     constexpr bool SLOTS = GATED && !SPLIT;
     __shared__ row_slot s_slot[SLOTS ? BM : 1];
+    __shared__ row_term s_term[EPI ? BM : 1];
     __shared__ int32_t s_meta_t[BM], s_meta_id[BM], s_esx[BM];
     const int32_t n_fused = (LORA && g.n_fused) ? *g.n_fused : T;   // short-segment rows: separate expand
     for (int i = tid; i < BM; i += WV * 64) {
@@ -284,10 +288,11 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
         int32_t id = -1;
         if ((LORA || GATED) && t >= 0 && (!g.n_fused || p < n_fused)) {
             const int32_t raw = g.ids[t];
-            if (raw >= 0 && raw < g.n_slots && (GATED || g.rank[raw] > 0)) id = raw;
+            if (raw >= 0 && raw < g.n_slots && (GATED || EPI || g.rank[raw] > 0)) id = raw;
         }
         s_meta_t[i] = t;
-        if constexpr (SLOTS) set_row(g, id, !LORA, s_meta_id[i], s_slot[i]);
+        if constexpr (EPI) set_row_term(g, id, s_meta_id[i], s_term[i]);
+        else if constexpr (SLOTS) set_row(g, id, !LORA, s_meta_id[i], s_slot[i]);
         else s_meta_id[i] = id;
         s_esx[i] = t >= 0 ? e8m0_of(g.xs[t]) : 127;
     }
@@ -321,6 +326,8 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
         lora_pass_lean<RB, CB / 2, 0>(g, acc, s_meta_t, s_meta_id, s_slot, wm * WM, gated_col(n0 + wn * WN), lane);
         lora_pass_lean<RB, CB / 2, 1>(g, acc, s_meta_t, s_meta_id, s_slot, wm * WM, gated_col(n0 + wn * WN), lane);
     }
+    else if constexpr (EPI)
+        act_pass_lean<RB, CB>(g, acc, s_meta_t, s_meta_id, s_term, wu / (WV / WR) * WM, n0 + wu % (WV / WR) * WN, lane);
     else if (LORA && !SPLIT)
         lora_pass_impl<RB, CB, (RB >= 4 ? RB : 1), 1, 0>(g, acc, s_meta_t, s_meta_id, n0, wm * WM, n0 + wn * WN, lane);
     wait_stage(min(NS - 1, nk - 1));
@@ -359,7 +366,9 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 
-    if constexpr (GATED && !SPLIT)
+    if constexpr (EPI)
+        act_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_meta_id, s_term, n0);
+    else if constexpr (GATED && !SPLIT)
         gated_store_tile<BM, BN, WV, WR>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, s_meta_id, s_slot, n0, w,
                                          lane);
     else if constexpr (GATED)
@@ -371,13 +380,16 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_fp8(gemm_args g) {
 
 // NST, WVT: stages and wavefronts of the split-K pieces.
 template <int BM, int BN, int NS = 2, int WV = 4, int WR = 2, int NST = NS, int WVT = WV>
-static void launch_fp8_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t s) {
+static void launch_fp8_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t s, bool epi) {
     if (pl.n_dp > 0) {
         g.tile_base = 0;
         g.n_tiles = pl.n_dp;
         g.splits = 1;
         g.k_chunk = g.K;
-        if (lora)
+        if (epi)
+            hipLaunchKernelGGL((k_gemm_fp8<true, BM, BN, NS, false, WV, WR, true>), dim3(pl.n_dp), dim3(WV * 64), 0, s,
+                               g);
+        else if (lora)
             hipLaunchKernelGGL((k_gemm_fp8<true, BM, BN, NS, false, WV, WR>), dim3(pl.n_dp), dim3(WV * 64), 0, s, g);
         else
             hipLaunchKernelGGL((k_gemm_fp8<false, BM, BN, NS, false, WV, WR>), dim3(pl.n_dp), dim3(WV * 64), 0, s, g);
@@ -390,7 +402,9 @@ static void launch_fp8_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStrea
         hipLaunchKernelGGL((k_gemm_fp8<false, BM, BN, NST, true, WVT, WR>), dim3(pl.tail * pl.splits),
                            dim3(WVT * 64), 0, s, g);
         const dim3 rgrid(pl.tail * (BM / (2048 / BN)));
-        if (lora)
+        if (epi)
+            hipLaunchKernelGGL((k_splitk_reduce<true, false, BM, BN, true>), rgrid, dim3(256), 0, s, g);
+        else if (lora)
             hipLaunchKernelGGL((k_splitk_reduce<true, false, BM, BN>), rgrid, dim3(256), 0, s, g);
         else
             hipLaunchKernelGGL((k_splitk_reduce<false, false, BM, BN>), rgrid, dim3(256), 0, s, g);
@@ -411,8 +425,11 @@ lora_status_t launch_quant_cols_fp8(const void *W, int32_t K, int32_t N, uint8_t
 lora_status_t launch_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t *wq, const float *wsc, void *y,
                               int32_t T, int32_t d_in, int32_t d_out, const lora_pool_t *pool,
                               const int32_t *ids, const float *v, int32_t v_stride, const int32_t *perm,
-                              float *partial, size_t partial_bytes, hipStream_t s, const int32_t *n_fused) {
+                              float *partial, size_t partial_bytes, hipStream_t s, const int32_t *n_fused,
+                              const epilogue *epi) {
+    if (epi && !pool) return LORA_ERR_INVALID_ARGUMENT;
     gemm_args g{};
+    set_epilogue(g, epi);
     g.xq = xq;
     g.wq = wq;
     g.xs = xs;
@@ -438,10 +455,10 @@ lora_status_t launch_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t 
     g.col_strips = col_strips_pay(T, d_out, g.n_tiles_n);
     g.partial = partial;
     const bool lora = pool != nullptr;
-    if (pl.bm == 256 && pl.bn == 256) launch_fp8_cfg<256, 256, 2, 4>(g, pl, lora, s);
-    else if (pl.bm == 256 && pl.bn == 128) launch_fp8_cfg<256, 128, 2, 8>(g, pl, lora, s);
-    else if (pl.bn == 128) launch_fp8_cfg<128, 128, 2, 4, 2, 4, 8>(g, pl, lora, s);
-    else launch_fp8_cfg<128, 64>(g, pl, lora, s);
+    if (pl.bm == 256 && pl.bn == 256) launch_fp8_cfg<256, 256, 2, 4>(g, pl, lora, s, epi != nullptr);
+    else if (pl.bm == 256 && pl.bn == 128) launch_fp8_cfg<256, 128, 2, 8>(g, pl, lora, s, epi != nullptr);
+    else if (pl.bn == 128) launch_fp8_cfg<128, 128, 2, 4, 2, 4, 8>(g, pl, lora, s, epi != nullptr);
+    else launch_fp8_cfg<128, 64>(g, pl, lora, s, epi != nullptr);
     return hip_status(hipGetLastError());
 }
 
@@ -452,7 +469,7 @@ static void launch_gated_fp8_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s
         g.n_tiles = pl.n_dp;
         g.splits = 1;
         g.k_chunk = g.K;
-        hipLaunchKernelGGL((k_gemm_fp8<true, BM, BN, NS, false, WV, WR, true>), dim3(pl.n_dp), dim3(WV * 64), 0, s,
+        hipLaunchKernelGGL((k_gemm_fp8<true, BM, BN, NS, false, WV, WR, false, true>), dim3(pl.n_dp), dim3(WV * 64), 0, s,
                            g);
     }
     if (pl.tail > 0) {
@@ -460,7 +477,7 @@ static void launch_gated_fp8_cfg(gemm_args g, const gemm_plan &pl, hipStream_t s
         g.n_tiles = pl.tail;
         g.splits = pl.splits;
         g.k_chunk = pl.k_chunk;
-        hipLaunchKernelGGL((k_gemm_fp8<false, BM, BN, NST, true, WVT, WRT, true>), dim3(pl.tail * pl.splits),
+        hipLaunchKernelGGL((k_gemm_fp8<false, BM, BN, NST, true, WVT, WRT, false, true>), dim3(pl.tail * pl.splits),
                            dim3(WVT * 64), 0, s, g);
         launch_gated_reduce<BM, BN>(g, s);
     }
@@ -473,9 +490,9 @@ static void launch_gated_fp8_few(gemm_args g, const gemm_plan &pl, hipStream_t s
     g.splits = pl.splits;
     g.k_chunk = pl.k_chunk;
     if (pl.splits == 1)
-        hipLaunchKernelGGL((k_gemm_fp8<false, 32, 128, 3, false, 4, 1, true>), dim3(g.n_tiles), dim3(256), 0, s, g);
+        hipLaunchKernelGGL((k_gemm_fp8<false, 32, 128, 3, false, 4, 1, false, true>), dim3(g.n_tiles), dim3(256), 0, s, g);
     else {
-        hipLaunchKernelGGL((k_gemm_fp8<false, 32, 128, 3, true, 4, 1, true>), dim3(g.n_tiles * pl.splits), dim3(256),
+        hipLaunchKernelGGL((k_gemm_fp8<false, 32, 128, 3, true, 4, 1, false, true>), dim3(g.n_tiles * pl.splits), dim3(256),
                            0, s, g);
         launch_gated_reduce<32, 128>(g, s);
     }

@@ -33,6 +33,7 @@ LORA_AUTO_SGMV_MIN_ROWS = 512      # AUTO builds segments from this many rows on
 LORA_ACT_SILU = 0
 LORA_ACT_GELU = 1
 LORA_ACT_GELU_TANH = 2
+LORA_ACT_NONE = 3                  # lora_linear_act_forward and _backward only
 
 LORA_FLAG_SEGMENTS_READY = 0x1
 LORA_FLAG_SEPARATE_EXPAND = 0x2
@@ -56,6 +57,7 @@ EXPORTED = (
     "lora_add_rmsnorm", "lora_add_rmsnorm_fp8",
     "lora_add_layernorm", "lora_add_layernorm_fp8", "lora_workspace_bytes_layernorm_backward",
     "lora_add_layernorm_backward",
+    "lora_linear_act_forward", "lora_linear_act_forward_fp8",
     "lora_workspace_bytes_orthogonalize", "lora_orthogonalize",
     "lora_workspace_bytes_gated", "lora_workspace_bytes_gated_fp8", "lora_gated_forward", "lora_gated_forward_fp8",
     "lora_workspace_bytes_gated_backward", "lora_gated_backward",
@@ -161,6 +163,10 @@ def load(path: str = LIB_PATH):
         "lora_workspace_bytes_layernorm_backward": (c_sz, [c_i32, c_i32]),
         "lora_add_layernorm_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp,
                                                 c_vp, c_vp, c_sz, c_vp]),
+        "lora_linear_act_forward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_i32,
+                                            c_u32, c_vp, c_sz, c_vp]),
+        "lora_linear_act_forward_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,
+                                                P(lora_pool_t), c_vp, c_i32, c_i32, c_u32, c_vp, c_sz, c_vp]),
         "lora_workspace_bytes_orthogonalize": (c_sz, [c_i32, c_i32, c_i32]),
         "lora_orthogonalize": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, P(c_f), c_i32, c_f, c_f, c_vp, c_vp, c_sz,
                                        c_vp]),
@@ -542,6 +548,32 @@ def lora_add_layernorm_backward(dy, dresidual, z, weight, mean, rstd, T, d, dtyp
         (rstd, f32, T), (dx, dt, n), (dweight, dt, d), (dbias, dt, d), (ws, torch.uint8, 0))
     _ok(load().lora_add_layernorm_backward(dy, dresidual, z, weight, mean, rstd, T, d, dtype, dx, dweight, dbias, ws,
                                            nbytes, _stream(stream)), "lora_add_layernorm_backward")
+
+
+def lora_linear_act_forward(x, W, bias, residual, y, T, pool, ids, act, mode, flags, ws, pre=None, stream=None):
+    """y = act(x W + s (x A) B + bias) + residual; bias, residual: tensors or None (residual may be y); pre: a tensor
+    that keeps act's argument for the backward pass, or None."""
+    dt, n = _TORCH_TYPES.get(pool.dtype), T * pool.d_out
+    nbytes = _ws_bytes(ws)
+    x, W, bias, residual, y, pre, ids, ws = _checked(
+        "lora_linear_act_forward", (x, dt, T * pool.d_in), (W, dt, pool.d_in * pool.d_out), (bias, dt, pool.d_out),
+        (residual, dt, n), (y, dt, n), (pre, dt, n), (ids, torch.int32, T), (ws, torch.uint8, 0))
+    _ok(load().lora_linear_act_forward(x, W, bias, residual, y, pre, T, ctypes.byref(pool), ids, act, mode, flags, ws,
+                                       nbytes, _stream(stream)), "lora_linear_act_forward")
+
+
+def lora_linear_act_forward_fp8(x, xq, x_scale, wq, w_scale, bias, residual, y, T, pool, ids, act, mode, flags, ws,
+                                pre=None, stream=None):
+    """The same on an FP8 base weight; xq, x_scale: the codes and scales of x's rows, or None (made in ws)."""
+    dt, f32, n = torch.bfloat16, torch.float32, T * pool.d_out
+    nbytes = _ws_bytes(ws)
+    x, xq, x_scale, wq, w_scale, bias, residual, y, pre, ids, ws = _checked(
+        "lora_linear_act_forward_fp8", (x, dt, T * pool.d_in), (xq, _CODES, T * pool.d_in), (x_scale, f32, T),
+        (wq, _CODES, pool.d_in * pool.d_out), (w_scale, f32, pool.d_out), (bias, dt, pool.d_out), (residual, dt, n),
+        (y, dt, n), (pre, dt, n), (ids, torch.int32, T), (ws, torch.uint8, 0))
+    _ok(load().lora_linear_act_forward_fp8(x, xq, x_scale, wq, w_scale, bias, residual, y, pre, T, ctypes.byref(pool),
+                                           ids, act, mode, flags, ws, nbytes, _stream(stream)),
+        "lora_linear_act_forward_fp8")
 
 
 def lora_workspace_bytes_orthogonalize(n, rows, cols) -> int:

@@ -106,3 +106,57 @@ def test_the_binding_refuses_tensors_the_kernels_would_misread():
         with pytest.raises(L.LoraError) as e:
             call()
         assert e.value.status == INVALID
+
+
+def pool(**change):
+    f = dict(n_slots=4, d_in=64, d_out=96, max_rank=16, dtype=L.LORA_BF16)
+    f.update(change)
+    P = [FAKE + (i << 32) for i in range(8, 12)]
+    return L.lora_pool_t(f["n_slots"], f["d_in"], f["d_out"], f["max_rank"], f["dtype"], *P)
+
+
+def test_linear_act_forward(lib):
+    need = L.lora_workspace_bytes(8, 4, 16, 0)
+    p0 = pool()
+
+    def call(x=A[0], w=A[1], b=A[2], r=A[3], y=A[4], pre=A[5], T=8, p=p0, ids=A[6], act=3, mode=0, flags=0, ws=A[7],
+             n=need):
+        return lib.lora_linear_act_forward(x, w, b, r, y, pre, T, p, ids, act, mode, flags, ws, n, None)
+
+    for bad in (dict(x=None), dict(w=None), dict(y=None), dict(ids=None), dict(T=-1), dict(act=4), dict(act=-1),
+                dict(mode=3), dict(flags=2), dict(flags=0x1000), dict(ws=None), dict(ws=A[7] + 8), dict(x=A[0] + 2),
+                dict(w=A[1] + 8), dict(b=A[2] + 4), dict(r=A[3] + 8), dict(y=A[4] + 8), dict(pre=A[5] + 8), dict(p=None),
+                dict(p=pool(d_in=60)), dict(p=pool(dtype=2)), dict(p=pool(max_rank=12)),
+                # outputs that meet another buffer (a residual that only partly is y's)
+                dict(y=A[0]), dict(y=A[1]), dict(y=A[2]), dict(y=A[5]), dict(y=A[7]), dict(pre=A[3]), dict(pre=A[0]),
+                dict(y=A[6]), dict(r=A[4] + 16), dict(ws=A[3]), dict(ws=A[2]), dict(y=p0.b), dict(pre=p0.scale)):
+        assert call(**bad) == INVALID, bad
+    assert call(n=need - 1) == SMALL
+    assert call(T=0, x=None, w=None, b=None, r=None, y=None, pre=None, ids=None) == OK
+
+
+def test_linear_act_forward_fp8(lib):
+    need, lean = L.lora_workspace_bytes_fp8(8, 4, 16, 64, 0), L.lora_workspace_bytes(8, 4, 16, 0)
+    p0 = pool()
+
+    def call(x=A[0], xq=None, xs=None, w=A[1], wsc=A[8], b=A[2], r=A[3], y=A[4], pre=A[5], T=8, p=p0, ids=A[6], act=3,
+             mode=0, flags=0, ws=A[7], n=need):
+        return lib.lora_linear_act_forward_fp8(x, xq, xs, w, wsc, b, r, y, pre, T, p, ids, act, mode, flags, ws, n, None)
+
+    for bad in (dict(x=None), dict(w=None), dict(wsc=None), dict(y=None), dict(ids=None), dict(xq=A[9]), dict(xs=A[9]),
+                dict(act=4), dict(mode=3), dict(flags=2), dict(ws=None), dict(x=A[0] + 2), dict(xq=A[9] + 1, xs=A[10]),
+                dict(xq=A[9], xs=A[10] + 4), dict(w=A[1] + 8), dict(wsc=A[8] + 4), dict(b=A[2] + 4), dict(r=A[3] + 8),
+                dict(y=A[4] + 8), dict(pre=A[5] + 8), dict(p=pool(d_in=72)), dict(p=pool(dtype=0)),
+                dict(y=A[0]), dict(y=A[1]), dict(y=A[8]), dict(y=A[9], xq=A[9], xs=A[10]),
+                dict(pre=A[10], xq=A[9], xs=A[10]), dict(r=A[4] + 16), dict(ws=A[3])):
+        assert call(**bad) == INVALID, bad
+    assert call(n=need - 1) == SMALL
+    assert call(n=lean - 1, xq=A[9], xs=A[10]) == SMALL
+    assert call(T=0, x=None) == OK
+
+
+def test_linear_act_refuses_rows_of_more_tiles_than_a_grid_holds(lib):
+    T, far = (1 << 31) - 1, [(1 << 40) + (i << 44) for i in range(8)]
+    p = pool(d_in=8, d_out=264, n_slots=1)
+    assert lib.lora_linear_act_forward(far[0], far[1], None, None, far[2], None, T, p, far[3], 3, 0, 0, far[4], 1 << 42,
+                                       None) == UNSUPPORTED
