@@ -677,6 +677,24 @@ lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, cons
                                           lora_act_t act, lora_mode_t mode, uint32_t flags, void *ws, size_t ws_bytes,
                                           lora_stream_t stream);
 
+/* Backward pass of the layer, the base weight frozen: from dy DEVICE [T, d_out], the
+ * gradient of y (which is the residual's own gradient too), and pre as the forward
+ * pass kept it for the same x, ids and adapters (act LORA_ACT_NONE: not read, may be
+ * NULL), with s = scale[a], a = ids[t]:
+ *     dp = dy act'(pre),   dv = s dp B_a^T,   dx = dp W^T + dv A_a^T
+ *     dA_a = sum over a's rows of x^T dv,   dB_a = s sum of (x A_a)^T dp,   dbias = sum of dp
+ * dx DEVICE [T, d_in], dA DEVICE [n_slots, d_in, max_rank] and dB DEVICE [n_slots,
+ * max_rank, d_out] (both or neither NULL), dbias DEVICE [d_out], each overwritten, or
+ * NULL: not computed.  Layouts, zeros, types, roundings and errors as
+ * lora_gated_backward's (with act LORA_ACT_NONE nothing but the outputs is rounded
+ * in bf16).   ws:
+ * lora_workspace_bytes_linear_act_backward, cleared by lora_workspace_init. */
+size_t lora_workspace_bytes_linear_act_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in,
+                                                int32_t d_out, lora_dtype_t dtype);
+lora_status_t lora_linear_act_backward(const void *x, const void *W, int32_t T, const lora_pool_t *pool,
+                                       const int32_t *ids, lora_act_t act, const void *pre, const void *dy, void *dx,
+                                       void *dA, void *dB, void *dbias, void *ws, size_t ws_bytes, lora_stream_t stream);
+
 /* ---- orthogonalised updates ---------------------------------------------------------- */
 
 /* What an orthogonalising optimiser makes of a gradient (or of its momentum): for

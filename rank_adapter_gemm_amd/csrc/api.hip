@@ -796,8 +796,8 @@ lora_status_t lora_gated_backward(const void *x, const void *W_gate, const void 
                                  {gate, rows}, {up, rows}, {dh, rows}};
     pair_spans(pools, read + 7);
     if (!outputs_clear(out, 6, read, 7 + kPairSpans)) return LORA_ERR_INVALID_ARGUMENT;
-    gated_bwd_call c{x, {W_gate, W_up}, gate, up, dh, dx, {nullptr, nullptr}, {nullptr, nullptr}, T, (int32_t)act,
-                     pools, ids, ws, ws_bytes};
+    bwd_call c{x, {W_gate, W_up}, {gate, up}, dh, dx, {nullptr, nullptr}, {nullptr, nullptr}, nullptr, T, (int32_t)act,
+               pools, ids, ws, ws_bytes};
     for (int i = 0; i < 2 && dA; ++i) {
         c.dA[i] = dA[i];
         c.dB[i] = dB[i];
@@ -957,6 +957,46 @@ lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, cons
     return launch_gemm_fp8(xq, x_scale, wq, w_scale, y, T, pool->d_in, pool->d_out, pool, ids, v, pool->max_rank,
                            sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr, ws_ptr<float>(ws, L.gemm_partial),
                            ws_bytes - L.gemm_partial, s, nullptr, &epi);
+}
+
+size_t lora_workspace_bytes_linear_act_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in,
+                                                int32_t d_out, lora_dtype_t dtype) {
+    if (lora_workspace_bytes(T, n_slots, max_rank, 0) == 0 || !valid_dtype(dtype) || d_in <= 0 || d_out <= 0 ||
+        !valid_dims(n_slots, d_in, d_out, max_rank))
+        return 0;
+    return make_bwd_layout(T, n_slots, max_rank, d_in, d_out, dtype, 1).total;
+}
+
+lora_status_t lora_linear_act_backward(const void *x, const void *W, int32_t T, const lora_pool_t *pool,
+                                       const int32_t *ids, lora_act_t act, const void *pre, const void *dy, void *dx,
+                                       void *dA, void *dB, void *dbias, void *ws, size_t ws_bytes, lora_stream_t stream) {
+    if (!valid_pool(pool) || T < 0 || !valid_act_or_none(act) || !dA != !dB || !aligned16(dA) || !aligned16(dB) ||
+        !aligned16(dbias))
+        return LORA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!x || !W || !ids || !dy || (act != LORA_ACT_NONE && !pre) || !aligned16(x) || !aligned16(W) ||
+                  !aligned16(pre) || !aligned16(dy) || !aligned16(dx)))
+        return LORA_ERR_INVALID_ARGUMENT;
+    const lora_pool_t &p = *pool;
+    const bwd_layout B = make_bwd_layout(T, p.n_slots, p.max_rank, p.d_in, p.d_out, p.dtype, 1);
+    if (!ws || !aligned16(ws)) return LORA_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < B.partial) return LORA_ERR_WORKSPACE_TOO_SMALL;
+    const hipStream_t s = hs(stream);
+    const size_t eb = dtype_bytes(p.dtype), slots = (size_t)p.n_slots * p.max_rank * eb, da = slots * p.d_in,
+                 db = slots * p.d_out, in = (size_t)T * p.d_in * eb, rows = (size_t)T * p.d_out * eb;
+    const span out[] = {{dx, in}, {ws, ws_bytes}, {dA, da}, {dB, db}, {dbias, (size_t)p.d_out * eb}};
+    span read[5 + kPoolSpans] = {{x, in}, {W, (size_t)p.d_in * p.d_out * eb}, {ids, 4 * (size_t)T}, {pre, rows}, {dy, rows}};
+    pool_spans(p, read + 5);
+    if (T == 0) {
+        if (!outputs_clear(out + 2, 3, nullptr, 0)) return LORA_ERR_INVALID_ARGUMENT;
+        lora_status_t st = dA ? launch_zero(dA, da, s) : LORA_OK;
+        if (st == LORA_OK && dB) st = launch_zero(dB, db, s);
+        if (st == LORA_OK && dbias) st = launch_zero(dbias, (size_t)p.d_out * eb, s);
+        return st;
+    }
+    if (!outputs_clear(out, 5, read, 5 + kPoolSpans)) return LORA_ERR_INVALID_ARGUMENT;
+    const bwd_call c{x, {W, nullptr}, {pre, nullptr}, dy, dx, {dA, nullptr}, {dB, nullptr}, dbias, T, (int32_t)act,
+                     pool, ids, ws, ws_bytes};
+    return launch_linear_backward(c, B, s);
 }
 
 // The layer norms': as valid_norm, with a bias and the kept statistics.

@@ -336,30 +336,34 @@ lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s);
 lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *pools, const int32_t *ids, float *v,
                                  int32_t *err, hipStream_t s);
 
-// Its backward pass: the workspace of a forward (segments, v and the shrink's
-// partials for 2 max_rank columns) and what follows it.
+// Its backward pass, and the linear layer's (one projection): the workspace of a
+// forward (segments, v and the shrink's partials for the projections' max_rank
+// columns) and what follows it.
 struct bwd_layout {
     ws_layout L;
-    size_t dy;          // dg, du: [2][T][d_out], the pools' dtype; bf16: first parts, then second parts
-    size_t dv;          // fp32 [T][2 max_rank]
+    size_t dy;          // dg, du (one projection: dp): [T][d_out] each, the pools' dtype; bf16: first parts, then second
+    size_t dv;          // fp32 [T][R2], see bwd_ranks
     size_t vt;          // bf16 parts of s v and dv, transposed (see k_rank_finish)
     size_t oct;         // bf16: both slices' A in rank octets, one set per segment
     size_t row0, rank, scale;   // their pool tables, [n_slots]
     size_t slot_blk;    // [n_slots]: first work block of a slot's segment
+    size_t sums;        // one projection: fp32 [stretches][d_out], dbias's partial sums
     size_t partial;     // dx's split-K partials
     size_t total;
 };
-struct gated_bwd_call {
-    const void *x, *W[2], *gate, *up, *dh;
-    void *dx, *dA[2], *dB[2];
+struct bwd_call {
+    const void *x, *W[2], *kept[2], *dh;   // kept: gate and up, or act's argument; dh: the gradient of the output
+    void *dx, *dA[2], *dB[2], *dbias;
     int32_t T, act;
     const lora_pool_t *pools;
     const int32_t *ids;
     void *ws;
     size_t ws_bytes;
 };
-bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out, int32_t dtype);
-lora_status_t launch_gated_backward(const gated_bwd_call &c, const bwd_layout &B, hipStream_t s);
+bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in, int32_t d_out, int32_t dtype,
+                           int32_t n_proj = 2);
+lora_status_t launch_gated_backward(const bwd_call &c, const bwd_layout &B, hipStream_t s);
+lora_status_t launch_linear_backward(const bwd_call &c, const bwd_layout &B, hipStream_t s);
 lora_status_t launch_zero(void *p, size_t bytes, hipStream_t s);   // bytes: a multiple of 16
 
 // z = x + residual (residual may be null), y = z / sqrt(mean(z^2) + eps) * weight

@@ -7,6 +7,10 @@
 // Rows are visited in adapter order (the segment builder's perm), so every
 // sum over an adapter's rows runs over neighbours, in row order, without
 // atomics: results repeat bitwise.
+//
+// And of the linear layer y = act(p) + residual, p = x W + s_a (x A_a) B_a + bias:
+//   dp = dy * act'(p),  dbias = sum of dp          k_act_grad, k_column_sums
+// and the same kernels for the one projection (NM, the number of projections, 1).
 #include "gated_common.hpp"
 
 namespace lora {
@@ -84,15 +88,15 @@ __global__ void __launch_bounds__(256) k_gated_dact(const typename elem<DT>::T *
 // thread strides the row's N values against the slot's B octets (190 rows, 1384
 // wide: 8 us, latency).
 // ---------------------------------------------------------------------------
-template <int DT>
+template <int DT, int NM>
 __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>::T *dy, int64_t dy_stride, int32_t T,
                                                         int32_t N, pair_pools pp, int32_t n_slots, int32_t R,
                                                         const int32_t *ids, float *dv) {
     typedef typename elem<DT>::T E;
     const int64_t wg = grid_index();
-    if (wg >= 2ll * T) return;
-    const int t = (int)(wg >> 1), m = (int)(wg & 1);
-    float *out = dv + (int64_t)t * 2 * R + m * R;
+    if (wg >= (int64_t)NM * T) return;
+    const int t = (int)(wg / NM), m = (int)(wg % NM);
+    float *out = dv + (int64_t)t * NM * R + m * R;
     const int32_t id = ids[t];
     const int32_t r = id >= 0 && id < n_slots ? min(pp.rank[m][id], R) : 0;
     const E *row = dy + m * dy_stride + (int64_t)t * N;
@@ -124,7 +128,8 @@ __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>:
 }
 
 // bf16: a grouped product over adapter segments, as k_shrink_grouped, of up to
-// 32 rows of dg (or du, blockIdx.z) with the adapter's B.  Both operands go
+// 32 rows of dg (or du, blockIdx.z) with the adapter's B.  (PARTS = 1: dp is dy
+// itself, bf16 with no second part.)  Both operands go
 // global -> LDS by DMA, NS stages of 128 n; B's octets ([n][8 ranks], 16 bytes
 // a column) lie in LDS as in memory and are read transposed
 // (ds_read_b64_tr_b16: 4 n of 16 ranks per instruction).  Each of the 4
@@ -133,27 +138,28 @@ __global__ void __launch_bounds__(256) k_rank_grad_rows(const typename elem<DT>:
 // of 14336: 57 us, with three stages 64; 16 ranks 46 and 40).
 // Partial sums go to part[m][split][sorted position][R].  Bound by the bytes of
 // dg's and du's parts (2048 rows of 14336: 43 us, 5.5 TB/s).
-template <int RCH> struct rank_grad_cfg {
+template <int RCH, int PARTS> struct rank_grad_cfg {
     static constexpr int BR = kShrinkRows, NR = RCH * 16, BK = 128, CH = BK / 8, NS = RCH > 2 ? 2 : 3;
     static constexpr int OCT = BK * 8 + 16;              // elements between octets (32 bytes apart in the banks)
-    static constexpr int YST = BR * BK, STAGE = 2 * YST + (NR / 8) * OCT;   // dy's two parts, B
+    static constexpr int YST = BR * BK, STAGE = PARTS * YST + (NR / 8) * OCT;   // dy's parts, B
     static constexpr int YI = BR * CH / 256, BI = NR / 8 * BK / 256;   // DMA instructions per wave per stage
     static constexpr int RED = 4 * BR * (NR + 1);
     static constexpr int LDS_BYTES = NS * STAGE * 2 > RED * 4 ? NS * STAGE * 2 : RED * 4;
 };
 
 struct rank_grad_args {
-    const uint16_t *dy;                // first and second parts: [2][2][T][N]
+    const uint16_t *dy;                // first and second parts: [2][NM][T][N]
     int32_t T, N, R, n_slots, n_chunk;
     const int32_t *perm, *seg_id, *seg_start, *n_seg, *blk_start, *blk_seg;
     float *part;
 };
 
-template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_args g, pair_pools pp) {
-    typedef rank_grad_cfg<RCH> C;
-    constexpr int BR = C::BR, NR = C::NR, BK = C::BK, CH = C::CH, NS = C::NS, PER = 2 * C::YI + C::BI;
+template <int RCH, int NM, int PARTS>
+__global__ void __launch_bounds__(256) k_rank_grad(rank_grad_args g, pair_pools pp) {
+    typedef rank_grad_cfg<RCH, PARTS> C;
+    constexpr int BR = C::BR, NR = C::NR, BK = C::BK, CH = C::CH, NS = C::NS, PER = PARTS * C::YI + C::BI;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[C::LDS_BYTES / 2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = NM > 1 ? blockIdx.z : 0;
     const int nseg = min(*g.n_seg, g.n_slots);
     if (nseg <= 0 || (int)blockIdx.x >= g.blk_start[nseg]) return;
     const int seg = g.blk_seg[blockIdx.x];
@@ -166,7 +172,7 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
     const int p0 = (int)q0, pend = (int)(s1 < q0 + BR ? s1 : q0 + BR);
     const int32_t rk = min(pp.rank[m][id], g.R);
     const int n_begin = blockIdx.y * g.n_chunk, n_end = min(g.N, n_begin + g.n_chunk);
-    const int64_t lo = 2ll * g.T * g.N;
+    const int64_t lo = (int64_t)NM * g.T * g.N;
     const uint16_t *dy = g.dy + (int64_t)m * g.T * g.N;
     const uint16_t *b = (const uint16_t *)pp.b[m] + slot_row0(pp.row0[m], id, g.R) * g.N;
 
@@ -180,10 +186,10 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
         ycol[j] = 8 * ((c % CH) ^ (r % CH));
     }
     auto dma_stage = [&](int kt, int buf) {
-        uint16_t *ys = smem + buf * C::STAGE, *bs = ys + 2 * C::YST;
+        uint16_t *ys = smem + buf * C::STAGE, *bs = ys + PARTS * C::YST;
         const int k0 = n_begin + kt * BK;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
             for (int j = 0; j < C::YI; ++j) {
                 const int n = k0 + ycol[j];
@@ -219,14 +225,14 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (kt + NS - 1 < nk) dma_stage(kt + NS - 1, (kt + NS - 1) % NS);
-        const uint16_t *ys = smem + (kt % NS) * C::STAGE, *bs = ys + 2 * C::YST;
-        uint4 yq[2][2];
+        const uint16_t *ys = smem + (kt % NS) * C::STAGE, *bs = ys + PARTS * C::YST;
+        uint4 yq[PARTS][2];
         bf16x8_t bq[RCH];
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb) {
             const int r = rb * 16 + l16;
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < PARTS; ++part)
                 yq[part][rb] = *reinterpret_cast<const uint4 *>(ys + part * C::YST + r * BK +
                                                                 8 * ((4 * wave + kg) ^ (r % CH)));
         }
@@ -244,7 +250,7 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
             bq[rc] = __builtin_bit_cast(bf16x8_t, hv);
         }
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
             for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
@@ -269,27 +275,29 @@ template <int RCH> __global__ void __launch_bounds__(256) k_rank_grad(rank_grad_
     }
 }
 
-// A of the batch's slots in rank octets, gate's ranks then up's: [segment][2R /
+// A of the batch's slots in rank octets, gate's ranks then up's: [segment][R2 /
 // 8][d_in][8], with the tables (row0, rank, scale) that make them one pool of
-// max_rank 2R for the low-rank pass of the dx product.  dv holds the scales
+// max_rank R2 for the low-rank pass of the dx product (R2: 2R of the pair, of one
+// projection R in whole 16s, with zeros from R on).  dv holds the scales
 // already, so the table's are 1.  Octet o of 256 values of d_in of segment i.
 struct a_octets_args {
     const int32_t *seg_id, *n_seg;
-    int32_t n_slots, K, R, k_blocks;
+    int32_t n_slots, K, R, R2, k_blocks;
     uint16_t *oct;
     int32_t *row0, *rank;
     float *scale;
 };
 
+template <int NM>
 __device__ __forceinline__ void a_octets(const a_octets_args &g, const pair_pools &pp, int i, int kb, int o) {
     if (i >= min(*g.n_seg, g.n_slots)) return;
     const int32_t id = g.seg_id[i], R = g.R;
     if (id < 0 || id >= g.n_slots) return;
-    const int m = 8 * o >= R, j0 = 8 * o - m * R;
-    const int32_t r[2] = {min(pp.rank[0][id], R), min(pp.rank[1][id], R)};
+    const int m = NM > 1 && 8 * o >= R, j0 = 8 * o - m * R;
+    const int32_t r[2] = {min(pp.rank[0][id], R), NM > 1 ? min(pp.rank[1][id], R) : 0};
     if (kb == 0 && o == 0 && threadIdx.x == 0) {
-        g.row0[id] = i * 2 * R;
-        g.rank[id] = r[0] > 0 || r[1] > 0 ? 2 * R : 0;
+        g.row0[id] = i * g.R2;
+        g.rank[id] = r[0] > 0 || r[1] > 0 ? g.R2 : 0;
         g.scale[id] = 1.0f;
     }
     const int k = kb * 256 + threadIdx.x;
@@ -298,13 +306,13 @@ __device__ __forceinline__ void a_octets(const a_octets_args &g, const pair_pool
     uint32_t e[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) e[q] = j0 + q < (m ? r[1] : r[0]) ? a[(int64_t)q * g.K] : 0u;
-    stg16(g.oct + (((int64_t)i * 2 * R / 8 + o) * g.K + k) * 8,
+    stg16(g.oct + (((int64_t)i * g.R2 / 8 + o) * g.K + k) * 8,
           make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16));
 }
 
-// The rank vectors as the products that follow read them.  dv, fp32 [T][2R]
+// The rank vectors as the products that follow read them.  dv, fp32 [T][R2]
 // in batch order: the partial sums added in split order, times the slot's
-// scale; zero for rows without an adapter.  vt, bf16 [2][2][2R][Tp]: s v and
+// scale; zero for rows without an adapter.  vt, bf16 [2][2][R2][Tp]: s v and
 // dv, transposed, in adapter order with every segment's start on a multiple
 // of 32 (its first work block), each value as two bf16 parts (hi = bf16(f),
 // lo = bf16(f - hi): together within 2^-17 of f, far below the rounding of
@@ -315,7 +323,7 @@ __device__ __forceinline__ void a_octets(const a_octets_args &g, const pair_pool
 // the chip busy.  2048 rows: 7 us, latency.
 struct rank_finish_args {
     const float *v, *part;
-    int32_t n_split, T, R, n_slots, n_work, Tp;
+    int32_t n_split, T, R, R2, n_slots, n_work, Tp;
     const int32_t *perm, *offsets, *seg_id, *seg_start, *n_seg, *blk_start, *blk_seg;
     float *dv;
     uint16_t *vt;
@@ -323,12 +331,13 @@ struct rank_finish_args {
     int32_t first_octet;
 };
 
+template <int NM>
 __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, a_octets_args oc, pair_pools pp) {
     constexpr int BR = kShrinkRows;
-    const int R2 = 2 * g.R;
+    const int R2 = NM > 1 ? NM * g.R : g.R2;
     if ((int)blockIdx.x >= g.first_octet) {
         const int item = (int)blockIdx.x - g.first_octet;
-        a_octets(oc, pp, item / oc.k_blocks, item % oc.k_blocks, blockIdx.y);
+        a_octets<NM>(oc, pp, item / oc.k_blocks, item % oc.k_blocks, blockIdx.y);
         return;
     }
     if ((int)blockIdx.x >= g.n_work) {
@@ -354,11 +363,11 @@ __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, a_octet
     const int64_t t = p >= 0 && p < pend ? perm_row(g.perm, p, g.T) : -1;
     const int64_t at = (int64_t)blockIdx.x * BR + i;
     {
-        const int j = blockIdx.y * 8 + (threadIdx.x >> 5), m = j >= g.R, jj = j - m * g.R;
+        const int j = blockIdx.y * 8 + (threadIdx.x >> 5), m = NM > 1 && j >= g.R, jj = j - m * g.R;
         float f[2] = {0.0f, 0.0f};                        // s v, dv
         if (t >= 0 && jj < min(pp.rank[m][id], g.R)) {
             const float s = pp.scale[m][id];
-            f[0] = s * g.v[t * R2 + j];
+            f[0] = s * g.v[t * NM * g.R + j];
             const float *part = g.part + ((int64_t)m * g.n_split * g.T + p) * g.R + jj;
             for (int c = 0; c < g.n_split; ++c) f[1] += part[(int64_t)c * g.T * g.R];
             f[1] *= s;
@@ -664,15 +673,16 @@ struct dx_f32_args {
     int32_t T, F, N, n_slots, R, n_tiles_n, splits, k_chunk;
 };
 
+template <int NM>
 __device__ __forceinline__ void dx_finish4(const dx_f32_args &g, const pair_pools &pp, int64_t t, int n,
                                            float (&o)[4]) {
     const int32_t id = g.ids[t];
     if (id >= 0 && id < g.n_slots) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < NM; ++m) {
             const int32_t rk = min(pp.rank[m][id], g.R);
             const float *a = (const float *)pp.a[m] + slot_row0(pp.row0[m], id, g.R) * g.N + n;
-            const float *dv = g.dv + t * 2 * g.R + m * g.R;
+            const float *dv = g.dv + t * NM * g.R + m * g.R;
             float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
             for (int j = 0; j < rk; ++j) {
@@ -691,7 +701,7 @@ __device__ __forceinline__ void dx_finish4(const dx_f32_args &g, const pair_pool
 }
 
 // Workgroup b of n.
-template <bool SPLIT>
+template <bool SPLIT, int NM>
 __device__ __forceinline__ void dx_f32(const dx_f32_args &g, const pair_pools &pp, int b, int n) {
     constexpr int BK = 32, NS = 3, AST = 64 * BK, STAGE = 2 * AST, LD = 64 + 4, PER = 4;
     __shared__ __attribute__((aligned(1024))) float smem[NS * STAGE];     // stages: [64][BK] of each; sums: [64][LD]
@@ -701,7 +711,7 @@ __device__ __forceinline__ void dx_f32(const dx_f32_args &g, const pair_pools &p
     f32_tile(b, n, (g.T + 63) / 64, SPLIT ? g.splits : 1, tm, tn, split);
     const int tile = tm * g.n_tiles_n + tn, m0 = tm * 64, n0 = tn * 64;
     const int Fp = (g.F + BK - 1) / BK * BK;
-    const int k_begin = split * g.k_chunk, k_end = min(2 * Fp, k_begin + g.k_chunk);
+    const int k_begin = split * g.k_chunk, k_end = min(NM * Fp, k_begin + g.k_chunk);
     // DMA: 16-byte chunk 256 j + tid of an operand is at row / 8, place % 8, and
     // holds the row's chunk place ^ (row % 8)
     int64_t arow[2], wrow[2];
@@ -716,7 +726,7 @@ __device__ __forceinline__ void dx_f32(const dx_f32_args &g, const pair_pools &p
     auto dma_stage = [&](int kt, int buf) {
         float *as = smem + buf * STAGE, *wsm = as + AST;
         const int k0 = k_begin + kt * BK;
-        const bool second = k0 >= Fp;                      // a step lies in one projection
+        const bool second = NM > 1 && k0 >= Fp;            // a step lies in one projection
         const float *a = second ? g.a1 : g.a0, *wt = second ? g.w1 : g.w0;
         const int f = k0 - (second ? Fp : 0) + kk;
 #pragma unroll
@@ -770,11 +780,11 @@ __device__ __forceinline__ void dx_f32(const dx_f32_args &g, const pair_pools &p
         if (t < 0 || n >= g.N) continue;
         float o[4];
         *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(smem + (i >> 4) * LD + c);
-        dx_finish4(g, pp, t, n, o);
+        dx_finish4<NM>(g, pp, t, n, o);
     }
 }
 
-__global__ void __launch_bounds__(256) k_dx_reduce_f32(dx_f32_args g, pair_pools pp) {
+template <int NM> __global__ void __launch_bounds__(256) k_dx_reduce_f32(dx_f32_args g, pair_pools pp) {
     const int tile = blockIdx.x >> 2, r = (blockIdx.x & 3) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
     const int p = tile / g.n_tiles_n * 64 + r, n = tile % g.n_tiles_n * 64 + c;
     const int64_t t = p < g.T ? perm_row(g.perm, p, g.T) : -1;
@@ -785,7 +795,7 @@ __global__ void __launch_bounds__(256) k_dx_reduce_f32(dx_f32_args g, pair_pools
         const float4 f = *reinterpret_cast<const float4 *>(part);
         o[0] += f.x; o[1] += f.y; o[2] += f.z; o[3] += f.w;
     }
-    dx_finish4(g, pp, t, n, o);
+    dx_finish4<NM>(g, pp, t, n, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -797,24 +807,25 @@ __global__ void __launch_bounds__(256) k_dx_reduce_f32(dx_f32_args g, pair_pools
 // rows of 6 slots, 520 and 1384 wide: 10 us, latency.)
 // ---------------------------------------------------------------------------
 struct outer_f32_args {
-    const float *x, *dg, *du, *v, *dv;  // [T][K], [T][F], [T][F], [T][2R] (times the scale: dv), [T][2R]
+    const float *x, *dg, *du, *v, *dv;  // [T][K], [T][F], [T][F], [T][NM R] (times the scale: dv), [T][NM R]
     float *dA0, *dA1, *dB0, *dB1;
     const int32_t *offsets, *perm;
     int32_t T, K, F, R, n_slots, tiles_k, tiles_f;
 };
 
+template <int NM>
 __device__ __forceinline__ void seg_outer_f32(const outer_f32_args &g, const pair_pools &pp, int64_t wg) {
     constexpr int J = 16, U = 8, CH = 64;
     __shared__ __attribute__((aligned(16))) float s_p[CH][J];
     __shared__ int32_t s_row[CH];
-    const int64_t n_a = 2ll * g.n_slots * g.tiles_k;
+    const int64_t n_a = (int64_t)NM * g.n_slots * g.tiles_k;
     const bool is_a = wg < n_a;
     const int tiles = is_a ? g.tiles_k : g.tiles_f;
     int item = (int)(is_a ? wg : wg - n_a);
-    if (!is_a && item >= 2 * g.n_slots * tiles) return;
+    if (!is_a && item >= NM * g.n_slots * tiles) return;
     const int tile = item % tiles;
     item /= tiles;
-    const int m = item & 1, slot = item >> 1;
+    const int m = item % NM, slot = item / NM;
     const int N = is_a ? g.K : g.F, R = g.R, n = tile * 256 + threadIdx.x;
     const int p0 = max(g.offsets[slot + 1], 0), p1 = min(g.offsets[slot + 2], g.T);
     const int32_t r = min(m ? pp.rank[1][slot] : pp.rank[0][slot], R);
@@ -834,7 +845,7 @@ __device__ __forceinline__ void seg_outer_f32(const outer_f32_args &g, const pai
                 {
                     const int i = threadIdx.x >> 2, j = (threadIdx.x & 3) * 4;
                     const int32_t t = i < rows ? perm_row(g.perm, p + i, g.T) : -1;
-                    *reinterpret_cast<f32x4_t *>(&s_p[i][j]) = load4(t >= 0 && j0 + j < R, pv + (int64_t)t * 2 * R + j0 + j);
+                    *reinterpret_cast<f32x4_t *>(&s_p[i][j]) = load4(t >= 0 && j0 + j < R, pv + (int64_t)t * NM * R + j0 + j);
                 }
                 __syncthreads();
                 for (int u0 = 0; u0 < rows; u0 += U) {
@@ -862,11 +873,11 @@ __device__ __forceinline__ void seg_outer_f32(const outer_f32_args &g, const pai
 // dx's tiles, then the adapters' gradients: neither needs the other, and
 // together they fill more of the chip (190 rows, 520 and 1384 wide: 17 us,
 // and 14 + 10 apart).
-template <bool SPLIT>
+template <bool SPLIT, int NM>
 __global__ void __launch_bounds__(256, 2) k_dx_outer_f32(dx_f32_args d, outer_f32_args o, pair_pools pp, int32_t n_dx) {
     const int64_t wg = grid_index();
-    if (wg < n_dx) dx_f32<SPLIT>(d, pp, (int)wg, n_dx);
-    else seg_outer_f32(o, pp, wg - n_dx);
+    if (wg < n_dx) dx_f32<SPLIT, NM>(d, pp, (int)wg, n_dx);
+    else seg_outer_f32<NM>(o, pp, wg - n_dx);
 }
 
 // bf16, on the matrix cores: out[j][n] = sum_t vt[j][t] q[t][n] over a slot's
@@ -879,9 +890,9 @@ __global__ void __launch_bounds__(256, 2) k_dx_outer_f32(dx_f32_args d, outer_f3
 // 14336 wide: 43 us, 5.9 TB/s).
 constexpr int kOuterCols = 128, kOuterRows = 1024;
 struct seg_outer_args {
-    const uint16_t *x, *dy, *vt;       // [T][K], [2][2][T][N] (both first parts, both second), see k_rank_finish
+    const uint16_t *x, *dy, *vt;       // [T][K], [2][NM][T][N] (the first parts, the second), see k_rank_finish
     uint16_t *dA[2], *dB[2];
-    int32_t T, K, N, R, n_slots, Tp;
+    int32_t T, K, N, R, R2, n_slots, Tp;
     const int32_t *perm, *offsets, *rank[2], *slot_blk;
     int32_t tiles_k, tiles_n;          // column tiles of x and of dy
 };
@@ -892,7 +903,7 @@ template <int MB, int QP> struct outer_cfg {              // QP: parts of q
     static constexpr int QI = QST / 8 / 256, PI = 2 * PST / 8 / 256;   // DMA instructions per wave per stage
 };
 
-// rank rows [0, nj) at vt + j Tp (and, 2 R Tp on, their second parts), rows p0..p1 of
+// rank rows [0, nj) at vt + j Tp (and, R2 Tp on, their second parts), rows p0..p1 of
 // perm at places b0.., columns [n0, n0 + 128) of q [T][N] (QP = 2: and of its
 // second part, q_lo on; the product of the second parts, 2^-16 of the whole, is
 // left out).
@@ -919,7 +930,7 @@ __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *sme
         for (int j = 0; j < PI; ++j) {                    // rank rows of 4 chunks: first parts, then second parts
             const int c = (wave * PI + j) * 64 + lane, part = c / (32 * MB * 4), r = c / 4 % (32 * MB);
             const int ch = (c & 3) ^ ((r >> 1) & 3);
-            dma16(r < nj ? (const void *)(vt + ((int64_t)part * 2 * g.R + r) * g.Tp + b0 + kt * BT + 8 * ch)
+            dma16(r < nj ? (const void *)(vt + ((int64_t)part * g.R2 + r) * g.Tp + b0 + kt * BT + 8 * ch)
                          : (const void *)g_zero16,
                   ps + (wave * PI + j) * 64 * 8);
         }
@@ -981,33 +992,34 @@ __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *sme
     }
 }
 
-template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
+template <int MBA, int MBB, int NM, int PARTS>
+__global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
     constexpr int LA = outer_cfg<MBA, 1>::NS * outer_cfg<MBA, 1>::STAGE;
-    constexpr int LB = outer_cfg<MBB, 2>::NS * outer_cfg<MBB, 2>::STAGE;
+    constexpr int LB = outer_cfg<MBB, PARTS>::NS * outer_cfg<MBB, PARTS>::STAGE;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[LA > LB ? LA : LB];
     __shared__ int32_t s_row[kOuterRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t wg = grid_index(), n_a = (int64_t)g.n_slots * g.tiles_k;
     const bool is_a = wg < n_a;
     int item = (int)(is_a ? wg : wg - n_a);
-    const int tiles = is_a ? g.tiles_k : 2 * g.tiles_n;
+    const int tiles = is_a ? g.tiles_k : NM * g.tiles_n;
     const int slot = item / tiles;
     if (slot >= g.n_slots) return;
     item -= slot * tiles;
-    const int m = !is_a && item >= g.tiles_n, tile = item - m * g.tiles_n;
+    const int m = NM > 1 && !is_a && item >= g.tiles_n, tile = item - m * g.tiles_n;
     const int n0 = tile * kOuterCols, N = is_a ? g.K : g.N;
     const int p0 = max(g.offsets[slot + 1], 0), p1 = min(g.offsets[slot + 2], g.T);
     const int64_t b0 = p1 > p0 ? (int64_t)g.slot_blk[slot] * kShrinkRows : 0;
     const int col = n0 + 32 * wave + (lane & 31), j4 = 4 * (lane >> 5);
     // ranks past the slot's get zeros whatever the rows hold
-    const int R = g.R, rk[2] = {min(g.rank[0][slot], R), min(g.rank[1][slot], R)};
+    const int R = g.R, rk[2] = {min(g.rank[0][slot], R), NM > 1 ? min(g.rank[1][slot], R) : 0};
     if (is_a) {
         f32x16_t acc[MBA];
 #pragma unroll
         for (int mb = 0; mb < MBA; ++mb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
-        seg_outer_sum<MBA, 1>(acc, smem, s_row, g, g.x, 0, N, n0, g.vt + (int64_t)2 * 2 * R * g.Tp, 2 * R, p0, p1, b0);
+        seg_outer_sum<MBA, 1>(acc, smem, s_row, g, g.x, 0, N, n0, g.vt + (int64_t)2 * g.R2 * g.Tp, NM * R, p0, p1, b0);
         if (col >= N) return;
         // [slot][k][j]: a lane's accumulators hold groups of 4 neighbouring ranks of its k
 #pragma unroll
@@ -1015,7 +1027,7 @@ template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_m
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int j = mb * 32 + 8 * q + j4;
-                if (j >= 2 * R) continue;
+                if (j >= NM * R) continue;
                 const int jj = j < R ? j : j - R, r = j < R ? rk[0] : rk[1];
                 uint16_t *out = (j < R ? g.dA[0] : g.dA[1]) + ((int64_t)slot * N + col) * R + jj;
                 float f[4];
@@ -1029,7 +1041,7 @@ template <int MBA, int MBB> __global__ void __launch_bounds__(256) k_seg_outer_m
         for (int mb = 0; mb < MBB; ++mb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
-        seg_outer_sum<MBB, 2>(acc, smem, s_row, g, g.dy + (int64_t)m * g.T * N, 2ll * g.T * N, N, n0,
+        seg_outer_sum<MBB, PARTS>(acc, smem, s_row, g, g.dy + (int64_t)m * g.T * N, (int64_t)NM * g.T * N, N, n0,
                               g.vt + (int64_t)m * R * g.Tp, R, p0, p1, b0);
         if (col >= N) return;
         uint16_t *out = (m ? g.dB[1] : g.dB[0]) + (int64_t)slot * R * N + col;
@@ -1048,21 +1060,117 @@ __global__ void __launch_bounds__(256) k_zero16(uint4 *p, int64_t n) {
 }
 
 // ---------------------------------------------------------------------------
-bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t R, int32_t d_in, int32_t d_out, int32_t dtype) {
+// dp of the linear layer, as k_gated_dact's dg, and the sums of its columns for
+// dbias.  A workgroup takes 32 vectors of columns and a stretch of rows, every
+// eighth of them a thread; the 8 strands are added through LDS to one partial sum
+// per column and stretch.  WRITE = false: dp is dy itself, only its sums are made.
+// ---------------------------------------------------------------------------
+constexpr int kActVecs = 32, kActStrands = 8;
+
+struct act_grad_args {
+    const void *pre, *dy;
+    void *dp;
+    float *part;                       // [stretches][N]
+    int32_t T, N, rows, act;
+    int64_t lo;                        // bf16: from dp's first parts to its second
+};
+
+template <int DT, bool WRITE, bool SUMS> __global__ void __launch_bounds__(256) k_act_grad(act_grad_args g) {
+    typedef typename elem<DT>::T E;
+    constexpr int VN = vec16<DT>::n;
+    const int vec = threadIdx.x % kActVecs, strand = threadIdx.x / kActVecs;
+    const int n = (blockIdx.x * kActVecs + vec) * VN;
+    const int64_t t0 = (int64_t)blockIdx.y * g.rows, t1 = t0 + g.rows < g.T ? t0 + g.rows : g.T;
+    float sum[VN] = {};
+    if (n < g.N) {
+#pragma unroll 2
+        for (int64_t t = t0 + strand; t < t1; t += kActStrands) {
+            const int64_t at = t * g.N + n;
+            float d[VN];
+            vec16<DT>::widen(ldg16((const E *)g.dy + at), d);
+            if constexpr (WRITE) {
+                float p[VN];
+                vec16<DT>::widen(ldg16((const E *)g.pre + at), p);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) {
+                    float a, da;
+                    act_both<DT == LORA_F32>(g.act, p[e], a, da);
+                    d[e] *= da;
+                }
+                const uint4 q = vec16<DT>::narrow(d);
+                stg16((E *)g.dp + at, q);
+                if constexpr (DT == LORA_BF16) {
+                    float h[VN];
+                    vec16<DT>::widen(q, h);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) h[e] = second_part(d[e] - h[e]);
+                    stg16((E *)g.dp + g.lo + at, vec16<DT>::narrow(h));
+                }
+            }
+            if constexpr (SUMS)
+#pragma unroll
+                for (int e = 0; e < VN; ++e) sum[e] += d[e];
+        }
+    }
+    if constexpr (SUMS) {
+        __shared__ float s[kActStrands][kActVecs * VN];
+#pragma unroll
+        for (int e = 0; e < VN; ++e) s[strand][vec * VN + e] = sum[e];
+        __syncthreads();
+        const int c = threadIdx.x, col = blockIdx.x * kActVecs * VN + c;
+        if (c < kActVecs * VN && col < g.N) {
+            float f = s[0][c];
+#pragma unroll
+            for (int i = 1; i < kActStrands; ++i) f += s[i][c];
+            g.part[(int64_t)blockIdx.y * g.N + col] = f;
+        }
+    }
+}
+
+// Rows of a stretch, and the number of stretches: about 1024 workgroups, of at
+// least 4 rows a strand (their partial sums are then few beside the rows).
+static int32_t act_grad_rows(int32_t T, int32_t N, int32_t dtype) {
+    const int tiles = ceil_div(N, kActVecs * (dtype == LORA_F32 ? 4 : 8));
+    int rows = ceil_div(T, ceil_div(1024, tiles));
+    if (rows < 4 * kActStrands) rows = 4 * kActStrands;
+    return ceil_div(rows, kActStrands) * kActStrands;
+}
+
+template <int DT> static lora_status_t launch_act_grad(act_grad_args &g, void *dbias, hipStream_t s) {
+    const bool write = g.act != LORA_ACT_NONE;
+    if (!write && !dbias) return LORA_OK;
+    g.rows = act_grad_rows(g.T, g.N, DT);
+    const int stretches = ceil_div(g.T, g.rows);
+    const dim3 grid(ceil_div(g.N, kActVecs * vec16<DT>::n), stretches);
+    if (write && dbias) hipLaunchKernelGGL((k_act_grad<DT, true, true>), grid, dim3(256), 0, s, g);
+    else if (write) hipLaunchKernelGGL((k_act_grad<DT, true, false>), grid, dim3(256), 0, s, g);
+    else hipLaunchKernelGGL((k_act_grad<DT, false, true>), grid, dim3(256), 0, s, g);
+    const lora_status_t st = hip_status(hipGetLastError());
+    return st == LORA_OK && dbias ? launch_column_sums(g.part, stretches, g.N, g.N, DT, dbias, nullptr, s) : st;
+}
+
+// ---------------------------------------------------------------------------
+// Rank columns of dv and vt.
+static int32_t bwd_ranks(int n_proj, int32_t R) { return n_proj > 1 ? n_proj * R : ceil_div(R, 16) * 16; }
+
+bwd_layout make_bwd_layout(int32_t T, int32_t n_slots, int32_t R, int32_t d_in, int32_t d_out, int32_t dtype,
+                           int32_t n_proj) {
     bwd_layout B;
-    B.L = make_ws_layout(T, n_slots, 2 * R, 0);
+    B.L = make_ws_layout(T, n_slots, n_proj * R, 0);
     const size_t t = (size_t)(T > 0 ? T : 1), eb = dtype == LORA_F32 ? 4 : 2;
-    const size_t segs = (size_t)n_slots < t ? (size_t)n_slots : t;
+    const size_t segs = (size_t)n_slots < t ? (size_t)n_slots : t, R2 = (size_t)bwd_ranks(n_proj, R);
     size_t o = B.L.total;
-    B.dy = o;      o = align256(o + (dtype == LORA_BF16 ? 4 : 2) * t * (size_t)d_out * eb);
-    B.dv = o;      o = align256(o + 4 * t * 2 * (size_t)R);
+    B.dy = o;      o = align256(o + (dtype == LORA_BF16 ? 2 : 1) * (size_t)n_proj * t * (size_t)d_out * eb);
+    B.dv = o;      o = align256(o + 4 * t * R2);
     // transposed bf16 parts of s v and dv, every segment from a work block on
-    B.vt = o;      o = align256(o + (dtype == LORA_BF16 ? 16 * (size_t)R * 32 * ((t + 31) / 32 + segs) : 0));
-    B.oct = o;     o = align256(o + (dtype == LORA_BF16 ? segs * 2 * (size_t)R * (size_t)d_in * 2 : 0));
+    B.vt = o;      o = align256(o + (dtype == LORA_BF16 ? 8 * R2 * 32 * ((t + 31) / 32 + segs) : 0));
+    B.oct = o;     o = align256(o + (dtype == LORA_BF16 ? segs * R2 * (size_t)d_in * 2 : 0));
     B.row0 = o;    o = align256(o + 4 * (size_t)n_slots);
     B.slot_blk = o; o = align256(o + 4 * (size_t)n_slots);
     B.rank = o;    o = align256(o + 4 * (size_t)n_slots);
     B.scale = o;   o = align256(o + 4 * (size_t)n_slots);
+    B.sums = o;
+    if (n_proj == 1 && T > 0) o = align256(o + 4 * (size_t)ceil_div(T, act_grad_rows(T, d_out, dtype)) * (size_t)d_out);
     B.partial = o;
     const size_t tp = (t + 255) / 256 * 256, np = ((size_t)d_in + 255) / 256 * 256;
     const size_t need = T > 0 ? 4 * (size_t)kMaxGemmSplit * tp * np : 0;
@@ -1078,10 +1186,13 @@ lora_status_t launch_zero(void *p, size_t bytes, hipStream_t s) {
     return hip_status(hipGetLastError());
 }
 
-template <int DT> static lora_status_t backward(const gated_bwd_call &c, const bwd_layout &B, hipStream_t s) {
+// NM projections; PARTS: bf16 parts of dy.  dg: dg and du (NM = 1: dp), where
+// k_gated_dact and k_act_grad leave them, or the layer's dy itself.
+template <int DT, int NM, int PARTS>
+static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_t s) {
     typedef typename elem<DT>::T E;
     const lora_pool_t *p = c.pools;
-    const int32_t T = c.T, K = p[0].d_in, F = p[0].d_out, R = p[0].max_rank, S = p[0].n_slots;
+    const int32_t T = c.T, K = p[0].d_in, F = p[0].d_out, R = p[0].max_rank, S = p[0].n_slots, R2 = bwd_ranks(NM, R);
     const ws_layout &L = B.L;
     void *ws = c.ws;
     // k_rank_finish has its workgroups in one grid dimension, which holds fewer than 2^32 threads
@@ -1091,21 +1202,29 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
     if (st != LORA_OK) return st;
     const int32_t *perm = ws_ptr<int32_t>(ws, L.perm), *offsets = ws_ptr<int32_t>(ws, L.offsets);
     float *v = ws_ptr<float>(ws, L.v), *dv = ws_ptr<float>(ws, B.dv);
-    E *dg = ws_ptr<E>(ws, B.dy), *du = dg + (int64_t)T * F;
-    const pair_pools pp = make_pair_pools(p);
-    const int64_t n_vec = (int64_t)T * F / vec16<DT>::n;
-    hipLaunchKernelGGL(k_gated_dact<DT>, dim3((uint32_t)(n_vec < (1 << 24) ? (n_vec + 255) / 256 : 1 << 16)),
-                       dim3(256), 0, s, (const E *)c.gate, (const E *)c.up, (const E *)c.dh, dg, du, 2ll * T * F, n_vec,
-                       c.act);
+    E *made = ws_ptr<E>(ws, B.dy);
+    const lora_pool_t two[2] = {p[0], p[NM - 1]};
+    const pair_pools pp = make_pair_pools(two);
+    if constexpr (NM > 1) {
+        const int64_t n_vec = (int64_t)T * F / vec16<DT>::n;
+        hipLaunchKernelGGL(k_gated_dact<DT>, dim3((uint32_t)(n_vec < (1 << 24) ? (n_vec + 255) / 256 : 1 << 16)),
+                           dim3(256), 0, s, (const E *)c.kept[0], (const E *)c.kept[1], (const E *)c.dh, made,
+                           made + (int64_t)T * F, 2ll * T * F, n_vec, c.act);
+    } else {
+        act_grad_args a{c.kept[0], c.dh, made, ws_ptr<float>(ws, B.sums), T, F, 0, c.act, (int64_t)T * F};
+        st = launch_act_grad<DT>(a, c.dbias, s);
+        if (st != LORA_OK) return st;
+    }
+    const E *dg = NM == 1 && c.act == LORA_ACT_NONE ? (const E *)c.dh : made, *du = dg + (NM - 1) * (int64_t)T * F;
     // v = x A (also records the bad ids); dv
-    st = DT == LORA_F32 ? launch_shrink_pair(c.x, T, p, c.ids, v, ws_ptr<int32_t>(ws, L.header), s)
-                        : launch_shrink(c.x, T, p, 2, c.ids, true, v, L, ws, s);
+    st = DT == LORA_F32 && NM > 1 ? launch_shrink_pair(c.x, T, p, c.ids, v, ws_ptr<int32_t>(ws, L.header), s)
+                        : launch_shrink(c.x, T, p, NM, c.ids, true, v, L, ws, s);
     if (st != LORA_OK) return st;
     const int32_t row_blocks = ceil_div(T, kShrinkRows), n_work = row_blocks + (S < T ? S : T), Tp = n_work * 32;
     uint16_t *vt = ws_ptr<uint16_t>(ws, B.vt);
     int32_t *slot_blk = ws_ptr<int32_t>(ws, B.slot_blk);
     if constexpr (DT == LORA_F32) {
-        hipLaunchKernelGGL(k_rank_grad_rows<DT>, grid_of(2ll * T), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R,
+        hipLaunchKernelGGL((k_rank_grad_rows<DT, NM>), grid_of((int64_t)NM * T), dim3(256), 0, s, dg, (int64_t)T * F, T, F, pp, S, R,
                            c.ids, dv);
     } else {
         // about 1024 workgroups with work, of at least 512 columns
@@ -1119,46 +1238,51 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         rank_grad_args g{(const uint16_t *)dg, T, F, R, S, n_chunk, perm, ws_ptr<int32_t>(ws, L.seg_id),
                          ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
                          ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg), part};
-        const dim3 grid(n_work, split, 2);
-        switch ((R + 15) / 16) {
-            case 1: hipLaunchKernelGGL(k_rank_grad<1>, grid, dim3(256), 0, s, g, pp); break;
-            case 2: hipLaunchKernelGGL(k_rank_grad<2>, grid, dim3(256), 0, s, g, pp); break;
-            case 3: hipLaunchKernelGGL(k_rank_grad<3>, grid, dim3(256), 0, s, g, pp); break;
-            default: hipLaunchKernelGGL(k_rank_grad<4>, grid, dim3(256), 0, s, g, pp); break;
+        const dim3 grid(n_work, split, NM);
+#define LORA_RANK_GRAD(RCH) hipLaunchKernelGGL((k_rank_grad<RCH, NM, PARTS>), grid, dim3(256), 0, s, g, pp)
+        const int rch = (R + 15) / 16;
+        if (rch == 1) LORA_RANK_GRAD(1);
+        else if (rch == 2) LORA_RANK_GRAD(2);
+        else if (rch == 3) LORA_RANK_GRAD(3);
+        else if (rch == 4) LORA_RANK_GRAD(4);
+        else if constexpr (NM == 1) {                     // (the pair's ranks end at 64)
+            if (rch <= 6) LORA_RANK_GRAD(6);
+            else LORA_RANK_GRAD(8);
         }
+#undef LORA_RANK_GRAD
         const int first_octet = n_work + row_blocks;
-        const rank_finish_args f{v, part, split, T, R, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
+        const rank_finish_args f{v, part, split, T, R, R2, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
                                  g.blk_start, g.blk_seg, dv, vt, slot_blk, first_octet};
-        const a_octets_args oc{g.seg_id, g.n_seg, S, K, R, ceil_div(K, 256), ws_ptr<uint16_t>(ws, B.oct),
+        const a_octets_args oc{g.seg_id, g.n_seg, S, K, R, R2, ceil_div(K, 256), ws_ptr<uint16_t>(ws, B.oct),
                                ws_ptr<int32_t>(ws, B.row0), ws_ptr<int32_t>(ws, B.rank), ws_ptr<float>(ws, B.scale)};
         const int octets = c.dx ? (S < T ? S : T) * oc.k_blocks : 0;
-        hipLaunchKernelGGL(k_rank_finish, dim3(first_octet + octets, 2 * R / 8), dim3(256), 0, s, f, oc, pp);
+        hipLaunchKernelGGL(k_rank_finish<NM>, dim3(first_octet + octets, R2 / 8), dim3(256), 0, s, f, oc, pp);
     }
     if constexpr (DT == LORA_F32) {
-        dx_f32_args g{(const float *)dg, (const float *)du, (const float *)c.W[0], (const float *)c.W[1],
+        dx_f32_args g{(const float *)dg, (const float *)du, (const float *)c.W[0], (const float *)c.W[NM - 1],
                       (float *)c.dx, dv, c.ids, perm, ws_ptr<float>(ws, B.partial), T, F, K, S, R, ceil_div(K, 64), 1, 0};
         const outer_f32_args o{(const float *)c.x, (const float *)dg, (const float *)du, v, dv,
                                (float *)c.dA[0], (float *)c.dA[1], (float *)c.dB[0], (float *)c.dB[1],
                                offsets, perm, T, K, F, R, c.dA[0] ? S : 0, ceil_div(K, 256), ceil_div(F, 256)};
         const int tiles = c.dx ? ceil_div(T, 64) * g.n_tiles_n : 0;
-        if (c.dx) g.splits = f32_splits(tiles, 2 * ceil_div(F, 32) * 32, 64 * 64, c.ws_bytes - B.partial, g.k_chunk);
+        if (c.dx) g.splits = f32_splits(tiles, NM * ceil_div(F, 32) * 32, 64 * 64, c.ws_bytes - B.partial, g.k_chunk);
         const int n_dx = tiles * g.splits;
-        const dim3 grid = grid_of(n_dx + 2ll * o.n_slots * (o.tiles_k + o.tiles_f));
+        const dim3 grid = grid_of(n_dx + (int64_t)NM * o.n_slots * (o.tiles_k + o.tiles_f));
         if (c.dx || c.dA[0]) {
-            if (g.splits == 1) hipLaunchKernelGGL(k_dx_outer_f32<false>, grid, dim3(256), 0, s, g, o, pp, n_dx);
-            else hipLaunchKernelGGL(k_dx_outer_f32<true>, grid, dim3(256), 0, s, g, o, pp, n_dx);
+            if (g.splits == 1) hipLaunchKernelGGL((k_dx_outer_f32<false, NM>), grid, dim3(256), 0, s, g, o, pp, n_dx);
+            else hipLaunchKernelGGL((k_dx_outer_f32<true, NM>), grid, dim3(256), 0, s, g, o, pp, n_dx);
         }
-        if (g.splits > 1) hipLaunchKernelGGL(k_dx_reduce_f32, dim3(tiles * 4), dim3(256), 0, s, g, pp);
+        if (g.splits > 1) hipLaunchKernelGGL(k_dx_reduce_f32<NM>, dim3(tiles * 4), dim3(256), 0, s, g, pp);
     } else if (c.dx) {
         uint16_t *oct = ws_ptr<uint16_t>(ws, B.oct);
         int32_t *row0 = ws_ptr<int32_t>(ws, B.row0), *rank = ws_ptr<int32_t>(ws, B.rank);
         float *scale = ws_ptr<float>(ws, B.scale);
-        nt_args nt{{(const uint16_t *)dg, (const uint16_t *)du}, {(const uint16_t *)c.W[0], (const uint16_t *)c.W[1]},
+        nt_args nt{{(const uint16_t *)dg, (const uint16_t *)du}, {(const uint16_t *)c.W[0], (const uint16_t *)c.W[NM - 1]},
                    F, ceil_div(F, 64) * 64, ws_ptr<int32_t>(ws, L.n_seg)};
         gemm_args g{};
         g.y = (uint16_t *)c.dx;
         g.T = T;
-        g.K = 2 * nt.Fp;
+        g.K = NM * nt.Fp;
         g.N = K;
         g.perm = perm;
         g.b = oct;
@@ -1166,10 +1290,10 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         g.rank = rank;
         g.row0 = row0;
         g.n_slots = S;
-        g.max_rank = 2 * R;
+        g.max_rank = R2;
         g.ids = c.ids;
         g.v = dv;
-        g.v_stride = 2 * R;
+        g.v_stride = R2;
         g.partial = ws_ptr<float>(ws, B.partial);
         const gemm_plan pl = plan_dx(T, g.K, g.N, c.ws_bytes - B.partial);
         g.n_tiles_m = ceil_div(T, pl.bm);
@@ -1180,23 +1304,41 @@ template <int DT> static lora_status_t backward(const gated_bwd_call &c, const b
         else if (pl.bn == 128) launch_nt_cfg<128, 128, 2, 4, 2, 4, 8>(g, nt, pl, s);
         else launch_nt_cfg<128, 64, 2, 4, 2, 2, 4>(g, nt, pl, s);
     }
-    if (c.dA[0] && DT == LORA_BF16) {
+    if constexpr (DT == LORA_BF16) {
+        if (!c.dA[0]) return hip_status(hipGetLastError());
         seg_outer_args g{(const uint16_t *)c.x, (const uint16_t *)dg, vt,
                          {(uint16_t *)c.dA[0], (uint16_t *)c.dA[1]}, {(uint16_t *)c.dB[0], (uint16_t *)c.dB[1]},
-                         T, K, F, R, S, Tp, perm, offsets, {p[0].rank, p[1].rank}, slot_blk, ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
-        const dim3 grid = grid_of((int64_t)S * (g.tiles_k + 2 * g.tiles_n));
-        switch ((R + 15) / 16) {
-            case 1: hipLaunchKernelGGL((k_seg_outer_mfma<1, 1>), grid, dim3(256), 0, s, g); break;
-            case 2: hipLaunchKernelGGL((k_seg_outer_mfma<2, 1>), grid, dim3(256), 0, s, g); break;
-            case 3: hipLaunchKernelGGL((k_seg_outer_mfma<3, 2>), grid, dim3(256), 0, s, g); break;
-            default: hipLaunchKernelGGL((k_seg_outer_mfma<4, 2>), grid, dim3(256), 0, s, g); break;
+                         T, K, F, R, R2, S, Tp, perm, offsets, {p[0].rank, p[NM - 1].rank}, slot_blk,
+                         ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
+        const dim3 grid = grid_of((int64_t)S * (g.tiles_k + NM * g.tiles_n));
+#define LORA_OUTER(MBA, MBB) hipLaunchKernelGGL((k_seg_outer_mfma<MBA, MBB, NM, PARTS>), grid, dim3(256), 0, s, g)
+        if constexpr (NM > 1) {
+            switch ((R + 15) / 16) {
+                case 1: LORA_OUTER(1, 1); break;
+                case 2: LORA_OUTER(2, 1); break;
+                case 3: LORA_OUTER(3, 2); break;
+                default: LORA_OUTER(4, 2); break;
+            }
+        } else {
+            switch ((R + 31) / 32) {
+                case 1: LORA_OUTER(1, 1); break;
+                case 2: LORA_OUTER(2, 2); break;
+                case 3: LORA_OUTER(3, 3); break;
+                default: LORA_OUTER(4, 4); break;
+            }
         }
+#undef LORA_OUTER
     }
     return hip_status(hipGetLastError());
 }
 
-lora_status_t launch_gated_backward(const gated_bwd_call &c, const bwd_layout &B, hipStream_t s) {
-    return c.pools[0].dtype == LORA_F32 ? backward<LORA_F32>(c, B, s) : backward<LORA_BF16>(c, B, s);
+lora_status_t launch_gated_backward(const bwd_call &c, const bwd_layout &B, hipStream_t s) {
+    return c.pools[0].dtype == LORA_F32 ? backward<LORA_F32, 2, 1>(c, B, s) : backward<LORA_BF16, 2, 2>(c, B, s);
+}
+
+lora_status_t launch_linear_backward(const bwd_call &c, const bwd_layout &B, hipStream_t s) {
+    if (c.pools[0].dtype == LORA_F32) return backward<LORA_F32, 1, 1>(c, B, s);
+    return c.act == LORA_ACT_NONE ? backward<LORA_BF16, 1, 1>(c, B, s) : backward<LORA_BF16, 1, 2>(c, B, s);
 }
 
 }  // namespace lora

@@ -58,6 +58,7 @@ EXPORTED = (
     "lora_add_layernorm", "lora_add_layernorm_fp8", "lora_workspace_bytes_layernorm_backward",
     "lora_add_layernorm_backward",
     "lora_linear_act_forward", "lora_linear_act_forward_fp8",
+    "lora_workspace_bytes_linear_act_backward", "lora_linear_act_backward",
     "lora_workspace_bytes_orthogonalize", "lora_orthogonalize",
     "lora_workspace_bytes_gated", "lora_workspace_bytes_gated_fp8", "lora_gated_forward", "lora_gated_forward_fp8",
     "lora_workspace_bytes_gated_backward", "lora_gated_backward",
@@ -167,6 +168,9 @@ def load(path: str = LIB_PATH):
                                             c_u32, c_vp, c_sz, c_vp]),
         "lora_linear_act_forward_fp8": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32,
                                                 P(lora_pool_t), c_vp, c_i32, c_i32, c_u32, c_vp, c_sz, c_vp]),
+        "lora_workspace_bytes_linear_act_backward": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+        "lora_linear_act_backward": (c_i32, [c_vp, c_vp, c_i32, P(lora_pool_t), c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp, c_sz, c_vp]),
         "lora_workspace_bytes_orthogonalize": (c_sz, [c_i32, c_i32, c_i32]),
         "lora_orthogonalize": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, P(c_f), c_i32, c_f, c_f, c_vp, c_vp, c_sz,
                                        c_vp]),
@@ -576,6 +580,23 @@ def lora_linear_act_forward_fp8(x, xq, x_scale, wq, w_scale, bias, residual, y, 
         "lora_linear_act_forward_fp8")
 
 
+def lora_workspace_bytes_linear_act_backward(T, n_slots, max_rank, d_in, d_out, dtype) -> int:
+    return int(load().lora_workspace_bytes_linear_act_backward(T, n_slots, max_rank, d_in, d_out, dtype))
+
+
+def lora_linear_act_backward(x, W, T, pool, ids, act, pre, dy, dx, dA, dB, dbias, ws, stream=None):
+    """Gradients of lora_linear_act_forward: dx, dA [n_slots, d_in, max_rank] with dB [n_slots, max_rank, d_out], and
+    dbias (each may be None); pre: act's argument as the forward pass kept it (None with LORA_ACT_NONE)."""
+    dt, n, nr = _TORCH_TYPES.get(pool.dtype), T * pool.d_out, pool.n_slots * pool.max_rank
+    nbytes = _ws_bytes(ws)
+    x, W, ids, pre, dy, dx, dA, dB, dbias, ws = _checked(
+        "lora_linear_act_backward", (x, dt, T * pool.d_in), (W, dt, pool.d_in * pool.d_out), (ids, torch.int32, T),
+        (pre, dt, n), (dy, dt, n), (dx, dt, T * pool.d_in), (dA, dt, nr * pool.d_in), (dB, dt, nr * pool.d_out),
+        (dbias, dt, pool.d_out), (ws, torch.uint8, 0))
+    _ok(load().lora_linear_act_backward(x, W, T, ctypes.byref(pool), ids, act, pre, dy, dx, dA, dB, dbias, ws, nbytes,
+                                        _stream(stream)), "lora_linear_act_backward")
+
+
 def lora_workspace_bytes_orthogonalize(n, rows, cols) -> int:
     return int(load().lora_workspace_bytes_orthogonalize(n, rows, cols))
 
@@ -722,13 +743,19 @@ class AdapterPool:
 class Workspace:
     """A device workspace sized for (T, n_slots, max_rank, d_out), initialised.
     With `gated` it serves the gated pair of width d_out, or with backward_d_in
-    (x's width) and dtype the pair's backward pass."""
+    (x's width) and dtype the pair's backward pass; with linear_backward_d_in and
+    dtype the linear layer's."""
 
     def __init__(self, T, n_slots, max_rank, d_out=0, device="cuda", stream=None, n_slices=1, fp8_d_in=0,
-                 gated=False, backward_d_in=0, dtype=torch.bfloat16):
+                 gated=False, backward_d_in=0, dtype=torch.bfloat16, linear_backward_d_in=0):
         if backward_d_in and not gated:
             raise LoraError(LORA_ERR_INVALID_ARGUMENT, "lora_workspace_bytes_gated_backward")
-        if backward_d_in:
+        if linear_backward_d_in:
+            if gated or fp8_d_in or n_slices != 1:
+                raise LoraError(LORA_ERR_INVALID_ARGUMENT, "lora_workspace_bytes_linear_act_backward")
+            n = lora_workspace_bytes_linear_act_backward(T, n_slots, max_rank, linear_backward_d_in, d_out,
+                                                         dtype_code(dtype))
+        elif backward_d_in:
             n_slices = 2
             n = lora_workspace_bytes_gated_backward(T, n_slots, max_rank, backward_d_in, d_out, dtype_code(dtype))
         elif gated:

@@ -123,3 +123,55 @@ def run_forward(p, act, mode=L.LORA_MODE_AUTO, keep=False, bias=True, residual=T
         L.lora_linear_act_forward(p.x, p.W, b, r, y, p.T, p.desc, p.ids_dev, ACTS[act], mode, flags, ws.buf, pre=pre,
                                   stream=stream)
     return y, pre, ws
+
+
+def backward64(p, act, pre, dy):
+    """The gradients in 64 bits for pre as given, and their bounds (as helpers_block.backward64): dp is a few fp32
+    steps and, in bf16, one rounding off in dx, 2^-17 elsewhere (none without an activation); every sum adds one
+    step per term; vectors of rank width reach the matrix cores as two bf16 parts (2^-17 left out)."""
+    half, step, bf16 = HALF[p.dtype], STEP32, p.dtype == torch.bfloat16
+    split = 2.0 ** -17 if bf16 else 0.0
+    x, dp = p.x.double(), dy.double()
+    ddp = rounded = torch.zeros_like(dp)
+    if act != "none":
+        g = pre.double()
+        _, slope = act64(act, g)
+        size = dp.abs()
+        dp = dp * slope
+        ddp = 32 * step * (1 + g.abs()) * size + split * dp.abs()
+        rounded = ddp + half * dp.abs()
+    W = p.W.double()
+    dx = dp @ W.t()
+    tx = rounded @ W.t().abs() + (p.f + p.R + 8) * step * (dp.abs() @ W.t().abs())
+    dA = torch.zeros(p.S, p.d, p.R, dtype=torch.float64, device="cuda")
+    dB = torch.zeros(p.S, p.R, p.f, dtype=torch.float64, device="cuda")
+    tA, tB = torch.zeros_like(dA), torch.zeros_like(dB)
+    for s, r, t, A, B, sc in p.adapters():
+        dv = sc * (dp[t] @ B.t())
+        tv = sc * (ddp[t] @ B.t().abs() + (p.f + 8) * step * (dp[t].abs() @ B.t().abs())) + split * dv.abs()
+        dx[t] += dv @ A.t()
+        tx[t] += tv @ A.t().abs() + (p.R + 8) * step * (dv.abs() @ A.t().abs())
+        n = len(t) + 8
+        dA[s, :, :r] = x[t].t() @ dv
+        tA[s, :, :r] = x[t].t().abs() @ tv + n * step * (x[t].t().abs() @ dv.abs())
+        v = x[t] @ A
+        dev_v = (p.d + 8) * step * (x[t].abs() @ A.abs()) + split * v.abs()
+        dB[s, :r] = sc * (v.t() @ dp[t])
+        tB[s, :r] = sc * (dev_v.t() @ dp[t].abs() + v.t().abs() @ ddp[t] + n * step * (v.t().abs() @ dp[t].abs()))
+    db, n = dp.sum(0), p.T / 256 + 256
+    tb = (ddp if bf16 else rounded).sum(0) + n * step * dp.abs().sum(0)
+    end = lambda v, t: (v, t * (1 + half) + half * v.abs() + TINY)  # noqa: E731
+    return end(dx, tx), end(dA, tA), end(dB, tB), end(db, tb)
+
+
+def run_backward(p, act, pre, dy, ws=None, stream=None, want=("dx", "ab", "bias"), fill=7.0):
+    """lora_linear_act_backward: dx, dA, dB, dbias and the workspace."""
+    new = lambda *shape: torch.full(shape, fill, dtype=p.dtype, device="cuda")  # noqa: E731
+    dx = new(p.T, p.d) if "dx" in want else None
+    dA, dB = (new(p.S, p.d, p.R), new(p.S, p.R, p.f)) if "ab" in want else (None, None)
+    db = new(p.f) if "bias" in want else None
+    if ws is None:
+        ws = L.Workspace(p.T, p.S, p.R, p.f, linear_backward_d_in=p.d, dtype=p.dtype, stream=stream)
+    L.lora_linear_act_backward(p.x, p.W, p.T, p.desc, p.ids_dev, ACTS[act], pre if act != "none" else None, dy, dx, dA,
+                               dB, db, ws.buf, stream=stream)
+    return dx, dA, dB, db, ws

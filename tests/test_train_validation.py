@@ -160,3 +160,28 @@ def test_linear_act_refuses_rows_of_more_tiles_than_a_grid_holds(lib):
     p = pool(d_in=8, d_out=264, n_slots=1)
     assert lib.lora_linear_act_forward(far[0], far[1], None, None, far[2], None, T, p, far[3], 3, 0, 0, far[4], 1 << 42,
                                        None) == UNSUPPORTED
+
+
+def test_linear_act_backward(lib):
+    need = L.lora_workspace_bytes_linear_act_backward(8, 4, 16, 64, 96, L.LORA_BF16)
+    assert need >= 2 * 8 * 96 * 2 + 8 * 16 * 4
+    for bad in ((-1, 4, 16, 64, 96, 1), (8, 0, 16, 64, 96, 1), (8, 4, 12, 64, 96, 1), (8, 4, 136, 64, 96, 1),
+                (8, 4, 16, 60, 96, 1), (8, 4, 16, 64, 0, 1), (8, 4, 16, 64, 96, 2)):
+        assert L.lora_workspace_bytes_linear_act_backward(*bad) == 0, bad
+    p0 = pool()
+
+    def call(x=A[0], w=A[1], T=8, p=p0, ids=A[2], act=0, pre=A[3], dy=A[4], dx=A[5], dA=A[6], dB=A[7], db=A[8], ws=A[9],
+             n=need):
+        return lib.lora_linear_act_backward(x, w, T, p, ids, act, pre, dy, dx, dA, dB, db, ws, n, None)
+
+    for bad in (dict(x=None), dict(w=None), dict(T=-1), dict(ids=None), dict(act=4), dict(act=-1), dict(pre=None),
+                dict(dy=None), dict(dA=None), dict(dB=None), dict(dx=A[5] + 8), dict(dy=A[4] + 2), dict(pre=A[3] + 8),
+                dict(dA=A[6] + 8), dict(dB=A[7] + 8), dict(db=A[8] + 8), dict(ws=None), dict(ws=A[9] + 4), dict(p=None),
+                dict(p=pool(d_in=60)), dict(p=pool(dtype=2)),
+                # outputs that meet another buffer
+                dict(dx=A[0]), dict(dx=A[4]), dict(dx=A[6]), dict(dA=A[7]), dict(db=A[6]), dict(db=A[3]), dict(dB=A[1]),
+                dict(ws=A[4]), dict(ws=A[8]), dict(dA=p0.a), dict(db=p0.scale), dict(dx=A[4] + 16)):
+        assert call(**bad) == INVALID, bad
+    assert call(n=1024) == SMALL
+    assert call(T=0, x=None, w=None, ids=None, pre=None, dy=None, dx=None, dA=None, dB=None, db=None) == OK
+    assert call(T=0, dA=A[6], dB=A[6], db=None) == INVALID
