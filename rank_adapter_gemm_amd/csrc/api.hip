@@ -904,7 +904,8 @@ lora_status_t lora_linear_act_forward(const void *x, const void *W, const void *
         return launch_gemm_fused_shrink(x, W, y, T, pool, ids, ws_ptr<float>(ws, L.partial),
                                         ws_ptr<int32_t>(ws, L.header), partial, partial_bytes, s, &epi);
     float *v = ws_ptr<float>(ws, L.v);
-    st = launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s);
+    st = sgmv ? launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s)
+              : launch_shrink_one(x, T, *pool, ids, v, ws_ptr<int32_t>(ws, L.header), s);
     if (st != LORA_OK) return st;
     return launch_gemm(x, W, y, T, pool->d_in, pool->d_out, pool->dtype, pool, ids, v, pool->max_rank,
                        sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr, partial, partial_bytes, s, nullptr, &epi);
@@ -938,20 +939,17 @@ lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, cons
         st = launch_segments(ids, T, pool->n_slots, L, ws, s, 1);
         if (st != LORA_OK) return st;
     }
-    float *v = ws_ptr<float>(ws, L.v);
     if (!xq) {
         uint8_t *q = ws_ptr<uint8_t>(ws, L.xq);
         float *qs = ws_ptr<float>(ws, L.xs);
-        // decode rows: quantized by the workgroup that shrinks them
-        st = sgmv ? launch_quant_rows_fp8(x, T, pool->d_in, q, qs, s)
-                  : launch_quant_shrink_rows(x, T, pool, ids, v, q, qs, ws_ptr<int32_t>(ws, L.header), s);
+        st = launch_quant_rows_fp8(x, T, pool->d_in, q, qs, s);
         if (st != LORA_OK) return st;
-        if (sgmv) st = launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s);
         xq = q;
         x_scale = qs;
-    } else {
-        st = launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s);
     }
+    float *v = ws_ptr<float>(ws, L.v);
+    st = sgmv ? launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s)
+              : launch_shrink_one(x, T, *pool, ids, v, ws_ptr<int32_t>(ws, L.header), s);
     if (st != LORA_OK) return st;
     const epilogue epi{bias, residual, pre, (int32_t)act};
     return launch_gemm_fp8(xq, x_scale, wq, w_scale, y, T, pool->d_in, pool->d_out, pool, ids, v, pool->max_rank,

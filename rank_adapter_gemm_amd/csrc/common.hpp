@@ -335,6 +335,9 @@ lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s);
 // The pair's rank vectors for rows in their own order: v[t][m max_rank + j].
 lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *pools, const int32_t *ids, float *v,
                                  int32_t *err, hipStream_t s);
+// The same of one pool: v[t][j].
+lora_status_t launch_shrink_one(const void *x, int32_t T, const lora_pool_t &p, const int32_t *ids, float *v,
+                                int32_t *err, hipStream_t s);
 
 // Its backward pass, and the linear layer's (one projection): the workspace of a
 // forward (segments, v and the shrink's partials for the projections' max_rank

@@ -1217,7 +1217,8 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
     }
     const E *dg = NM == 1 && c.act == LORA_ACT_NONE ? (const E *)c.dh : made, *du = dg + (NM - 1) * (int64_t)T * F;
     // v = x A (also records the bad ids); dv
-    st = DT == LORA_F32 && NM > 1 ? launch_shrink_pair(c.x, T, p, c.ids, v, ws_ptr<int32_t>(ws, L.header), s)
+    st = DT == LORA_F32 ? (NM > 1 ? launch_shrink_pair(c.x, T, p, c.ids, v, ws_ptr<int32_t>(ws, L.header), s)
+                                  : launch_shrink_one(c.x, T, p[0], c.ids, v, ws_ptr<int32_t>(ws, L.header), s))
                         : launch_shrink(c.x, T, p, NM, c.ids, true, v, L, ws, s);
     if (st != LORA_OK) return st;
     const int32_t row_blocks = ceil_div(T, kShrinkRows), n_work = row_blocks + (S < T ? S : T), Tp = n_work * 32;
