@@ -73,6 +73,69 @@ __device__ __forceinline__ void row_term8(const gemm_args &g, const row_term &rt
     }
 }
 
+constexpr int kRowRanks = 4;
+
+// Four ranks j0.. of one row's v = x A, by a workgroup of WV wavefronts that share the
+// row's length (one wavefront to a row of 14336 values: 28 us, all of it latency).
+// `item`: of T R / kRowRanks.  Records the row's id where it names no usable slot.
+template <int DT, int WV>
+__device__ __forceinline__ void shrink_row(const typename elem<DT>::T *x, int32_t T, int32_t d, const void *pool_a,
+                                           const int32_t *rank, const int32_t *row0, int32_t n_slots, int32_t R,
+                                           const int32_t *ids, float *v, int32_t *err, int64_t item) {
+    typedef typename elem<DT>::T E;
+    constexpr int VN = vec16<DT>::n, U = 4;
+    __shared__ float s_v[WV][kRowRanks];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, groups = R / kRowRanks;
+    const int64_t t = item / groups;
+    if (t >= T) return;                                   // (the whole workgroup)
+    const int j0 = (int)(item - t * groups) * kRowRanks;
+    const int32_t id = ids[t];
+    const bool in = id >= 0 && id < n_slots;
+    const int32_t r = in ? min(rank[id], R) : 0;
+    float acc[kRowRanks] = {};
+    if (in && (!row0 || j0 < r)) {                        // as in k_shrink_pair
+        const E *row = x + t * d, *a = (const E *)pool_a + (slot_row0(row0, id, R) + j0) * d;
+        const int n = d / VN;
+        for (int c0 = tid; c0 < n; c0 += 64 * WV * U) {
+            uint4 xq[U], aq[U][kRowRanks];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = (int64_t)min(c0 + 64 * WV * u, n - 1) * VN;
+                xq[u] = ldg16(row + c);
+#pragma unroll
+                for (int q = 0; q < kRowRanks; ++q) aq[u][q] = ldg16(a + q * (int64_t)d + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + 64 * WV * u >= n) break;
+                float xf[VN], af[VN];
+                vec16<DT>::widen(xq[u], xf);
+#pragma unroll
+                for (int q = 0; q < kRowRanks; ++q) {
+                    vec16<DT>::widen(aq[u][q], af);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) acc[q] = fmaf(xf[e], af[e], acc[q]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kRowRanks; ++q)
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) acc[q] += __shfl_xor(acc[q], o, 64);
+    if (lane == 0)
+#pragma unroll
+        for (int q = 0; q < kRowRanks; ++q) s_v[w][q] = acc[q];
+    __syncthreads();
+    if (tid < kRowRanks) {
+        float f = s_v[0][tid];
+#pragma unroll
+        for (int u = 1; u < WV; ++u) f += s_v[u][tid];
+        v[t * R + j0 + tid] = j0 + tid < r ? f : 0.0f;
+    }
+    if (tid == 0 && j0 == 0 && (id < -1 || id >= n_slots || (in && r <= 0))) flag_bad_row(err, (int32_t)t);
+}
+
 // The store of a whole tile: the fp32 sums of WR * 32 rows at a time go through
 // LDS, where the terms that are not in them yet are added; a thread then owns 8
 // neighbouring columns of one row (16-byte loads and stores, one rounding).

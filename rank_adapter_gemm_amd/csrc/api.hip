@@ -899,11 +899,16 @@ lora_status_t lora_linear_act_forward(const void *x, const void *W, const void *
     const epilogue epi{bias, residual, pre, (int32_t)act};
     float *partial = ws_ptr<float>(ws, L.gemm_partial);
     const size_t partial_bytes = ws_bytes - L.gemm_partial;
+    float *v = ws_ptr<float>(ws, L.v);
+    int splits, k_chunk;
+    if (!sgmv && pool->dtype == LORA_BF16 &&
+        linear_few_plan(T, pool->d_in, pool->d_out, false, partial_bytes, splits, k_chunk))
+        return launch_linear_few(x, W, nullptr, nullptr, nullptr, nullptr, y, T, *pool, ids, v,
+                                 ws_ptr<int32_t>(ws, L.header), partial, partial_bytes, epi, s);
     if (!sgmv && pool->dtype == LORA_BF16 &&
         gemm_fused_shrink_ok(T, pool->d_in, pool->d_out, pool->max_rank, partial_bytes))
         return launch_gemm_fused_shrink(x, W, y, T, pool, ids, ws_ptr<float>(ws, L.partial),
                                         ws_ptr<int32_t>(ws, L.header), partial, partial_bytes, s, &epi);
-    float *v = ws_ptr<float>(ws, L.v);
     st = sgmv ? launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s)
               : launch_shrink_one(x, T, *pool, ids, v, ws_ptr<int32_t>(ws, L.header), s);
     if (st != LORA_OK) return st;
@@ -947,14 +952,18 @@ lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, cons
         xq = q;
         x_scale = qs;
     }
-    float *v = ws_ptr<float>(ws, L.v);
+    float *v = ws_ptr<float>(ws, L.v), *partial = ws_ptr<float>(ws, L.gemm_partial);
+    const size_t partial_bytes = ws_bytes - L.gemm_partial;
+    const epilogue epi{bias, residual, pre, (int32_t)act};
+    int splits, k_chunk;
+    if (!sgmv && linear_few_plan(T, pool->d_in, pool->d_out, true, partial_bytes, splits, k_chunk))
+        return launch_linear_few(x, nullptr, xq, x_scale, wq, w_scale, y, T, *pool, ids, v, ws_ptr<int32_t>(ws, L.header),
+                                 partial, partial_bytes, epi, s);
     st = sgmv ? launch_shrink(x, T, pool, 1, ids, sgmv, v, L, ws, s)
               : launch_shrink_one(x, T, *pool, ids, v, ws_ptr<int32_t>(ws, L.header), s);
     if (st != LORA_OK) return st;
-    const epilogue epi{bias, residual, pre, (int32_t)act};
     return launch_gemm_fp8(xq, x_scale, wq, w_scale, y, T, pool->d_in, pool->d_out, pool, ids, v, pool->max_rank,
-                           sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr, ws_ptr<float>(ws, L.gemm_partial),
-                           ws_bytes - L.gemm_partial, s, nullptr, &epi);
+                           sgmv ? ws_ptr<int32_t>(ws, L.perm) : nullptr, partial, partial_bytes, s, nullptr, &epi);
 }
 
 size_t lora_workspace_bytes_linear_act_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in,

@@ -302,6 +302,14 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
 lora_status_t launch_linear_f32(const void *x, const void *W, void *y, int32_t T, const lora_pool_t &p,
                                 const int32_t *ids, const float *v, int32_t v_stride, const int32_t *perm,
                                 float *partial, size_t partial_bytes, const epilogue &epi, hipStream_t s);
+// The layer of up to kFewRows rows (bf16 from x and W, or FP8 from the codes and
+// scales), rank vectors (from x into v) included, where the partial buffer holds what
+// linear_few_plan asks for.
+constexpr int32_t kFewRows = 64;
+bool linear_few_plan(int32_t T, int32_t K, int32_t N, bool fp8, size_t partial_bytes, int &splits, int &k_chunk);
+lora_status_t launch_linear_few(const void *x, const void *W, const uint8_t *xq, const float *xs, const uint8_t *wq,
+                                const float *wsc, void *y, int32_t T, const lora_pool_t &p, const int32_t *ids, float *v,
+                                int32_t *err, float *partial, size_t partial_bytes, const epilogue &epi, hipStream_t s);
 // FP8 base (E4M3 codes, fp32 scales): per-row and per-column quantizers and
 // y = s_x s_w (xq wq^T) (+ s v B when pool != nullptr), bf16 y.
 lora_status_t launch_quant_rows_fp8(const void *x, int32_t T, int32_t K, uint8_t *xq, float *xs, hipStream_t s);

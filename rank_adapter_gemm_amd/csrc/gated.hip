@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
 }
 
 // ---------------------------------------------------------------------------
-// v = x A of both slices (NM = 1: of one pool) for rows in their own order.  A wavefront sums four
+// v = x A of both slices for rows in their own order.  A wavefront sums four
 // ranks of one row and slice: the row's few workgroups spread over the chip
 // (a single token's 2 x 16 ranks over 8 wavefronts, not one workgroup), and
 // each lane has all its loads of a stretch of 8 vectors in flight.  x is read
@@ -227,22 +227,22 @@ __global__ void __launch_bounds__(256) k_gated_reduce_f32(gated_f32_args g) {
 // ---------------------------------------------------------------------------
 constexpr int kPairRanks = 4;
 
-template <int DT, int NM>
+template <int DT>
 __global__ void __launch_bounds__(256) k_shrink_pair(const typename elem<DT>::T *x, int32_t T, int32_t d, pair_pools pp,
                                                      int32_t n_slots, int32_t R, const int32_t *ids, float *v,
                                                      int32_t *err) {
     typedef typename elem<DT>::T E;
     constexpr int VN = vec16<DT>::n, U = 8;
     const int lane = threadIdx.x & 63;
-    const int groups = NM * R / kPairRanks;               // per row; R is a multiple of 8
+    const int groups = 2 * R / kPairRanks;                // per row; R is a multiple of 8
     const int64_t item = grid_index() * 4 + (threadIdx.x >> 6);
     const int64_t t = item / groups;
     if (t >= T) return;
-    const int j2 = (int)(item - t * groups) * kPairRanks, m = NM > 1 && j2 >= R, j0 = j2 - m * R;
+    const int j2 = (int)(item - t * groups) * kPairRanks, m = j2 >= R, j0 = j2 - m * R;
     const int32_t id = ids[t];
     const bool in = id >= 0 && id < n_slots;
     int32_t r = in ? min(pp.rank[m][id], R) : 0;
-    const int32_t other = NM > 1 && in ? pp.rank[1][id] : 1;
+    const int32_t other = in ? pp.rank[1][id] : 1;
     float acc[kPairRanks] = {};
     // A padded slot has all its max_rank rows (zeros from its rank on), so its
     // loads need not wait for the rank; a packed one ends with its capacity.
@@ -279,32 +279,23 @@ __global__ void __launch_bounds__(256) k_shrink_pair(const typename elem<DT>::T 
     if (lane == 0 && j2 == 0 && (id < -1 || id >= n_slots || (in && (r <= 0 || other <= 0))))
         flag_bad_row(err, (int32_t)t);
     if (lane == 0)
-        *reinterpret_cast<float4 *>(v + t * NM * R + j2) =
+        *reinterpret_cast<float4 *>(v + t * 2 * R + j2) =
             make_float4(j0 < r ? acc[0] : 0.f, j0 + 1 < r ? acc[1] : 0.f, j0 + 2 < r ? acc[2] : 0.f,
                         j0 + 3 < r ? acc[3] : 0.f);
 }
 
-template <int DT, int NM>
-static lora_status_t shrink_pair(const void *x, int32_t T, const lora_pool_t *p, const int32_t *ids, float *v,
-                                 int32_t *err, hipStream_t s) {
-    const lora_pool_t two[2] = {p[0], p[NM - 1]};
-    const int64_t items = (int64_t)T * (NM * p[0].max_rank / kPairRanks);
-    hipLaunchKernelGGL((k_shrink_pair<DT, NM>), grid_of((items + 3) / 4), dim3(256), 0, s,
-                       (const typename elem<DT>::T *)x, T, p[0].d_in, make_pair_pools(two), p[0].n_slots, p[0].max_rank,
-                       ids, v, err);
-    return hip_status(hipGetLastError());
-}
-
 lora_status_t launch_shrink_pair(const void *x, int32_t T, const lora_pool_t *p, const int32_t *ids, float *v,
                                  int32_t *err, hipStream_t s) {
-    return p[0].dtype == LORA_F32 ? shrink_pair<LORA_F32, 2>(x, T, p, ids, v, err, s)
-                                  : shrink_pair<LORA_BF16, 2>(x, T, p, ids, v, err, s);
-}
-
-lora_status_t launch_shrink_one(const void *x, int32_t T, const lora_pool_t &p, const int32_t *ids, float *v,
-                                int32_t *err, hipStream_t s) {
-    return p.dtype == LORA_F32 ? shrink_pair<LORA_F32, 1>(x, T, &p, ids, v, err, s)
-                               : shrink_pair<LORA_BF16, 1>(x, T, &p, ids, v, err, s);
+    const pair_pools pp = make_pair_pools(p);
+    const int64_t items = (int64_t)T * (2 * p[0].max_rank / kPairRanks);
+    const dim3 grid = grid_of((items + 3) / 4);
+    if (p[0].dtype == LORA_F32)
+        hipLaunchKernelGGL(k_shrink_pair<LORA_F32>, grid, dim3(256), 0, s, (const float *)x, T, p[0].d_in, pp,
+                           p[0].n_slots, p[0].max_rank, ids, v, err);
+    else
+        hipLaunchKernelGGL(k_shrink_pair<LORA_BF16>, grid, dim3(256), 0, s, (const uint16_t *)x, T, p[0].d_in, pp,
+                           p[0].n_slots, p[0].max_rank, ids, v, err);
+    return hip_status(hipGetLastError());
 }
 
 lora_status_t launch_gated_forward(const gated_call &c, hipStream_t s) {

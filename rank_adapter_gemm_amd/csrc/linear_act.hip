@@ -15,6 +15,7 @@
 // of one workgroup a CU has before its first and after its last step.  4 wavefronts
 // and no split 49 us, 4 split in two 30 us and 7 for the sums' launch.
 #include "act_common.hpp"
+#include "fp8_common.hpp"
 
 namespace lora {
 
@@ -269,6 +270,388 @@ static int linear_f32_splits(int tiles, int K, size_t partial_bytes, int &k_chun
     }
     k_chunk = ceil_div(ceil_div(K, best), 32) * 32;
     return ceil_div(K, k_chunk);
+}
+
+// ---------------------------------------------------------------------------
+// The bf16 layer of up to 64 rows, bound by the bytes of W: W goes from memory to
+// the matrix cores without LDS.  A wavefront takes 128 columns and 32 k at a time:
+// a lane reads 8 neighbouring columns of each of 8 rows of W (16 bytes each) and
+// exchanges rows for columns in its registers (32 byte permutes for 128 bytes),
+// which gives the B operands of 8 products whose columns are 8 apart; x's rows are
+// the A operand as they lie.  The WV wavefronts of a workgroup share its K range,
+// step by step, and add their sums through LDS; the K ranges' sums go to the
+// partial buffer, and k_few_finish finishes them.  The first workgroups compute
+// the rank vectors v = x A meanwhile, which only that second launch reads.
+// ---------------------------------------------------------------------------
+template <int MT, int WV>
+__global__ void __launch_bounds__(WV * 64, WV == 4 ? 2 : 1) k_linear_few(gemm_args g, int32_t n_shrink) {
+    constexpr int SLD = 128 + 4, BM = 16 * MT;
+    __shared__ __attribute__((aligned(16))) float s_sum[WV / 2][BM][SLD];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, p = lane & 15, kg = lane >> 4;
+    if ((int)blockIdx.x < n_shrink) {
+        shrink_row<LORA_BF16, WV>(g.x, g.T, g.K, g.a, g.rank, g.row0, g.n_slots, g.max_rank, g.ids, g.vpart, g.err,
+                                  blockIdx.x);
+        return;
+    }
+    // neighbouring workgroups take neighbouring columns of one K range
+    const int wg = (int)blockIdx.x - n_shrink, tn = wg % g.n_tiles_n, split = wg / g.n_tiles_n;
+    const int N = g.N, K = g.K, T = g.T, n = tn * 128 + 8 * p;
+    const int k_begin = split * g.k_chunk, k_end = min(K, k_begin + g.k_chunk);
+    const uint16_t *wp = g.W + n;
+    const bool n_ok = n < N;
+    f32x4_t acc[MT][8];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int s = 0; s < 8; ++s) acc[m][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    uint4 wq[2][8], xq[2][MT];
+    // K is a multiple of 8, so a lane's 8 rows are all in the range or none is
+    auto load = [&](int k0, uint4 (&wr)[8], uint4 (&xr)[MT]) {
+        const int k = k0 + 8 * kg;
+        const bool in = k < k_end;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) wr[h] = in && n_ok ? ldg16(wp + (int64_t)(k + h) * N) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int t = 16 * m + p;
+            xr[m] = in && t < T ? ldg16(g.x + (int64_t)t * K + k) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto products = [&](const uint4 (&wr)[8], const uint4 (&xr)[MT]) {
+        uint32_t r[8][4];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            r[h][0] = wr[h].x; r[h][1] = wr[h].y; r[h][2] = wr[h].z; r[h][3] = wr[h].w;
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {                     // column s of a lane's 8: its values of the 8 rows
+            uint32_t o[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                o[h] = __builtin_amdgcn_perm(r[2 * h + 1][s >> 1], r[2 * h][s >> 1], (s & 1) ? 0x07060302u : 0x05040100u);
+            const bf16x8_t b = __builtin_bit_cast(bf16x8_t, make_uint4(o[0], o[1], o[2], o[3]));
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[m][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xr[m]), b, acc[m][s], 0, 0, 0);
+        }
+    };
+    constexpr int STRIDE = 32 * WV;
+    int k0 = k_begin + 32 * w;
+    load(k0, wq[0], xq[0]);
+    for (; k0 < k_end; k0 += 2 * STRIDE) {
+        load(k0 + STRIDE, wq[1], xq[1]);
+        products(wq[0], xq[0]);
+        load(k0 + 2 * STRIDE, wq[0], xq[0]);
+        products(wq[1], xq[1]);
+    }
+    // the upper half of the wavefronts hands its sums to the lower, and so on
+#pragma unroll
+    for (int half = WV / 2; half >= 1; half /= 2) {
+        if (w >= half && w < 2 * half)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float *at = &s_sum[w - half][16 * m + 4 * kg + e][8 * p];
+                    *reinterpret_cast<f32x4_t *>(at) = f32x4_t{acc[m][0][e], acc[m][1][e], acc[m][2][e], acc[m][3][e]};
+                    *reinterpret_cast<f32x4_t *>(at + 4) = f32x4_t{acc[m][4][e], acc[m][5][e], acc[m][6][e], acc[m][7][e]};
+                }
+        __syncthreads();
+        if (w < half)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float *at = &s_sum[w][16 * m + 4 * kg + e][8 * p];
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) acc[m][s][e] += at[s];
+                }
+        if (half > 1) __syncthreads();
+    }
+    if (w > 0) return;
+    float *part = g.partial + ((int64_t)tn * g.splits + split) * BM * 128 + 8 * p;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 16 * m + 4 * kg + e;
+            if (r >= T) continue;
+            float *at = part + r * 128;
+            *reinterpret_cast<f32x4_t *>(at) = f32x4_t{acc[m][0][e], acc[m][1][e], acc[m][2][e], acc[m][3][e]};
+            *reinterpret_cast<f32x4_t *>(at + 4) = f32x4_t{acc[m][4][e], acc[m][5][e], acc[m][6][e], acc[m][7][e]};
+        }
+}
+
+// The same on an FP8 base weight: 64 columns and 128 codes of k a wavefront and step;
+// rows of wq and of xq lie along k, so a lane reads 32 codes of each of 4 columns and of
+// each 16 rows as v_mfma_scale_f32_16x16x128_f8f6f4 takes them (lane l: A row and B
+// column l % 16, k = 32 (l / 16) + 0..31, and their E8M0 scales).
+typedef int few_i32x8_t __attribute__((ext_vector_type(8)));
+
+template <int MT, int WV>
+__global__ void __launch_bounds__(WV * 64) k_linear_few_fp8(gemm_args g, int32_t n_shrink) {
+    constexpr int SLD = 64 + 4, BM = 16 * MT, CB = 4;
+    __shared__ __attribute__((aligned(16))) float s_sum[WV / 2][BM][SLD];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, p = lane & 15, kg = lane >> 4;
+    if ((int)blockIdx.x < n_shrink) {
+        shrink_row<LORA_BF16, WV>(g.x, g.T, g.K, g.a, g.rank, g.row0, g.n_slots, g.max_rank, g.ids, g.vpart, g.err,
+                                  blockIdx.x);
+        return;
+    }
+    const int strips = 2 * g.n_tiles_n, wg = (int)blockIdx.x - n_shrink, strip = wg % strips, split = wg / strips;
+    const int N = g.N, K = g.K, T = g.T, n0 = strip * 64;
+    const int k_begin = split * g.k_chunk, k_end = min(K, k_begin + g.k_chunk);
+    int esa[MT], esb[CB];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) esa[m] = 16 * m + p < T ? e8m0_of(g.xs[16 * m + p]) : 127;
+#pragma unroll
+    for (int c = 0; c < CB; ++c) esb[c] = n0 + 16 * c + p < N ? e8m0_of(g.wsc[n0 + 16 * c + p]) : 127;
+    f32x4_t acc[MT][CB];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    uint4 wq[2][CB][2], xq[2][MT][2];
+    auto load = [&](int k0, uint4 (&wr)[CB][2], uint4 (&xr)[MT][2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = k0 + 32 * kg + 16 * h;          // K is a multiple of 16
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+                const int n = n0 + 16 * c + p;
+                wr[c][h] = k < k_end && n < N ? ldg16(g.wq + (int64_t)n * K + k) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int t = 16 * m + p;
+                xr[m][h] = k < k_end && t < T ? ldg16(g.xq + (int64_t)t * K + k) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+    auto operand = [](const uint4 (&q)[2]) {
+        few_i32x8_t v;
+        v[0] = (int)q[0].x; v[1] = (int)q[0].y; v[2] = (int)q[0].z; v[3] = (int)q[0].w;
+        v[4] = (int)q[1].x; v[5] = (int)q[1].y; v[6] = (int)q[1].z; v[7] = (int)q[1].w;
+        return v;
+    };
+    auto products = [&](const uint4 (&wr)[CB][2], const uint4 (&xr)[MT][2]) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[m][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(xr[m]), operand(wr[c]), acc[m][c], 0, 0,
+                                                                             0, esa[m], 0, esb[c]);
+    };
+    constexpr int STRIDE = 128 * WV;
+    int k0 = k_begin + 128 * w;
+    load(k0, wq[0], xq[0]);
+    for (; k0 < k_end; k0 += 2 * STRIDE) {
+        load(k0 + STRIDE, wq[1], xq[1]);
+        products(wq[0], xq[0]);
+        load(k0 + 2 * STRIDE, wq[0], xq[0]);
+        products(wq[1], xq[1]);
+    }
+#pragma unroll
+    for (int half = WV / 2; half >= 1; half /= 2) {       // as in k_linear_few
+        if (w >= half && w < 2 * half)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) s_sum[w - half][16 * m + 4 * kg + e][16 * c + p] = acc[m][c][e];
+        __syncthreads();
+        if (w < half)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) acc[m][c][e] += s_sum[w][16 * m + 4 * kg + e][16 * c + p];
+        if (half > 1) __syncthreads();
+    }
+    if (w > 0) return;
+    float *part = g.partial + ((int64_t)(strip >> 1) * g.splits + split) * BM * 128 + 64 * (strip & 1) + p;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 16 * m + 4 * kg + e;
+            if (r >= T) continue;
+#pragma unroll
+            for (int c = 0; c < CB; ++c) part[r * 128 + 16 * c] = acc[m][c][e];
+        }
+}
+
+// The K ranges' sums in their order, the row's low-rank term and the epilogue.  All of
+// it is latency, so a thread has 4 neighbouring columns of a row only, and asks for
+// everything as soon as its address is known: the partial sums, bias and residual with
+// the row's id, then the slot's first two octets of B and of v with its rank (a padded
+// slot has all its max_rank rows, a packed one at least 8).  16 x 4096, 8 ranges:
+// with 8 columns a thread and 4 ranges ahead 7.0 us.
+__global__ void __launch_bounds__(256) k_few_finish(gemm_args g, int32_t rows) {
+    constexpr int PRE = 2;
+    const int n = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y, N = g.N;
+    if (n >= N) return;
+    const int32_t id = g.ids[t];
+    const float *part = g.partial + ((int64_t)(n >> 7) * g.splits * rows + t) * 128 + (n & 127);
+    f32x4_t f[kMaxGemmSplit];
+#pragma unroll
+    for (int s = 0; s < kMaxGemmSplit; ++s) f[s] = load4(s < g.splits, part + (int64_t)s * rows * 128);
+    const int64_t at = (int64_t)t * N + n;
+    uint2 bias = make_uint2(0u, 0u), res = make_uint2(0u, 0u);
+    if (g.bias) bias = *reinterpret_cast<const uint2 *>(g.bias + n);
+    if (g.residual) res = *reinterpret_cast<const uint2 *>(g.residual + at);
+    const bool in = id >= 0 && id < g.n_slots;
+    const int32_t rk = in ? min(g.rank[id], g.max_rank) : 0;
+    const float sc = in ? g.scale[id] : 0.0f;
+    const uint16_t *b = g.b + ((in ? slot_row0(g.row0, id, g.max_rank) : 0) * N + (int64_t)n * 8);
+    const float *v = g.v + (int64_t)t * g.v_stride;
+    const int ahead = !in ? 0 : g.row0 ? 1 : min(PRE, g.max_rank / 8);
+    uint4 bq[PRE][4];
+    f32x4_t vq[PRE][2];
+#pragma unroll
+    for (int o = 0; o < PRE; ++o) {
+        const bool ok = o < ahead;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bq[o][q] = ok ? ldg16(b + (int64_t)o * N * 8 + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) vq[o][h] = load4(ok, v + 8 * o + 4 * h);
+    }
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    auto octet = [&](const uint4 (&bw)[4], const f32x4_t (&vw)[2]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float bf[8];
+            vec16<LORA_BF16>::widen(bw[q], bf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[q] = fmaf(vw[e >> 2][e & 3], bf[e], d[q]);
+        }
+    };
+#pragma unroll
+    for (int o = 0; o < PRE; ++o)
+        if (o < ahead && 8 * o < rk) octet(bq[o], vq[o]);
+    for (int o = ahead; 8 * o < rk; ++o) {
+        uint4 bw[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bw[q] = ldg16(b + (int64_t)o * N * 8 + 8 * q);
+        const f32x4_t vw[2] = {*reinterpret_cast<const f32x4_t *>(v + 8 * o), *reinterpret_cast<const f32x4_t *>(v + 8 * o + 4)};
+        octet(bw, vw);
+    }
+    f32x4_t o = f[0];
+#pragma unroll
+    for (int s = 1; s < kMaxGemmSplit; ++s)
+        if (s < g.splits)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += f[s][e];
+    const float bf[4] = {bf16_lo(bias.x), bf16_hi(bias.x), bf16_lo(bias.y), bf16_hi(bias.y)};
+    const float rf[4] = {bf16_lo(res.x), bf16_hi(res.x), bf16_lo(res.y), bf16_hi(res.y)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (rk > 0) o[e] = fmaf(sc, d[e], o[e]);
+        o[e] += bf[e];
+    }
+    if (g.pre) *reinterpret_cast<uint2 *>(g.pre + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = act_or_none<false>(g.act, o[e]) + rf[e];
+    *reinterpret_cast<uint2 *>(g.y + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+}
+
+template <int MT, int WV>
+static lora_status_t launch_few(const gemm_args &g, hipStream_t s) {
+    const int n_shrink = g.T * (g.max_rank / kRowRanks);
+    if constexpr (MT < 4)
+        if (g.xq)
+            hipLaunchKernelGGL((k_linear_few_fp8<MT, WV>), dim3(n_shrink + 2 * g.n_tiles_n * g.splits), dim3(WV * 64), 0, s,
+                               g, n_shrink);
+    if (!g.xq)
+        hipLaunchKernelGGL((k_linear_few<MT, WV>), dim3(n_shrink + g.n_tiles_n * g.splits), dim3(WV * 64), 0, s, g, n_shrink);
+    hipLaunchKernelGGL(k_few_finish, dim3(ceil_div(g.N, 1024), g.T), dim3(256), 0, s, g, 16 * MT);
+    return hip_status(hipGetLastError());
+}
+
+// K ranges per strip of columns (128, FP8 64), each of whole steps of the workgroup's
+// wavefronts: the count whose time is least by this estimate -- rounds of 256
+// workgroups that stream their part of W at a CU's 22 KB a microsecond, a
+// microsecond a round beside that, and the partial sums written and read at 4 TB/s.
+// (bf16, 4096 x 14336, 2 ranges: one row 29 us, 64 rows 45; 3 ranges 32 and 52; 5 29
+// and 51.)
+bool linear_few_plan(int32_t T, int32_t K, int32_t N, bool fp8, size_t partial_bytes, int &splits, int &k_chunk) {
+    // FP8: from 33 rows on the tiles of the base GEMM are faster (64 rows 53 us, here 64)
+    if (T <= 0 || T > (fp8 ? 32 : kFewRows)) return false;
+    const int tiles = ceil_div(N, 128), strips = fp8 ? 2 * tiles : tiles, rows = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    const int step = (T <= 32 ? 8 : 4) * (fp8 ? 128 : 32);
+    double best_us = 1e30;
+    splits = 0;
+    for (int s = 1; s <= kMaxGemmSplit && (s == 1 || s * step <= K); ++s) {
+        const int chunk = ceil_div(ceil_div(K, s), step) * step;
+        const double sums = (double)tiles * s * rows * 128 * 4;
+        if (sums > (double)partial_bytes) break;
+        const double us = ceil_div((int64_t)strips * s, 256) * (chunk * (fp8 ? 64.0 : 256.0) / 22e3 + 1) +
+                          2 * sums * T / rows / 4e6;
+        if (us < best_us) {
+            best_us = us;
+            splits = ceil_div(K, chunk);
+            k_chunk = chunk;
+        }
+    }
+    return splits > 0;
+}
+
+// v = x A of one pool, rows in their own order: a workgroup for four ranks of a row.
+template <int DT>
+__global__ void __launch_bounds__(256) k_shrink_one(const typename elem<DT>::T *x, int32_t T, int32_t d, const void *a,
+                                                    const int32_t *rank, const int32_t *row0, int32_t n_slots, int32_t R,
+                                                    const int32_t *ids, float *v, int32_t *err) {
+    shrink_row<DT, 4>(x, T, d, a, rank, row0, n_slots, R, ids, v, err, grid_index());
+}
+
+lora_status_t launch_shrink_one(const void *x, int32_t T, const lora_pool_t &p, const int32_t *ids, float *v,
+                                int32_t *err, hipStream_t s) {
+    const dim3 grid = grid_of((int64_t)T * (p.max_rank / kRowRanks));
+    if (p.dtype == LORA_F32)
+        hipLaunchKernelGGL(k_shrink_one<LORA_F32>, grid, dim3(256), 0, s, (const float *)x, T, p.d_in, p.a, p.rank, p.row0,
+                           p.n_slots, p.max_rank, ids, v, err);
+    else
+        hipLaunchKernelGGL(k_shrink_one<LORA_BF16>, grid, dim3(256), 0, s, (const uint16_t *)x, T, p.d_in, p.a, p.rank,
+                           p.row0, p.n_slots, p.max_rank, ids, v, err);
+    return hip_status(hipGetLastError());
+}
+
+lora_status_t launch_linear_few(const void *x, const void *W, const uint8_t *xq, const float *xs, const uint8_t *wq,
+                                const float *wsc, void *y, int32_t T, const lora_pool_t &p, const int32_t *ids, float *v,
+                                int32_t *err, float *partial, size_t partial_bytes, const epilogue &epi, hipStream_t s) {
+    gemm_args g{};
+    set_epilogue(g, &epi);
+    if (!linear_few_plan(T, p.d_in, p.d_out, xq != nullptr, partial_bytes, g.splits, g.k_chunk)) return LORA_ERR_UNSUPPORTED;
+    g.x = (const uint16_t *)x;
+    g.W = (const uint16_t *)W;
+    g.xq = xq;
+    g.xs = xs;
+    g.wq = wq;
+    g.wsc = wsc;
+    g.y = (uint16_t *)y;
+    g.T = T;
+    g.K = p.d_in;
+    g.N = p.d_out;
+    g.a = (const uint16_t *)p.a;
+    g.b = (const uint16_t *)p.b;
+    g.scale = p.scale;
+    g.rank = p.rank;
+    g.row0 = p.row0;
+    g.n_slots = p.n_slots;
+    g.max_rank = p.max_rank;
+    g.ids = ids;
+    g.v = v;
+    g.vpart = v;
+    g.v_stride = p.max_rank;
+    g.err = err;
+    g.partial = partial;
+    g.n_tiles_m = 1;
+    g.n_tiles_n = g.n_tiles = ceil_div(g.N, 128);
+    if (T <= 16) return launch_few<1, 8>(g, s);
+    if (T <= 32) return launch_few<2, 8>(g, s);
+    return launch_few<4, 4>(g, s);
 }
 
 lora_status_t launch_linear_f32(const void *x, const void *W, void *y, int32_t T, const lora_pool_t &p,
