@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(256) k_gemm_f32(gemm_f32_args g) {
 }
 
 // NST, WVT: stages and wavefronts of the split-K pieces (their LDS holds no
-// row tables).
+// row tables), and of the whole tiles with an epilogue, which read their rows'
+// terms after the last step (see gemm_fp8.hip for both sides).
 template <int BM, int BN, int NS = 2, int WV = 4, int WR = 2, int BK = 64, int NST = NS, int WVT = WV>
 static void launch_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t s, bool epi = false) {
     if (pl.n_dp > 0) {
@@ -481,8 +482,8 @@ static void launch_cfg(gemm_args g, const gemm_plan &pl, bool lora, hipStream_t 
         g.splits = 1;
         g.k_chunk = g.K;
         if (epi)
-            hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, BK, NS, false, false, WV, WR, true>), dim3(pl.n_dp),
-                               dim3(WV * 64), 0, s, g);
+            hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, BK, NST, false, false, WVT, WR, true>), dim3(pl.n_dp),
+                               dim3(WVT * 64), 0, s, g);
         else if (lora)
             hipLaunchKernelGGL((k_gemm_bf16<true, BM, BN, BK, NS, false, false, WV, WR>), dim3(pl.n_dp), dim3(WV * 64),
                                0, s, g);
@@ -714,7 +715,9 @@ lora_status_t launch_gemm(const void *x, const void *W, void *y, int32_t T, int3
         g.v = v;
         g.v_stride = v_stride;
         g.n_fused = n_fused;
-        const gemm_plan pl = plan_gemm(T, d_in, d_out, partial ? partial_bytes : 0);
+        if (!partial) partial_bytes = 0;
+        const gemm_plan pl = epi ? plan_linear(T, d_in, d_out, partial_bytes, 2, 64)
+                                 : plan_gemm(T, d_in, d_out, partial_bytes);
         g.n_tiles_m = ceil_div(T, pl.bm);
         g.n_tiles_n = ceil_div(d_out, pl.bn);
         g.col_strips = col_strips_pay(T, d_out, g.n_tiles_n);

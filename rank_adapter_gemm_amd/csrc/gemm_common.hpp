@@ -753,4 +753,33 @@ inline gemm_plan plan_gemm(int T, int K, int N, size_t partial_bytes, int kgran 
     return plan_gemm(T, K, &n, 1, partial_bytes, kgran, wide_small);
 }
 
+// The layer with an epilogue.  plan_gemm, whose sums the plain layer keeps,
+// gives a small grid whole tiles of 64 columns or the first split past one
+// workgroup per CU, often a second round of few; here the split is the one with the least estimated time: rounds
+// of 256 workgroups (one per CU: their stages fill LDS) at the rate at which
+// one takes its operands (K step bytes of a tile at about 25 KB / us), and the
+// partial sums written and read back at 4 TB/s.  100 rows, 4096 x 14336: bf16
+// 85 -> 55 us, FP8 62 -> 41 (2 ranges for 224 whole tiles).
+inline gemm_plan plan_linear(int T, int K, int N, size_t partial_bytes, int elem_bytes, int kgran) {
+    const gemm_plan whole = plan_gemm(T, K, N, partial_bytes, kgran);
+    if (whole.n_dp > 0 && whole.bn > 64) return whole;
+    const int tiles = ceil_div(T, 128) * ceil_div(N, 128);
+    gemm_plan p{128, 128, 0, tiles, 1, K};
+    double best_us = 1e30;
+    for (int s = 1; s <= kMaxGemmSplit && (s == 1 || K / s >= 256); ++s) {
+        const double sums = s > 1 ? (double)tiles * s * p.bm * p.bn * 4 : 0;
+        if (sums > (double)partial_bytes) break;
+        const int chunk = ceil_div(ceil_div(K, s), kgran) * kgran;
+        const double us = ceil_div((int64_t)tiles * s, 256) * ((double)chunk * elem_bytes * (p.bm + p.bn) / 25e3 + 3) +
+                          2 * sums / 4e6;
+        if (us < best_us) {
+            best_us = us;
+            p.splits = ceil_div(K, chunk);
+            p.k_chunk = chunk;
+        }
+    }
+    if (p.splits > 1) return p;
+    return whole.n_dp > 0 ? whole : gemm_plan{128, 128, tiles, 0, 1, K};
+}
+
 }  // namespace lora
