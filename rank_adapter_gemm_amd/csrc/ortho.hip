@@ -46,8 +46,8 @@ template <int W, bool TALL> __device__ __forceinline__ int ortho_index(int s, in
 struct ortho_args {
     const void *g;
     void *out;
-    double *part;                      // [n][splits][tiles][256]: a tile's sums, element by element
-    double *poly;                      // [n][r][r]
+    double *part;                      // [n][splits][tiles][64][4]: a tile's sums, lane by lane
+    double *poly;                      // [n][16 W][16 W], zeros past r
     double *factor;                    // [n]: scale / (|G| + eps)
     int32_t D, n, r, splits, chunk;    // chunk: long-side indices per split, a multiple of 64
     int32_t rows, blocks;              // k_ortho_apply: long-side indices per workgroup, workgroups per matrix
@@ -57,9 +57,9 @@ struct ortho_args {
 };
 
 // ---------------------------------------------------------------------------
-// G^T G.  Four wavefronts share a split's long side and add their sums through
+// G^T G.  Eight wavefronts share a split's long side and add their sums through
 // LDS in a fixed order.  Of 8 tiles a side a wavefront holds half the rows of
-// tiles (0, 3, 4, 7 or 1, 2, 5, 6: 18 tiles each), and two share a part.
+// tiles (0, 3, 4, 7 or 1, 2, 5, 6: 18 tiles each), and two of four share a part.
 // ---------------------------------------------------------------------------
 template <int W> __device__ __forceinline__ constexpr bool gram_owns(int half, int a) {
     return W < 8 || (((a + 1) >> 1) & 1) == half;
@@ -93,10 +93,15 @@ template <int DT> __device__ __forceinline__ float value_of(const uint32_t *q, i
     return (i & 1) ? bf16_hi(q[i >> 1]) : bf16_lo(q[i >> 1]);
 }
 
+// Wavefronts, and of those the ones that share a part's long side.
+template <int W> struct gram_cfg {
+    static constexpr int WAVES = W == 8 ? 4 : 8, KW = W == 8 ? 2 : 8;
+};
+
 template <int DT, int W, bool TALL, int HALF, int N>
 __device__ __forceinline__ void gram_wave(const ortho_args &g, const typename elem<DT>::T *base, int begin, int end,
                                           int kw, int lane, f64x4_t (&acc)[N]) {
-    constexpr int VN = vec16<DT>::n, KW = W == 8 ? 2 : 4, EB = elem<DT>::bytes;
+    constexpr int VN = vec16<DT>::n, KW = gram_cfg<W>::KW, EB = elem<DT>::bytes;
     // a wavefront reads U groups of STEP long-side indices at once: a value of W
     // short-side indices for each of 4 (tall), or 16 bytes of each tile's 16 rows
     constexpr int STEP = TALL ? 4 : 4 * VN, U = TALL ? 16 / W : 1;
@@ -146,9 +151,10 @@ __device__ __forceinline__ void gram_wave(const ortho_args &g, const typename el
     }
 }
 
-template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ortho_gram(ortho_args g) {
-    constexpr int NT = ortho_tiles(W), KW = W == 8 ? 2 : 4, HALVES = 4 / KW, N = NT / HALVES;
-    __shared__ double s_sum[KW - 1][NT][256];
+template <int DT, int W, bool TALL>
+__global__ void __launch_bounds__(gram_cfg<W>::WAVES * 64) k_ortho_gram(ortho_args g) {
+    constexpr int NT = ortho_tiles(W), KW = gram_cfg<W>::KW, HALVES = gram_cfg<W>::WAVES / KW, N = NT / HALVES;
+    __shared__ f64x4_t s_sum[KW - 1][NT][64];
     const int64_t item = grid_index();
     if (item >= (int64_t)g.n * g.splits) return;
     const int64_t mat = item / g.splits;
@@ -168,38 +174,179 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
                 if (W == 8 && gram_owns<W>(1, a) && half == 1) f(ortho_tile(a, b), acc[gram_at<W>(1, a, b) < N ? gram_at<W>(1, a, b) : 0]);
             }
     };
-    if (kw > 0)
-        each([&](int tile, const f64x4_t &c) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s_sum[kw - 1][tile][64 * e + lane] = c[e];
-        });
+    // wavefront tile % KW of a part adds up a tile, the others hand theirs over
+    each([&](int tile, const f64x4_t &c) {
+        const int to = tile % KW;
+        if (kw != to) s_sum[kw < to ? kw : kw - 1][tile][lane] = c;
+    });
     __syncthreads();
-    if (kw > 0) return;
-    double *part = g.part + item * NT * 256;
-    each([&](int tile, f64x4_t &c) {
+    f64x4_t *part = reinterpret_cast<f64x4_t *>(g.part) + item * NT * 64 + lane;
+    each([&](int tile, const f64x4_t &c) {
+        if (kw != tile % KW) return;
+        f64x4_t f = c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-#pragma unroll
-            for (int k = 0; k < KW - 1; ++k) c[e] += s_sum[k][tile][64 * e + lane];
-            part[tile * 256 + 64 * e + lane] = c[e];
-        }
+        for (int k = 0; k < KW - 1; ++k) f += s_sum[k][tile][lane];
+        part[tile * 64] = f;
     });
 }
 
 // ---------------------------------------------------------------------------
-// The steps on the r x r matrices, one workgroup a matrix: a wavefront holds one
-// tile (three of 8 a side) of M, P and what is made of them; the two factors of a
-// product lie in LDS, the tiles on and under the diagonal, in rows of 17 values
-// (both ways of reading a tile then spread over the banks).  Bound by the chain of
-// 4 products a step.
+// The steps on the r x r matrices, one workgroup a matrix.  All matrices are
+// symmetric and commute, so a product is symmetric too, and only its tiles on and
+// under the diagonal are computed.  Symmetry also makes a tile its own operand: the
+// result's element e of a lane, X[16 a + 4 e + kg][16 b + p], is what the lane gives
+// to product e as the right operand (k in a, column in b) and as the left one (row
+// in b, k in a).  So a matrix of one tile stays in registers through all steps, and
+// larger ones lie in LDS lane by lane, both triangles, one of them written across.
 // ---------------------------------------------------------------------------
+// Tile (a, b), a >= b, of P at its place in memory, and its mirror image.
+template <int W, bool TALL>
+__device__ __forceinline__ void poly_store(const ortho_args &g, int64_t mat, int a, int b, const f64x4_t &v, int lane) {
+    double *poly = g.poly + mat * 256 * W * W;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = ortho_index<W, TALL>(a, mfma64_row(e, lane)), j = ortho_index<W, TALL>(b, lane & 15);
+        const double f = i < g.r && j < g.r ? v[e] : 0.0;
+        poly[i * 16 * W + j] = f;
+        if (a != b) poly[j * 16 * W + i] = f;
+    }
+}
+
+__device__ __forceinline__ double wave_sum64(double d) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
+    return d;
+}
+
+// One of the tiles of product's operands after the other, four k at a time.
+__device__ __forceinline__ f64x4_t mfma64_tile(const f64x4_t &x, const f64x4_t &y, f64x4_t c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = mfma64(x[s], y[s], c);
+    return c;
+}
+
+// The sum of a tile over the splits, in their order.
+template <int NT> __device__ __forceinline__ f64x4_t poly_part(const ortho_args &g, int64_t mat, int tile, int lane) {
+    const f64x4_t *part = reinterpret_cast<const f64x4_t *>(g.part) + (mat * g.splits * NT + tile) * 64 + lane;
+    f64x4_t m = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+    for (int s = 0; s < g.splits; ++s) m += part[(int64_t)s * NT * 64];
+    return m;
+}
+
+// One tile: a wavefront a matrix, no LDS.
+template <bool TALL> __global__ void __launch_bounds__(64) k_ortho_poly1(ortho_args g) {
+    const int64_t mat = grid_index();
+    if (mat >= g.n) return;
+    const int lane = threadIdx.x, p = lane & 15;
+    f64x4_t m = poly_part<1>(g, mat, 0, lane), one, pr;
+    double d = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        one[e] = mfma64_row(e, lane) == p ? 1.0 : 0.0;
+        d += one[e] * m[e];
+    }
+    const double inv = 1.0 / (sqrt(wave_sum64(d)) + (double)g.eps);
+    if (lane == 0) g.factor[mat] = (double)g.scale * inv;
+    const f64x4_t zero = {0.0, 0.0, 0.0, 0.0};
+    m *= inv * inv;
+    pr = one;
+    for (int step = 0; step < g.steps; ++step) {
+        const f64x4_t q = (double)g.coef[step][0] * one + (double)g.coef[step][1] * m +
+                          (double)g.coef[step][2] * mfma64_tile(m, m, zero);
+        const f64x4_t t = mfma64_tile(m, q, zero);
+        pr = step == 0 ? q : mfma64_tile(pr, q, zero);
+        m = mfma64_tile(t, q, zero);
+    }
+    poly_store<1, TALL>(g, mat, 0, 0, pr, lane);
+}
+
+// 2 or 4 tiles a side.  A step is three rounds with a barrier each: M M and from it
+// Q; T = M Q and the new P = P Q; and the new M = T Q.  A wavefront has one tile of a
+// product; of the second round's it has one of T and one of P, given out so that
+// the four SIMDs have equally many.  Bound by the 64-bit products of one CU: 4
+// tiles, 5 steps: 170 tiles, 64 clocks a product.
 template <int W> struct poly_cfg {
-    static constexpr int NT = ortho_tiles(W), OWN = W == 8 ? 3 : 1, WAVES = NT / OWN, TILE = 16 * 17;
+    static constexpr int NT = ortho_tiles(W), WAVES = W == 4 ? 12 : 6;
 };
 
 template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES * 64) k_ortho_poly(ortho_args g) {
-    typedef poly_cfg<W> C;
-    constexpr int NT = C::NT, OWN = C::OWN, TILE = C::TILE;
+    constexpr int NT = poly_cfg<W>::NT;
+    __shared__ f64x4_t s_m[W * W][64], s_q[W * W][64], s_t[W * W][64], s_p[W * W][64];
+    __shared__ double s_trace[W];
+    const int64_t mat = grid_index();
+    if (mat >= g.n) return;
+    const int lane = threadIdx.x & 63, wave = uniform_i(threadIdx.x >> 6), p = lane & 15, kg = lane >> 4;
+    // wave's tile of M, Q and T, and its tile of P, or none (wavefronts 4 apart share a SIMD)
+    const bool own = wave < NT, own_p = W == 4 ? wave < 8 || wave >= 10 : wave >= NT;
+    const int tm = own ? wave : 0, tp = !own_p ? 0 : W == 4 ? (wave < 8 ? wave : wave - 2) : wave - NT;
+    auto row_of = [](int tile) {
+        int a = 0;
+        while ((a + 1) * (a + 2) / 2 <= tile) ++a;
+        return a;
+    };
+    const int ma = row_of(tm), mb = tm - ma * (ma + 1) / 2, pa = row_of(tp), pb = tp - pa * (pa + 1) / 2;
+    auto put = [&](f64x4_t (*to)[64], int a, int b, const f64x4_t &v) {
+        to[a * W + b][lane] = v;
+        if (a != b)                                       // element e is row 4 e + kg, column p
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                reinterpret_cast<double *>(&to[b * W + a][16 * (p & 3) + 4 * e + kg])[p >> 2] = v[e];
+    };
+    auto product = [&](const f64x4_t (*x)[64], const f64x4_t (*y)[64], int a, int b) {
+        f64x4_t c = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+        for (int k = 0; k < W; ++k) c = mfma64_tile(x[k * W + a][lane], y[k * W + b][lane], c);
+        return c;
+    };
+    f64x4_t m = {0.0, 0.0, 0.0, 0.0}, one, r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) one[e] = ma == mb && mfma64_row(e, lane) == p ? 1.0 : 0.0;
+    if (own) {
+        m = poly_part<NT>(g, mat, tm, lane);
+        if (ma == mb) {
+            const double d = wave_sum64(one[0] * m[0] + one[1] * m[1] + one[2] * m[2] + one[3] * m[3]);
+            if (lane == 0) s_trace[ma] = d;
+        }
+    }
+    __syncthreads();
+    double trace = s_trace[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) trace += s_trace[i];
+    const double inv = 1.0 / (sqrt(trace) + (double)g.eps);
+    if (threadIdx.x == 0) g.factor[mat] = (double)g.scale * inv;
+    m *= inv * inv;
+    if (own) put(s_m, ma, mb, m);
+    __syncthreads();
+    for (int step = 0; step < g.steps; ++step) {
+        const bool last = step + 1 == g.steps;
+        if (own) {
+            const f64x4_t q = (double)g.coef[step][0] * one + (double)g.coef[step][1] * m +
+                              (double)g.coef[step][2] * product(s_m, s_m, ma, mb);
+            put(s_q, ma, mb, q);
+            if (step == 0) put(s_p, ma, mb, q);
+        }
+        __syncthreads();
+        if (step > 0 && own_p) r = product(s_p, s_q, pa, pb);
+        if (last) break;
+        if (own) put(s_t, ma, mb, product(s_m, s_q, ma, mb));
+        __syncthreads();
+        if (step > 0 && own_p) put(s_p, pa, pb, r);
+        if (own) {
+            m = product(s_t, s_q, ma, mb);
+            put(s_m, ma, mb, m);
+        }
+        __syncthreads();
+    }
+    if (own_p) poly_store<W, TALL>(g, mat, pa, pb, g.steps > 1 ? r : s_p[pa * W + pb][lane], lane);
+}
+
+// 8 tiles a side: both triangles of four matrices would not fit in LDS, so the two
+// factors of a product lie there, the tiles on and under the diagonal, in rows of 17
+// values (both ways of reading a tile then spread over the banks); a wavefront has
+// three tiles of each matrix.
+template <bool TALL> __global__ void __launch_bounds__(768) k_ortho_poly8(ortho_args g) {
+    constexpr int W = 8, NT = ortho_tiles(W), OWN = 3, TILE = 16 * 17;
     __shared__ double s_x[NT * TILE], s_y[NT * TILE];
     __shared__ double s_trace;
     const int64_t mat = grid_index();
@@ -242,13 +389,11 @@ template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES
     auto one = [&](int o, int e) { return ta[o] == tb[o] && mfma64_row(e, lane) == p ? 1.0 : 0.0; };
 #pragma unroll
     for (int o = 0; o < OWN; ++o) m[o] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-    const double *part = g.part + mat * g.splits * NT * 256 + lane;
-#pragma unroll 4
-    for (int s = 0; s < g.splits; ++s, part += NT * 256)
+    const f64x4_t *part = reinterpret_cast<const f64x4_t *>(g.part) + mat * g.splits * NT * 64 + lane;
+#pragma unroll 2
+    for (int s = 0; s < g.splits; ++s, part += NT * 64)
 #pragma unroll
-        for (int o = 0; o < OWN; ++o)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[o][e] += part[tt[o] * 256 + 64 * e];
+        for (int o = 0; o < OWN; ++o) m[o] += part[tt[o] * 64];
     put(s_x, m);
     __syncthreads();
     if (wave == 0) {
@@ -295,16 +440,8 @@ template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES
             __syncthreads();
         }
     }
-    double *poly = g.poly + mat * g.r * g.r;
 #pragma unroll
-    for (int o = 0; o < OWN; ++o)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = ortho_index<W, TALL>(ta[o], mfma64_row(e, lane)), j = ortho_index<W, TALL>(tb[o], p);
-            if (i >= g.r || j >= g.r) continue;
-            poly[i * g.r + j] = pr[o][e];
-            if (ta[o] != tb[o]) poly[j * g.r + i] = pr[o][e];
-        }
+    for (int o = 0; o < OWN; ++o) poly_store<W, TALL>(g, mat, ta[o], tb[o], pr[o], lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -315,133 +452,179 @@ template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES
 // fp32: 64-bit products.  tall: a block is 16 rows i of G, and a lane reads 4
 // neighbouring values j of one; wide: 64 columns i, and a lane reads 4
 // neighbouring ones of row j.
-template <int W, bool TALL>
-__device__ __forceinline__ void apply_f32(const ortho_args &g, const float *in, float *out, const double *s_p,
-                                          double factor, int i0, int lane) {
-    constexpr int LD = 16 * W + 4, CB = W < 2 ? W : 2, R4 = TALL ? W : 4 * W, S = TALL ? 1 : 4;
-    const int p = lane & 15, kg = lane >> 4, r = g.r;
+template <int W, bool TALL> struct apply_f32 {
+    static constexpr int LD = 16 * W + 4, CB = TALL && W > 1 ? 2 : 1, R4 = TALL ? W : 4 * W, S = TALL ? 1 : 4;
     f32x4_t x[R4];
+
+    __device__ __forceinline__ void load(const ortho_args &g, const float *in, int i0, int lane) {
+            const int p = lane & 15, kg = lane >> 4, r = g.r;
 #pragma unroll
-    for (int k = 0; k < R4; ++k) {
-        // tall: j = 16 k + 4 kg + (0..3) of row i0 + p; wide: row j = 4 k + kg, columns i0 + 4 p + (0..3)
-        const int j = TALL ? 16 * k + 4 * kg : 4 * k + kg, i = TALL ? i0 + p : i0 + 4 * p;
-        x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        if (j < r && i < g.D) x[k] = *reinterpret_cast<const f32x4_t *>(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
+        for (int k = 0; k < R4; ++k) {
+            // tall: j = 16 k + 4 kg + (0..3) of row i0 + p; wide: row j = 4 k + kg, columns i0 + 4 p + (0..3)
+            const int j = TALL ? 16 * k + 4 * kg : 4 * k + kg, i = TALL ? i0 + p : i0 + 4 * p;
+            x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (j < r && i < g.D) x[k] = *reinterpret_cast<const f32x4_t *>(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
+        }
     }
+
+    __device__ __forceinline__ void store(const ortho_args &g, float *out, const double *s_p, double factor, int i0,
+                                          int lane) {
+        const int p = lane & 15, kg = lane >> 4, r = g.r;
 #pragma unroll 1                                           // (unrolled, the wide ones spill)
-    for (int c0 = 0; c0 < W; c0 += CB) {
-        f64x4_t acc[CB][S];
+        for (int c0 = 0; c0 < W; c0 += CB) {
+            f64x4_t acc[CB][S];
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+            for (int k = 0; k < R4; ++k) asm volatile("" : "+v"(x[k]));   // widened here, not once and kept
 #pragma unroll
-            for (int s = 0; s < S; ++s) acc[cb][s] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+            for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-        for (int k = 0; k < 4 * W; ++k)
+                for (int s = 0; s < S; ++s) acc[cb][s] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int k = 0; k < 4 * W; ++k)
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                    // the result's row 4 e + kg is the tile's column 4 kg + e where lanes store along it (tall)
+                    const int c = 16 * (c0 + cb) + (TALL ? 4 * (p & 3) + (p >> 2) : p);
+                    const double a = s_p[c * LD + 4 * k + kg];
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        acc[cb][s] = mfma64(a, (double)(TALL ? x[k >> 2][k & 3] : x[k][s]), acc[cb][s]);
+                }
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
-                // the result's row 4 e + kg is the tile's column 4 kg + e where lanes store along it (tall)
-                const int c = 16 * (c0 + cb) + (TALL ? 4 * (p & 3) + (p >> 2) : p);
-                const double a = s_p[c * LD + 4 * k + kg];
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    acc[cb][s] = mfma64(a, (double)(TALL ? x[k >> 2][k & 3] : x[k][s]), acc[cb][s]);
-            }
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            if constexpr (TALL) {
-                const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
-                if (c < r && i < g.D)
-                    *reinterpret_cast<f32x4_t *>(out + (int64_t)i * r + c) =
-                        f32x4_t{(float)(factor * acc[cb][0][0]), (float)(factor * acc[cb][0][1]),
-                                (float)(factor * acc[cb][0][2]), (float)(factor * acc[cb][0][3])};
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = 16 * (c0 + cb) + mfma64_row(e, lane), i = i0 + 4 * p;
+                if constexpr (TALL) {
+                    const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
                     if (c < r && i < g.D)
-                        *reinterpret_cast<f32x4_t *>(out + (int64_t)c * g.D + i) =
-                            f32x4_t{(float)(factor * acc[cb][0][e]), (float)(factor * acc[cb][S > 1 ? 1 : 0][e]),
-                                    (float)(factor * acc[cb][S > 2 ? 2 : 0][e]), (float)(factor * acc[cb][S > 3 ? 3 : 0][e])};
+                        *reinterpret_cast<f32x4_t *>(out + (int64_t)i * r + c) =
+                            f32x4_t{(float)(factor * acc[cb][0][0]), (float)(factor * acc[cb][0][1]),
+                                    (float)(factor * acc[cb][0][2]), (float)(factor * acc[cb][0][3])};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 16 * (c0 + cb) + mfma64_row(e, lane), i = i0 + 4 * p;
+                        if (c < r && i < g.D)
+                            *reinterpret_cast<f32x4_t *>(out + (int64_t)c * g.D + i) =
+                                f32x4_t{(float)(factor * acc[cb][0][e]), (float)(factor * acc[cb][S > 1 ? 1 : 0][e]),
+                                        (float)(factor * acc[cb][S > 2 ? 2 : 0][e]), (float)(factor * acc[cb][S > 3 ? 3 : 0][e])};
+                    }
                 }
             }
         }
     }
-}
+};
 
 // bf16: v_mfma_f32_16x16x32_bf16 (lane l: A row and B column l % 16, k = 8 (l / 16)
 // + (0..7); the result's row 4 (l / 16) + e, column l % 16).  tall: a block is 16
 // rows i, and a lane reads 8 neighbouring values of one; wide: 128 columns, and a
 // lane reads 8 neighbouring columns of each of 8 rows j, and exchanges rows for
 // columns in its registers.
-template <int W, bool TALL>
-__device__ __forceinline__ void apply_bf16(const ortho_args &g, const uint16_t *in, uint16_t *out, const uint16_t *s_p,
-                                           float factor, int i0, int lane) {
-    constexpr int RP = W < 2 ? 32 : 16 * W, LD = RP + 8, PART = 16 * W * LD, KT = RP / 32, CB = W < 2 ? W : 2, S = TALL ? 1 : 8;
-    const int p = lane & 15, kg = lane >> 4, r = g.r;
+template <int W, bool TALL> struct apply_bf16 {
+    static constexpr int RP = W < 2 ? 32 : 16 * W, LD = RP + 8, PART = 16 * W * LD, KT = RP / 32, CB = W < 2 ? W : 2, S = TALL ? 1 : 8;
     uint4 x[KT][S];
+
+    __device__ __forceinline__ void load(const ortho_args &g, const uint16_t *in, int i0, int lane) {
+        const int p = lane & 15, kg = lane >> 4, r = g.r;
 #pragma unroll
-    for (int k = 0; k < KT; ++k) {
-        if constexpr (TALL) {
-            const int j = 32 * k + 8 * kg, i = i0 + p;
-            x[k][0] = j < r && i < g.D ? ldg16(in + (int64_t)i * r + j) : make_uint4(0u, 0u, 0u, 0u);
-        } else {
-            uint32_t w[8][4];                             // rows j = 32 k + 8 kg + (0..7), columns i0 + 8 p + (0..7)
+        for (int k = 0; k < KT; ++k) {
+            if constexpr (TALL) {
+                const int j = 32 * k + 8 * kg, i = i0 + p;
+                x[k][0] = j < r && i < g.D ? ldg16(in + (int64_t)i * r + j) : make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                uint32_t w[8][4];                             // rows j = 32 k + 8 kg + (0..7), columns i0 + 8 p + (0..7)
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const int j = 32 * k + 8 * kg + h, i = i0 + 8 * p;
-                const uint4 v = j < r && i < g.D ? ldg16(in + (int64_t)j * g.D + i) : make_uint4(0u, 0u, 0u, 0u);
-                w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
-            }
+                for (int h = 0; h < 8; ++h) {
+                    const int j = 32 * k + 8 * kg + h, i = i0 + 8 * p;
+                    const uint4 v = j < r && i < g.D ? ldg16(in + (int64_t)j * g.D + i) : make_uint4(0u, 0u, 0u, 0u);
+                    w[h][0] = v.x; w[h][1] = v.y; w[h][2] = v.z; w[h][3] = v.w;
+                }
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {                 // column s of the 8: its values of the 8 rows
-                uint32_t o[4];
+                for (int s = 0; s < 8; ++s) {                 // column s of the 8: its values of the 8 rows
+                    uint32_t o[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    o[h] = __builtin_amdgcn_perm(w[2 * h + 1][s >> 1], w[2 * h][s >> 1], (s & 1) ? 0x07060302u : 0x05040100u);
-                x[k][S > 1 ? s : 0] = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int h = 0; h < 4; ++h)
+                        o[h] = __builtin_amdgcn_perm(w[2 * h + 1][s >> 1], w[2 * h][s >> 1], (s & 1) ? 0x07060302u : 0x05040100u);
+                    x[k][S > 1 ? s : 0] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
         }
     }
+
+    __device__ __forceinline__ void store(const ortho_args &g, uint16_t *out, const uint16_t *s_p, double factor64, int i0,
+                                          int lane) {
+        const int p = lane & 15, kg = lane >> 4, r = g.r;
+        const float factor = (float)factor64;
 #pragma unroll 1                                           // (unrolled, the wide ones spill)
-    for (int c0 = 0; c0 < W; c0 += CB) {
-        f32x4_t acc[CB][S];
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int s = 0; s < S; ++s) acc[cb][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
+        for (int c0 = 0; c0 < W; c0 += CB) {
+            f32x4_t acc[CB][S];
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                for (int part = 2; part >= 0; --part) {   // the small parts first
-                    const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(s_p + part * PART + (16 * (c0 + cb) + p) * LD +
-                                                                           32 * k + 8 * kg);
+                for (int s = 0; s < S; ++s) acc[cb][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int s = 0; s < S; ++s)
-                        acc[cb][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[k][s]),
-                                                                             acc[cb][s], 0, 0, 0);
-                }
+            for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            if constexpr (TALL) {
-                const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
-                if (c < r && i < g.D)
-                    *reinterpret_cast<uint2 *>(out + (int64_t)i * r + c) =
-                        make_uint2(pack_bf16x2(factor * acc[cb][0][0], factor * acc[cb][0][1]),
-                                   pack_bf16x2(factor * acc[cb][0][2], factor * acc[cb][0][3]));
-            } else {
+                for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = 16 * (c0 + cb) + 4 * kg + e, i = i0 + 8 * p;
-                    if (c >= r || i >= g.D) continue;
-                    float f[8];
+                    for (int part = 2; part >= 0; --part) {   // the small parts first
+                        const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(s_p + part * PART + (16 * (c0 + cb) + p) * LD +
+                                                                               32 * k + 8 * kg);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) f[s] = factor * acc[cb][S > 1 ? s : 0][e];
-                    stg16(out + (int64_t)c * g.D + i, vec16<LORA_BF16>::narrow(f));
+                        for (int s = 0; s < S; ++s)
+                            acc[cb][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[k][s]),
+                                                                                 acc[cb][s], 0, 0, 0);
+                    }
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                if constexpr (TALL) {
+                    const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
+                    if (c < r && i < g.D)
+                        *reinterpret_cast<uint2 *>(out + (int64_t)i * r + c) =
+                            make_uint2(pack_bf16x2(factor * acc[cb][0][0], factor * acc[cb][0][1]),
+                                       pack_bf16x2(factor * acc[cb][0][2], factor * acc[cb][0][3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 16 * (c0 + cb) + 4 * kg + e, i = i0 + 8 * p;
+                        if (c >= r || i >= g.D) continue;
+                        float f[8];
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) f[s] = factor * acc[cb][S > 1 ? s : 0][e];
+                        stg16(out + (int64_t)c * g.D + i, vec16<LORA_BF16>::narrow(f));
+                    }
                 }
             }
         }
+    }
+};
+
+// Values j, j + 1 of row c of P, pair i of the matrix, to their place in LDS.
+template <bool F32, int W, bool TALL, typename V> __device__ __forceinline__ void stage_pair(char *s_p, int i, V v) {
+    const int c = i / (8 * W), j = 2 * (i % (8 * W));
+    if constexpr (F32) {
+        double *s = reinterpret_cast<double *>(s_p) + c * (16 * W + 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // tall: products take j = 16 k + 4 kg + s in the order of s, then kg
+            const int jj = j + h;
+            s[TALL ? (jj & ~15) + 4 * (jj & 3) + ((jj >> 2) & 3) : jj] = v[h];
+        }
+    } else {
+        constexpr int LD = (W < 2 ? 32 : 16 * W) + 8;
+        // three bf16 parts carry the value to 2^-27: hi = bf16(f), then what is left
+        uint32_t o[3] = {0u, 0u, 0u};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float f = (float)v[h];
+            const uint32_t hi = f32_to_bf16_bits(f);
+            const float r1 = f - __uint_as_float(hi << 16);
+            const uint32_t mid = f32_to_bf16_bits(r1);
+            o[0] |= (hi & 0xffffu) << (16 * h);
+            o[1] |= (mid & 0xffffu) << (16 * h);
+            o[2] |= (f32_to_bf16_bits(r1 - __uint_as_float(mid << 16)) & 0xffffu) << (16 * h);
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(s_p) + part * 16 * W * LD + c * LD + j) = o[part];
     }
 }
 
@@ -454,38 +637,39 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
     if (item >= (int64_t)g.n * g.blocks) return;
     const int64_t mat = item / g.blocks;
     const int begin = (int)(item - mat * g.blocks) * g.rows, end = min(g.D, begin + g.rows);
-    const double *poly = g.poly + mat * g.r * g.r;
-    const double factor = g.factor[mat];
-    if constexpr (F32) {
-        double *s = reinterpret_cast<double *>(s_p);
-        for (int i = threadIdx.x; i < 16 * W * 16 * W; i += 256) {
-            const int c = i / (16 * W), j = i % (16 * W);
-            // tall: products take j = 16 k + 4 kg + s in the order of s, then kg
-            const int at = TALL ? (j & ~15) + 4 * (j & 3) + ((j >> 2) & 3) : j;
-            s[c * (16 * W + 4) + at] = c < g.r && j < g.r ? poly[c * g.r + j] : 0.0;
-        }
-    } else {
-        uint16_t *s = reinterpret_cast<uint16_t *>(s_p);
-        for (int i = threadIdx.x; i < 16 * W * RP; i += 256) {
-            const int c = i / RP, j = i % RP;
-            // three bf16 parts carry the value to 2^-27: hi = bf16(f), then what is left
-            const float f = c < g.r && j < g.r ? (float)poly[c * g.r + j] : 0.0f;
-            const uint32_t hi = f32_to_bf16_bits(f);
-            const float r1 = f - __uint_as_float(hi << 16);
-            const uint32_t mid = f32_to_bf16_bits(r1);
-            uint16_t *at = s + c * (RP + 8) + j;
-            at[0] = (uint16_t)hi;
-            at[16 * W * (RP + 8)] = (uint16_t)mid;
-            at[2 * 16 * W * (RP + 8)] = (uint16_t)f32_to_bf16_bits(r1 - __uint_as_float(mid << 16));
-        }
-    }
-    __syncthreads();
     const E *in = (const E *)g.g + mat * g.D * g.r;
     E *out = (E *)g.out + mat * g.D * g.r;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i0 = begin + wave * BLOCK; i0 < end; i0 += 4 * BLOCK) {
-        if constexpr (F32) apply_f32<W, TALL>(g, in, out, reinterpret_cast<const double *>(s_p), factor, i0, lane);
-        else apply_bf16<W, TALL>(g, in, out, reinterpret_cast<const uint16_t *>(s_p), (float)factor, i0, lane);
+    typename std::conditional<F32, apply_f32<W, TALL>, apply_bf16<W, TALL>>::type block;
+    int i0 = begin + wave * BLOCK;
+    if (i0 < end) block.load(g, in, i0, lane);            // under way while P is staged
+    const double factor = g.factor[mat];
+    typedef double f64x2_t __attribute__((ext_vector_type(2)));
+    const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(g.poly + mat * 256 * W * W);
+    constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 * 8 ? PAIRS / 256 : 8;
+    if constexpr (W == 1) {
+        if (threadIdx.x < PAIRS) stage_pair<F32, W, TALL>(s_p, threadIdx.x, poly[threadIdx.x]);
+        if (!F32 && threadIdx.x < 16) {                   // the products' k 16..31
+            uint16_t *s = reinterpret_cast<uint16_t *>(s_p) + threadIdx.x * (RP + 8) + 16;
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4 *>(s + part * 16 * W * (RP + 8) + 8 * h) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    } else {
+        for (int i = threadIdx.x; i < PAIRS; i += 256 * STEP) {
+            f64x2_t v[STEP];
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) v[u] = poly[i + 256 * u];
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) stage_pair<F32, W, TALL>(s_p, i + 256 * u, v[u]);
+        }
+    }
+    __syncthreads();
+    for (; i0 < end; i0 += 4 * BLOCK) {
+        if constexpr (F32) block.store(g, out, reinterpret_cast<const double *>(s_p), factor, i0, lane);
+        else block.store(g, out, reinterpret_cast<const uint16_t *>(s_p), factor, i0, lane);
+        if (i0 + 4 * BLOCK < end) block.load(g, in, i0 + 4 * BLOCK, lane);
     }
 }
 
@@ -500,15 +684,16 @@ static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
     L.r = rows < cols ? rows : cols;
     L.D = rows < cols ? cols : rows;
     L.W = L.r <= 16 ? 1 : L.r <= 32 ? 2 : L.r <= 64 ? 4 : 8;
-    // about two workgroups a CU over all matrices, of at least 256 indices
-    int splits = ceil_div(512, n > 0 ? n : 1);
+    // about a workgroup a CU over all matrices, of at least 256 indices (two of half the
+    // wavefronts: twice the sums for k_ortho_poly to read, 32 x 4096 x 16 17.6 us for 15.9)
+    int splits = ceil_div(256, n > 0 ? n : 1);
     if (splits > 32) splits = 32;
     if (splits > ceil_div(L.D, 256)) splits = ceil_div(L.D, 256);
     L.chunk = ceil_div(ceil_div(L.D, splits), 64) * 64;
     L.splits = ceil_div(L.D, L.chunk);
     size_t o = 0;
     L.part = o;   o = align256(o + (size_t)n * L.splits * ortho_tiles(L.W) * 256 * 8);
-    L.poly = o;   o = align256(o + (size_t)n * L.r * L.r * 8);
+    L.poly = o;   o = align256(o + (size_t)n * 256 * L.W * L.W * 8);
     L.factor = o; o = align256(o + (size_t)n * 8);
     L.total = o;
     return L;
@@ -517,8 +702,10 @@ static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
 size_t ortho_workspace_bytes(int32_t n, int32_t rows, int32_t cols) { return make_ortho_layout(n, rows, cols).total; }
 
 template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, hipStream_t s) {
-    hipLaunchKernelGGL((k_ortho_gram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits), dim3(256), 0, s, g);
-    hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
+    hipLaunchKernelGGL((k_ortho_gram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits), dim3(gram_cfg<W>::WAVES * 64), 0, s, g);
+    if constexpr (W == 1) hipLaunchKernelGGL(k_ortho_poly1<TALL>, grid_of(g.n), dim3(64), 0, s, g);
+    else if constexpr (W == 8) hipLaunchKernelGGL(k_ortho_poly8<TALL>, grid_of(g.n), dim3(768), 0, s, g);
+    else hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
     // about three workgroups a CU, of whole rounds of their wavefronts' blocks
     constexpr int ROUND = 4 * (TALL ? 16 : DT == LORA_F32 ? 64 : 128);
     int blocks = ceil_div(768, g.n);
