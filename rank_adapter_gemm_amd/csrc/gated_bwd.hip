@@ -9,9 +9,10 @@
 // atomics: results repeat bitwise.
 //
 // And of the linear layer y = act(p) + residual, p = x W + s_a (x A_a) B_a + bias:
-//   dp = dy * act'(p),  dbias = sum of dp          k_act_grad, k_column_sums
+//   dp = dy * act'(p),  dbias = sum of dp          k_act_grad, k_rank_finish
 // and the same kernels for the one projection (NM, the number of projections, 1).
 #include "gated_common.hpp"
+#include "norm_common.hpp"
 
 namespace lora {
 
@@ -319,8 +320,8 @@ __device__ __forceinline__ void a_octets(const a_octets_args &g, const pair_pool
 // the bf16 gradients they add up to).  Places past a segment's rows are
 // filled with zeros.  A workgroup: 32 positions of one work block and 8 ranks
 // (blockIdx.y), or 32 rows of the base block (grid.x from n_work on), or, from
-// first_octet on, A's octets, in the same launch because neither alone keeps
-// the chip busy.  2048 rows: 7 us, latency.
+// first_octet on, A's octets, and from first_sum on, dbias, in the same launch
+// because none alone keeps the chip busy.  2048 rows: 7 us, latency.
 struct rank_finish_args {
     const float *v, *part;
     int32_t n_split, T, R, R2, n_slots, n_work, Tp;
@@ -328,13 +329,21 @@ struct rank_finish_args {
     float *dv;
     uint16_t *vt;
     int32_t *slot_blk;                 // [n_slots]: a segment's first work block, by its slot
-    int32_t first_octet;
+    int32_t first_octet, first_sum;    // first_sum on: the columns of bias_part [stretches][F], 64 a workgroup
+    const float *bias_part;
+    int32_t stretches, F;
+    uint16_t *dbias;
 };
 
 template <int NM>
 __global__ void __launch_bounds__(256) k_rank_finish(rank_finish_args g, a_octets_args oc, pair_pools pp) {
     constexpr int BR = kShrinkRows;
     const int R2 = NM > 1 ? NM * g.R : g.R2;
+    if (NM == 1 && (int)blockIdx.x >= g.first_sum) {
+        if (blockIdx.y == 0)
+            column_sums<LORA_BF16>(g.bias_part, g.stretches, g.F, g.F, g.dbias, nullptr, (int)blockIdx.x - g.first_sum);
+        return;
+    }
     if ((int)blockIdx.x >= g.first_octet) {
         const int item = (int)blockIdx.x - g.first_octet;
         a_octets<NM>(oc, pp, item / oc.k_blocks, item % oc.k_blocks, blockIdx.y);
@@ -643,7 +652,7 @@ static void launch_nt_cfg(gemm_args g, const nt_args &nt, const gemm_plan &pl, h
 // not fill the chip with the largest tiles splits it over K rather than take
 // smaller tiles (2048 x 28672 x 4096: 128 tiles in two pieces each against
 // 256 tiles of 256 x 128).
-static gemm_plan plan_dx(int T, int K, int N, size_t partial_bytes) {
+static gemm_plan plan_dx(int T, int K, int N, size_t partial_bytes, bool pair) {
     const int tiles = ceil_div(T, 256) * ceil_div(N, 256);
     if (tiles < 208 && K >= 8192 && T >= 256) {
         int splits = 256 / tiles;
@@ -654,7 +663,7 @@ static gemm_plan plan_dx(int T, int K, int N, size_t partial_bytes) {
             return gemm_plan{256, 256, 0, tiles, ceil_div(K, kc), kc};
         }
     }
-    return plan_gemm(T, K, N, partial_bytes);
+    return pair ? plan_gemm(T, K, N, partial_bytes) : plan_linear(T, K, N, partial_bytes, 2, 64);
 }
 
 // ---------------------------------------------------------------------------
@@ -1136,6 +1145,7 @@ static int32_t act_grad_rows(int32_t T, int32_t N, int32_t dtype) {
     return ceil_div(rows, kActStrands) * kActStrands;
 }
 
+// (dbias, bf16: k_rank_finish adds up the stretches.)
 template <int DT> static lora_status_t launch_act_grad(act_grad_args &g, void *dbias, hipStream_t s) {
     const bool write = g.act != LORA_ACT_NONE;
     if (!write && !dbias) return LORA_OK;
@@ -1146,7 +1156,8 @@ template <int DT> static lora_status_t launch_act_grad(act_grad_args &g, void *d
     else if (write) hipLaunchKernelGGL((k_act_grad<DT, true, false>), grid, dim3(256), 0, s, g);
     else hipLaunchKernelGGL((k_act_grad<DT, false, true>), grid, dim3(256), 0, s, g);
     const lora_status_t st = hip_status(hipGetLastError());
-    return st == LORA_OK && dbias ? launch_column_sums(g.part, stretches, g.N, g.N, DT, dbias, nullptr, s) : st;
+    return st == LORA_OK && dbias && DT == LORA_F32 ? launch_column_sums(g.part, stretches, g.N, g.N, DT, dbias, nullptr, s)
+                                                    : st;
 }
 
 // ---------------------------------------------------------------------------
@@ -1196,7 +1207,7 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
     const ws_layout &L = B.L;
     void *ws = c.ws;
     // k_rank_finish has its workgroups in one grid dimension, which holds fewer than 2^32 threads
-    const int64_t finish = 2 * ceil_div(T, kShrinkRows) + (S < T ? S : T) * (1ll + (c.dx ? ceil_div(K, 256) : 0));
+    const int64_t finish = 2 * ceil_div(T, kShrinkRows) + (S < T ? S : T) * (1ll + (c.dx ? ceil_div(K, 256) : 0)) + (c.dbias ? ceil_div(F, 64) : 0);
     if (DT == LORA_BF16 && finish * 256 >= 1ll << 32) return LORA_ERR_UNSUPPORTED;
     lora_status_t st = launch_segments(c.ids, T, S, L, ws, s, 1);
     if (st != LORA_OK) return st;
@@ -1252,12 +1263,14 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
         }
 #undef LORA_RANK_GRAD
         const int first_octet = n_work + row_blocks;
-        const rank_finish_args f{v, part, split, T, R, R2, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
-                                 g.blk_start, g.blk_seg, dv, vt, slot_blk, first_octet};
         const a_octets_args oc{g.seg_id, g.n_seg, S, K, R, R2, ceil_div(K, 256), ws_ptr<uint16_t>(ws, B.oct),
                                ws_ptr<int32_t>(ws, B.row0), ws_ptr<int32_t>(ws, B.rank), ws_ptr<float>(ws, B.scale)};
-        const int octets = c.dx ? (S < T ? S : T) * oc.k_blocks : 0;
-        hipLaunchKernelGGL(k_rank_finish<NM>, dim3(first_octet + octets, R2 / 8), dim3(256), 0, s, f, oc, pp);
+        const int octets = c.dx ? (S < T ? S : T) * oc.k_blocks : 0, sums = c.dbias ? ceil_div(F, 64) : 0;
+        const int stretches = NM > 1 ? 0 : ceil_div(T, act_grad_rows(T, F, DT));
+        const rank_finish_args f{v, part, split, T, R, R2, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
+                                 g.blk_start, g.blk_seg, dv, vt, slot_blk, first_octet, first_octet + octets,
+                                 ws_ptr<float>(ws, B.sums), stretches, F, (uint16_t *)c.dbias};
+        hipLaunchKernelGGL(k_rank_finish<NM>, dim3(first_octet + octets + sums, R2 / 8), dim3(256), 0, s, f, oc, pp);
     }
     if constexpr (DT == LORA_F32) {
         dx_f32_args g{(const float *)dg, (const float *)du, (const float *)c.W[0], (const float *)c.W[NM - 1],
@@ -1296,7 +1309,7 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
         g.v = dv;
         g.v_stride = R2;
         g.partial = ws_ptr<float>(ws, B.partial);
-        const gemm_plan pl = plan_dx(T, g.K, g.N, c.ws_bytes - B.partial);
+        const gemm_plan pl = plan_dx(T, g.K, g.N, c.ws_bytes - B.partial, NM > 1);
         g.n_tiles_m = ceil_div(T, pl.bm);
         g.n_tiles_n = ceil_div(g.N, pl.bn);
         g.col_strips = col_strips_pay(T, g.N, g.n_tiles_n);

@@ -45,4 +45,33 @@ __device__ __forceinline__ uint2 codes_of(const float *yr, float inv) {
                       e4m3x4(yr[4] * inv, yr[5] * inv, yr[6] * inv, yr[7] * inv));
 }
 
+// Columns of part [groups][n] added up, in order within each of 16 strands and
+// then over the strands: 64 columns a workgroup, 4 a thread.  The first d
+// columns go to out0, the rest to out1 (either may be null), in type DT.
+template <int DT>
+__device__ __forceinline__ void column_sums(const float *part, int32_t groups, int32_t n, int32_t d,
+                                            typename elem<DT>::T *out0, typename elem<DT>::T *out1, int block) {
+    __shared__ float s[16][64];
+    const int strand = threadIdx.x >> 4, c0 = block * 64, c = c0 + (threadIdx.x & 15) * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < n)
+#pragma unroll 8
+        for (int g = strand; g < groups; g += 16) {
+            const float4 f = *reinterpret_cast<const float4 *>(part + (int64_t)g * n + c);
+            sum.x += f.x;
+            sum.y += f.y;
+            sum.z += f.z;
+            sum.w += f.w;
+        }
+    *reinterpret_cast<float4 *>(&s[strand][(threadIdx.x & 15) * 4]) = sum;
+    __syncthreads();
+    const int col = c0 + (int)threadIdx.x;
+    if (threadIdx.x >= 64 || col >= n) return;
+    float f = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f += s[i][threadIdx.x];
+    typename elem<DT>::T *out = col < d ? out0 : out1;
+    if (out) elem<DT>::store(out, col < d ? col : col - d, f);
+}
+
 }  // namespace lora
