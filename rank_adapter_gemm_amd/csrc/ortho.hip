@@ -8,6 +8,7 @@
 // commute, and the last X is G times one r x r matrix P:
 //   k_ortho_gram    G^T G, split over the long side                 one read of G
 //   k_ortho_poly    the pieces' sum, and the steps on r x r         a workgroup a matrix
+//                   (r <= 16: k_ortho_apply does it)
 //   k_ortho_apply   G P                                     one more read, one write
 //
 // 64 bits: small singular values are amplified, by c0 at every step (485-fold in 5
@@ -234,20 +235,19 @@ template <int NT> __device__ __forceinline__ f64x4_t poly_part(const ortho_args 
     return m;
 }
 
-// One tile: a wavefront a matrix, no LDS.
-template <bool TALL> __global__ void __launch_bounds__(64) k_ortho_poly1(ortho_args g) {
-    const int64_t mat = grid_index();
-    if (mat >= g.n) return;
-    const int lane = threadIdx.x, p = lane & 15;
+// One tile: P in a wavefront's registers, and scale / (|G| + eps).  Few enough
+// products for k_ortho_apply to do them itself, every workgroup of a matrix the
+// same (as a launch of its own: 32 x 4096 x 16 15.9 us for 14.5).
+__device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, int lane, double &factor) {
     f64x4_t m = poly_part<1>(g, mat, 0, lane), one, pr;
     double d = 0.0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        one[e] = mfma64_row(e, lane) == p ? 1.0 : 0.0;
+        one[e] = mfma64_row(e, lane) == (lane & 15) ? 1.0 : 0.0;
         d += one[e] * m[e];
     }
     const double inv = 1.0 / (sqrt(wave_sum64(d)) + (double)g.eps);
-    if (lane == 0) g.factor[mat] = (double)g.scale * inv;
+    factor = (double)g.scale * inv;
     const f64x4_t zero = {0.0, 0.0, 0.0, 0.0};
     m *= inv * inv;
     pr = one;
@@ -258,7 +258,7 @@ template <bool TALL> __global__ void __launch_bounds__(64) k_ortho_poly1(ortho_a
         pr = step == 0 ? q : mfma64_tile(pr, q, zero);
         m = mfma64_tile(t, q, zero);
     }
-    poly_store<1, TALL>(g, mat, 0, 0, pr, lane);
+    return pr;
 }
 
 // 2 or 4 tiles a side.  A step is three rounds with a barrier each: M M and from it
@@ -643,20 +643,36 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
     typename std::conditional<F32, apply_f32<W, TALL>, apply_bf16<W, TALL>>::type block;
     int i0 = begin + wave * BLOCK;
     if (i0 < end) block.load(g, in, i0, lane);            // under way while P is staged
-    const double factor = g.factor[mat];
+    double factor;
     typedef double f64x2_t __attribute__((ext_vector_type(2)));
-    const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(g.poly + mat * 256 * W * W);
-    constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 * 8 ? PAIRS / 256 : 8;
     if constexpr (W == 1) {
-        if (threadIdx.x < PAIRS) stage_pair<F32, W, TALL>(s_p, threadIdx.x, poly[threadIdx.x]);
+        __shared__ __attribute__((aligned(16))) double s_tile[256];
+        __shared__ double s_factor;
+        if (wave == 0) {
+            const f64x4_t pr = poly_one(g, mat, lane, factor);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = mfma64_row(e, lane), j = lane & 15;
+                s_tile[16 * i + j] = i < g.r && j < g.r ? pr[e] : 0.0;
+            }
+            if (lane == 0) s_factor = factor;
+        }
+        __syncthreads();
+        factor = s_factor;
+        if (threadIdx.x < 128)
+            stage_pair<F32, W, TALL>(s_p, threadIdx.x, reinterpret_cast<const f64x2_t *>(s_tile)[threadIdx.x]);
         if (!F32 && threadIdx.x < 16) {                   // the products' k 16..31
             uint16_t *s = reinterpret_cast<uint16_t *>(s_p) + threadIdx.x * (RP + 8) + 16;
 #pragma unroll
             for (int part = 0; part < 3; ++part)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4 *>(s + part * 16 * W * (RP + 8) + 8 * h) = make_uint4(0u, 0u, 0u, 0u);
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<uint4 *>(s + part * 16 * W * (RP + 8) + 8 * h) = make_uint4(0u, 0u, 0u, 0u);
         }
     } else {
+        factor = g.factor[mat];
+        const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(g.poly + mat * 256 * W * W);
+        constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 * 8 ? PAIRS / 256 : 8;
         for (int i = threadIdx.x; i < PAIRS; i += 256 * STEP) {
             f64x2_t v[STEP];
 #pragma unroll
@@ -703,12 +719,11 @@ size_t ortho_workspace_bytes(int32_t n, int32_t rows, int32_t cols) { return mak
 
 template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, hipStream_t s) {
     hipLaunchKernelGGL((k_ortho_gram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits), dim3(gram_cfg<W>::WAVES * 64), 0, s, g);
-    if constexpr (W == 1) hipLaunchKernelGGL(k_ortho_poly1<TALL>, grid_of(g.n), dim3(64), 0, s, g);
-    else if constexpr (W == 8) hipLaunchKernelGGL(k_ortho_poly8<TALL>, grid_of(g.n), dim3(768), 0, s, g);
-    else hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
-    // about three workgroups a CU, of whole rounds of their wavefronts' blocks
+    if constexpr (W == 8) hipLaunchKernelGGL(k_ortho_poly8<TALL>, grid_of(g.n), dim3(768), 0, s, g);
+    else if constexpr (W > 1) hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
+    // about three workgroups a CU (two where each makes P), of whole rounds of their wavefronts' blocks
     constexpr int ROUND = 4 * (TALL ? 16 : DT == LORA_F32 ? 64 : 128);
-    int blocks = ceil_div(768, g.n);
+    int blocks = ceil_div(W == 1 ? 512 : 768, g.n);
     if (blocks > ceil_div(g.D, ROUND)) blocks = ceil_div(g.D, ROUND);
     g.rows = ceil_div(ceil_div(g.D, blocks), ROUND) * ROUND;
     g.blocks = ceil_div(g.D, g.rows);
