@@ -457,13 +457,14 @@ template <int W, bool TALL> struct apply_f32 {
     f32x4_t x[R4];
 
     __device__ __forceinline__ void load(const ortho_args &g, const float *in, int i0, int lane) {
-            const int p = lane & 15, kg = lane >> 4, r = g.r;
+        const int p = lane & 15, kg = lane >> 4, r = g.r;
 #pragma unroll
         for (int k = 0; k < R4; ++k) {
             // tall: j = 16 k + 4 kg + (0..3) of row i0 + p; wide: row j = 4 k + kg, columns i0 + 4 p + (0..3)
             const int j = TALL ? 16 * k + 4 * kg : 4 * k + kg, i = TALL ? i0 + p : i0 + 4 * p;
             x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            if (j < r && i < g.D) x[k] = *reinterpret_cast<const f32x4_t *>(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
+            if (j < r && i < g.D)
+                x[k] = *reinterpret_cast<const f32x4_t *>(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
         }
     }
 
@@ -505,7 +506,8 @@ template <int W, bool TALL> struct apply_f32 {
                         if (c < r && i < g.D)
                             *reinterpret_cast<f32x4_t *>(out + (int64_t)c * g.D + i) =
                                 f32x4_t{(float)(factor * acc[cb][0][e]), (float)(factor * acc[cb][S > 1 ? 1 : 0][e]),
-                                        (float)(factor * acc[cb][S > 2 ? 2 : 0][e]), (float)(factor * acc[cb][S > 3 ? 3 : 0][e])};
+                                        (float)(factor * acc[cb][S > 2 ? 2 : 0][e]),
+                                        (float)(factor * acc[cb][S > 3 ? 3 : 0][e])};
                     }
                 }
             }
@@ -519,7 +521,8 @@ template <int W, bool TALL> struct apply_f32 {
 // lane reads 8 neighbouring columns of each of 8 rows j, and exchanges rows for
 // columns in its registers.
 template <int W, bool TALL> struct apply_bf16 {
-    static constexpr int RP = W < 2 ? 32 : 16 * W, LD = RP + 8, PART = 16 * W * LD, KT = RP / 32, CB = W < 2 ? W : 2, S = TALL ? 1 : 8;
+    static constexpr int RP = W < 2 ? 32 : 16 * W, LD = RP + 8, PART = 16 * W * LD, KT = RP / 32;
+    static constexpr int CB = W < 2 ? W : 2, S = TALL ? 1 : 8;
     uint4 x[KT][S];
 
     __device__ __forceinline__ void load(const ortho_args &g, const uint16_t *in, int i0, int lane) {

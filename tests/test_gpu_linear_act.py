@@ -46,6 +46,20 @@ def test_bf16(T, d, f):
         assert L.lora_get_device_error(got[2].buf) == p.bad_row()
 
 
+# grids of few tiles: K ranges in whole rounds of workgroups (two of 112 tiles, three of 80, one of 224), and tiles of
+# 64 columns where K is too short for ranges
+@pytest.mark.parametrize("T,d,f", [(100, 1040, 14336), (65, 1288, 10240), (192, 520, 14336), (127, 264, 14328)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_grids_of_few_tiles(T, d, f, fp8):
+    d = d // 16 * 16 if fp8 else d
+    p = Layer(T, d, f, RANKS, 16, BF16, seed=T + d)
+    parts, base, extra = p.fp8() if fp8 else (None, None, 0.0)
+    for mode in MODES[1:]:
+        got = run_forward(p, "gelu_tanh", mode, keep=True, fp8=parts)
+        check(p, "gelu_tanh", got, "mode %d" % mode, base=base, extra=extra)
+        assert L.lora_get_device_error(got[2].buf) == p.bad_row()
+
+
 @pytest.mark.parametrize("T,d,f", [(1, 64, 8), (5, 136, 72), (64, 256, 264), (130, 1032, 136), (333, 64, 520),
                                    (900, 264, 2056)])
 @pytest.mark.parametrize("act", list(ACTS))

@@ -52,6 +52,14 @@ def test_bf16(T, d, f, act):
     assert L.lora_get_device_error(got[4].buf) == p.bad_row()
 
 
+@pytest.mark.parametrize("T,d,f", [(777, 1048, 1032), (129, 2056, 1288), (500, 4096, 520)])
+def test_ranges_of_the_sum_in_whole_rounds(T, d, f):
+    for act in ("none", "gelu"):
+        p = Layer(T, d, f, RANKS, 16, BF16, seed=T + d)
+        k = kept(p)
+        check(p, act, *k, run_backward(p, act, *k), "bf16")
+
+
 @pytest.mark.parametrize("T,d,f", [(1, 64, 8), (5, 136, 72), (64, 264, 256), (130, 136, 1032), (333, 520, 64),
                                    (700, 264, 520)])
 @pytest.mark.parametrize("act", list(ACTS))

@@ -101,6 +101,22 @@ def test_ranks_past_a_matrix_s_own_and_zero_matrices_stay_zero(wide, dtype):
         assert not (out[i, k:] if wide else out[i, :, k:]).any()
 
 
+@pytest.mark.parametrize("r", [8, 24, 64, 120])
+@pytest.mark.parametrize("count", [1, 2])
+def test_one_and_two_steps(r, count):
+    for dtype, wide in ((BF16, False), (F32, True)):
+        g = gradients(2, r if wide else 392, 392 if wide else r, dtype, seed=7)
+        check(run(g, USUAL[:count]), g, USUAL[:count])
+
+
+@pytest.mark.parametrize("n,D", [(300, 264), (1, 100000), (513, 24)])
+def test_many_matrices_and_long_ones_of_one_tile(n, D):
+    for dtype, wide in ((BF16, False), (BF16, True), (F32, True)):
+        g = gradients(n, 16 if wide else D, D if wide else 16, dtype, seed=8)
+        out, some = run(g), sorted({0, n // 3, n - 1})
+        check(out[some], g[some])
+
+
 @pytest.mark.parametrize("coef,scale", [([(1.0, 0.0, 0.0)], 1.0), ([(1.5, -0.5, 0.0)] * 9, 0.25),
                                         ([(2.0, -1.5, 0.5)] * 3, -3.0), ([(3.4445, -4.775, 2.0315), (1.5, -0.5, 0.0)], 2.0)])
 def test_other_coefficients_and_counts(coef, scale):
