@@ -138,7 +138,10 @@ __device__ __forceinline__ void shrink_row(const typename elem<DT>::T *x, int32_
 
 // The store of a whole tile: the fp32 sums of WR * 32 rows at a time go through
 // LDS, where the terms that are not in them yet are added; a thread then owns 8
-// neighbouring columns of one row (16-byte loads and stores, one rounding).
+// neighbouring columns of one row (16-byte loads and stores, one rounding).  FP8,
+// 192 rows of 64 adapters, 4096 x 14336: 43 us, of which the rows' terms are 12 (0.5
+// MB of B a tile beside 0.9 MB of operands, at 33 KB / us into a CU; asked for
+// further ahead they take the same).
 template <int BM, int BN, int WV, int WR, int RB, int CB>
 __device__ __forceinline__ void act_store_tile(const gemm_args &g, f32x16_t (&acc)[RB][CB], float *smem_f,
                                                const int32_t *s_t, const int32_t *s_id, const row_term *s_term,

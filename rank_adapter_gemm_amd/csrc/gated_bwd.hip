@@ -1073,6 +1073,8 @@ __global__ void __launch_bounds__(256) k_zero16(uint4 *p, int64_t n) {
 // dbias.  A workgroup takes 32 vectors of columns and a stretch of rows, every
 // eighth of them a thread; the 8 strands are added through LDS to one partial sum
 // per column and stretch.  WRITE = false: dp is dy itself, only its sums are made.
+// 2048 x 4096: 5 us without dp; 777 x 2744 through GELU: 11 us, the activation's
+// slope and latency.
 // ---------------------------------------------------------------------------
 constexpr int kActVecs = 32, kActStrands = 8;
 

@@ -755,11 +755,12 @@ inline gemm_plan plan_gemm(int T, int K, int N, size_t partial_bytes, int kgran 
 
 // The layer with an epilogue.  plan_gemm, whose sums the plain layer keeps,
 // gives a small grid whole tiles of 64 columns or the first split past one
-// workgroup per CU, often a second round of few; here the split is the one with the least estimated time: rounds
-// of 256 workgroups (one per CU: their stages fill LDS) at the rate at which
-// one takes its operands (K step bytes of a tile at about 25 KB / us), and the
-// partial sums written and read back at 4 TB/s.  100 rows, 4096 x 14336: bf16
-// 85 -> 55 us, FP8 62 -> 41 (2 ranges for 224 whole tiles).
+// workgroup per CU, often a second round of few; here the split is the one with
+// the least estimated time: rounds of 256 workgroups (one per CU: their stages
+// fill LDS) at the rate at which one takes its operands (a tile's bytes at about
+// 25 KB / us), and the partial sums written and read back at 4 TB/s.  100 rows,
+// 4096 x 14336: bf16 55 us (2 ranges; 224 whole tiles of 64 columns 85), FP8 41
+// (62); dx of 777 rows, 1048 x 2744: 17 us (4 ranges; 5 in two rounds 23).
 inline gemm_plan plan_linear(int T, int K, int N, size_t partial_bytes, int elem_bytes, int kgran) {
     const gemm_plan whole = plan_gemm(T, K, N, partial_bytes, kgran);
     if (whole.n_dp > 0 && whole.bn > 64) return whole;

@@ -282,6 +282,10 @@ static int linear_f32_splits(int tiles, int K, size_t partial_bytes, int &k_chun
 // step by step, and add their sums through LDS; the K ranges' sums go to the
 // partial buffer, and k_few_finish finishes them.  The first workgroups compute
 // the rank vectors v = x A meanwhile, which only that second launch reads.
+//
+// One row, 14336 x 4096 (117 MB of W): 21 us, 5.6 TB/s, and 4 us for the second
+// launch; a call 29 us.  4096 x 14336: 1 row 29 us, 64 rows 44; through LDS, by the
+// tiles of the base GEMM, 70 and 80.
 // ---------------------------------------------------------------------------
 template <int MT, int WV>
 __global__ void __launch_bounds__(WV * 64, WV == 4 ? 2 : 1) k_linear_few(gemm_args g, int32_t n_shrink) {
@@ -385,7 +389,8 @@ __global__ void __launch_bounds__(WV * 64, WV == 4 ? 2 : 1) k_linear_few(gemm_ar
 // The same on an FP8 base weight: 64 columns and 128 codes of k a wavefront and step;
 // rows of wq and of xq lie along k, so a lane reads 32 codes of each of 4 columns and of
 // each 16 rows as v_mfma_scale_f32_16x16x128_f8f6f4 takes them (lane l: A row and B
-// column l % 16, k = 32 (l / 16) + 0..31, and their E8M0 scales).
+// column l % 16, k = 32 (l / 16) + 0..31, and their E8M0 scales).  4096 x 14336: 1
+// row 19 us (35 by tiles), 16 rows 24, 32 rows 30.
 typedef int few_i32x8_t __attribute__((ext_vector_type(8)));
 
 template <int MT, int WV>
