@@ -416,17 +416,21 @@ __device__ __forceinline__ bool term_in_reduction(const gemm_args &g, const nt_a
     return (int64_t)*nt.n_seg * 64 > g.T;
 }
 
+template <int BM, int BN, int NS, int WV, int WR> constexpr int nt_lds() {          // bytes
+    constexpr int STAGES = NS * (BM + BN) * 64 * 2, EPI = WV * 32 * (BN / (WV / WR) + 4) * 4;
+    return STAGES > EPI ? STAGES : EPI;
+}
+
+// Workgroup `block` of `blocks`; smem: nt_lds bytes.
 template <int BM, int BN, int NS, bool SPLIT, int WV, int WR>
-__global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
+__device__ __forceinline__ void gemm_nt(const gemm_args &g, const nt_args &nt, uint16_t *smem, int block, int blocks) {
     constexpr int BK = 64, CH = BK / 8, WM = BM / WR, WN = BN / (WV / WR), RB = WM / 32, CB = WN / 32;
     constexpr int XSTAGE = BM * BK, STAGE = XSTAGE + BN * BK;
     constexpr int XI = BM * CH / (64 * WV), WI = BN * CH / (64 * WV);
-    constexpr int EPI = WV * 32 * (WN + 4) * 4, LDS = NS * STAGE * 2 > EPI ? NS * STAGE * 2 : EPI;
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[LDS / 2];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int wm = w / (WV / WR), wn = w % (WV / WR);
     int tm, tn, split, tidx;
-    tile_of(blockIdx.x, gridDim.x, g, tm, tn, split, tidx);
+    tile_of(block, blocks, g, tm, tn, split, tidx);
     const int m0 = tm * BM, n0 = tn * BN;
     const int N = g.N, T = g.T, F = nt.F;
     const int k_begin = SPLIT ? split * g.k_chunk : 0;
@@ -564,6 +568,12 @@ __global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
     __syncthreads();
     gemm_store_tile<BM, BN, WV, WR, SPLIT, false>(g, acc, reinterpret_cast<float *>(smem), s_meta_t, n0, w, lane,
                                                   tidx, split);
+}
+
+template <int BM, int BN, int NS, bool SPLIT, int WV, int WR>
+__global__ void __launch_bounds__(WV * 64) k_gemm_nt(gemm_args g, nt_args nt) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[nt_lds<BM, BN, NS, WV, WR>() / 2];
+    gemm_nt<BM, BN, NS, SPLIT, WV, WR>(g, nt, smem, blockIdx.x, gridDim.x);
 }
 
 // The pieces' sums in split order; a thread owns 8 columns of one row.
@@ -920,10 +930,10 @@ template <int MB, int QP>
 __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *smem, int32_t *s_row,
                                               const seg_outer_args &g,
                                               const uint16_t *q, int64_t q_lo, int N, int n0, const uint16_t *vt, int nj,
-                                              int p0, int p1, int64_t b0) {
+                                              int p0, int p1, int64_t b0, int tid) {
     typedef outer_cfg<MB, QP> C;
     constexpr int BT = C::BT, NS = C::NS, QI = C::QI, PI = C::PI, PER = QP * QI + PI;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int lane = tid & 63, wave = tid >> 6;
     auto dma_stage = [&](int kt, int buf) {
         uint16_t *qs = smem + buf * C::STAGE, *ps = qs + QP * C::QST;
 #pragma unroll
@@ -1001,20 +1011,27 @@ __device__ __forceinline__ void seg_outer_sum(f32x16_t (&acc)[MB], uint16_t *sme
     }
 }
 
-template <int MBA, int MBB, int NM, int PARTS>
-__global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
+template <int MBA, int MBB, int PARTS> constexpr int outer_lds() {                  // values
     constexpr int LA = outer_cfg<MBA, 1>::NS * outer_cfg<MBA, 1>::STAGE;
     constexpr int LB = outer_cfg<MBB, PARTS>::NS * outer_cfg<MBB, PARTS>::STAGE;
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[LA > LB ? LA : LB];
-    __shared__ int32_t s_row[kOuterRows];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t wg = grid_index(), n_a = (int64_t)g.n_slots * g.tiles_k;
+    return LA > LB ? LA : LB;
+}
+
+// Item `wg`, by 256 threads (tid); of a workgroup with twice as many, each half
+// takes one of two neighbouring tiles of one slot (a tile past the last stores
+// nothing), so that all its wavefronts meet at the same barriers.
+template <int MBA, int MBB, int NM, int PARTS, int HALVES>
+__device__ __forceinline__ void seg_outer(const seg_outer_args &g, uint16_t *smem, int32_t *s_row, int64_t wg, int half,
+                                          int tid) {
+    const int lane = tid & 63, wave = tid >> 6;
+    const int tiles_a = (g.tiles_k + HALVES - 1) / HALVES;
+    const int64_t n_a = (int64_t)g.n_slots * tiles_a;
     const bool is_a = wg < n_a;
     int item = (int)(is_a ? wg : wg - n_a);
-    const int tiles = is_a ? g.tiles_k : NM * g.tiles_n;
+    const int tiles = is_a ? tiles_a : (NM * g.tiles_n + HALVES - 1) / HALVES;
     const int slot = item / tiles;
     if (slot >= g.n_slots) return;
-    item -= slot * tiles;
+    item = (item - slot * tiles) * HALVES + half;
     const int m = NM > 1 && !is_a && item >= g.tiles_n, tile = item - m * g.tiles_n;
     const int n0 = tile * kOuterCols, N = is_a ? g.K : g.N;
     const int p0 = max(g.offsets[slot + 1], 0), p1 = min(g.offsets[slot + 2], g.T);
@@ -1028,7 +1045,7 @@ __global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
         for (int mb = 0; mb < MBA; ++mb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
-        seg_outer_sum<MBA, 1>(acc, smem, s_row, g, g.x, 0, N, n0, g.vt + (int64_t)2 * g.R2 * g.Tp, NM * R, p0, p1, b0);
+        seg_outer_sum<MBA, 1>(acc, smem, s_row, g, g.x, 0, N, n0, g.vt + (int64_t)2 * g.R2 * g.Tp, NM * R, p0, p1, b0, tid);
         if (col >= N) return;
         // [slot][k][j]: a lane's accumulators hold groups of 4 neighbouring ranks of its k
 #pragma unroll
@@ -1051,7 +1068,7 @@ __global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[mb][e] = 0.0f;
         seg_outer_sum<MBB, PARTS>(acc, smem, s_row, g, g.dy + (int64_t)m * g.T * N, (int64_t)NM * g.T * N, N, n0,
-                              g.vt + (int64_t)m * R * g.Tp, R, p0, p1, b0);
+                              g.vt + (int64_t)m * R * g.Tp, R, p0, p1, b0, tid);
         if (col >= N) return;
         uint16_t *out = (m ? g.dB[1] : g.dB[0]) + (int64_t)slot * R * N + col;
 #pragma unroll
@@ -1062,6 +1079,42 @@ __global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
                 if (j < R) out[(int64_t)j * N] = j < rk[m] ? (uint16_t)f32_to_bf16_bits(acc[mb][e]) : (uint16_t)0;
             }
     }
+}
+
+template <int MBA, int MBB, int NM, int PARTS>
+__global__ void __launch_bounds__(256) k_seg_outer_mfma(seg_outer_args g) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[outer_lds<MBA, MBB, PARTS>()];
+    __shared__ int32_t s_row[kOuterRows];
+    seg_outer<MBA, MBB, NM, PARTS, 1>(g, smem, s_row, grid_index(), 0, threadIdx.x);
+}
+
+// dx's whole tiles of 256 x 256 (the first n_dx workgroups), and the adapters'
+// gradients on the CUs that the last round of tiles leaves idle: ranks up to 32, of
+// which two tiles fit the stages' LDS.  2048 rows of 4 adapters, 14336 x 4096, 448
+// tiles: 260 us (one after the other 258 and 23).
+template <int PARTS> __global__ void __launch_bounds__(512) k_nt_outer(gemm_args g, nt_args nt, seg_outer_args o, int32_t n_dx) {
+    constexpr int LDS = nt_lds<256, 256, 2, 8, 2>(), OUT = outer_lds<1, 1, PARTS>();
+    static_assert(2 * (OUT * 2 + kOuterRows * 4) <= LDS, "two tiles of the gradients fit");
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[LDS / 2];
+    if ((int)blockIdx.x < n_dx) {
+        gemm_nt<256, 256, 2, false, 8, 2>(g, nt, smem, blockIdx.x, n_dx);
+    } else {
+        const int half = uniform_i(threadIdx.x >> 8);
+        seg_outer<1, 1, 1, PARTS, 2>(o, smem + half * OUT, reinterpret_cast<int32_t *>(smem + 2 * OUT) + half * kOuterRows,
+                                     (int64_t)blockIdx.x - n_dx, half, threadIdx.x & 255);
+    }
+}
+
+// Workgroups of the gradients to run beside n_dx tiles of dx, 0 where they do not
+// fit in what the last round leaves idle.  Estimates: a tile of dx takes its
+// products at 4.2 TFLOP/s; two tiles of a slot's gradients a microsecond for 32
+// rows and 3 beside them.
+static int outer_beside_dx(int n_dx, const seg_outer_args &o, int F) {
+    const int rem = n_dx % 256, idle = 256 - rem;
+    if (o.R > 32 || n_dx < 256 || rem == 0) return 0;
+    const int64_t pairs = (o.tiles_k + 1) / 2 + (o.tiles_n + 1) / 2;
+    const double us = (double)pairs * (o.T / 32.0 + 3.0 * o.n_slots) / idle, tile_us = 2.0 * 256 * 256 * F / 4.2e6;
+    return us <= tile_us && pairs * o.n_slots < 1 << 20 ? (int)(pairs * o.n_slots) : 0;
 }
 
 __global__ void __launch_bounds__(256) k_zero16(uint4 *p, int64_t n) {
@@ -1274,6 +1327,11 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
                                  ws_ptr<float>(ws, B.sums), stretches, F, (uint16_t *)c.dbias};
         hipLaunchKernelGGL(k_rank_finish<NM>, dim3(first_octet + octets + sums, R2 / 8), dim3(256), 0, s, f, oc, pp);
     }
+    const seg_outer_args outer{(const uint16_t *)c.x, (const uint16_t *)dg, vt,
+                               {(uint16_t *)c.dA[0], (uint16_t *)c.dA[1]}, {(uint16_t *)c.dB[0], (uint16_t *)c.dB[1]},
+                               T, K, F, R, R2, S, Tp, perm, offsets, {p[0].rank, p[NM - 1].rank}, slot_blk,
+                               ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
+    int beside = 0;                                       // the gradients' workgroups in dx's launch
     if constexpr (DT == LORA_F32) {
         dx_f32_args g{(const float *)dg, (const float *)du, (const float *)c.W[0], (const float *)c.W[NM - 1],
                       (float *)c.dx, dv, c.ids, perm, ws_ptr<float>(ws, B.partial), T, F, K, S, R, ceil_div(K, 64), 1, 0};
@@ -1315,17 +1373,21 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
         g.n_tiles_m = ceil_div(T, pl.bm);
         g.n_tiles_n = ceil_div(g.N, pl.bn);
         g.col_strips = col_strips_pay(T, g.N, g.n_tiles_n);
-        if (pl.bm == 256 && pl.bn == 256) launch_nt_cfg<256, 256, 2, 8, 2, 2, 8>(g, nt, pl, s);
+        if constexpr (NM == 1)
+            if (c.dA[0] && pl.bm == 256 && pl.bn == 256 && pl.tail == 0) beside = outer_beside_dx(pl.n_dp, outer, F);
+        if (beside) {
+            g.n_tiles = pl.n_dp;
+            g.splits = 1;
+            g.k_chunk = g.K;
+            hipLaunchKernelGGL(k_nt_outer<PARTS>, dim3(pl.n_dp + beside), dim3(512), 0, s, g, nt, outer, pl.n_dp);
+        } else if (pl.bm == 256 && pl.bn == 256) launch_nt_cfg<256, 256, 2, 8, 2, 2, 8>(g, nt, pl, s);
         else if (pl.bm == 256 && pl.bn == 128) launch_nt_cfg<256, 128, 2, 8, 2, 2, 8>(g, nt, pl, s);
         else if (pl.bn == 128) launch_nt_cfg<128, 128, 2, 4, 2, 4, 8>(g, nt, pl, s);
         else launch_nt_cfg<128, 64, 2, 4, 2, 2, 4>(g, nt, pl, s);
     }
     if constexpr (DT == LORA_BF16) {
-        if (!c.dA[0]) return hip_status(hipGetLastError());
-        seg_outer_args g{(const uint16_t *)c.x, (const uint16_t *)dg, vt,
-                         {(uint16_t *)c.dA[0], (uint16_t *)c.dA[1]}, {(uint16_t *)c.dB[0], (uint16_t *)c.dB[1]},
-                         T, K, F, R, R2, S, Tp, perm, offsets, {p[0].rank, p[NM - 1].rank}, slot_blk,
-                         ceil_div(K, kOuterCols), ceil_div(F, kOuterCols)};
+        if (!c.dA[0] || beside) return hip_status(hipGetLastError());
+        const seg_outer_args &g = outer;
         const dim3 grid = grid_of((int64_t)S * (g.tiles_k + NM * g.tiles_n));
 #define LORA_OUTER(MBA, MBB) hipLaunchKernelGGL((k_seg_outer_mfma<MBA, MBB, NM, PARTS>), grid, dim3(256), 0, s, g)
         if constexpr (NM > 1) {

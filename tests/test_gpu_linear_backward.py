@@ -60,6 +60,24 @@ def test_ranges_of_the_sum_in_whole_rounds(T, d, f):
         check(p, act, *k, run_backward(p, act, *k), "bf16")
 
 
+# 306 whole tiles of 256 x 256: the adapters' gradients run beside the last round, two column tiles a workgroup (35 and
+# 7 of them here); one adapter of over 1024 rows, and none with rows
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("ids", ["random", "one", "none"])
+@pytest.mark.parametrize("R", [16, 32])
+def test_gradients_beside_dx(act, ids, R):
+    T, d, f = 4100, 4360, 888
+    ranks = [min(R, r) for r in (32, 3, 8, 0, 13, 30, 1)]
+    p = Layer(T, d, f, ranks, R, BF16, seed=R,
+              ids=None if ids == "random" else np.full(T, 0 if ids == "one" else -1, np.int32))
+    k = kept(p)
+    got = run_backward(p, act, *k)
+    check(p, act, *k, got, ids)
+    assert L.lora_get_device_error(got[4].buf) == p.bad_row()
+    again = run_backward(p, act, *k)
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], again[:4]))
+
+
 @pytest.mark.parametrize("T,d,f", [(1, 64, 8), (5, 136, 72), (64, 264, 256), (130, 136, 1032), (333, 520, 64),
                                    (700, 264, 520)])
 @pytest.mark.parametrize("act", list(ACTS))
