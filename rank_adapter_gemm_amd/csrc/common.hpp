@@ -262,8 +262,11 @@ lora_status_t launch_copy_batch(const copy_batch &c, hipStream_t s);
 lora_status_t launch_ws_init(void *ws, hipStream_t s, bool err_only = false);
 // Segments of ids (short_len: segments of fewer rows take the per-row path;
 // 1 = none do) into the workspace, with the GEMM's row order.
+// act (may be null): dp of the linear layer's backward pass, in the same launch.
+struct act_beside;
 lora_status_t launch_segments(const int32_t *ids, int32_t T, int32_t n_slots, const ws_layout &L,
-                              void *ws, hipStream_t s, int32_t short_len = 1);
+                              void *ws, hipStream_t s, int32_t short_len = 1,
+                              const act_beside *act = nullptr);
 // Separate expand of the short segments' rows (the GEMM left their term out),
 // one work item per short segment and column chunk.
 lora_status_t launch_expand_tiles(const float *v, int32_t v_stride, int32_t T, const lora_pool_t &p,

@@ -9,37 +9,13 @@
 // atomics: results repeat bitwise.
 //
 // And of the linear layer y = act(p) + residual, p = x W + s_a (x A_a) B_a + bias:
-//   dp = dy * act'(p),  dbias = sum of dp          k_act_grad, k_rank_finish
+//   dp = dy * act'(p),  dbias = sum of dp          act_grad, k_rank_finish
 // and the same kernels for the one projection (NM, the number of projections, 1).
+#include "act_grad.hpp"
 #include "gated_common.hpp"
 #include "norm_common.hpp"
 
 namespace lora {
-
-// What is left of a value beside its first bf16 part; an infinite or NaN value
-// has no second part.
-__device__ __forceinline__ float second_part(float rest) {
-    return fabsf(rest) < __builtin_inff() ? rest : 0.0f;
-}
-
-// act and its derivative at x.
-template <bool FINE> __device__ __forceinline__ void act_both(int act, float x, float &a, float &da) {
-    if (act == LORA_ACT_SILU) {
-        const float q = logistic<FINE>(x);
-        a = x * q;
-        da = fmaf(a, 1.0f - q, q);
-    } else if (act == LORA_ACT_GELU) {
-        const float cdf = 0.5f * erfcf(-0.70710678118654752f * x);
-        a = x * cdf;
-        // the density at x; exp(-x^2/2) is 0 long before x^2 overflows
-        da = fmaf(x, 0.39894228040143268f * (FINE ? expf(-0.5f * x * x) : __expf(-0.5f * x * x)), cdf);
-    } else {
-        const float q = logistic<FINE>(kGeluTanhK * fmaf(kGeluTanhC * x * x, x, x));
-        a = x * q;
-        // q is 0 or 1 long before x^2 overflows, where 0 times its slope is 0
-        da = fmaf(a * (1.0f - q), kGeluTanhK * fmaf(3.0f * kGeluTanhC, fminf(x * x, 1e30f), 1.0f), q);
-    }
-}
 
 // dg and du of 16 bytes of values per thread.  bf16: two bf16 parts each, hi =
 // bf16(f) and, `lo` values on, bf16(f - hi), together within 2^-17 of f.  The
@@ -1122,100 +1098,6 @@ __global__ void __launch_bounds__(256) k_zero16(uint4 *p, int64_t n) {
 }
 
 // ---------------------------------------------------------------------------
-// dp of the linear layer, as k_gated_dact's dg, and the sums of its columns for
-// dbias.  A workgroup takes 32 vectors of columns and a stretch of rows, every
-// eighth of them a thread; the 8 strands are added through LDS to one partial sum
-// per column and stretch.  WRITE = false: dp is dy itself, only its sums are made.
-// 2048 x 4096: 5 us without dp; 777 x 2744 through GELU: 11 us, the activation's
-// slope and latency.
-// ---------------------------------------------------------------------------
-constexpr int kActVecs = 32, kActStrands = 8;
-
-struct act_grad_args {
-    const void *pre, *dy;
-    void *dp;
-    float *part;                       // [stretches][N]
-    int32_t T, N, rows, act;
-    int64_t lo;                        // bf16: from dp's first parts to its second
-};
-
-template <int DT, bool WRITE, bool SUMS> __global__ void __launch_bounds__(256) k_act_grad(act_grad_args g) {
-    typedef typename elem<DT>::T E;
-    constexpr int VN = vec16<DT>::n;
-    const int vec = threadIdx.x % kActVecs, strand = threadIdx.x / kActVecs;
-    const int n = (blockIdx.x * kActVecs + vec) * VN;
-    const int64_t t0 = (int64_t)blockIdx.y * g.rows, t1 = t0 + g.rows < g.T ? t0 + g.rows : g.T;
-    float sum[VN] = {};
-    if (n < g.N) {
-#pragma unroll 2
-        for (int64_t t = t0 + strand; t < t1; t += kActStrands) {
-            const int64_t at = t * g.N + n;
-            float d[VN];
-            vec16<DT>::widen(ldg16((const E *)g.dy + at), d);
-            if constexpr (WRITE) {
-                float p[VN];
-                vec16<DT>::widen(ldg16((const E *)g.pre + at), p);
-#pragma unroll
-                for (int e = 0; e < VN; ++e) {
-                    float a, da;
-                    act_both<DT == LORA_F32>(g.act, p[e], a, da);
-                    d[e] *= da;
-                }
-                const uint4 q = vec16<DT>::narrow(d);
-                stg16((E *)g.dp + at, q);
-                if constexpr (DT == LORA_BF16) {
-                    float h[VN];
-                    vec16<DT>::widen(q, h);
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) h[e] = second_part(d[e] - h[e]);
-                    stg16((E *)g.dp + g.lo + at, vec16<DT>::narrow(h));
-                }
-            }
-            if constexpr (SUMS)
-#pragma unroll
-                for (int e = 0; e < VN; ++e) sum[e] += d[e];
-        }
-    }
-    if constexpr (SUMS) {
-        __shared__ float s[kActStrands][kActVecs * VN];
-#pragma unroll
-        for (int e = 0; e < VN; ++e) s[strand][vec * VN + e] = sum[e];
-        __syncthreads();
-        const int c = threadIdx.x, col = blockIdx.x * kActVecs * VN + c;
-        if (c < kActVecs * VN && col < g.N) {
-            float f = s[0][c];
-#pragma unroll
-            for (int i = 1; i < kActStrands; ++i) f += s[i][c];
-            g.part[(int64_t)blockIdx.y * g.N + col] = f;
-        }
-    }
-}
-
-// Rows of a stretch, and the number of stretches: about 1024 workgroups, of at
-// least 4 rows a strand (their partial sums are then few beside the rows).
-static int32_t act_grad_rows(int32_t T, int32_t N, int32_t dtype) {
-    const int tiles = ceil_div(N, kActVecs * (dtype == LORA_F32 ? 4 : 8));
-    int rows = ceil_div(T, ceil_div(1024, tiles));
-    if (rows < 4 * kActStrands) rows = 4 * kActStrands;
-    return ceil_div(rows, kActStrands) * kActStrands;
-}
-
-// (dbias, bf16: k_rank_finish adds up the stretches.)
-template <int DT> static lora_status_t launch_act_grad(act_grad_args &g, void *dbias, hipStream_t s) {
-    const bool write = g.act != LORA_ACT_NONE;
-    if (!write && !dbias) return LORA_OK;
-    g.rows = act_grad_rows(g.T, g.N, DT);
-    const int stretches = ceil_div(g.T, g.rows);
-    const dim3 grid(ceil_div(g.N, kActVecs * vec16<DT>::n), stretches);
-    if (write && dbias) hipLaunchKernelGGL((k_act_grad<DT, true, true>), grid, dim3(256), 0, s, g);
-    else if (write) hipLaunchKernelGGL((k_act_grad<DT, true, false>), grid, dim3(256), 0, s, g);
-    else hipLaunchKernelGGL((k_act_grad<DT, false, true>), grid, dim3(256), 0, s, g);
-    const lora_status_t st = hip_status(hipGetLastError());
-    return st == LORA_OK && dbias && DT == LORA_F32 ? launch_column_sums(g.part, stretches, g.N, g.N, DT, dbias, nullptr, s)
-                                                    : st;
-}
-
-// ---------------------------------------------------------------------------
 // Rank columns of dv and vt.
 static int32_t bwd_ranks(int n_proj, int32_t R) { return n_proj > 1 ? n_proj * R : ceil_div(R, 16) * 16; }
 
@@ -1253,7 +1135,7 @@ lora_status_t launch_zero(void *p, size_t bytes, hipStream_t s) {
 }
 
 // NM projections; PARTS: bf16 parts of dy.  dg: dg and du (NM = 1: dp), where
-// k_gated_dact and k_act_grad leave them, or the layer's dy itself.
+// k_gated_dact and act_grad leave them, or the layer's dy itself.
 template <int DT, int NM, int PARTS>
 static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_t s) {
     typedef typename elem<DT>::T E;
@@ -1264,21 +1146,27 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
     // k_rank_finish has its workgroups in one grid dimension, which holds fewer than 2^32 threads
     const int64_t finish = 2 * ceil_div(T, kShrinkRows) + (S < T ? S : T) * (1ll + (c.dx ? ceil_div(K, 256) : 0)) + (c.dbias ? ceil_div(F, 64) : 0);
     if (DT == LORA_BF16 && finish * 256 >= 1ll << 32) return LORA_ERR_UNSUPPORTED;
-    lora_status_t st = launch_segments(c.ids, T, S, L, ws, s, 1);
-    if (st != LORA_OK) return st;
     const int32_t *perm = ws_ptr<int32_t>(ws, L.perm), *offsets = ws_ptr<int32_t>(ws, L.offsets);
     float *v = ws_ptr<float>(ws, L.v), *dv = ws_ptr<float>(ws, B.dv);
     E *made = ws_ptr<E>(ws, B.dy);
     const lora_pool_t two[2] = {p[0], p[NM - 1]};
     const pair_pools pp = make_pair_pools(two);
+    lora_status_t st;
+    int32_t stretches = 0;
     if constexpr (NM > 1) {
+        st = launch_segments(c.ids, T, S, L, ws, s, 1);
+        if (st != LORA_OK) return st;
         const int64_t n_vec = (int64_t)T * F / vec16<DT>::n;
         hipLaunchKernelGGL(k_gated_dact<DT>, dim3((uint32_t)(n_vec < (1 << 24) ? (n_vec + 255) / 256 : 1 << 16)),
                            dim3(256), 0, s, (const E *)c.kept[0], (const E *)c.kept[1], (const E *)c.dh, made,
                            made + (int64_t)T * F, 2ll * T * F, n_vec, c.act);
     } else {
-        act_grad_args a{c.kept[0], c.dh, made, ws_ptr<float>(ws, B.sums), T, F, 0, c.act, (int64_t)T * F};
-        st = launch_act_grad<DT>(a, c.dbias, s);
+        const act_beside act{{c.kept[0], c.dh, made, ws_ptr<float>(ws, B.sums), T, F, act_grad_rows(T, F, DT), c.act,
+                              (int64_t)T * F}, DT, c.act != LORA_ACT_NONE, c.dbias != nullptr};
+        stretches = act.stretches();
+        st = launch_segments(c.ids, T, S, L, ws, s, 1, act.write || act.sums ? &act : nullptr);
+        if (st == LORA_OK && DT == LORA_F32 && c.dbias)   // (bf16: k_rank_finish)
+            st = launch_column_sums(act.args.part, stretches, F, F, DT, c.dbias, nullptr, s);
         if (st != LORA_OK) return st;
     }
     const E *dg = NM == 1 && c.act == LORA_ACT_NONE ? (const E *)c.dh : made, *du = dg + (NM - 1) * (int64_t)T * F;
@@ -1321,7 +1209,6 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
         const a_octets_args oc{g.seg_id, g.n_seg, S, K, R, R2, ceil_div(K, 256), ws_ptr<uint16_t>(ws, B.oct),
                                ws_ptr<int32_t>(ws, B.row0), ws_ptr<int32_t>(ws, B.rank), ws_ptr<float>(ws, B.scale)};
         const int octets = c.dx ? (S < T ? S : T) * oc.k_blocks : 0, sums = c.dbias ? ceil_div(F, 64) : 0;
-        const int stretches = NM > 1 ? 0 : ceil_div(T, act_grad_rows(T, F, DT));
         const rank_finish_args f{v, part, split, T, R, R2, S, n_work, Tp, perm, offsets, g.seg_id, g.seg_start, g.n_seg,
                                  g.blk_start, g.blk_seg, dv, vt, slot_blk, first_octet, first_octet + octets,
                                  ws_ptr<float>(ws, B.sums), stretches, F, (uint16_t *)c.dbias};

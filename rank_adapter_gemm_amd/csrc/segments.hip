@@ -24,7 +24,7 @@
 //      order.
 // A batch of one tile takes one launch of one workgroup (k_seg_one): all of it
 // is latency (64 slots, rows at random: 1024 rows 9.7 us, 1025 in three launches 13).
-#include "common.hpp"
+#include "act_grad.hpp"
 
 namespace lora {
 
@@ -209,7 +209,7 @@ __device__ __forceinline__ int32_t tile_rank(int32_t key, int32_t nb, int32_t *c
 
 constexpr int kScanItems = 4;
 
-__global__ void __launch_bounds__(1024) k_seg_scan(int32_t *__restrict__ tile_hist, int32_t n_slots,
+__device__ __forceinline__ void seg_scan(int32_t *s_off, int32_t *__restrict__ tile_hist, int32_t n_slots,
                                                    int32_t n_tiles, int32_t T, int32_t short_len,
                                                    int32_t *__restrict__ offsets,
                                                    int32_t *__restrict__ seg_id,
@@ -220,8 +220,7 @@ __global__ void __launch_bounds__(1024) k_seg_scan(int32_t *__restrict__ tile_hi
                                                    int32_t *__restrict__ gbase,
                                                    int4 *__restrict__ srec,
                                                    int32_t *__restrict__ header) {
-    extern __shared__ int32_t s_off[];        // [n_slots + 2]
-    __shared__ int32_t s_wave[48];
+    __shared__ int32_t s_wave[48];            // s_off: [n_slots + 2], LDS
     const int32_t nb = n_slots + 1;
     const int64_t N = (int64_t)nb * n_tiles;
     int32_t carry = 0;
@@ -255,6 +254,22 @@ __global__ void __launch_bounds__(1024) k_seg_scan(int32_t *__restrict__ tile_hi
     compact_segments(s_off, nb, T, s_wave, seg_id, seg_start, n_seg, blk_start, blk_seg);
 }
 
+__global__ void __launch_bounds__(1024) k_seg_scan(int32_t *__restrict__ tile_hist, int32_t n_slots,
+                                                   int32_t n_tiles, int32_t T, int32_t short_len,
+                                                   int32_t *__restrict__ offsets,
+                                                   int32_t *__restrict__ seg_id,
+                                                   int32_t *__restrict__ seg_start,
+                                                   int32_t *__restrict__ n_seg,
+                                                   int32_t *__restrict__ blk_start,
+                                                   int32_t *__restrict__ blk_seg,
+                                                   int32_t *__restrict__ gbase,
+                                                   int4 *__restrict__ srec,
+                                                   int32_t *__restrict__ header) {
+    extern __shared__ int32_t s_off[];
+    seg_scan(s_off, tile_hist, n_slots, n_tiles, T, short_len, offsets, seg_id, seg_start, n_seg, blk_start, blk_seg,
+             gbase, srec, header);
+}
+
 __global__ void __launch_bounds__(1024) k_seg_scatter(const int32_t *__restrict__ ids, int32_t T,
                                                       int32_t n_slots,
                                                       const int32_t *__restrict__ tile_hist,
@@ -273,7 +288,7 @@ __global__ void __launch_bounds__(1024) k_seg_scatter(const int32_t *__restrict_
 }
 
 // Batches of one tile: everything above by one workgroup, in one launch.
-__global__ void __launch_bounds__(1024) k_seg_one(const int32_t *__restrict__ ids, int32_t T, int32_t n_slots,
+__device__ __forceinline__ void seg_one(int32_t *s_off, const int32_t *__restrict__ ids, int32_t T, int32_t n_slots,
                                                   int32_t short_len, int32_t *__restrict__ offsets,
                                                   int32_t *__restrict__ seg_id, int32_t *__restrict__ seg_start,
                                                   int32_t *__restrict__ n_seg, int32_t *__restrict__ blk_start,
@@ -281,8 +296,7 @@ __global__ void __launch_bounds__(1024) k_seg_one(const int32_t *__restrict__ id
                                                   int4 *__restrict__ srec, int32_t *__restrict__ header,
                                                   int32_t *__restrict__ perm, int32_t *__restrict__ gperm,
                                                   int32_t *err) {
-    extern __shared__ int32_t s_off[];        // [n_slots + 2]: counts, then first positions
-    __shared__ int32_t s_wave[48];
+    __shared__ int32_t s_wave[48];            // s_off: [n_slots + 2], LDS: counts, then first positions
     const int32_t nb = n_slots + 1, t = threadIdx.x;
     const int32_t id = t < T ? ids[t] : -1;
     const int32_t key = t < T ? row_key(id, n_slots) : -1;
@@ -308,20 +322,137 @@ __global__ void __launch_bounds__(1024) k_seg_one(const int32_t *__restrict__ id
     gperm[gbase[key] + rank] = t;
 }
 
+__global__ void __launch_bounds__(1024) k_seg_one(const int32_t *__restrict__ ids, int32_t T, int32_t n_slots,
+                                                  int32_t short_len, int32_t *__restrict__ offsets,
+                                                  int32_t *__restrict__ seg_id, int32_t *__restrict__ seg_start,
+                                                  int32_t *__restrict__ n_seg, int32_t *__restrict__ blk_start,
+                                                  int32_t *__restrict__ blk_seg, int32_t *gbase,
+                                                  int4 *__restrict__ srec, int32_t *__restrict__ header,
+                                                  int32_t *__restrict__ perm, int32_t *__restrict__ gperm,
+                                                  int32_t *err) {
+    extern __shared__ int32_t s_off[];
+    seg_one(s_off, ids, T, n_slots, short_len, offsets, seg_id, seg_start, n_seg, blk_start, blk_seg, gbase, srec,
+            header, perm, gperm, err);
+}
+
+// The one workgroup of the above, and beside it the cells of act_grad, four a
+// workgroup, which need the chip and no segments (777 rows, 24 adapters, 2744
+// columns through tanh GELU: 10 us, one after the other 8 and 12).
+struct seg_one_args {
+    const int32_t *ids;
+    int32_t T;
+    int32_t n_slots;
+    int32_t short_len;
+    int32_t *offsets;
+    int32_t *seg_id;
+    int32_t *seg_start;
+    int32_t *n_seg;
+    int32_t *blk_start;
+    int32_t *blk_seg;
+    int32_t *gbase;
+    int4 *srec;
+    int32_t *header;
+    int32_t *perm;
+    int32_t *gperm;
+    int32_t *err;
+};
+struct seg_scan_args {
+    int32_t *tile_hist;
+    int32_t n_slots;
+    int32_t n_tiles;
+    int32_t T;
+    int32_t short_len;
+    int32_t *offsets;
+    int32_t *seg_id;
+    int32_t *seg_start;
+    int32_t *n_seg;
+    int32_t *blk_start;
+    int32_t *blk_seg;
+    int32_t *gbase;
+    int4 *srec;
+    int32_t *header;
+};
+
+template <int DT, bool WRITE, bool SUMS>
+__device__ __forceinline__ void act_cells(const act_grad_args &g, int cols, int block, int32_t *lds) {
+    const int quarter = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), cell = block * 4 + quarter;
+    act_grad<DT, WRITE, SUMS>(g, cell % cols, cell / cols, threadIdx.x & 255,
+                              reinterpret_cast<float *>(lds) + quarter * act_grad_lds<DT>());
+}
+
+template <int DT, bool WRITE, bool SUMS>
+__global__ void __launch_bounds__(1024) k_seg_one_act(seg_one_args a, act_grad_args g, int32_t cols) {
+    extern __shared__ __attribute__((aligned(16))) int32_t s_lds[];
+    if (blockIdx.x == 0)
+        seg_one(s_lds, a.ids, a.T, a.n_slots, a.short_len, a.offsets, a.seg_id, a.seg_start, a.n_seg, a.blk_start,
+                a.blk_seg, a.gbase, a.srec, a.header, a.perm, a.gperm, a.err);
+    else
+        act_cells<DT, WRITE, SUMS>(g, cols, blockIdx.x - 1, s_lds);
+}
+
+template <int DT, bool WRITE, bool SUMS>
+__global__ void __launch_bounds__(1024) k_seg_scan_act(seg_scan_args a, act_grad_args g, int32_t cols) {
+    extern __shared__ __attribute__((aligned(16))) int32_t s_lds[];
+    if (blockIdx.x == 0)
+        seg_scan(s_lds, a.tile_hist, a.n_slots, a.n_tiles, a.T, a.short_len, a.offsets, a.seg_id, a.seg_start, a.n_seg,
+                 a.blk_start, a.blk_seg, a.gbase, a.srec, a.header);
+    else
+        act_cells<DT, WRITE, SUMS>(g, cols, blockIdx.x - 1, s_lds);
+}
+
+template <int DT, bool WRITE, bool SUMS>
+static void launch_beside(const seg_one_args *one, const seg_scan_args &scan, const act_beside &act, size_t lds,
+                          hipStream_t s) {
+    const int cols = act.cols();
+    const int64_t cells = (int64_t)cols * act.stretches();
+    const size_t need = SUMS ? 4 * 4 * (size_t)act_grad_lds<DT>() : 0;
+    if (lds < need) lds = need;
+    const dim3 grid((uint32_t)(1 + (cells + 3) / 4));
+    if (one) hipLaunchKernelGGL((k_seg_one_act<DT, WRITE, SUMS>), grid, dim3(1024), lds, s, *one, act.args, cols);
+    else hipLaunchKernelGGL((k_seg_scan_act<DT, WRITE, SUMS>), grid, dim3(1024), lds, s, scan, act.args, cols);
+}
+
+template <int DT>
+static void launch_beside_dt(const seg_one_args *one, const seg_scan_args &scan, const act_beside &act, size_t lds,
+                             hipStream_t s) {
+    if (act.write && act.sums) launch_beside<DT, true, true>(one, scan, act, lds, s);
+    else if (act.write) launch_beside<DT, true, false>(one, scan, act, lds, s);
+    else launch_beside<DT, false, true>(one, scan, act, lds, s);
+}
+
 lora_status_t launch_ws_init(void *ws, hipStream_t s, bool err_only) {
     hipLaunchKernelGGL(k_ws_init, dim3(1), dim3(64), 0, s, ws_ptr<int32_t>(ws, 0), err_only ? 0 : 1);
     return hip_status(hipGetLastError());
 }
 
 lora_status_t launch_segments(const int32_t *ids, int32_t T, int32_t n_slots, const ws_layout &L,
-                              void *ws, hipStream_t s, int32_t short_len) {
+                              void *ws, hipStream_t s, int32_t short_len, const act_beside *act) {
     if (short_len < 1) short_len = 1;
     const int32_t n_tiles = (T + kSegTile - 1) / kSegTile;
     int32_t *err = ws_ptr<int32_t>(ws, L.header);
     int32_t *tile_hist = ws_ptr<int32_t>(ws, L.tile_hist);
     const size_t lds_hist = sizeof(int32_t) * (size_t)(n_slots + 1);
     const size_t lds_off = sizeof(int32_t) * (size_t)(n_slots + 2);
+    const seg_scan_args scan{tile_hist, n_slots, n_tiles, T, short_len,
+                       ws_ptr<int32_t>(ws, L.offsets), ws_ptr<int32_t>(ws, L.seg_id),
+                       ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
+                       ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg),
+                       ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int4>(ws, L.srec), ws_ptr<int32_t>(ws, L.header)};
+    auto beside = [&](const seg_one_args *one) {
+        if (act->dtype == LORA_F32) launch_beside_dt<LORA_F32>(one, scan, *act, lds_off, s);
+        else launch_beside_dt<LORA_BF16>(one, scan, *act, lds_off, s);
+    };
     if (n_tiles == 1) {
+        if (act) {
+            const seg_one_args one{ids, T, n_slots, short_len,
+                           ws_ptr<int32_t>(ws, L.offsets), ws_ptr<int32_t>(ws, L.seg_id),
+                           ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
+                           ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg),
+                           ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int4>(ws, L.srec), ws_ptr<int32_t>(ws, L.header),
+                           ws_ptr<int32_t>(ws, L.perm), ws_ptr<int32_t>(ws, L.gperm), err};
+            beside(&one);
+            return hip_status(hipGetLastError());
+        }
         hipLaunchKernelGGL(k_seg_one, dim3(1), dim3(kSegTile), lds_off, s, ids, T, n_slots, short_len,
                            ws_ptr<int32_t>(ws, L.offsets), ws_ptr<int32_t>(ws, L.seg_id),
                            ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
@@ -332,11 +463,13 @@ lora_status_t launch_segments(const int32_t *ids, int32_t T, int32_t n_slots, co
     }
     hipLaunchKernelGGL(k_seg_hist, dim3(n_tiles), dim3(256), lds_hist, s, ids, T, n_slots,
                        tile_hist, n_tiles, err);
-    hipLaunchKernelGGL(k_seg_scan, dim3(1), dim3(1024), lds_off, s, tile_hist, n_slots, n_tiles, T, short_len,
-                       ws_ptr<int32_t>(ws, L.offsets), ws_ptr<int32_t>(ws, L.seg_id),
-                       ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
-                       ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg),
-                       ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int4>(ws, L.srec), ws_ptr<int32_t>(ws, L.header));
+    if (act) beside(nullptr);
+    else
+        hipLaunchKernelGGL(k_seg_scan, dim3(1), dim3(1024), lds_off, s, tile_hist, n_slots, n_tiles, T, short_len,
+                           ws_ptr<int32_t>(ws, L.offsets), ws_ptr<int32_t>(ws, L.seg_id),
+                           ws_ptr<int32_t>(ws, L.seg_start), ws_ptr<int32_t>(ws, L.n_seg),
+                           ws_ptr<int32_t>(ws, L.blk_start), ws_ptr<int32_t>(ws, L.blk_seg),
+                           ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int4>(ws, L.srec), ws_ptr<int32_t>(ws, L.header));
     hipLaunchKernelGGL(k_seg_scatter, dim3(n_tiles), dim3(kSegTile), lds_hist, s, ids, T, n_slots,
                        tile_hist, n_tiles, ws_ptr<int32_t>(ws, L.perm), ws_ptr<int32_t>(ws, L.offsets),
                        ws_ptr<int32_t>(ws, L.gbase), ws_ptr<int32_t>(ws, L.gperm));
