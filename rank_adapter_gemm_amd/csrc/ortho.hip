@@ -54,7 +54,7 @@ struct ortho_args {
     void *out;
     double *part;                      // [n][splits][tiles][64][4]: a tile's sums, lane by lane
     double *poly;                      // [n][16 W][16 W], zeros past r
-    double *factor;                    // [n]: scale / (|G| + eps)
+    double *inv;                       // [n]: 1 / (|G| + eps)
     int32_t D, n, r, splits, chunk;    // chunk: long-side indices per split, a multiple of 64
     int32_t rows, blocks;              // k_ortho_apply: long-side indices per workgroup, workgroups per matrix
     int32_t steps;
@@ -240,10 +240,10 @@ template <int NT> __device__ __forceinline__ f64x4_t poly_part(const ortho_args 
     return m;
 }
 
-// One tile: P in a wavefront's registers, and scale / (|G| + eps).  Few enough
+// One tile: P in a wavefront's registers, and 1 / (|G| + eps).  Few enough
 // products for k_ortho_apply to do them itself, every workgroup of a matrix the
 // same (as a launch of its own: 32 x 4096 x 16 15.9 us for 14.5).
-__device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, int lane, double &factor) {
+__device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, int lane, double &inv) {
     f64x4_t m = poly_part<1>(g, mat, 0, lane), one, pr;
     double d = 0.0;
 #pragma unroll
@@ -251,8 +251,7 @@ __device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, in
         one[e] = mfma64_row(e, lane) == (lane & 15) ? 1.0 : 0.0;
         d += one[e] * m[e];
     }
-    const double inv = 1.0 / (sqrt(wave_sum64(d)) + (double)g.eps);
-    factor = (double)g.scale * inv;
+    inv = 1.0 / (sqrt(wave_sum64(d)) + (double)g.eps);
     const f64x4_t zero = {0.0, 0.0, 0.0, 0.0};
     m *= inv * inv;
     pr = one;
@@ -319,7 +318,7 @@ template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES
 #pragma unroll
     for (int i = 1; i < W; ++i) trace += s_trace[i];
     const double inv = 1.0 / (sqrt(trace) + (double)g.eps);
-    if (threadIdx.x == 0) g.factor[mat] = (double)g.scale * inv;
+    if (threadIdx.x == 0) g.inv[mat] = inv;
     m *= inv * inv;
     if (own) put(s_m, ma, mb, m);
     __syncthreads();
@@ -410,7 +409,7 @@ template <bool TALL> __global__ void __launch_bounds__(768) k_ortho_poly8(ortho_
     }
     __syncthreads();
     const double inv = 1.0 / (sqrt(s_trace) + (double)g.eps);
-    if (threadIdx.x == 0) g.factor[mat] = (double)g.scale * inv;
+    if (threadIdx.x == 0) g.inv[mat] = inv;
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
 #pragma unroll
@@ -557,10 +556,10 @@ template <int W, bool TALL> struct apply_bf16 {
         }
     }
 
-    __device__ __forceinline__ void store(const ortho_args &g, uint16_t *out, const uint16_t *s_p, double factor64, int i0,
+    __device__ __forceinline__ void store(const ortho_args &g, uint16_t *out, const uint16_t *s_p, int exponent, int i0,
                                           int lane) {
         const int p = lane & 15, kg = lane >> 4, r = g.r;
-        const float factor = (float)factor64;
+        auto scaled = [&](float f) { return ldexpf(f, exponent); };
 #pragma unroll 1                                           // (unrolled, the wide ones spill)
         for (int c0 = 0; c0 < W; c0 += CB) {
             f32x4_t acc[CB][S];
@@ -587,8 +586,8 @@ template <int W, bool TALL> struct apply_bf16 {
                     const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
                     if (c < r && i < g.D)
                         *reinterpret_cast<uint2 *>(out + (int64_t)i * r + c) =
-                            make_uint2(pack_bf16x2(factor * acc[cb][0][0], factor * acc[cb][0][1]),
-                                       pack_bf16x2(factor * acc[cb][0][2], factor * acc[cb][0][3]));
+                            make_uint2(pack_bf16x2(scaled(acc[cb][0][0]), scaled(acc[cb][0][1])),
+                                       pack_bf16x2(scaled(acc[cb][0][2]), scaled(acc[cb][0][3])));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -596,12 +595,29 @@ template <int W, bool TALL> struct apply_bf16 {
                         if (c >= r || i >= g.D) continue;
                         float f[8];
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) f[s] = factor * acc[cb][S > 1 ? s : 0][e];
+                        for (int s = 0; s < 8; ++s) f[s] = scaled(acc[cb][S > 1 ? s : 0][e]);
                         stg16(out + (int64_t)c * g.D + i, vec16<LORA_BF16>::narrow(f));
                     }
                 }
             }
         }
+    }
+};
+
+// scale / (|G| + eps) = times 2^exponent.  It need not be a number of 32 bits (a zero matrix
+// and a small eps: up to 2^277), nor need G P be (G of up to 2^128, P of several
+// hundred): the 32-bit sums are of G and times P, whose power of two brings G near 1 as
+// far as P's parts allow, and the rest of the power goes to the result.
+struct split_factor {
+    double times;
+    int exponent;
+    __device__ __forceinline__ split_factor(float scale, double inv) {
+        int e, to;
+        (void)frexp(inv, &to);
+        const double m = frexp((double)scale * inv, &e);
+        to = to < -60 ? -60 : to > 60 ? 60 : to;
+        times = ldexp(m, to);
+        exponent = e - to;
     }
 };
 
@@ -651,24 +667,26 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
     typename std::conditional<F32, apply_f32<W, TALL>, apply_bf16<W, TALL>>::type block;
     int i0 = begin + wave * BLOCK;
     if (i0 < end) block.load(g, in, i0, lane);            // under way while P is staged
-    double factor;
+    double inv;
     typedef double f64x2_t __attribute__((ext_vector_type(2)));
     if constexpr (W == 1) {
         __shared__ __attribute__((aligned(16))) double s_tile[256];
-        __shared__ double s_factor;
+        __shared__ double s_inv;
         if (wave == 0) {
-            const f64x4_t pr = poly_one(g, mat, lane, factor);
+            const f64x4_t pr = poly_one(g, mat, lane, inv);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = mfma64_row(e, lane), j = lane & 15;
                 s_tile[16 * i + j] = i < g.r && j < g.r ? pr[e] : 0.0;
             }
-            if (lane == 0) s_factor = factor;
+            if (lane == 0) s_inv = inv;
         }
         __syncthreads();
-        factor = s_factor;
-        if (threadIdx.x < 128)
-            stage_pair<F32, W, TALL>(s_p, threadIdx.x, reinterpret_cast<const f64x2_t *>(s_tile)[threadIdx.x]);
+        inv = s_inv;
+        if (threadIdx.x < 128) {
+            const f64x2_t v = reinterpret_cast<const f64x2_t *>(s_tile)[threadIdx.x];
+            stage_pair<F32, W, TALL>(s_p, threadIdx.x, F32 ? v : v * split_factor(g.scale, inv).times);
+        }
         if (!F32 && threadIdx.x < 16) {                   // the products' k 16..31
             uint16_t *s = reinterpret_cast<uint16_t *>(s_p) + threadIdx.x * (RP + 8) + 16;
 #pragma unroll
@@ -678,7 +696,8 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
                     *reinterpret_cast<uint4 *>(s + part * 16 * W * (RP + 8) + 8 * h) = make_uint4(0u, 0u, 0u, 0u);
         }
     } else {
-        factor = g.factor[mat];
+        inv = g.inv[mat];
+        const double times = F32 ? 1.0 : split_factor(g.scale, inv).times;
         const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(g.poly + mat * 256 * W * W);
         constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 * 8 ? PAIRS / 256 : 8;
         for (int i = threadIdx.x; i < PAIRS; i += 256 * STEP) {
@@ -686,13 +705,15 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
 #pragma unroll
             for (int u = 0; u < STEP; ++u) v[u] = poly[i + 256 * u];
 #pragma unroll
-            for (int u = 0; u < STEP; ++u) stage_pair<F32, W, TALL>(s_p, i + 256 * u, v[u]);
+            for (int u = 0; u < STEP; ++u) stage_pair<F32, W, TALL>(s_p, i + 256 * u, F32 ? v[u] : v[u] * times);
         }
     }
     __syncthreads();
+    const double factor = (double)g.scale * inv;
+    const int exponent = split_factor(g.scale, inv).exponent;
     for (; i0 < end; i0 += 4 * BLOCK) {
         if constexpr (F32) block.store(g, out, reinterpret_cast<const double *>(s_p), factor, i0, lane);
-        else block.store(g, out, reinterpret_cast<const uint16_t *>(s_p), factor, i0, lane);
+        else block.store(g, out, reinterpret_cast<const uint16_t *>(s_p), exponent, i0, lane);
         if (i0 + 4 * BLOCK < end) block.load(g, in, i0 + 4 * BLOCK, lane);
     }
 }
@@ -700,7 +721,7 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
 // ---------------------------------------------------------------------------
 struct ortho_layout {
     int32_t r, D, W, splits, chunk;
-    size_t part, poly, factor, total;
+    size_t part, poly, inv, total;
 };
 
 static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
@@ -718,7 +739,7 @@ static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
     size_t o = 0;
     L.part = o;   o = align256(o + (size_t)n * L.splits * ortho_tiles(L.W) * 256 * 8);
     L.poly = o;   o = align256(o + (size_t)n * 256 * L.W * L.W * 8);
-    L.factor = o; o = align256(o + (size_t)n * 8);
+    L.inv = o;    o = align256(o + (size_t)n * 8);
     L.total = o;
     return L;
 }
@@ -754,7 +775,7 @@ lora_status_t launch_orthogonalize(const void *in, int32_t n, int32_t rows, int3
     g.out = out;
     g.part = ws_ptr<double>(ws, L.part);
     g.poly = ws_ptr<double>(ws, L.poly);
-    g.factor = ws_ptr<double>(ws, L.factor);
+    g.inv = ws_ptr<double>(ws, L.inv);
     g.D = L.D;
     g.n = n;
     g.r = L.r;
