@@ -705,7 +705,9 @@ lora_status_t lora_linear_act_backward(const void *x, const void *W, int32_t T, 
  *     X <- c0 X + c1 (X X^T) X + c2 (X X^T)^2 X   for the steps in turn;   out[i] = scale X
  * (Newton-Schulz products, which bring the singular values near 1 and keep the
  * singular vectors).  coef HOST fp32 [steps][3] (c0, c1, c2 of each step), 1 <= steps
- * <= LORA_MAX_ORTHO_STEPS.  g and out DEVICE of `dtype`; out may be g's own buffer,
+ * <= LORA_MAX_ORTHO_STEPS; the product of |c0| over steps that follow each other at most
+ * 2^30 (else LORA_ERR_UNSUPPORTED; 16 steps of c0 = 3.4445: 2^28.6): a direction that g[i]
+ * does not have is a rounding of 2^-53 that grows by it.  g and out DEVICE of `dtype`; out may be g's own buffer,
  * else it shares no byte with it or ws.  rows and cols positive multiples of 8, the
  * smaller at most LORA_MAX_ORTHO_SIDE, the larger below 2^28 (LORA_ERR_UNSUPPORTED
  * past these).  Zero rows and columns (ranks past an adapter's) and zero matrices

@@ -1104,6 +1104,7 @@ lora_status_t lora_orthogonalize(const void *g, int32_t n, int32_t rows, int32_t
         return LORA_ERR_INVALID_ARGUMENT;
     for (int i = 0; i < 3 * steps; ++i)
         if (!(coef[i] < inf) || !(coef[i] > -inf)) return LORA_ERR_INVALID_ARGUMENT;
+    if (!ortho_steps_ok(coef, steps)) return LORA_ERR_UNSUPPORTED;
     if (n == 0) return LORA_OK;
     if (!g || !out || !ws || !aligned16(g) || !aligned16(out) || !aligned16(ws)) return LORA_ERR_INVALID_ARGUMENT;
     if (ws_bytes < ortho_workspace_bytes(n, rows, cols)) return LORA_ERR_WORKSPACE_TOO_SMALL;

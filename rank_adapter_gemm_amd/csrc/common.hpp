@@ -406,6 +406,8 @@ lora_status_t launch_column_sums(const float *part, int32_t groups, int32_t n, i
 // matrices [rows][cols], the shorter side at most kMaxOrthoSide.
 constexpr int32_t kMaxOrthoSteps = 16, kMaxOrthoSide = 128;
 size_t ortho_workspace_bytes(int32_t n, int32_t rows, int32_t cols);
+// False where the product of |c0| over steps that follow each other passes what 64 bits bear.
+bool ortho_steps_ok(const float *coef, int32_t steps);
 lora_status_t launch_orthogonalize(const void *in, int32_t n, int32_t rows, int32_t cols, int32_t dtype,
                                    const float *coef, int32_t steps, float eps, float scale, void *out, void *ws,
                                    hipStream_t s);

@@ -11,6 +11,16 @@
 //                   (r <= 16: k_ortho_apply does it)
 //   k_ortho_apply   G P                                     one more read, one write
 //
+// Passes: M cannot say which way a direction that is not in X is to go.  Its
+// eigenvalue there is a rounding, 2^-53 of either sign, and c0^2 times as large after
+// each step; a negative one is not held back by the polynomial.  (Rank 1 in 16 columns:
+// 10 steps of 3.4445 2e-6 off, 12 2e-4, 16 70 times the result.)  So where the product of
+// c0^2 would pass 2^22, 6 such steps, M is made anew from X itself, that is from G P
+// (k_ortho_regram, one more read of G), and the next steps' matrix is joined to P by
+// a product of all its tiles (k_ortho_join: P is symmetric but for roundings, and c0's
+// product makes those large).  What is left is c0's product times 2^-53, as with the steps on
+// X in 64 bits; callers may ask for 2^30.
+//
 // 64 bits: small singular values are amplified, by c0 at every step (485-fold in 5
 // steps of 3.4445), and an error e of M by up to 3e4 e relative to what those
 // directions get.  32-bit sums of M (6e-8) would show in the result; 64-bit ones
@@ -53,11 +63,13 @@ struct ortho_args {
     const void *g;
     void *out;
     double *part;                      // [n][splits][tiles][64][4]: a tile's sums, lane by lane
-    double *poly;                      // [n][16 W][16 W], zeros past r
+    double *poly;                      // [n][16 W][16 W], zeros past r: these steps' matrix
+    const double *before;              // k_ortho_regram, k_ortho_join: P of the steps before, transposed
+    double *joined;                    // k_ortho_join: P of all steps, transposed
     double *inv;                       // [n]: 1 / (|G| + eps)
     int32_t D, n, r, splits, chunk;    // chunk: long-side indices per split, a multiple of 64
     int32_t rows, blocks;              // k_ortho_apply: long-side indices per workgroup, workgroups per matrix
-    int32_t steps;
+    int32_t steps, first;              // first: the steps start at G
     float eps, scale;
     float coef[kMaxOrthoSteps][3];
 };
@@ -157,6 +169,40 @@ __device__ __forceinline__ void gram_wave(const ortho_args &g, const typename el
     }
 }
 
+// The sums of the KW wavefronts (kw) that share a part: wavefront tile % KW adds up a
+// tile, the others hand theirs over through LDS, then all add and store.
+template <int W, int KW, int HALF, bool ADD, int N>
+__device__ __forceinline__ void gram_sums(f64x4_t *part, const f64x4_t (&acc)[N], f64x4_t (*s_sum)[ortho_tiles(W)][64],
+                                          int kw, int lane) {
+#pragma unroll
+    for (int a = 0; a < W; ++a)
+        if (gram_owns<W>(HALF, a))
+#pragma unroll
+            for (int b = 0; b <= a; ++b) {
+                const int tile = ortho_tile(a, b), to = tile % KW;
+                f64x4_t f = acc[gram_at<W>(HALF, a, b)];
+                if constexpr (!ADD) {
+                    if (kw != to) s_sum[kw < to ? kw : kw - 1][tile][lane] = f;
+                } else if (kw == to) {
+#pragma unroll
+                    for (int k = 0; k < KW - 1; ++k) f += s_sum[k][tile][lane];
+                    part[tile * 64 + lane] = f;
+                }
+            }
+}
+
+// To split `item`'s place; the whole workgroup calls it.
+template <int W, int KW, int N>
+__device__ __forceinline__ void gram_finish(const ortho_args &g, const f64x4_t (&acc)[N],
+                                            f64x4_t (*s_sum)[ortho_tiles(W)][64], int64_t item, int kw, int half, int lane) {
+    f64x4_t *part = reinterpret_cast<f64x4_t *>(g.part) + item * ortho_tiles(W) * 64;
+    if (W == 8 && half) gram_sums<W, KW, 1, false>(part, acc, s_sum, kw, lane);
+    else gram_sums<W, KW, 0, false>(part, acc, s_sum, kw, lane);
+    __syncthreads();
+    if (W == 8 && half) gram_sums<W, KW, 1, true>(part, acc, s_sum, kw, lane);
+    else gram_sums<W, KW, 0, true>(part, acc, s_sum, kw, lane);
+}
+
 template <int DT, int W, bool TALL>
 __global__ void __launch_bounds__(gram_cfg<W>::WAVES * 64) k_ortho_gram(ortho_args g) {
     constexpr int NT = ortho_tiles(W), KW = gram_cfg<W>::KW, HALVES = gram_cfg<W>::WAVES / KW, N = NT / HALVES;
@@ -171,29 +217,7 @@ __global__ void __launch_bounds__(gram_cfg<W>::WAVES * 64) k_ortho_gram(ortho_ar
     f64x4_t acc[N];
     if (half) gram_wave<DT, W, TALL, 1>(g, base, begin, end, kw, lane, acc);
     else gram_wave<DT, W, TALL, 0>(g, base, begin, end, kw, lane, acc);
-    auto each = [&](auto &&f) {
-#pragma unroll
-        for (int a = 0; a < W; ++a)
-#pragma unroll
-            for (int b = 0; b <= a; ++b) {
-                if (gram_owns<W>(0, a) && half == 0) f(ortho_tile(a, b), acc[gram_at<W>(0, a, b) < N ? gram_at<W>(0, a, b) : 0]);
-                if (W == 8 && gram_owns<W>(1, a) && half == 1) f(ortho_tile(a, b), acc[gram_at<W>(1, a, b) < N ? gram_at<W>(1, a, b) : 0]);
-            }
-    };
-    // wavefront tile % KW of a part adds up a tile, the others hand theirs over
-    each([&](int tile, const f64x4_t &c) {
-        const int to = tile % KW;
-        if (kw != to) s_sum[kw < to ? kw : kw - 1][tile][lane] = c;
-    });
-    __syncthreads();
-    f64x4_t *part = reinterpret_cast<f64x4_t *>(g.part) + item * NT * 64 + lane;
-    each([&](int tile, const f64x4_t &c) {
-        if (kw != tile % KW) return;
-        f64x4_t f = c;
-#pragma unroll
-        for (int k = 0; k < KW - 1; ++k) f += s_sum[k][tile][lane];
-        part[tile * 64] = f;
-    });
+    gram_finish<W, KW>(g, acc, s_sum, item, kw, half, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -240,9 +264,14 @@ template <int NT> __device__ __forceinline__ f64x4_t poly_part(const ortho_args 
     return m;
 }
 
+// 1 / (|G| + eps): from the trace of G^T G, or as the first steps left it.
+__device__ __forceinline__ double poly_inv(const ortho_args &g, int64_t mat, double trace) {
+    return g.first ? 1.0 / (sqrt(trace) + (double)g.eps) : g.inv[mat];
+}
+
 // One tile: P in a wavefront's registers, and 1 / (|G| + eps).  Few enough
 // products for k_ortho_apply to do them itself, every workgroup of a matrix the
-// same (as a launch of its own: 32 x 4096 x 16 15.9 us for 14.5).
+// same (as a launch of its own: 32 x 4096 x 16 15.9 us for 14.5), where one pass is all.
 __device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, int lane, double &inv) {
     f64x4_t m = poly_part<1>(g, mat, 0, lane), one, pr;
     double d = 0.0;
@@ -251,7 +280,7 @@ __device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, in
         one[e] = mfma64_row(e, lane) == (lane & 15) ? 1.0 : 0.0;
         d += one[e] * m[e];
     }
-    inv = 1.0 / (sqrt(wave_sum64(d)) + (double)g.eps);
+    inv = poly_inv(g, mat, wave_sum64(d));
     const f64x4_t zero = {0.0, 0.0, 0.0, 0.0};
     m *= inv * inv;
     pr = one;
@@ -263,6 +292,16 @@ __device__ __forceinline__ f64x4_t poly_one(const ortho_args &g, int64_t mat, in
         m = mfma64_tile(t, q, zero);
     }
     return pr;
+}
+
+// As a launch of its own, where several passes follow each other.
+template <bool TALL> __global__ void __launch_bounds__(64) k_ortho_poly_one(ortho_args g) {
+    const int64_t mat = grid_index();
+    if (mat >= g.n) return;
+    const int lane = threadIdx.x & 63;
+    double inv;
+    poly_store<1, TALL>(g, mat, 0, 0, poly_one(g, mat, lane, inv), lane);
+    if (g.first && lane == 0) g.inv[mat] = inv;
 }
 
 // 2 or 4 tiles a side.  A step is three rounds with a barrier each: M M and from it
@@ -317,8 +356,8 @@ template <int W, bool TALL> __global__ void __launch_bounds__(poly_cfg<W>::WAVES
     double trace = s_trace[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) trace += s_trace[i];
-    const double inv = 1.0 / (sqrt(trace) + (double)g.eps);
-    if (threadIdx.x == 0) g.inv[mat] = inv;
+    const double inv = poly_inv(g, mat, trace);
+    if (g.first && threadIdx.x == 0) g.inv[mat] = inv;
     m *= inv * inv;
     if (own) put(s_m, ma, mb, m);
     __syncthreads();
@@ -408,8 +447,8 @@ template <bool TALL> __global__ void __launch_bounds__(768) k_ortho_poly8(ortho_
         if (lane == 0) s_trace = d;
     }
     __syncthreads();
-    const double inv = 1.0 / (sqrt(s_trace) + (double)g.eps);
-    if (threadIdx.x == 0) g.inv[mat] = inv;
+    const double inv = poly_inv(g, mat, s_trace);
+    if (g.first && threadIdx.x == 0) g.inv[mat] = inv;
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
 #pragma unroll
@@ -448,32 +487,57 @@ template <bool TALL> __global__ void __launch_bounds__(768) k_ortho_poly8(ortho_
     for (int o = 0; o < OWN; ++o) poly_store<W, TALL>(g, mat, ta[o], tb[o], pr[o], lane);
 }
 
+// P of the steps before and of these, P Q, by a wavefront a tile: transposed, Q P^T
+// (Q is symmetric, what lies in memory is P^T).
+template <int W> __global__ void __launch_bounds__(64) k_ortho_join(ortho_args g) {
+    constexpr int LD = 16 * W;
+    const int64_t item = grid_index(), mat = item / (W * W);
+    if (mat >= g.n) return;
+    const int tile = (int)(item - mat * (W * W)), lane = threadIdx.x & 63, p = lane & 15, kg = lane >> 4;
+    const double *q = g.poly + (mat * LD + tile / W * 16 + p) * LD, *pt = g.before + mat * LD * LD + tile % W * 16 + p;
+    f64x4_t c = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+    for (int k = 0; k < LD; k += 4) c = mfma64(q[k + kg], pt[(k + kg) * LD], c);
+    double *out = g.joined + (mat * LD + tile / W * 16) * LD + tile % W * 16 + p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[mfma64_row(e, lane) * LD] = c[e];
+}
+
 // ---------------------------------------------------------------------------
 // G P.  P lies in LDS (bf16: in three parts); the result's rows are P's, its
 // columns long-side indices, so that a lane holds neighbouring values of the
 // result in either layout.
 // ---------------------------------------------------------------------------
+// 4 neighbouring values, and back.
+__device__ __forceinline__ f32x4_t load_4(const float *p) { return *reinterpret_cast<const f32x4_t *>(p); }
+__device__ __forceinline__ f32x4_t load_4(const uint16_t *p) {
+    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+    return f32x4_t{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+}
+__device__ __forceinline__ void store_4(float *p, const f32x4_t &v) { *reinterpret_cast<f32x4_t *>(p) = v; }
+
 // fp32: 64-bit products.  tall: a block is 16 rows i of G, and a lane reads 4
 // neighbouring values j of one; wide: 64 columns i, and a lane reads 4
 // neighbouring ones of row j.
-template <int W, bool TALL> struct apply_f32 {
+template <int W, bool TALL> struct apply_f64 {
     static constexpr int LD = 16 * W + 4, CB = TALL && W > 1 ? 2 : 1, R4 = TALL ? W : 4 * W, S = TALL ? 1 : 4;
     f32x4_t x[R4];
 
-    __device__ __forceinline__ void load(const ortho_args &g, const float *in, int i0, int lane) {
+    template <typename E> __device__ __forceinline__ void load(const ortho_args &g, const E *in, int i0, int lane) {
         const int p = lane & 15, kg = lane >> 4, r = g.r;
 #pragma unroll
         for (int k = 0; k < R4; ++k) {
             // tall: j = 16 k + 4 kg + (0..3) of row i0 + p; wide: row j = 4 k + kg, columns i0 + 4 p + (0..3)
             const int j = TALL ? 16 * k + 4 * kg : 4 * k + kg, i = TALL ? i0 + p : i0 + 4 * p;
             x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            if (j < r && i < g.D)
-                x[k] = *reinterpret_cast<const f32x4_t *>(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
+            if (j < r && i < g.D) x[k] = load_4(in + (TALL ? (int64_t)i * r + j : (int64_t)j * g.D + i));
         }
     }
+    // G's value in product k: of row (tall) p or column (wide) 4 p + s of the block, and j as P's in place 4 k + kg
+    __device__ __forceinline__ double value(int k, int s) const { return (double)(TALL ? x[k >> 2][k & 3] : x[k][s]); }
 
-    __device__ __forceinline__ void store(const ortho_args &g, float *out, const double *s_p, double factor, int i0,
-                                          int lane) {
+    template <typename E>
+    __device__ __forceinline__ void store(const ortho_args &g, E *out, const double *s_p, double factor, int i0, int lane) {
         const int p = lane & 15, kg = lane >> 4, r = g.r;
 #pragma unroll 1                                           // (unrolled, the wide ones spill)
         for (int c0 = 0; c0 < W; c0 += CB) {
@@ -493,25 +557,25 @@ template <int W, bool TALL> struct apply_f32 {
                     const double a = s_p[c * LD + 4 * k + kg];
 #pragma unroll
                     for (int s = 0; s < S; ++s)
-                        acc[cb][s] = mfma64(a, (double)(TALL ? x[k >> 2][k & 3] : x[k][s]), acc[cb][s]);
+                        acc[cb][s] = mfma64(a, value(k, s), acc[cb][s]);
                 }
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
                 if constexpr (TALL) {
                     const int c = 16 * (c0 + cb) + 4 * kg, i = i0 + p;
                     if (c < r && i < g.D)
-                        *reinterpret_cast<f32x4_t *>(out + (int64_t)i * r + c) =
-                            f32x4_t{(float)(factor * acc[cb][0][0]), (float)(factor * acc[cb][0][1]),
-                                    (float)(factor * acc[cb][0][2]), (float)(factor * acc[cb][0][3])};
+                        store_4(out + (int64_t)i * r + c,
+                                f32x4_t{(float)(factor * acc[cb][0][0]), (float)(factor * acc[cb][0][1]),
+                                        (float)(factor * acc[cb][0][2]), (float)(factor * acc[cb][0][3])});
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int c = 16 * (c0 + cb) + mfma64_row(e, lane), i = i0 + 4 * p;
                         if (c < r && i < g.D)
-                            *reinterpret_cast<f32x4_t *>(out + (int64_t)c * g.D + i) =
-                                f32x4_t{(float)(factor * acc[cb][0][e]), (float)(factor * acc[cb][S > 1 ? 1 : 0][e]),
-                                        (float)(factor * acc[cb][S > 2 ? 2 : 0][e]),
-                                        (float)(factor * acc[cb][S > 3 ? 3 : 0][e])};
+                            store_4(out + (int64_t)c * g.D + i,
+                                    f32x4_t{(float)(factor * acc[cb][0][e]), (float)(factor * acc[cb][S > 1 ? 1 : 0][e]),
+                                            (float)(factor * acc[cb][S > 2 ? 2 : 0][e]),
+                                            (float)(factor * acc[cb][S > 3 ? 3 : 0][e])});
                     }
                 }
             }
@@ -652,7 +716,22 @@ template <bool F32, int W, bool TALL, typename V> __device__ __forceinline__ voi
     }
 }
 
-template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ortho_apply(ortho_args g) {
+// All of P, read by 256 threads.
+template <bool F32, int W, bool TALL> __device__ __forceinline__ void stage_poly(char *s_p, const double *p, double times) {
+    typedef double f64x2_t __attribute__((ext_vector_type(2)));
+    const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(p);
+    constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 ? 1 : PAIRS < 256 * 8 ? PAIRS / 256 : 8;
+    for (int i = threadIdx.x; i < PAIRS; i += 256 * STEP) {
+        f64x2_t v[STEP];
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) v[u] = poly[i + 256 * u];
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) stage_pair<F32, W, TALL>(s_p, i + 256 * u, F32 ? v[u] : v[u] * times);
+    }
+}
+
+// POLY: the one tile's steps are made here, P is not in memory.
+template <int DT, int W, bool TALL, bool POLY> __global__ void __launch_bounds__(256) k_ortho_apply(ortho_args g) {
     typedef typename elem<DT>::T E;
     constexpr bool F32 = DT == LORA_F32;
     constexpr int RP = W < 2 ? 32 : 16 * W, BLOCK = TALL ? 16 : F32 ? 64 : 128;
@@ -664,12 +743,21 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
     const E *in = (const E *)g.g + mat * g.D * g.r;
     E *out = (E *)g.out + mat * g.D * g.r;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    typename std::conditional<F32, apply_f32<W, TALL>, apply_bf16<W, TALL>>::type block;
+    typename std::conditional<F32, apply_f64<W, TALL>, apply_bf16<W, TALL>>::type block;
     int i0 = begin + wave * BLOCK;
     if (i0 < end) block.load(g, in, i0, lane);            // under way while P is staged
     double inv;
     typedef double f64x2_t __attribute__((ext_vector_type(2)));
-    if constexpr (W == 1) {
+    if (W == 1 && !F32 && threadIdx.x < 16) {             // the products' k 16..31
+        uint16_t *s = reinterpret_cast<uint16_t *>(s_p) + threadIdx.x * (RP + 8) + 16;
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4 *>(s + part * 16 * W * (RP + 8) + 8 * h) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if constexpr (POLY) {
+        static_assert(W == 1, "one tile");
         __shared__ __attribute__((aligned(16))) double s_tile[256];
         __shared__ double s_inv;
         if (wave == 0) {
@@ -687,26 +775,10 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
             const f64x2_t v = reinterpret_cast<const f64x2_t *>(s_tile)[threadIdx.x];
             stage_pair<F32, W, TALL>(s_p, threadIdx.x, F32 ? v : v * split_factor(g.scale, inv).times);
         }
-        if (!F32 && threadIdx.x < 16) {                   // the products' k 16..31
-            uint16_t *s = reinterpret_cast<uint16_t *>(s_p) + threadIdx.x * (RP + 8) + 16;
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<uint4 *>(s + part * 16 * W * (RP + 8) + 8 * h) = make_uint4(0u, 0u, 0u, 0u);
-        }
     } else {
         inv = g.inv[mat];
         const double times = F32 ? 1.0 : split_factor(g.scale, inv).times;
-        const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(g.poly + mat * 256 * W * W);
-        constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 * 8 ? PAIRS / 256 : 8;
-        for (int i = threadIdx.x; i < PAIRS; i += 256 * STEP) {
-            f64x2_t v[STEP];
-#pragma unroll
-            for (int u = 0; u < STEP; ++u) v[u] = poly[i + 256 * u];
-#pragma unroll
-            for (int u = 0; u < STEP; ++u) stage_pair<F32, W, TALL>(s_p, i + 256 * u, F32 ? v[u] : v[u] * times);
-        }
+        stage_poly<F32, W, TALL>(s_p, g.poly + mat * 256 * W * W, times);
     }
     __syncthreads();
     const double factor = (double)g.scale * inv;
@@ -719,9 +791,71 @@ template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ort
 }
 
 // ---------------------------------------------------------------------------
+// (G P)^T G P, as k_ortho_gram's sums.  A block's G P comes out of the products (A: G's
+// rows i, B: P's columns) with k = i of a product for the sums where its lanes have it.
+// Four wavefronts share a split's blocks; of 8 tiles a side two of them make the same G P
+// and half the sums each.
+// ---------------------------------------------------------------------------
+template <int DT, int W, bool TALL, int HALF, int N>
+__device__ __forceinline__ void regram_wave(const ortho_args &g, const typename elem<DT>::T *in, const double *s_p,
+                                            int begin, int end, int stride, int lane, f64x4_t (&acc)[N]) {
+    typedef apply_f64<W, TALL> A;
+    constexpr int BLOCK = TALL ? 16 : 64;
+    const int p = lane & 15, kg = lane >> 4;
+    A block;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    for (int i0 = begin; i0 < end; i0 += stride * BLOCK) {
+        block.load(g, in, i0, lane);
+#pragma unroll 1                                           // (unrolled, the wide ones spill)
+        for (int s = 0; s < A::S; ++s) {
+            f64x4_t y[W];                                 // element e: i = 4 e + kg, column ortho_index(c, p)
+#pragma unroll
+            for (int c = 0; c < W; ++c) y[c] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int k = 0; k < 4 * W; ++k) {
+                double x = block.value(k, 0);
+                if constexpr (!TALL) x = s == 0 ? x : s == 1 ? block.value(k, 1) : s == 2 ? block.value(k, 2) : block.value(k, 3);
+#pragma unroll
+                for (int c = 0; c < W; ++c) y[c] = mfma64(x, s_p[ortho_index<W, TALL>(c, p) * A::LD + 4 * k + kg], y[c]);
+                if constexpr (W > 2) asm volatile("" ::: "memory");   // P's values are read as they are wanted (all at once, they spill)
+            }
+#pragma unroll
+            for (int a = 0; a < W; ++a)
+                if (gram_owns<W>(HALF, a))
+#pragma unroll
+                    for (int b = 0; b <= a; ++b)
+                        acc[gram_at<W>(HALF, a, b)] = mfma64_tile(y[a], y[b], acc[gram_at<W>(HALF, a, b)]);
+        }
+    }
+}
+
+template <int DT, int W, bool TALL> __global__ void __launch_bounds__(256) k_ortho_regram(ortho_args g) {
+    constexpr int NT = ortho_tiles(W), HALVES = W == 8 ? 2 : 1, KW = 4 / HALVES, N = NT / HALVES;
+    constexpr int P_BYTES = 16 * W * apply_f64<W, TALL>::LD * 8, SUMS = (KW - 1) * NT * 64 * 32;
+    __shared__ __attribute__((aligned(32))) char smem[P_BYTES > SUMS ? P_BYTES : SUMS];
+    const int64_t item = grid_index();
+    if (item >= (int64_t)g.n * g.splits) return;
+    const int64_t mat = item / g.splits;
+    const int split = (int)(item - mat * g.splits), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int kw = wave / HALVES, half = wave % HALVES;
+    const typename elem<DT>::T *in = (const typename elem<DT>::T *)g.g + mat * g.D * g.r;
+    stage_poly<true, W, TALL>(smem, g.before + mat * 256 * W * W, 1.0);
+    __syncthreads();
+    const double *s_p = reinterpret_cast<const double *>(smem);
+    // a chunk is whole blocks, but for the last of G, whose loads stop at D
+    const int begin = split * g.chunk + kw * (TALL ? 16 : 64), end = min(g.D, (split + 1) * g.chunk);
+    f64x4_t acc[N];
+    if (half) regram_wave<DT, W, TALL, 1>(g, in, s_p, begin, end, KW, lane, acc);
+    else regram_wave<DT, W, TALL, 0>(g, in, s_p, begin, end, KW, lane, acc);
+    __syncthreads();                                      // P's place is the sums' now
+    gram_finish<W, KW>(g, acc, reinterpret_cast<f64x4_t(*)[NT][64]>(smem), item, kw, half, lane);
+}
+
+// ---------------------------------------------------------------------------
 struct ortho_layout {
     int32_t r, D, W, splits, chunk;
-    size_t part, poly, inv, total;
+    size_t part, poly, join[2], inv, total;
 };
 
 static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
@@ -739,6 +873,9 @@ static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
     size_t o = 0;
     L.part = o;   o = align256(o + (size_t)n * L.splits * ortho_tiles(L.W) * 256 * 8);
     L.poly = o;   o = align256(o + (size_t)n * 256 * L.W * L.W * 8);
+    for (size_t &j : L.join) {
+        j = o;    o = align256(o + (size_t)n * 256 * L.W * L.W * 8);
+    }
     L.inv = o;    o = align256(o + (size_t)n * 8);
     L.total = o;
     return L;
@@ -746,24 +883,89 @@ static ortho_layout make_ortho_layout(int32_t n, int32_t rows, int32_t cols) {
 
 size_t ortho_workspace_bytes(int32_t n, int32_t rows, int32_t cols) { return make_ortho_layout(n, rows, cols).total; }
 
-template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, hipStream_t s) {
-    hipLaunchKernelGGL((k_ortho_gram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits), dim3(gram_cfg<W>::WAVES * 64), 0, s, g);
-    if constexpr (W == 8) hipLaunchKernelGGL(k_ortho_poly8<TALL>, grid_of(g.n), dim3(768), 0, s, g);
-    else if constexpr (W > 1) hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
+struct ortho_steps {
+    const float *coef;                 // [n][3], host
+    int32_t n;
+    double *join[2];                   // P of several passes, in turn
+};
+
+// The steps in passes (see the top): the first step of each, and their number.
+constexpr double kPassGrowth = 0x1p22, kMostGrowth = 0x1p30;
+static int ortho_passes(const float *coef, int steps, int (&first)[kMaxOrthoSteps + 1]) {
+    int n = 0;
+    double growth = 1.0;                                  // the largest product of c0^2 over steps of the pass up to here
+    for (int i = 0; i < steps; ++i) {
+        const double c = (double)coef[3 * i] * coef[3 * i], next = growth * c;
+        if (i == 0 || next > kPassGrowth) {
+            first[n++] = i;
+            growth = c > 1.0 ? c : 1.0;
+        } else {
+            growth = next > 1.0 ? next : 1.0;
+        }
+    }
+    first[n] = steps;
+    return n;
+}
+
+bool ortho_steps_ok(const float *coef, int32_t steps) {
+    double growth = 1.0;
+    for (int i = 0; i < steps; ++i) {
+        growth *= fabs((double)coef[3 * i]);
+        if (growth > kMostGrowth) return false;
+        if (growth < 1.0) growth = 1.0;
+    }
+    return true;
+}
+
+template <int DT, int W, bool TALL, bool POLY> static void launch_apply(ortho_args g, hipStream_t s) {
     // about three workgroups a CU (two where each makes P), of whole rounds of their wavefronts' blocks
     constexpr int ROUND = 4 * (TALL ? 16 : DT == LORA_F32 ? 64 : 128);
     int blocks = ceil_div(W == 1 ? 512 : 768, g.n);
     if (blocks > ceil_div(g.D, ROUND)) blocks = ceil_div(g.D, ROUND);
     g.rows = ceil_div(ceil_div(g.D, blocks), ROUND) * ROUND;
     g.blocks = ceil_div(g.D, g.rows);
-    hipLaunchKernelGGL((k_ortho_apply<DT, W, TALL>), grid_of((int64_t)g.n * g.blocks), dim3(256), 0, s, g);
+    hipLaunchKernelGGL((k_ortho_apply<DT, W, TALL, POLY>), grid_of((int64_t)g.n * g.blocks), dim3(256), 0, s, g);
 }
 
-template <int DT, bool TALL> static void launch_ortho_w(ortho_args &g, int W, hipStream_t s) {
-    if (W == 1) launch_ortho_cfg<DT, 1, TALL>(g, s);
-    else if (W == 2) launch_ortho_cfg<DT, 2, TALL>(g, s);
-    else if (W == 4) launch_ortho_cfg<DT, 4, TALL>(g, s);
-    else launch_ortho_cfg<DT, 8, TALL>(g, s);
+template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, const ortho_steps &c, hipStream_t s) {
+    int first[kMaxOrthoSteps + 1];
+    const int passes = ortho_passes(c.coef, c.n, first);
+    double *const own = g.poly;
+    for (int i = 0; i < passes; ++i) {
+        g.first = i == 0;
+        g.steps = first[i + 1] - first[i];
+        for (int j = 0; j < 3 * g.steps; ++j) g.coef[j / 3][j % 3] = c.coef[3 * first[i] + j];
+        if (i > 0) {
+            g.before = g.poly;
+            g.joined = c.join[i & 1];
+            g.poly = own;
+            hipLaunchKernelGGL((k_ortho_regram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits), dim3(256), 0, s, g);
+        } else {
+            if (passes > 1) g.poly = c.join[0];
+            hipLaunchKernelGGL((k_ortho_gram<DT, W, TALL>), grid_of((int64_t)g.n * g.splits),
+                               dim3(gram_cfg<W>::WAVES * 64), 0, s, g);
+        }
+        if constexpr (W == 1) {
+            if (passes == 1) return launch_apply<DT, W, TALL, true>(g, s);
+            hipLaunchKernelGGL(k_ortho_poly_one<TALL>, grid_of(g.n), dim3(64), 0, s, g);
+        } else if constexpr (W == 8) {
+            hipLaunchKernelGGL(k_ortho_poly8<TALL>, grid_of(g.n), dim3(768), 0, s, g);
+        } else {
+            hipLaunchKernelGGL((k_ortho_poly<W, TALL>), grid_of(g.n), dim3(poly_cfg<W>::WAVES * 64), 0, s, g);
+        }
+        if (i > 0) {
+            hipLaunchKernelGGL(k_ortho_join<W>, grid_of((int64_t)g.n * W * W), dim3(64), 0, s, g);
+            g.poly = g.joined;
+        }
+    }
+    launch_apply<DT, W, TALL, false>(g, s);
+}
+
+template <int DT, bool TALL> static void launch_ortho_w(ortho_args &g, const ortho_steps &c, int W, hipStream_t s) {
+    if (W == 1) launch_ortho_cfg<DT, 1, TALL>(g, c, s);
+    else if (W == 2) launch_ortho_cfg<DT, 2, TALL>(g, c, s);
+    else if (W == 4) launch_ortho_cfg<DT, 4, TALL>(g, c, s);
+    else launch_ortho_cfg<DT, 8, TALL>(g, c, s);
 }
 
 lora_status_t launch_orthogonalize(const void *in, int32_t n, int32_t rows, int32_t cols, int32_t dtype,
@@ -781,18 +983,16 @@ lora_status_t launch_orthogonalize(const void *in, int32_t n, int32_t rows, int3
     g.r = L.r;
     g.splits = L.splits;
     g.chunk = L.chunk;
-    g.steps = steps;
     g.eps = eps;
     g.scale = scale;
-    for (int i = 0; i < steps; ++i)
-        for (int j = 0; j < 3; ++j) g.coef[i][j] = coef[3 * i + j];
+    const ortho_steps c{coef, steps, {ws_ptr<double>(ws, L.join[0]), ws_ptr<double>(ws, L.join[1])}};
     const bool tall = rows >= cols;
     if (dtype == LORA_F32) {
-        if (tall) launch_ortho_w<LORA_F32, true>(g, L.W, s);
-        else launch_ortho_w<LORA_F32, false>(g, L.W, s);
+        if (tall) launch_ortho_w<LORA_F32, true>(g, c, L.W, s);
+        else launch_ortho_w<LORA_F32, false>(g, c, L.W, s);
     } else {
-        if (tall) launch_ortho_w<LORA_BF16, true>(g, L.W, s);
-        else launch_ortho_w<LORA_BF16, false>(g, L.W, s);
+        if (tall) launch_ortho_w<LORA_BF16, true>(g, c, L.W, s);
+        else launch_ortho_w<LORA_BF16, false>(g, c, L.W, s);
     }
     return hip_status(hipGetLastError());
 }

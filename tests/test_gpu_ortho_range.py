@@ -1,0 +1,88 @@
+"""lora_orthogonalize over the steps it accepts, on matrices of fewer directions than columns (the gradient of an
+adapter with fewer rows in the batch than ranks): against the steps on X in extended precision, on the CPU.
+
+Bound, relative to the norm of the row of X = g / |g| that a result's row is made of.  Directions that a matrix does not
+have hold the 64-bit roundings of its sums, and every step multiplies them by its c0.  growth: the largest product of c0
+over steps up to the last.  16 steps of 4 products whose sums have r <= 72 terms, root of r roundings each, are at most 2^9
+roundings on the way to one value, independent too: their root, 2^4.5, and 4 deviations: 2^-53 2^6.5 growth.  Where
+the steps go on from M = X^T X alone, P's products lose their symmetry by growth^2 root(r) 2^-53 in a step (P is growth
+where M is nothing, and M's part there is as far off), the steps before add 0.4 of it, and a tile stands for its mirror
+image: 4 deviations of 3 products, 10 root(r) 2^-53 growth^2, and M is made anew before growth^2 passes 2^22.
+The result is rounded once to its type.  The reference's own roundings (2^-64) are below 2^-10 of all that."""
+import numpy as np
+import pytest
+import torch
+
+from helpers_block import HALF, STEP32
+from rank_adapter_gemm_amd import lora as L
+from test_gpu_orthogonalize import EPS, F32, run
+
+pytestmark = pytest.mark.gpu
+STEP = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    L.load()
+
+
+def few_directions(kind, D, r, seed):
+    rng = np.random.default_rng(seed)
+    if kind == "rows":                                    # exactly so: three rows of values, zeros else
+        g = np.zeros((D, r), np.float32)
+        g[rng.choice(D, 3, replace=False)] = rng.standard_normal((3, r))
+    elif kind == "repeated":                              # exactly so: four rows, over and over
+        g = rng.standard_normal((4, r)).astype(np.float32)[rng.integers(0, 4, D)]
+    elif kind == "graded":                                # down to 1e-8 of the largest
+        u, v = (np.linalg.qr(rng.standard_normal((k, r)))[0] for k in (D, r))
+        g = (u * 10.0 ** (-8 * np.arange(r) / r)) @ v.T
+    else:                                                 # up to the type's rounding
+        g = rng.standard_normal((D, kind)) @ rng.standard_normal((kind, r))
+    return torch.from_numpy(np.asarray(g, np.float32)) * 1e-3
+
+
+def steps_extended(g, coef, eps):
+    x = g.double().numpy().astype(np.longdouble)
+    x = x / (np.sqrt((x * x).sum()) + np.longdouble(np.float32(eps)))
+    x0 = x
+    for c in coef:
+        a, b, c2 = (np.longdouble(np.float32(v)) for v in c)
+        m = x.T @ x
+        x = a * x + x @ (b * m + c2 * (m @ m))
+    return x0, x
+
+
+def check_range(dtype, kinds, D, r, wide, coef):
+    g = torch.stack([few_directions(k, D, r, 10 * i + r) for i, k in enumerate(kinds)]).to(dtype)
+    arg = (g.transpose(1, 2) if wide else g).contiguous().cuda()
+    out = run(arg, coef).cpu().double()
+    out = out.transpose(1, 2) if wide else out
+    growth = 1.0
+    for c in coef:
+        growth = max(growth, 1.0) * abs(float(np.float32(c[0])))
+    growth = max(growth, 1.0)
+    for i, k in enumerate(kinds):
+        x0, ref = steps_extended(g[i], coef, EPS)
+        ref = ref.astype(np.float64)
+        rows = np.sqrt((x0 * x0).sum(1, keepdims=True)).astype(np.float64)
+        tol = 2.0 ** -53 * (2.0 ** 6.5 * growth + 10 * r ** 0.5 * min(growth ** 2, 2.0 ** 22)) * rows
+        tol = tol + 4 * STEP32 * np.abs(ref)
+        tol = tol * (1 + HALF[dtype]) + HALF[dtype] * np.abs(ref) + 2.0 ** -120
+        worst = float((np.abs(out[i].numpy() - ref) / tol).max())
+        assert worst <= 1.0, (k, len(coef), worst, float(np.abs(out[i].numpy() - ref).max()))
+
+
+@pytest.mark.parametrize("count", [5, 8, 9, 10, 12, 14, 16])
+@pytest.mark.parametrize("r,wide", [(16, False), (16, True), (8, False), (32, False), (64, True), (72, False)])
+def test_fp32_of_few_directions(r, wide, count):
+    check_range(F32, [1, 5, "rows", "repeated", "graded"], 520, r, wide, [STEP] * count)
+
+
+@pytest.mark.parametrize("dtype", [F32])
+def test_steps_that_grow_and_shrink(dtype):
+    """Large and small c0 in turn, and steps of one kind after another."""
+    for coef in ([STEP, STEP, (1.875, -1.25, 0.375)] * 4, [(1.875, -1.25, 0.375)] * 16,
+                 [(0.25, 0.0, 0.0)] * 4 + [STEP] * 12, [STEP] * 11 + [(1.5, -0.5, 0.0)] * 5):
+        check_range(dtype, [1, "rows", "graded"], 264, 24, False, coef)
