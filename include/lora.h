@@ -713,7 +713,8 @@ lora_status_t lora_linear_act_backward(const void *x, const void *W, int32_t T, 
  * past these).  Zero rows and columns (ranks past an adapter's) and zero matrices
  * stay zero; a matrix with infinite or NaN values gives NaN, and leaves the others as
  * they are.  eps finite and positive, scale finite.  Sums of products of g and the steps are in 64 bits, and
- * for fp32 also the last product; the order of the sums is fixed.  ws DEVICE, ws_bytes at least
+ * so is the last product, but for bf16 g and steps whose polynomial is at most 2^11 (6 of
+ * the above), where it is in fp32 sums of exact products; the order of the sums is fixed.  ws DEVICE, ws_bytes at least
  * lora_workspace_bytes_orthogonalize (0 on bad arguments); it needs no lora_workspace_init. */
 #define LORA_MAX_ORTHO_SIDE 128
 #define LORA_MAX_ORTHO_STEPS 16

@@ -18,15 +18,17 @@
 // c0^2 would pass 2^22, 6 such steps, M is made anew from X itself, that is from G P
 // (k_ortho_regram, one more read of G), and the next steps' matrix is joined to P by
 // a product of all its tiles (k_ortho_join: P is symmetric but for roundings, and c0's
-// product makes those large).  What is left is c0's product times 2^-53, as with the steps on
-// X in 64 bits; callers may ask for 2^30.
+// product makes those large): 7 steps of 32 x 4096 x 16 take 28 us, 6 14.6.  What is
+// left is c0's product times 2^-53, as with the steps on X in 64 bits; callers may ask
+// for 2^30.
 //
 // 64 bits: small singular values are amplified, by c0 at every step (485-fold in 5
 // steps of 3.4445), and an error e of M by up to 3e4 e relative to what those
 // directions get.  32-bit sums of M (6e-8) would show in the result; 64-bit ones
-// (v_mfma_f64_16x16x4_f64) do not.  So M, the steps and P are 64-bit; G P is 64-bit
-// products for fp32 G, and exact bf16 products of P in three parts, summed in fp32,
-// for bf16 G, whose result is rounded to bf16.
+// (v_mfma_f64_16x16x4_f64) do not.  So M, the steps and P are 64-bit, and G P is 64-bit
+// products.  For bf16 G and P of at most 2^11, 6 such steps, it is exact bf16 products of P
+// in three parts, summed in fp32: P's large values, where G has nothing, cancel there to
+// 2^-24 2^11 of a row, a sixteenth of the result's half step.
 //
 // Tiles: W tiles of 16 indices of the short side hold it (W = 1, 2, 4, 8); only those
 // on and under the diagonal are computed.  G goes from memory to the products
@@ -515,8 +517,11 @@ __device__ __forceinline__ f32x4_t load_4(const uint16_t *p) {
     return f32x4_t{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
 }
 __device__ __forceinline__ void store_4(float *p, const f32x4_t &v) { *reinterpret_cast<f32x4_t *>(p) = v; }
+__device__ __forceinline__ void store_4(uint16_t *p, const f32x4_t &v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
 
-// fp32: 64-bit products.  tall: a block is 16 rows i of G, and a lane reads 4
+// 64-bit products.  tall: a block is 16 rows i of G, and a lane reads 4
 // neighbouring values j of one; wide: 64 columns i, and a lane reads 4
 // neighbouring ones of row j.
 template <int W, bool TALL> struct apply_f64 {
@@ -583,7 +588,7 @@ template <int W, bool TALL> struct apply_f64 {
     }
 };
 
-// bf16: v_mfma_f32_16x16x32_bf16 (lane l: A row and B column l % 16, k = 8 (l / 16)
+// bf16 products: v_mfma_f32_16x16x32_bf16 (lane l: A row and B column l % 16, k = 8 (l / 16)
 // + (0..7); the result's row 4 (l / 16) + e, column l % 16).  tall: a block is 16
 // rows i, and a lane reads 8 neighbouring values of one; wide: 128 columns, and a
 // lane reads 8 neighbouring columns of each of 8 rows j, and exchanges rows for
@@ -686,9 +691,9 @@ struct split_factor {
 };
 
 // Values j, j + 1 of row c of P, pair i of the matrix, to their place in LDS.
-template <bool F32, int W, bool TALL, typename V> __device__ __forceinline__ void stage_pair(char *s_p, int i, V v) {
+template <bool F64, int W, bool TALL, typename V> __device__ __forceinline__ void stage_pair(char *s_p, int i, V v) {
     const int c = i / (8 * W), j = 2 * (i % (8 * W));
-    if constexpr (F32) {
+    if constexpr (F64) {
         double *s = reinterpret_cast<double *>(s_p) + c * (16 * W + 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -698,17 +703,17 @@ template <bool F32, int W, bool TALL, typename V> __device__ __forceinline__ voi
         }
     } else {
         constexpr int LD = (W < 2 ? 32 : 16 * W) + 8;
-        // three bf16 parts carry the value to 2^-27: hi = bf16(f), then what is left
+        // three bf16 parts carry the value to 2^-27 (a part what the ones before leave, to 2^-9)
         uint32_t o[3] = {0u, 0u, 0u};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float f = (float)v[h];
-            const uint32_t hi = f32_to_bf16_bits(f);
-            const float r1 = f - __uint_as_float(hi << 16);
-            const uint32_t mid = f32_to_bf16_bits(r1);
-            o[0] |= (hi & 0xffffu) << (16 * h);
-            o[1] |= (mid & 0xffffu) << (16 * h);
-            o[2] |= (f32_to_bf16_bits(r1 - __uint_as_float(mid << 16)) & 0xffffu) << (16 * h);
+            double rest = v[h];
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                const uint32_t b = f32_to_bf16_bits((float)rest) & 0xffffu;
+                o[part] |= b << (16 * h);
+                rest -= (double)__uint_as_float(b << 16);
+            }
         }
 #pragma unroll
         for (int part = 0; part < 3; ++part)
@@ -717,7 +722,7 @@ template <bool F32, int W, bool TALL, typename V> __device__ __forceinline__ voi
 }
 
 // All of P, read by 256 threads.
-template <bool F32, int W, bool TALL> __device__ __forceinline__ void stage_poly(char *s_p, const double *p, double times) {
+template <bool F64, int W, bool TALL> __device__ __forceinline__ void stage_poly(char *s_p, const double *p, double times) {
     typedef double f64x2_t __attribute__((ext_vector_type(2)));
     const f64x2_t *poly = reinterpret_cast<const f64x2_t *>(p);
     constexpr int PAIRS = 128 * W * W, STEP = PAIRS < 256 ? 1 : PAIRS < 256 * 8 ? PAIRS / 256 : 8;
@@ -726,16 +731,16 @@ template <bool F32, int W, bool TALL> __device__ __forceinline__ void stage_poly
 #pragma unroll
         for (int u = 0; u < STEP; ++u) v[u] = poly[i + 256 * u];
 #pragma unroll
-        for (int u = 0; u < STEP; ++u) stage_pair<F32, W, TALL>(s_p, i + 256 * u, F32 ? v[u] : v[u] * times);
+        for (int u = 0; u < STEP; ++u) stage_pair<F64, W, TALL>(s_p, i + 256 * u, F64 ? v[u] : v[u] * times);
     }
 }
 
-// POLY: the one tile's steps are made here, P is not in memory.
-template <int DT, int W, bool TALL, bool POLY> __global__ void __launch_bounds__(256) k_ortho_apply(ortho_args g) {
+// POLY: the one tile's steps are made here, P is not in memory.  F64: 64-bit products.
+template <int DT, int W, bool TALL, bool POLY, bool F64> __global__ void __launch_bounds__(256) k_ortho_apply(ortho_args g) {
     typedef typename elem<DT>::T E;
-    constexpr bool F32 = DT == LORA_F32;
-    constexpr int RP = W < 2 ? 32 : 16 * W, BLOCK = TALL ? 16 : F32 ? 64 : 128;
-    __shared__ __attribute__((aligned(16))) char s_p[F32 ? 16 * W * (16 * W + 4) * 8 : 3 * 16 * W * (RP + 8) * 2];
+    static_assert(F64 || DT == LORA_BF16, "fp32 has 64-bit products only");
+    constexpr int RP = W < 2 ? 32 : 16 * W, BLOCK = TALL ? 16 : F64 ? 64 : 128;
+    __shared__ __attribute__((aligned(16))) char s_p[F64 ? 16 * W * (16 * W + 4) * 8 : 3 * 16 * W * (RP + 8) * 2];
     const int64_t item = grid_index();
     if (item >= (int64_t)g.n * g.blocks) return;
     const int64_t mat = item / g.blocks;
@@ -743,12 +748,12 @@ template <int DT, int W, bool TALL, bool POLY> __global__ void __launch_bounds__
     const E *in = (const E *)g.g + mat * g.D * g.r;
     E *out = (E *)g.out + mat * g.D * g.r;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    typename std::conditional<F32, apply_f64<W, TALL>, apply_bf16<W, TALL>>::type block;
+    typename std::conditional<F64, apply_f64<W, TALL>, apply_bf16<W, TALL>>::type block;
     int i0 = begin + wave * BLOCK;
     if (i0 < end) block.load(g, in, i0, lane);            // under way while P is staged
     double inv;
     typedef double f64x2_t __attribute__((ext_vector_type(2)));
-    if (W == 1 && !F32 && threadIdx.x < 16) {             // the products' k 16..31
+    if (W == 1 && !F64 && threadIdx.x < 16) {             // the products' k 16..31
         uint16_t *s = reinterpret_cast<uint16_t *>(s_p) + threadIdx.x * (RP + 8) + 16;
 #pragma unroll
         for (int part = 0; part < 3; ++part)
@@ -773,18 +778,18 @@ template <int DT, int W, bool TALL, bool POLY> __global__ void __launch_bounds__
         inv = s_inv;
         if (threadIdx.x < 128) {
             const f64x2_t v = reinterpret_cast<const f64x2_t *>(s_tile)[threadIdx.x];
-            stage_pair<F32, W, TALL>(s_p, threadIdx.x, F32 ? v : v * split_factor(g.scale, inv).times);
+            stage_pair<F64, W, TALL>(s_p, threadIdx.x, F64 ? v : v * split_factor(g.scale, inv).times);
         }
     } else {
         inv = g.inv[mat];
-        const double times = F32 ? 1.0 : split_factor(g.scale, inv).times;
-        stage_poly<F32, W, TALL>(s_p, g.poly + mat * 256 * W * W, times);
+        const double times = F64 ? 1.0 : split_factor(g.scale, inv).times;
+        stage_poly<F64, W, TALL>(s_p, g.poly + mat * 256 * W * W, times);
     }
     __syncthreads();
     const double factor = (double)g.scale * inv;
     const int exponent = split_factor(g.scale, inv).exponent;
     for (; i0 < end; i0 += 4 * BLOCK) {
-        if constexpr (F32) block.store(g, out, reinterpret_cast<const double *>(s_p), factor, i0, lane);
+        if constexpr (F64) block.store(g, out, reinterpret_cast<const double *>(s_p), factor, i0, lane);
         else block.store(g, out, reinterpret_cast<const uint16_t *>(s_p), exponent, i0, lane);
         if (i0 + 4 * BLOCK < end) block.load(g, in, i0 + 4 * BLOCK, lane);
     }
@@ -890,7 +895,7 @@ struct ortho_steps {
 };
 
 // The steps in passes (see the top): the first step of each, and their number.
-constexpr double kPassGrowth = 0x1p22, kMostGrowth = 0x1p30;
+constexpr double kPassGrowth = 0x1p22, kMostGrowth = 0x1p30, kPartsMost = 0x1p11, kPartsLeast = 0x1p-20;
 static int ortho_passes(const float *coef, int steps, int (&first)[kMaxOrthoSteps + 1]) {
     int n = 0;
     double growth = 1.0;                                  // the largest product of c0^2 over steps of the pass up to here
@@ -917,20 +922,51 @@ bool ortho_steps_ok(const float *coef, int32_t steps) {
     return true;
 }
 
-template <int DT, int W, bool TALL, bool POLY> static void launch_apply(ortho_args g, hipStream_t s) {
+// What no value of P passes while X is below its bound: the product of the largest |c0 + c1 m
+// + c2 m^2| of each step, m the squares of the singular values, at most 1 before the first.
+static double ortho_bound(const float *coef, int steps) {
+    double x = 1.0, bound = 1.0;                          // x: of the singular values
+    for (int i = 0; i < steps; ++i) {
+        const double c0 = coef[3 * i], c1 = coef[3 * i + 1], c2 = coef[3 * i + 2], most = x * x;
+        auto q = [&](double m) { return fabs(c0 + m * (c1 + m * c2)); };
+        double qs = fmax(q(0.0), q(most)), xs = x * q(most);
+        auto look = [&](double m, bool turn_of_q) {       // where the derivative of q, or of x q, is zero
+            if (!(m > 0.0 && m < most)) return;
+            if (turn_of_q) qs = fmax(qs, q(m));
+            else xs = fmax(xs, sqrt(m) * q(m));
+        };
+        look(-c1 / (2 * c2), true);
+        const double root = sqrt(9 * c1 * c1 - 20 * c0 * c2);   // c0 + 3 c1 m + 5 c2 m^2 = 0
+        look((-3 * c1 + root) / (10 * c2), false);
+        look((-3 * c1 - root) / (10 * c2), false);
+        if (c2 == 0.0) look(-c0 / (3 * c1), false);
+        bound *= qs;
+        x = xs;
+    }
+    return bound;
+}
+
+template <int DT, int W, bool TALL, bool POLY, bool F64> static void launch_apply(ortho_args g, hipStream_t s) {
     // about three workgroups a CU (two where each makes P), of whole rounds of their wavefronts' blocks
-    constexpr int ROUND = 4 * (TALL ? 16 : DT == LORA_F32 ? 64 : 128);
+    constexpr int ROUND = 4 * (TALL ? 16 : F64 ? 64 : 128);
     int blocks = ceil_div(W == 1 ? 512 : 768, g.n);
     if (blocks > ceil_div(g.D, ROUND)) blocks = ceil_div(g.D, ROUND);
     g.rows = ceil_div(ceil_div(g.D, blocks), ROUND) * ROUND;
     g.blocks = ceil_div(g.D, g.rows);
-    hipLaunchKernelGGL((k_ortho_apply<DT, W, TALL, POLY>), grid_of((int64_t)g.n * g.blocks), dim3(256), 0, s, g);
+    hipLaunchKernelGGL((k_ortho_apply<DT, W, TALL, POLY, F64>), grid_of((int64_t)g.n * g.blocks), dim3(256), 0, s, g);
 }
 
 template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, const ortho_steps &c, hipStream_t s) {
     int first[kMaxOrthoSteps + 1];
     const int passes = ortho_passes(c.coef, c.n, first);
     double *const own = g.poly;
+    // bf16 products of P's parts where they carry it, neither large nor near the smallest
+    // numbers (5 steps of 32 x 4096 x 16: 14.4 us, by 64-bit products 15.1; 8 x 64 x 14336 61 and 80)
+    bool parts = false;
+    if (DT == LORA_BF16 && passes == 1) {
+        const double bound = ortho_bound(c.coef, c.n);
+        parts = bound <= kPartsMost && bound >= kPartsLeast;
+    }
     for (int i = 0; i < passes; ++i) {
         g.first = i == 0;
         g.steps = first[i + 1] - first[i];
@@ -946,7 +982,9 @@ template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, 
                                dim3(gram_cfg<W>::WAVES * 64), 0, s, g);
         }
         if constexpr (W == 1) {
-            if (passes == 1) return launch_apply<DT, W, TALL, true>(g, s);
+            if constexpr (DT == LORA_BF16)
+                if (parts) return launch_apply<DT, W, TALL, true, false>(g, s);
+            if (passes == 1) return launch_apply<DT, W, TALL, true, true>(g, s);
             hipLaunchKernelGGL(k_ortho_poly_one<TALL>, grid_of(g.n), dim3(64), 0, s, g);
         } else if constexpr (W == 8) {
             hipLaunchKernelGGL(k_ortho_poly8<TALL>, grid_of(g.n), dim3(768), 0, s, g);
@@ -958,7 +996,9 @@ template <int DT, int W, bool TALL> static void launch_ortho_cfg(ortho_args &g, 
             g.poly = g.joined;
         }
     }
-    launch_apply<DT, W, TALL, false>(g, s);
+    if constexpr (DT == LORA_BF16 && W > 1)
+        if (parts) return launch_apply<DT, W, TALL, false, false>(g, s);
+    launch_apply<DT, W, TALL, false, true>(g, s);
 }
 
 template <int DT, bool TALL> static void launch_ortho_w(ortho_args &g, const ortho_steps &c, int W, hipStream_t s) {
