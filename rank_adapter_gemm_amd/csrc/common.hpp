@@ -399,7 +399,7 @@ lora_status_t launch_layernorm_backward(const void *dy, const void *dres, const 
                                         void *dx, void *dweight, void *dbias, float *part, hipStream_t s);
 // part fp32 [groups][n], its columns added up in a fixed order: the first d into
 // out0, the rest into out1 (either may be null), of dtype.
-lora_status_t launch_column_sums(const float *part, int32_t groups, int32_t n, int32_t d, int32_t dtype, void *out0,
+lora_status_t launch_column_sums(const float *part, int32_t groups, int64_t n, int32_t d, int32_t dtype, void *out0,
                                  void *out1, hipStream_t s);
 
 // out = scale times the Newton-Schulz steps (coef [steps][3], host) on each of n

@@ -416,14 +416,14 @@ template <int DT> __global__ void __launch_bounds__(256) k_layernorm_sums_wide(l
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) k_column_sums(const float *part, int32_t groups, int32_t n, int32_t d,
+__global__ void __launch_bounds__(256) k_column_sums(const float *part, int32_t groups, int64_t n, int32_t d,
                                                      typename elem<DT>::T *out0, typename elem<DT>::T *out1) {
-    column_sums<DT>(part, groups, n, d, out0, out1, blockIdx.x);
+    column_sums<DT>(part, groups, n, d, out0, out1, grid_index());
 }
 
-lora_status_t launch_column_sums(const float *part, int32_t groups, int32_t n, int32_t d, int32_t dtype, void *out0,
+lora_status_t launch_column_sums(const float *part, int32_t groups, int64_t n, int32_t d, int32_t dtype, void *out0,
                                  void *out1, hipStream_t s) {
-    const dim3 grid((n + 63) / 64);
+    const dim3 grid = grid_of((n + 63) / 64);
     if (dtype == LORA_F32)
         hipLaunchKernelGGL(k_column_sums<LORA_F32>, grid, dim3(256), 0, s, part, groups, n, d, (float *)out0,
                            (float *)out1);
@@ -478,7 +478,7 @@ static lora_status_t launch_backward(const layernorm_bwd_args &a, void *dweight,
 #undef LORA_BWD
     const lora_status_t st = hip_status(hipGetLastError());
     if (st != LORA_OK || !a.part) return st;
-    return launch_column_sums(a.part, groups, 2 * a.d, a.d, DT, dweight, dbias, s);
+    return launch_column_sums(a.part, groups, 2ll * a.d, a.d, DT, dweight, dbias, s);
 }
 
 lora_status_t launch_layernorm_backward(const void *dy, const void *dres, const void *z, const void *weight,

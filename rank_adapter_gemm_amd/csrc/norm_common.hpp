@@ -49,15 +49,16 @@ __device__ __forceinline__ uint2 codes_of(const float *yr, float inv) {
 // then over the strands: 64 columns a workgroup, 4 a thread.  The first d
 // columns go to out0, the rest to out1 (either may be null), in type DT.
 template <int DT>
-__device__ __forceinline__ void column_sums(const float *part, int32_t groups, int32_t n, int32_t d,
-                                            typename elem<DT>::T *out0, typename elem<DT>::T *out1, int block) {
+__device__ __forceinline__ void column_sums(const float *part, int32_t groups, int64_t n, int32_t d,
+                                            typename elem<DT>::T *out0, typename elem<DT>::T *out1, int64_t block) {
     __shared__ float s[16][64];
-    const int strand = threadIdx.x >> 4, c0 = block * 64, c = c0 + (threadIdx.x & 15) * 4;
+    const int strand = threadIdx.x >> 4;
+    const int64_t c0 = block * 64, c = c0 + (threadIdx.x & 15) * 4;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < n)
 #pragma unroll 8
         for (int g = strand; g < groups; g += 16) {
-            const float4 f = *reinterpret_cast<const float4 *>(part + (int64_t)g * n + c);
+            const float4 f = *reinterpret_cast<const float4 *>(part + g * n + c);
             sum.x += f.x;
             sum.y += f.y;
             sum.z += f.z;
@@ -65,7 +66,7 @@ __device__ __forceinline__ void column_sums(const float *part, int32_t groups, i
         }
     *reinterpret_cast<float4 *>(&s[strand][(threadIdx.x & 15) * 4]) = sum;
     __syncthreads();
-    const int col = c0 + (int)threadIdx.x;
+    const int64_t col = c0 + threadIdx.x;
     if (threadIdx.x >= 64 || col >= n) return;
     float f = 0.0f;
 #pragma unroll
