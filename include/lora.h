@@ -685,10 +685,12 @@ lora_status_t lora_linear_act_forward_fp8(const void *x, const uint8_t *xq, cons
  *     dA_a = sum over a's rows of x^T dv,   dB_a = s sum of (x A_a)^T dp,   dbias = sum of dp
  * dx DEVICE [T, d_in], dA DEVICE [n_slots, d_in, max_rank] and dB DEVICE [n_slots,
  * max_rank, d_out] (both or neither NULL), dbias DEVICE [d_out], each overwritten, or
- * NULL: not computed.  Layouts, zeros, types, roundings and errors as
- * lora_gated_backward's (with act LORA_ACT_NONE nothing but the outputs is rounded
- * in bf16).   ws:
- * lora_workspace_bytes_linear_act_backward, cleared by lora_workspace_init. */
+ * NULL: not computed.  Layouts, zeros, types and errors as lora_gated_backward's.  bf16
+ * pools: dp is rounded once to bf16 in dx's base term, dp W^T, and kept to 2^-17 (two bf16
+ * parts) in all others; with act LORA_ACT_NONE it is dy itself, and nothing but the
+ * outputs is rounded.  There is no backward pass on an FP8 base weight: W is the weight
+ * in the pool's dtype, which a caller of lora_linear_act_forward_fp8 keeps beside the
+ * codes.  ws: lora_workspace_bytes_linear_act_backward, cleared by lora_workspace_init. */
 size_t lora_workspace_bytes_linear_act_backward(int32_t T, int32_t n_slots, int32_t max_rank, int32_t d_in,
                                                 int32_t d_out, lora_dtype_t dtype);
 lora_status_t lora_linear_act_backward(const void *x, const void *W, int32_t T, const lora_pool_t *pool,

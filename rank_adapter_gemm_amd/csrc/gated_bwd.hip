@@ -1238,6 +1238,8 @@ static lora_status_t backward(const bwd_call &c, const bwd_layout &B, hipStream_
         uint16_t *oct = ws_ptr<uint16_t>(ws, B.oct);
         int32_t *row0 = ws_ptr<int32_t>(ws, B.row0), *rank = ws_ptr<int32_t>(ws, B.rank);
         float *scale = ws_ptr<float>(ws, B.scale);
+        // dp's first part alone, rounded to bf16; its second one as a second operand of the same
+        // product: 777 x 1048 x 2744 76 -> 79 us, 2048 x 4096 x 14336 372 -> 556
         nt_args nt{{(const uint16_t *)dg, (const uint16_t *)du}, {(const uint16_t *)c.W[0], (const uint16_t *)c.W[NM - 1]},
                    F, ceil_div(F, 64) * 64, ws_ptr<int32_t>(ws, L.n_seg)};
         gemm_args g{};

@@ -433,9 +433,14 @@ lora_status_t launch_column_sums(const float *part, int32_t groups, int64_t n, i
     return hip_status(hipGetLastError());
 }
 
-// Groups of rows in the backward pass: a partial sum of each column is written
-// and read for each, so no more than keep the chip busy, of at least 4 rows where
-// there are many.  (A workgroup of narrow rows holds up to 4, some without a row.)
+// Groups of rows in the backward pass, each with a partial sum of each column to be
+// written and read: a row each up to half the most, then that half, then 4 rows each up to
+// the most.  512 threads a row and more: at most 256 (see above for more).  Narrower
+// rows, whose threads have one or two vectors of them: at most 2048, whose sums pass the
+// data up to 1024 rows.  Four such rows share a workgroup where 64 threads hold one (some
+// groups are then without a row): 34811 x 512 bf16 32 us, with 512 groups 61, 256 108.
+// Rows of 256 threads would gain by 512 groups: 1000 x 2048 15.1 us, then 11.2;
+// 34811 x 2048 96, then 83, with 256 122.
 constexpr int32_t kNormGroups = 256, kNormGroupsNarrow = 2048;
 
 static int32_t norm_groups(int32_t T, int32_t most) {

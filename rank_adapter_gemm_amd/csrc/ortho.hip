@@ -13,9 +13,9 @@
 //
 // Passes: M cannot say which way a direction that is not in X is to go.  Its
 // eigenvalue there is a rounding, 2^-53 of either sign, and c0^2 times as large after
-// each step; a negative one is not held back by the polynomial.  (Rank 1 in 16 columns:
-// 10 steps of 3.4445 2e-6 off, 12 2e-4, 16 70 times the result.)  So where the product of
-// c0^2 would pass 2^22, 6 such steps, M is made anew from X itself, that is from G P
+// each step; a negative one is not held back by the polynomial.  (On one M, rank 1 in 8 to
+// 72 columns: 8 steps of 3.4445 up to 3e-7 off, 10 3e-4, 12 0.3, 16 5e5.)  So where the
+// product of c0^2 would pass 2^22, 6 such steps, M is made anew from X itself, that is from G P
 // (k_ortho_regram, one more read of G), and the next steps' matrix is joined to P by
 // a product of all its tiles (k_ortho_join: P is symmetric but for roundings, and c0's
 // product makes those large): 7 steps of 32 x 4096 x 16 take 28 us, 6 14.6.  What is
