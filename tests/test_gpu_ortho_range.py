@@ -139,3 +139,37 @@ def test_many_steps_in_place_in_graphs_and_in_bounds(r, wide, dtype):
         torch.cuda.synchronize()
         assert torch.equal(bufs[0], ref[0]) and torch.equal(bufs[1], ref[1])
     assert (raw[:4096] == 255).all() and (raw[4096 + size:] == 255).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("r,wide", [(8, False), (16, True), (40, False), (128, True)])
+def test_zeros_stay_zero_and_others_nan_through_many_steps(r, wide, dtype):
+    g = torch.stack([few_directions(5, 264, r, i) for i in range(4)]).to(dtype)
+    g[0, :, 3:] = 0
+    g[1] = 0
+    g[2, 9, 1] = float("nan")
+    ref = run((g[3:].transpose(1, 2) if wide else g[3:]).contiguous().cuda(), [STEP] * 16)
+    out = run((g.transpose(1, 2) if wide else g).contiguous().cuda(), [STEP] * 16)
+    assert torch.equal(out[3:], ref)
+    out = out.transpose(1, 2) if wide else out
+    assert out[0, :, :3].any() and not out[0, :, 3:].any() and not out[1].any() and torch.isnan(out[2]).all()
+
+
+@pytest.mark.parametrize("count", [5, 12])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("r,wide", [(16, False), (24, True), (64, False), (72, True)])
+def test_powers_of_two_change_nothing(r, wide, dtype, count):
+    """eps is below every rounding of |g|; all sums scale with g to the bit, and the result does not."""
+    g = torch.stack([few_directions(k, 264, r, 3) for k in (5, "rows")]).to(dtype)
+    g = (g.transpose(1, 2) if wide else g).contiguous().cuda()
+    ref = run(g, [STEP] * count, eps=2.0 ** -126)
+    for e in (30, 70, 110, -30, -50):
+        h = g.double() * 2.0 ** e
+        assert torch.equal(h.to(dtype).double(), h)
+        assert torch.equal(run(h.to(dtype), [STEP] * count, eps=2.0 ** -126), ref), e
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_bf16_of_one_tile_by_64_bit_products(wide):
+    for coef in ([STEP] * 3 + [(0.5, 3000.0, 0.0)], [(2.0 ** -21, 2.0 ** -21, 0.0)]):
+        check_range(BF16, ["rows", "graded"], 264, 16, wide, coef)
